@@ -373,6 +373,138 @@ int attn_mha_fwd(const void* x_q, const void* x_kv, const void* w_q, const void*
                  int B, int n_q, int n_k, int d_model, int h, int d_k, int d_v, float scale, int mask_mode,
                  const int32_t* key_lens, void* workspace, size_t workspace_bytes, void* stream);
 
+/* flags of attn_norm_rope, attn_norm_rope_bwd, attn_paged_append (both) and attn_paged_decode (the second) */
+enum { ATTN_ROPE_INTERLEAVED = 1, ATTN_CACHE_E4M3 = 2 };
+
+/*
+ * attn_norm_rope -- what a decoder does to its projected queries and keys before the
+ * attention, in one pass: the RMS norm of every head and the position rotation.
+ * (An addition of this library; the paper adds position encodings to the embeddings.)
+ * For each head row x of d columns, with w the norm's weight,
+ *   y = x / sqrt(mean(x^2) + eps) * w          (no weights: y = x)
+ *   o_a = y_a cos t_i - y_b sin t_i,  o_b = y_b cos t_i + y_a sin t_i   for the column pairs (a, b)
+ * where t_i is angle i of the token's position: pairs (i, i + d_rot / 2), or with
+ * ATTN_ROPE_INTERLEAVED (2 i, 2 i + 1), i < d_rot / 2; columns from d_rot on are not turned.
+ *   q, k    bf16, token-major: head h of token x (of B * n) starts at q + x * q_stride + h * d
+ *           (strides in elements, multiples of 8, at least heads * d): slices of one fused
+ *           projection, for instance
+ *   q_out [B, h_q, n, d], k_out [B, h_kv, n, d]: bf16, the layout attn_fwd reads; they must
+ *           not overlap q or k
+ *   q_weight, k_weight [d]: bf16, or both NULL for no norm;   eps >= 0, finite
+ *   cos_sin [n_pos, d_rot]: float32, row = position: d_rot / 2 cosines, then their sines
+ *           (any scaling of the angles is in the table); not read when d_rot is 0
+ *   positions [B, n]: int32, or NULL for 0 .. n - 1 in every sequence (then n <= n_pos).
+ *           A token whose position is negative or, with d_rot > 0, not below n_pos, is
+ *           padding: its outputs are zero.
+ *   flags   0 or ATTN_ROPE_INTERLEAVED
+ * Supported: d in {64, 128}, d_rot a multiple of 16 in [0, d]; data pointers 16-byte
+ * aligned. fp32 arithmetic, one rounding to bf16. One launch on `stream`.
+ */
+int attn_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride, const void* q_weight,
+                   const void* k_weight, float eps, const float* cos_sin, int n_pos, int d_rot,
+                   const int32_t* positions, void* q_out, void* k_out, int B, int n, int h_q, int h_kv, int d,
+                   int flags, void* stream);
+
+/*
+ * attn_norm_rope_bwd_workspace_size -- bytes of device workspace attn_norm_rope_bwd needs
+ * with a norm (each CTA's share of the weights' gradients). Returns 0 for an invalid shape.
+ */
+size_t attn_norm_rope_bwd_workspace_size(int B, int n, int h_q, int h_kv, int d);
+
+/*
+ * attn_norm_rope_bwd -- gradients of attn_norm_rope. With g the gradient of one output row,
+ * gy that row turned back, r = 1 / sqrt(mean(x^2) + eps) and u = gy w:
+ *   dx = r (u - x r^2 mean(u x)),   dw = sum over tokens and heads of gy x r   (no norm: dx = gy)
+ *   q, k, q_stride .. positions, B .. flags: as in the forward call
+ *   dq_out [B, h_q, n, d], dk_out [B, h_kv, n, d]: bf16, what attn_bwd returns
+ *   dq, dk  bf16, token-major with strides dq_stride, dk_stride; written in full (columns
+ *           between the heads' and the stride are left as they were); no overlap with inputs
+ *   dq_weight, dk_weight [d]: float32, written; required with a norm, NULL without
+ *   workspace: with a norm, device scratch of at least attn_norm_rope_bwd_workspace_size
+ *           bytes, 16-byte aligned, owned by the caller, contents undefined on return;
+ *           concurrent calls must not share it. Without a norm it may be NULL.
+ * Padding tokens get dq = dk = 0 and add nothing to the weights' gradients. fp32
+ * arithmetic; no atomics: the same bits on every run. Two launches with a norm, else one.
+ */
+int attn_norm_rope_bwd(const void* q, const void* k, int64_t q_stride, int64_t k_stride, const void* q_weight,
+                       const void* k_weight, float eps, const float* cos_sin, int n_pos, int d_rot,
+                       const int32_t* positions, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                       int64_t dq_stride, int64_t dk_stride, float* dq_weight, float* dk_weight, int B, int n,
+                       int h_q, int h_kv, int d, int flags, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * attn_paged_append -- writes the keys and values of T new tokens into a paged cache, with
+ * the norm and rotation of attn_norm_rope applied to the keys on the way, and (q not NULL)
+ * normalises and rotates the tokens' queries: the step before attn_paged_decode, or a
+ * packed batch of prompts of different lengths. (An addition of this library.)
+ *   q [T, h_q, d], k, v [T, h_kv, d]: bf16, token-major with strides as in attn_norm_rope
+ *   q_out [T, h_q, d]: bf16, contiguous; NULL exactly when q is (then q_weight is NULL too)
+ *   q_weight, k_weight, eps, cos_sin, n_pos, d_rot: as in attn_norm_rope (values are neither
+ *           normalised nor turned)
+ *   positions [T]: int32, the token's place in its sequence: its angle and its cache row
+ *   seq_ids [T]: int32, the token's sequence, or NULL: token x belongs to sequence x (T <= n_seqs)
+ *   page_table [n_seqs, max_pages]: int32; entry (s, p) is the page that holds positions
+ *           p * page_size .. of sequence s
+ *   k_pages, v_pages [n_pages, h_kv, page_size, d]: bf16, or with ATTN_CACHE_E4M3 8-bit
+ *           floats (4 exponent, 3 mantissa bits) of value / k_scale[h] and value / v_scale[h],
+ *           rounded to nearest, saturated at 448
+ *   k_scale, v_scale [h_kv]: float32, positive; required with ATTN_CACHE_E4M3, else NULL
+ * A token is skipped whole (nothing of it is written, q_out included) when its position is
+ * negative, not below n_pos (d_rot > 0) or beyond max_pages pages, when its sequence id is
+ * outside [0, n_seqs), or when its page table entry is outside [0, n_pages): a batch padded
+ * to a fixed size marks its padding with position -1. Cache rows of no token stay as they
+ * were. Two tokens with the same sequence and position leave either's values, column by
+ * column. Supported: d in {64, 128}, d_rot a multiple of 16, any page size (n_pages * h_kv
+ * * page_size < 2^31, max_pages * page_size <= 2^30). One launch on `stream`.
+ */
+int attn_paged_append(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                      int64_t v_stride, const void* q_weight, const void* k_weight, float eps, const float* cos_sin,
+                      int n_pos, int d_rot, const int32_t* positions, const int32_t* seq_ids,
+                      const int32_t* page_table, int n_seqs, int max_pages, void* q_out, void* k_pages,
+                      void* v_pages, int n_pages, int page_size, const float* k_scale, const float* v_scale, int T,
+                      int h_q, int h_kv, int d, int flags, void* stream);
+
+/*
+ * attn_paged_decode_workspace_size -- bytes of device workspace attn_paged_decode needs.
+ * Independent of B and of the lengths (two partial results per resident CTA). Returns 0
+ * for an invalid or unsupported shape.
+ */
+size_t attn_paged_decode_workspace_size(int B, int n_q, int h_q, int h_kv, int d);
+
+/*
+ * attn_paged_decode -- attn_decode over a paged cache: the newest n_q tokens of each of B
+ * sequences attend to the cached keys up to their own position. Query head h uses
+ * key/value head h / (h_q / h_kv).
+ *   q, out  bf16 [B, n_q, h_q, d] (token-major: what attn_paged_append returns for B * n_q
+ *           tokens, and what the output projection reads)
+ *   lse     float32 [B, n_q, h_q], or NULL
+ *   k_pages, v_pages, page_table, max_pages, n_pages, page_size: the cache, as in
+ *           attn_paged_append, one page table row per sequence
+ *   cache_lens [B]: int32, tokens in the cache including the new ones, clamped to [0,
+ *           max_pages * page_size]. Query i stands at position cache_lens[b] - n_q + i; one
+ *           whose position is negative has no legal key: out = 0, lse = -inf.
+ *   window  -1, or the radius of attn_fwd_local: key j is legal for position x only if
+ *           x - window <= j <= x ...
+ *   sinks   ... or j < sinks, j <= x: the first tokens that stay visible (>= 0; nothing
+ *           without a window)
+ *   k_scale, v_scale, flags: ATTN_CACHE_E4M3 and the scales as in attn_paged_append, or 0, NULL
+ *   workspace: device scratch of at least attn_paged_decode_workspace_size(...) bytes,
+ *           16-byte aligned, owned by the caller, contents undefined on return; concurrent
+ *           calls must not share it.
+ * A page table entry outside [0, n_pages) names no page: its keys count as illegal. Cache
+ * rows behind the length are never used, whatever they hold; a key that one of the rows
+ * may not see does not reach that row, infinities and NaN included.
+ * Supported: 1 <= n_q <= 16, d in {64, 128}, h_q a multiple of h_kv, any page size (limits
+ * as in attn_paged_append). Numerics: the products accumulate in fp32 on the tensor cores,
+ * softmax statistics in fp32; the weights are rounded to bf16 (8-bit cache: to f16) before
+ * the second product, the output once to bf16. One or two launches on `stream`.
+ */
+int attn_paged_decode(const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,
+                      const int32_t* page_table, const int32_t* cache_lens, int B, int n_q, int h_q, int h_kv, int d,
+                      int n_pages, int page_size, int max_pages, float scale, int window, int sinks,
+                      const float* k_scale, const float* v_scale, int flags, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
 /*
  * attn_fault_status -- synchronises `stream`, then reports whether any kernel of
  * this library on the current device gave up waiting on one of its internal

@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libattn_gb3
 
 ATTN_OK, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA, ATTN_ERR_TIMEOUT = 0, -1, -2, -3, -4
 MASK_NONE, MASK_CAUSAL, MASK_KEY_PADDING = 0, 1, 2
+ROPE_INTERLEAVED, CACHE_E4M3 = 1, 2  # flags of the rotation and of the paged cache
 BWD_DETERMINISTIC = 1  # attn_bwd flag: the two-kernel schedule, bit-identical on every run
 
 _lib = None
@@ -74,6 +75,22 @@ def lib() -> ctypes.CDLL:
         L.attn_mha_workspace_size.restype = ctypes.c_size_t
         L.attn_mha_fwd.argtypes = [vp] * 11 + [i, i, i, i, i, i, i, f, i, vp, vp, ctypes.c_size_t, vp]
         L.attn_mha_fwd.restype = i
+        i64, sz = ctypes.c_int64, ctypes.c_size_t
+        # q, k, strides, weights, eps, cos_sin, n_pos, d_rot, positions
+        rope = [vp, vp, i64, i64, vp, vp, f, vp, i, i, vp]
+        L.attn_norm_rope.argtypes = rope + [vp, vp, i, i, i, i, i, i, vp]
+        L.attn_norm_rope.restype = i
+        L.attn_norm_rope_bwd_workspace_size.argtypes = [i, i, i, i, i]
+        L.attn_norm_rope_bwd_workspace_size.restype = sz
+        L.attn_norm_rope_bwd.argtypes = rope + [vp, vp, vp, vp, i64, i64, vp, vp, i, i, i, i, i, i, vp, sz, vp]
+        L.attn_norm_rope_bwd.restype = i
+        L.attn_paged_append.argtypes = [vp, vp, vp, i64, i64, i64, vp, vp, f, vp, i, i, vp, vp, vp, i, i, vp, vp, vp,
+                                        i, i, vp, vp, i, i, i, i, i, vp]
+        L.attn_paged_append.restype = i
+        L.attn_paged_decode_workspace_size.argtypes = [i, i, i, i, i]
+        L.attn_paged_decode_workspace_size.restype = sz
+        L.attn_paged_decode.argtypes = [vp] * 7 + [i] * 8 + [f, i, i, vp, vp, i, vp, sz, vp]
+        L.attn_paged_decode.restype = i
         L.attn_fault_status.argtypes = [vp, i, ctypes.POINTER(ctypes.c_uint32)]
         L.attn_fault_status.restype = i
         L.attn_status_string.argtypes = [i]
@@ -435,6 +452,220 @@ def attn_linear(x, w, y, bias=None, stream=None):
     if st != ATTN_OK:
         raise AttnError(st, "attn_linear")
     return y
+
+
+def _same_device(first, *others):
+    """The launch goes to the current device: every tensor has to be there."""
+    dev = first.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on one device")
+
+
+def _check_rows(t, name, ndim):
+    """bf16 head rows by token, [..., heads, d]: a token's heads side by side, tokens one stride apart."""
+    if t.dtype != torch.bfloat16 or t.dim() != ndim or not t.is_cuda:
+        raise ValueError(f"{name} must be a {ndim}-D CUDA bfloat16 tensor, got {t.dtype} {tuple(t.shape)}")
+    st, sh = t.stride(), t.shape
+    if (st[-1] != 1 or (sh[-2] != 1 and st[-2] != sh[-1])
+            or (ndim == 4 and sh[0] != 1 and sh[1] != 1 and st[0] != sh[1] * st[1])):
+        raise ValueError(f"{name}: a token's heads must lie side by side and tokens one stride apart, got strides {st}")
+
+
+def _row_stride(t):
+    """Elements between tokens; of a single token, those of its heads."""
+    if t.dim() == 4 and t.shape[1] == 1:
+        return t.stride(0) if t.shape[0] > 1 else t.shape[2] * t.shape[3]
+    return t.stride(-3) if t.shape[-3] > 1 else t.shape[-2] * t.shape[-1]
+
+
+def _check_rotation(cos_sin, q_weight, k_weight, d):
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _check(t, n, torch.bfloat16, 1)
+            if t.shape[0] != d:
+                raise ValueError(f"{n} must have shape [{d}]")
+    if cos_sin is None:
+        return 0, 0
+    _check(cos_sin, "cos_sin", torch.float32, 2)
+    return cos_sin.shape
+
+
+def attn_norm_rope(q, k, q_out, k_out, cos_sin, q_weight=None, k_weight=None, positions=None, eps=1e-6,
+                   interleaved=False, stream=None):
+    """RMS norm of every head (with weights) and position rotation, bf16: ``q [B, n, h_q, d]``
+    and ``k [B, n, h_kv, d]`` token-major (views of a fused projection are fine) into
+    ``q_out [B, h_q, n, d]`` and ``k_out [B, h_kv, n, d]``. ``cos_sin`` is float32
+    ``[n_pos, d_rot]`` (cosines, then sines; None: no rotation), ``positions`` int32 ``[B, n]``
+    or None for 0 .. n - 1; ``interleaved`` turns adjacent columns instead of the halves."""
+    _check_rows(q, "q", 4)
+    _check_rows(k, "k", 4)
+    _check(q_out, "q_out", torch.bfloat16)
+    _check(k_out, "k_out", torch.bfloat16)
+    B, n, h_q, d = q.shape
+    h_kv = k.shape[2]
+    if k.shape != (B, n, h_kv, d) or q_out.shape != (B, h_q, n, d) or k_out.shape != (B, h_kv, n, d):
+        raise ValueError(f"shape mismatch: q{tuple(q.shape)} k{tuple(k.shape)} q_out{tuple(q_out.shape)} "
+                         f"k_out{tuple(k_out.shape)}")
+    n_pos, d_rot = _check_rotation(cos_sin, q_weight, k_weight, d)
+    if positions is not None:
+        _check(positions, "positions", torch.int32, 2)
+        if positions.shape != (B, n):
+            raise ValueError("positions must have shape [B, n]")
+    _same_device(q, k, q_out, k_out, cos_sin, q_weight, k_weight, positions)
+    st = lib().attn_norm_rope(_ptr(q), _ptr(k), _row_stride(q), _row_stride(k), _ptr(q_weight), _ptr(k_weight),
+                              float(eps), _ptr(cos_sin), n_pos, d_rot, _ptr(positions), _ptr(q_out), _ptr(k_out), B, n,
+                              h_q, h_kv, d, ROPE_INTERLEAVED if interleaved else 0, _stream_handle(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_norm_rope")
+    return q_out, k_out
+
+
+def attn_norm_rope_bwd_workspace_size(B, n, h_q, h_kv, d) -> int:
+    return int(lib().attn_norm_rope_bwd_workspace_size(B, n, h_q, h_kv, d))
+
+
+def attn_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, workspace, cos_sin, q_weight=None, k_weight=None, dq_weight=None,
+                       dk_weight=None, positions=None, eps=1e-6, interleaved=False, stream=None):
+    """Gradients of attn_norm_rope: ``dq_out``, ``dk_out`` (shaped like its outputs) into
+    ``dq``, ``dk`` (token-major like ``q``, ``k``) and, with a norm, float32 ``dq_weight``,
+    ``dk_weight [d]``; ``workspace``: a CUDA tensor of at least
+    ``attn_norm_rope_bwd_workspace_size`` bytes (None without a norm)."""
+    for t, m in ((q, "q"), (k, "k"), (dq, "dq"), (dk, "dk")):
+        _check_rows(t, m, 4)
+    _check(dq_out, "dq_out", torch.bfloat16)
+    _check(dk_out, "dk_out", torch.bfloat16)
+    B, n, h_q, d = q.shape
+    h_kv = k.shape[2]
+    if (k.shape != (B, n, h_kv, d) or dq_out.shape != (B, h_q, n, d) or dk_out.shape != (B, h_kv, n, d)
+            or dq.shape != q.shape or dk.shape != k.shape):
+        raise ValueError("shape mismatch between q, k, their gradients and the outputs' gradients")
+    n_pos, d_rot = _check_rotation(cos_sin, q_weight, k_weight, d)
+    for t, m in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
+        if t is not None:
+            _check(t, m, torch.float32, 1)
+            if t.shape[0] != d:
+                raise ValueError(f"{m} must have shape [{d}]")
+    if positions is not None:
+        _check(positions, "positions", torch.int32, 2)
+        if positions.shape != (B, n):
+            raise ValueError("positions must have shape [B, n]")
+    if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    _same_device(q, k, dq_out, dk_out, dq, dk, workspace, cos_sin, q_weight, k_weight, dq_weight, dk_weight, positions)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = lib().attn_norm_rope_bwd(_ptr(q), _ptr(k), _row_stride(q), _row_stride(k), _ptr(q_weight), _ptr(k_weight),
+                                  float(eps), _ptr(cos_sin), n_pos, d_rot, _ptr(positions), _ptr(dq_out), _ptr(dk_out),
+                                  _ptr(dq), _ptr(dk), _row_stride(dq), _row_stride(dk), _ptr(dq_weight),
+                                  _ptr(dk_weight), B, n, h_q, h_kv, d, ROPE_INTERLEAVED if interleaved else 0,
+                                  _ptr(workspace), nbytes, _stream_handle(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_norm_rope_bwd")
+    return dq, dk
+
+
+def _check_pages(k_pages, v_pages, k_scale, v_scale, page_table, h_kv, d):
+    """Flags of a paged cache ``[n_pages, h_kv, page_size, d]`` in bf16 or float8_e4m3fn."""
+    e4m3 = k_pages.dtype == torch.float8_e4m3fn
+    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _check(t, n, torch.float8_e4m3fn if e4m3 else torch.bfloat16)
+    if k_pages.shape != v_pages.shape or k_pages.shape[1] != h_kv or k_pages.shape[3] != d:
+        raise ValueError(f"k_pages, v_pages must be [n_pages, {h_kv}, page_size, {d}], got {tuple(k_pages.shape)} "
+                         f"{tuple(v_pages.shape)}")
+    _check(page_table, "page_table", torch.int32, 2)
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if (t is not None) != e4m3:
+            raise ValueError(f"{n} is required with an e4m3 cache, and only there")
+        if t is not None:
+            _check(t, n, torch.float32, 1)
+            if t.shape[0] != h_kv:
+                raise ValueError(f"{n} must have shape [{h_kv}]")
+    return CACHE_E4M3 if e4m3 else 0
+
+
+def attn_paged_append(k, v, k_pages, v_pages, positions, page_table, seq_ids=None, q=None, q_out=None, cos_sin=None,
+                      q_weight=None, k_weight=None, k_scale=None, v_scale=None, eps=1e-6, interleaved=False,
+                      stream=None):
+    """Writes new tokens' keys (normalised and rotated as in attn_norm_rope) and values,
+    ``k, v [T, h_kv, d]`` bf16, into the pages ``k_pages, v_pages [n_pages, h_kv, page_size, d]``
+    (bf16, or float8_e4m3fn with the float32 scales ``k_scale, v_scale [h_kv]``), and the
+    tokens' queries ``q [T, h_q, d]`` into ``q_out`` (contiguous). ``positions`` int32 ``[T]``
+    (negative: padding, skipped), ``seq_ids`` int32 ``[T]`` (None: token x is sequence x's),
+    ``page_table`` int32 ``[n_seqs, max_pages]``."""
+    _check_rows(k, "k", 3)
+    _check_rows(v, "v", 3)
+    T, h_kv, d = k.shape
+    if v.shape != k.shape:
+        raise ValueError(f"shape mismatch: k{tuple(k.shape)} v{tuple(v.shape)}")
+    flags = _check_pages(k_pages, v_pages, k_scale, v_scale, page_table, h_kv, d)
+    h_q = q_stride = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        _check_rows(q, "q", 3)
+        _check(q_out, "q_out", torch.bfloat16, 3)
+        h_q, q_stride = q.shape[1], _row_stride(q)
+        if q.shape != (T, h_q, d) or q_out.shape != q.shape:
+            raise ValueError(f"shape mismatch: q{tuple(q.shape)} q_out{tuple(q_out.shape)} k{tuple(k.shape)}")
+    n_pos, d_rot = _check_rotation(cos_sin, q_weight, k_weight, d)
+    _check(positions, "positions", torch.int32, 1)
+    if positions.shape[0] != T:
+        raise ValueError("positions must have shape [T]")
+    if seq_ids is not None:
+        _check(seq_ids, "seq_ids", torch.int32, 1)
+        if seq_ids.shape[0] != T:
+            raise ValueError("seq_ids must have shape [T]")
+    _same_device(k, v, k_pages, v_pages, positions, page_table, seq_ids, q, q_out, cos_sin, q_weight, k_weight,
+                 k_scale, v_scale)
+    st = lib().attn_paged_append(_ptr(q), _ptr(k), _ptr(v), q_stride, _row_stride(k), _row_stride(v), _ptr(q_weight),
+                                 _ptr(k_weight), float(eps), _ptr(cos_sin), n_pos, d_rot, _ptr(positions),
+                                 _ptr(seq_ids), _ptr(page_table), page_table.shape[0], page_table.shape[1],
+                                 _ptr(q_out), _ptr(k_pages), _ptr(v_pages), k_pages.shape[0], k_pages.shape[2],
+                                 _ptr(k_scale), _ptr(v_scale), T, h_q, h_kv, d,
+                                 flags | (ROPE_INTERLEAVED if interleaved else 0), _stream_handle(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_append")
+    return q_out
+
+
+def attn_paged_decode_workspace_size(B, n_q, h_q, h_kv, d) -> int:
+    return int(lib().attn_paged_decode_workspace_size(B, n_q, h_q, h_kv, d))
+
+
+def attn_paged_decode(q, k_pages, v_pages, out, page_table, cache_lens, workspace, lse=None, scale=None, window=-1,
+                      sinks=0, k_scale=None, v_scale=None, stream=None):
+    """The newest ``n_q`` tokens of each sequence, ``q [B, n_q, h_q, d]`` bf16, attend over the
+    paged cache (see attn_paged_append) of ``cache_lens`` int32 ``[B]`` tokens, the new ones
+    included, into ``out`` (like ``q``) and optional float32 ``lse [B, n_q, h_q]``. ``window`` >= 0:
+    only keys within that distance and the first ``sinks``. ``workspace``: a CUDA tensor of
+    at least ``attn_paged_decode_workspace_size`` bytes."""
+    _check(q, "q", torch.bfloat16)
+    _check(out, "out", torch.bfloat16)
+    B, n_q, h_q, d = q.shape
+    h_kv = k_pages.shape[1] if k_pages.dim() == 4 else 0
+    flags = _check_pages(k_pages, v_pages, k_scale, v_scale, page_table, h_kv, d)
+    _check(cache_lens, "cache_lens", torch.int32, 1)
+    if out.shape != q.shape or page_table.shape[0] != B or cache_lens.shape[0] != B:
+        raise ValueError("shape mismatch between q, out, page_table and cache_lens")
+    if lse is not None:
+        _check(lse, "lse", torch.float32, 3)
+        if lse.shape != (B, n_q, h_q):
+            raise ValueError("lse must have shape [B, n_q, h_q]")
+    if not (workspace.is_cuda and workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    _same_device(q, k_pages, v_pages, out, page_table, cache_lens, workspace, lse, k_scale, v_scale)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    st = lib().attn_paged_decode(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(lse), _ptr(page_table),
+                                 _ptr(cache_lens), B, n_q, h_q, h_kv, d, k_pages.shape[0], k_pages.shape[2],
+                                 page_table.shape[1], float(scale), int(window), int(sinks), _ptr(k_scale),
+                                 _ptr(v_scale), flags, _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                 _stream_handle(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_decode")
+    return out
 
 
 def _internal_arm_wait_timeout(wait_ns: int, skip_v_tile: int) -> None:

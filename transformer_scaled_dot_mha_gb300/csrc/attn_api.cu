@@ -44,6 +44,49 @@ int check_common(const void* q, const void* k, const void* v, const void* out, c
   return ATTN_OK;
 }
 
+// Heads' rows laid out by token: `tokens` rows of h * d columns, `stride` elements apart.
+bool bad_rows(const void* x, long long tokens, int64_t stride, int h, int d) {
+  return !x || !aligned(x, 16) || stride < (long long)h * d || stride % 8 != 0 || stride > (1LL << 40) / tokens;
+}
+
+// The norm and rotation arguments that attn_norm_rope, its gradients and attn_paged_append
+// share; d is checked by the caller.
+int check_rope(const void* q_weight, const void* k_weight, float eps, const float* cos_sin, int n_pos, int d_rot,
+               int d) {
+  if ((q_weight && !aligned(q_weight, 16)) || (k_weight && !aligned(k_weight, 16))) return ATTN_ERR_INVALID;
+  if (!std::isfinite(eps) || eps < 0.0f) return ATTN_ERR_INVALID;
+  if (d_rot < 0 || d_rot > d) return ATTN_ERR_INVALID;
+  if (d_rot > 0 && (!cos_sin || !aligned(cos_sin, 16) || n_pos <= 0)) return ATTN_ERR_INVALID;
+  return d_rot % 16 == 0 ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
+}
+
+// The checks of attn_norm_rope and its gradients on the forward's operands.
+int check_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride, const void* q_weight,
+                    const void* k_weight, float eps, const float* cos_sin, int n_pos, int d_rot,
+                    const int32_t* positions, int B, int n, int h_q, int h_kv, int d, int flags) {
+  if (B <= 0 || n <= 0 || h_q <= 0 || h_kv <= 0 || d <= 0) return ATTN_ERR_INVALID;
+  const long long tokens = (long long)B * n;
+  if (tokens > 0x7fffff00LL || (long long)h_q + h_kv > (1LL << 40) / d / tokens) return ATTN_ERR_INVALID;
+  if (bad_rows(q, tokens, q_stride, h_q, d) || bad_rows(k, tokens, k_stride, h_kv, d)) return ATTN_ERR_INVALID;
+  if ((q_weight == nullptr) != (k_weight == nullptr)) return ATTN_ERR_INVALID;
+  if (flags & ~ATTN_ROPE_INTERLEAVED) return ATTN_ERR_INVALID;
+  if (positions && !aligned(positions, 4)) return ATTN_ERR_INVALID;
+  if (!positions && d_rot > 0 && n > n_pos) return ATTN_ERR_INVALID;
+  const int st = check_rope(q_weight, k_weight, eps, cos_sin, n_pos, d_rot, d);
+  if (st != ATTN_OK) return st;
+  return d == 64 || d == 128 ? ATTN_OK : ATTN_ERR_UNSUPPORTED;
+}
+
+// A paged cache's geometry: rows addressed by 31 bits, lengths by 30.
+bool bad_cache(const void* k_pages, const void* v_pages, int n_pages, int page_size, int max_pages, int h_kv,
+               const int32_t* page_table) {
+  if (!k_pages || !v_pages || !aligned(k_pages, 16) || !aligned(v_pages, 16)) return true;
+  if (!page_table || !aligned(page_table, 4)) return true;
+  if (n_pages <= 0 || page_size <= 0 || max_pages <= 0 || h_kv <= 0) return true;
+  if ((long long)n_pages * page_size > 0x7fffffffLL / h_kv) return true;
+  return (long long)max_pages * page_size > (1LL << 30);
+}
+
 }  // namespace
 
 extern "C" {
@@ -279,6 +322,110 @@ int attn_mha_fwd(const void* x_q, const void* x_kv, const void* w_q, const void*
   attn::MhaArgs a{x_q, x_kv, w_q, b_q, w_k, b_k, w_v, b_v, w_o, b_o, out, B, n_q, n_k, d_model, h, d_k, scale,
                   mask_mode, key_lens, static_cast<cudaStream_t>(stream)};
   return attn::launch_attn_mha(a, enc, workspace);
+}
+
+int attn_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride, const void* q_weight,
+                   const void* k_weight, float eps, const float* cos_sin, int n_pos, int d_rot,
+                   const int32_t* positions, void* q_out, void* k_out, int B, int n, int h_q, int h_kv, int d,
+                   int flags, void* stream) {
+  const int st = check_norm_rope(q, k, q_stride, k_stride, q_weight, k_weight, eps, cos_sin, n_pos, d_rot, positions,
+                                 B, n, h_q, h_kv, d, flags);
+  if (st != ATTN_OK) return st;
+  if (!q_out || !k_out || !aligned(q_out, 16) || !aligned(k_out, 16)) return ATTN_ERR_INVALID;
+  attn::RopeArgs a{q, k, q_stride, k_stride, q_weight, k_weight, eps, cos_sin, n_pos, d_rot, positions, q_out, k_out,
+                   B, n, h_q, h_kv, d, (flags & ATTN_ROPE_INTERLEAVED) != 0, static_cast<cudaStream_t>(stream)};
+  return attn::launch_attn_norm_rope(a);
+}
+
+size_t attn_norm_rope_bwd_workspace_size(int B, int n, int h_q, int h_kv, int d) {
+  if (B <= 0 || n <= 0 || h_q <= 0 || h_kv <= 0 || (d != 64 && d != 128)) return 0;
+  const long long tokens = (long long)B * n;
+  if (tokens > 0x7fffff00LL || (long long)h_q + h_kv > (1LL << 40) / d / tokens) return 0;
+  return attn::norm_rope_bwd_workspace_bytes(B, n, h_q, h_kv, d);
+}
+
+int attn_norm_rope_bwd(const void* q, const void* k, int64_t q_stride, int64_t k_stride, const void* q_weight,
+                       const void* k_weight, float eps, const float* cos_sin, int n_pos, int d_rot,
+                       const int32_t* positions, const void* dq_out, const void* dk_out, void* dq, void* dk,
+                       int64_t dq_stride, int64_t dk_stride, float* dq_weight, float* dk_weight, int B, int n,
+                       int h_q, int h_kv, int d, int flags, void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = check_norm_rope(q, k, q_stride, k_stride, q_weight, k_weight, eps, cos_sin, n_pos, d_rot, positions,
+                                 B, n, h_q, h_kv, d, flags);
+  if (st != ATTN_OK) return st;
+  if (!dq_out || !dk_out || !aligned(dq_out, 16) || !aligned(dk_out, 16)) return ATTN_ERR_INVALID;
+  const long long tokens = (long long)B * n;
+  if (bad_rows(dq, tokens, dq_stride, h_q, d) || bad_rows(dk, tokens, dk_stride, h_kv, d)) return ATTN_ERR_INVALID;
+  if (q_weight) {
+    if (!dq_weight || !dk_weight || !aligned(dq_weight, 4) || !aligned(dk_weight, 4)) return ATTN_ERR_INVALID;
+    if (!workspace || !aligned(workspace, 16)) return ATTN_ERR_INVALID;
+    if (workspace_bytes < attn::norm_rope_bwd_workspace_bytes(B, n, h_q, h_kv, d)) return ATTN_ERR_INVALID;
+  } else if (dq_weight || dk_weight) {
+    return ATTN_ERR_INVALID;  // no norm: there is no such gradient
+  }
+  attn::RopeBwdArgs a{q, k, q_stride, k_stride, q_weight, k_weight, eps, cos_sin, n_pos, d_rot, positions, dq_out,
+                      dk_out, dq, dk, dq_stride, dk_stride, dq_weight, dk_weight, B, n, h_q, h_kv, d,
+                      (flags & ATTN_ROPE_INTERLEAVED) != 0, static_cast<cudaStream_t>(stream)};
+  return attn::launch_attn_norm_rope_bwd(a, workspace);
+}
+
+int attn_paged_append(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                      int64_t v_stride, const void* q_weight, const void* k_weight, float eps, const float* cos_sin,
+                      int n_pos, int d_rot, const int32_t* positions, const int32_t* seq_ids,
+                      const int32_t* page_table, int n_seqs, int max_pages, void* q_out, void* k_pages,
+                      void* v_pages, int n_pages, int page_size, const float* k_scale, const float* v_scale, int T,
+                      int h_q, int h_kv, int d, int flags, void* stream) {
+  if (T <= 0 || T > 0x7fffff00 || h_kv <= 0 || d <= 0 || n_seqs <= 0) return ATTN_ERR_INVALID;
+  if (flags & ~(ATTN_ROPE_INTERLEAVED | ATTN_CACHE_E4M3)) return ATTN_ERR_INVALID;
+  if ((long long)h_kv + (q && h_q > 0 ? h_q : 0) > (1LL << 40) / d / T) return ATTN_ERR_INVALID;
+  if (bad_cache(k_pages, v_pages, n_pages, page_size, max_pages, h_kv, page_table)) return ATTN_ERR_INVALID;
+  if (bad_rows(k, T, k_stride, h_kv, d) || bad_rows(v, T, v_stride, h_kv, d)) return ATTN_ERR_INVALID;
+  if (q) {
+    if (h_q <= 0 || bad_rows(q, T, q_stride, h_q, d) || !q_out || !aligned(q_out, 16)) return ATTN_ERR_INVALID;
+    if ((q_weight == nullptr) != (k_weight == nullptr)) return ATTN_ERR_INVALID;
+  } else if (q_out || q_weight) {
+    return ATTN_ERR_INVALID;
+  }
+  if (!positions || !aligned(positions, 4) || (seq_ids && !aligned(seq_ids, 4))) return ATTN_ERR_INVALID;
+  if (!seq_ids && T > n_seqs) return ATTN_ERR_INVALID;
+  const bool e4m3 = (flags & ATTN_CACHE_E4M3) != 0;
+  if ((k_scale != nullptr) != e4m3 || (v_scale != nullptr) != e4m3) return ATTN_ERR_INVALID;
+  if (e4m3 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))) return ATTN_ERR_INVALID;
+  const int st = check_rope(q_weight, k_weight, eps, cos_sin, n_pos, d_rot, d);
+  if (st != ATTN_OK) return st;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  attn::AppendArgs a{q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, eps, cos_sin, n_pos, d_rot,
+                     positions, seq_ids, page_table, n_seqs, max_pages, q_out, k_pages, v_pages, n_pages, page_size,
+                     k_scale, v_scale, T, h_q, h_kv, d, (flags & ATTN_ROPE_INTERLEAVED) != 0, e4m3,
+                     static_cast<cudaStream_t>(stream)};
+  return attn::launch_attn_paged_append(a);
+}
+
+size_t attn_paged_decode_workspace_size(int B, int n_q, int h_q, int h_kv, int d) {
+  if (B <= 0 || n_q < 1 || n_q > 16 || h_q <= 0 || h_kv <= 0 || h_q % h_kv != 0 || (d != 64 && d != 128)) return 0;
+  return attn::paged_decode_workspace_bytes(n_q, h_q / h_kv, d);
+}
+
+int attn_paged_decode(const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,
+                      const int32_t* page_table, const int32_t* cache_lens, int B, int n_q, int h_q, int h_kv, int d,
+                      int n_pages, int page_size, int max_pages, float scale, int window, int sinks,
+                      const float* k_scale, const float* v_scale, int flags, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  if (!q || !out || !cache_lens || !workspace) return ATTN_ERR_INVALID;
+  if (B <= 0 || n_q <= 0 || h_q <= 0 || h_kv <= 0 || d <= 0 || h_q % h_kv != 0) return ATTN_ERR_INVALID;
+  if (!std::isfinite(scale) || window < -1 || sinks < 0 || (flags & ~ATTN_CACHE_E4M3)) return ATTN_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(cache_lens, 4) ||
+      (lse && !aligned(lse, 4)))
+    return ATTN_ERR_INVALID;
+  if (bad_cache(k_pages, v_pages, n_pages, page_size, max_pages, h_kv, page_table)) return ATTN_ERR_INVALID;
+  const bool e4m3 = (flags & ATTN_CACHE_E4M3) != 0;
+  if ((k_scale != nullptr) != e4m3 || (v_scale != nullptr) != e4m3) return ATTN_ERR_INVALID;
+  if (e4m3 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))) return ATTN_ERR_INVALID;
+  if (n_q > 16 || (d != 64 && d != 128)) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)B * n_q > (1LL << 40) / d / h_q) return ATTN_ERR_INVALID;
+  if (workspace_bytes < attn::paged_decode_workspace_bytes(n_q, h_q / h_kv, d)) return ATTN_ERR_INVALID;
+  attn::PagedArgs a{q, k_pages, v_pages, out, lse, page_table, cache_lens, B, n_q, h_q, h_kv, d, n_pages, page_size,
+                    max_pages, scale, window, sinks, k_scale, v_scale, e4m3, static_cast<cudaStream_t>(stream)};
+  return attn::launch_attn_paged_decode(a, workspace);
 }
 
 int attn_fault_status(void* stream, int clear, uint32_t* fault_code) {

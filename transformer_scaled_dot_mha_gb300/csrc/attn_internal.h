@@ -120,6 +120,91 @@ struct LinearJob {
   int M, N, K;
 };
 
+// Validated arguments of one attn_norm_rope call. Strides: elements between tokens.
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  long long q_stride, k_stride;
+  const void* q_weight;  // nullptr: no norm
+  const void* k_weight;
+  float eps;
+  const float* cos_sin;
+  int n_pos, d_rot;
+  const int32_t* positions;  // nullptr: 0 .. n - 1
+  void* q_out;
+  void* k_out;
+  int B, n, h_q, h_kv, d;
+  bool pairs;  // adjacent columns turn together
+  cudaStream_t stream;
+};
+
+// Validated arguments of one attn_norm_rope_bwd call.
+struct RopeBwdArgs {
+  const void* q;
+  const void* k;
+  long long q_stride, k_stride;
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  const float* cos_sin;
+  int n_pos, d_rot;
+  const int32_t* positions;
+  const void* dq_out;
+  const void* dk_out;
+  void* dq;
+  void* dk;
+  long long dq_stride, dk_stride;
+  float* dq_weight;
+  float* dk_weight;
+  int B, n, h_q, h_kv, d;
+  bool pairs;
+  cudaStream_t stream;
+};
+
+// Validated arguments of one attn_paged_append call.
+struct AppendArgs {
+  const void* q;  // nullptr: keys and values only
+  const void* k;
+  const void* v;
+  long long q_stride, k_stride, v_stride;
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+  const float* cos_sin;
+  int n_pos, d_rot;
+  const int32_t* positions;
+  const int32_t* seq_ids;  // nullptr: token t belongs to sequence t
+  const int32_t* page_table;
+  int n_seqs, max_pages;
+  void* q_out;
+  void* k_pages;
+  void* v_pages;
+  int n_pages, page_size;
+  const float* k_scale;
+  const float* v_scale;
+  int T, h_q, h_kv, d;
+  bool pairs, e4m3;
+  cudaStream_t stream;
+};
+
+// Validated arguments of one attn_paged_decode call.
+struct PagedArgs {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  void* out;
+  float* lse;
+  const int32_t* page_table;
+  const int32_t* cache_lens;
+  int B, n_q, h_q, h_kv, d, n_pages, page_size, max_pages;
+  float scale;
+  int window, sinks;  // window -1: none
+  const float* k_scale;
+  const float* v_scale;
+  bool e4m3;
+  cudaStream_t stream;
+};
+
 int launch_attn_tc(const TcArgs& a, PFN_encodeTiled enc);   // attn_fwd_tc.cu
 int launch_attn_f32(const F32Args& a);                       // attn_fwd_f32.cu
 int read_fault_word(cudaStream_t stream, int clear, uint32_t* out);  // attn_fwd_tc.cu
@@ -140,6 +225,12 @@ int launch_linear(const LinearJob* jobs, int n_jobs, PFN_encodeTiled enc, cudaSt
 int read_linear_fault_word(int clear, uint32_t* out);                    // attn_linear.cu
 int launch_attn_weights(const WeightsArgs& a, PFN_encodeTiled enc);     // attn_weights.cu
 int read_weights_fault_word(int clear, uint32_t* out);                   // attn_weights.cu
+int launch_attn_norm_rope(const RopeArgs& a);                            // attn_rope.cu
+size_t norm_rope_bwd_workspace_bytes(int B, int n, int h_q, int h_kv, int d);  // attn_rope.cu
+int launch_attn_norm_rope_bwd(const RopeBwdArgs& a, void* workspace);    // attn_rope.cu
+int launch_attn_paged_append(const AppendArgs& a);                       // attn_rope.cu
+size_t paged_decode_workspace_bytes(int n_q, int group, int d);          // attn_paged.cu
+int launch_attn_paged_decode(const PagedArgs& a, void* workspace);       // attn_paged.cu
 size_t mha_workspace_bytes(int B, int n_q, int n_k, int H, int d);         // attn_mha.cu
 int launch_attn_mha(const MhaArgs& a, PFN_encodeTiled enc, void* workspace);  // attn_mha.cu
 // Host-operand pipelines (attn_host.cu, attn_bwd_host.cu): chunks of the flattened
