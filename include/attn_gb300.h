@@ -466,7 +466,7 @@ int attn_paged_append(const void* q, const void* k, const void* v, int64_t q_str
 
 /*
  * attn_paged_decode_workspace_size -- bytes of device workspace attn_paged_decode needs.
- * Independent of B and of the lengths (two partial results per resident CTA). Returns 0
+ * Independent of B and of the lengths (two partial results per resident warp). Returns 0
  * for an invalid or unsupported shape.
  */
 size_t attn_paged_decode_workspace_size(int B, int n_q, int h_q, int h_kv, int d);

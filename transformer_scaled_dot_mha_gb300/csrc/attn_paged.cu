@@ -17,24 +17,26 @@
 // The products are formed transposed, S^T = K Q^T and O^T = V^T P^T, so that the keys (then
 // the columns) are the 16 rows of an MMA and the query rows its 8 columns (NT column tiles
 // for up to 8 NT rows):
-//   * K fragments come straight from global memory: the order of the contracted columns is
-//     free, so a lane takes 16-byte pieces of "its" key (row lane / 4) and Q is loaded in
-//     the same order;
+//   * the order of the contracted columns is free: a lane takes 16-byte pieces of "its" key
+//     (row lane / 4) of K as they lie, and Q is loaded in the same order;
 //   * S^T leaves a lane with (key lane / 4, rows 2 (lane % 4) and + 1); a register
 //     transpose (movmatrix) turns the rounded P^T into the second product's operand;
-//   * V fragments too come straight from global memory: a lane holds 16 bytes of columns
-//     (all 8 or 16 of "its" columns) of each of four keys and pairs up the keys by byte
-//     permutes; the order of the columns is free again.
-// No shared memory, barrier or wait in the stream: K of the next tile is requested when the
-// scores are done with this one's registers, V when the second product is.
+//   * of V a lane takes 16 bytes of columns (all 8 or 16 of "its" columns) of each of four
+//     keys and pairs up the keys by byte permutes; the order of the columns is free again.
+// Tiles come by asynchronous copies (cp.async) into a ring of shared memory of the warp's own,
+// STAGES tiles in flight without registers to hold them, whole rows side by side in one
+// instruction: a copy of 512 contiguous bytes streams at 6.6 TB/s where the fragments' own
+// pattern (8 rows x 64 bytes) stayed at 5.0 (402 MB, 12 warps per SM). The 16-byte pieces of
+// a row are swapped by its number so that the fragment reads meet no bank conflict. Waits
+// are cp.async.wait_group, which ends by itself; no block barrier in the stream.
 //
 // Work split: the tiles (KT keys) of all (sequence, key/value head) pairs form one list,
-// cut into equal parts, one per resident CTA, by the lengths on the device -- ragged
-// batches and capacities far above the lengths cost nothing. A CTA's four warps take a
-// pair's tiles in turn and join their (m, l, O) through shared memory. A pair that lies
-// within one CTA's part is finished there; of one that does not, every part leaves (m, l, O)
-// in the workspace and attn_paged_merge_kernel joins them. When no sequence can be longer
-// than a few tiles, each pair gets a CTA of its own and there is no second launch.
+// cut into equal parts, one per resident warp, by the lengths on the device -- ragged
+// batches and capacities far above the lengths cost nothing. A warp is on its own: it
+// streams its part from one pair into the next without a pause in its copies. A pair that
+// lies within one warp's part is finished there; of one that does not, every part leaves
+// (m, l, O) in the workspace and attn_paged_merge_kernel joins them. When no sequence can be
+// longer than a few tiles, each pair gets a warp of its own and there is no second launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -50,22 +52,30 @@ namespace {
 constexpr int kSMs = 152;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCtasPerSM = 4;
-constexpr int kMinTiles = 2 * kWarps;      // tiles per CTA, at least: two per warp
-constexpr int kWholeTiles = 8 * kWarps;    // up to here a pair is one CTA's
+constexpr int kMaxParts = 3 * kSMs * kWarps;  // parts of the list of tiles at most, one per resident warp
+constexpr int kMinTiles = 2;               // tiles per part, at least
+constexpr int kWholeTiles = 8;             // up to here a pair is not worth splitting
+constexpr int kMergeThreads = 256;
 constexpr uint32_t kAll = 0xffffffffu;
 
 // D columns, NT tiles of 8 query rows, FP8: e4m3 pages.
 template <int D, int NT, bool FP8>
 struct Cfg {
-  static constexpr int KT = (D == 128 && !FP8) ? 16 : 32;  // keys per warp tile: 32 registers of K, 32 of V at most
+  static constexpr int KT = (D == 128 && !FP8) ? 16 : 32;  // keys per warp tile
   static constexpr int KB = KT / 16;                       // 16-key blocks
   static constexpr int KC = FP8 ? D / 64 : D / 32;         // 16-byte pieces of a key per lane
   static constexpr int VW = FP8 ? D / 32 : D / 16;         // 32-bit words of a value row per lane
+  static constexpr int ROW_BYTES = D * (FP8 ? 1 : 2);
+  static constexpr int PIECES = ROW_BYTES / 16;            // of a row
+  static constexpr int SIDE = 32 / PIECES;                 // rows that one copy instruction covers
   static constexpr int S = D / 16;                         // MMA steps over the columns; column tiles of O
   static constexpr int ROWS = 8 * NT;
-  static constexpr int CTAS_PER_SM = NT == 1 ? (D == 64 ? 4 : 3) : (D == 64 ? 3 : 2);
-  static constexpr int O_PITCH = D + 4;  // floats
+  static constexpr int TILE_BYTES = KT * ROW_BYTES;          // of K, and of V
+  static constexpr int CTAS_PER_SM = D == 128 && NT == 2 ? 2 : 3;  // 255 or 168 registers
+  static constexpr int PARTS = CTAS_PER_SM * kSMs * kWarps;
+  static constexpr int STAGES = 49152 / CTAS_PER_SM / (2 * TILE_BYTES);  // tiles in flight per warp: 192 KB per SM
+  static constexpr int WARP_BYTES = STAGES * 2 * TILE_BYTES;
+  static constexpr int SMEM_BYTES = kWarps * WARP_BYTES;
 };
 
 struct PagedParams {
@@ -78,12 +88,12 @@ struct PagedParams {
   const int32_t* cache_lens;
   const float* k_scale;
   const float* v_scale;
-  float* ws_o;   // [2 * CTAs][ROWS][D]: slot 2 c for the pair CTA c's part begins in, 2 c + 1 for the one it ends in
-  float* ws_ml;  // [2 * CTAs][ROWS][2]
+  float* ws_o;   // [2 * PARTS][ROWS][D]: slot 2 c for the pair that part c begins in, 2 c + 1 for the one it ends in
+  float* ws_ml;  // [2 * PARTS][ROWS][2]
   int B, n_q, h_q, h_kv, group, rows, m_tiles;  // rows = n_q * group
   int n_pages, page_size, page_shift, max_pages, max_len;  // page_shift < 0: not a power of two
   int window, sinks;
-  int whole;  // one CTA per pair, no split
+  int whole;  // one warp per pair, no split
   float scale_log2;
 };
 
@@ -119,17 +129,33 @@ __device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t x, bool high) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(h));
   return r;
 }
-__device__ __forceinline__ uint4 load16(const void* p) {
+// 16 bytes to shared memory, zeros where `there` is false (then nothing is read).
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
+               : "r"(addr)
+               : "memory");
   return r;
 }
-__device__ __forceinline__ uint2 load8(const void* p) {
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr) : "memory");
   return r;
+}
+
+// a / b; most lists of tiles are numbered in 32 bits, where the division is far shorter.
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
 }
 
 // ---------------------------------------------------------------- ranges
@@ -157,237 +183,284 @@ __device__ __forceinline__ int tiles_of(const PagedParams& p, int b) {
   return (visible_of(p, b).count + KT - 1) / KT;
 }
 
-// Where the list of tiles stands. Sequence b holds pairs (head, row tile) one after the
-// other, each of tiles_of(b) tiles.
+// The list of tiles. Sequence b holds its pairs (head, row tile) one after the other, each
+// of tiles_of(b) tiles; part c of the list is [c * part, (c + 1) * part), up to total. Made by
+// every warp for itself; before = tiles of one pair of the sequences below b_stop.
 struct Split {
-  long long total;  // tiles of all pairs
-  int ctas;         // parts: cta c has tiles [total c / ctas, total (c + 1) / ctas)
-  __device__ long long first(long long c) const { return total * c / ctas; }
+  long long total, part, before;
 };
 
-// Sums tiles_of over the sequences with the whole CTA: thread t takes `per` sequences in a
-// row; sums[t] = tiles before them. All threads get the split.
-template <int KT>
-__device__ __forceinline__ Split make_split(const PagedParams& p, long long (&sums)[kThreads + 1], int max_ctas,
-                                            int& per) {
-  __shared__ long long warp_sum[kWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  per = (p.B + kThreads - 1) / kThreads;
-  long long mine = 0;
-  for (int x = 0; x < per; ++x) {
-    const long long b = (long long)tid * per + x;
-    if (b < p.B) mine += tiles_of<KT>(p, (int)b);
-  }
-  long long x = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(kAll, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) warp_sum[warp] = x;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) x += warp_sum[w];
-  sums[tid] = x - mine;
-  if (tid == kThreads - 1) sums[kThreads] = x;
-  __syncthreads();
-  const long long pairs = (long long)p.h_kv * p.m_tiles;
+template <int KT, int PARTS>
+__device__ __forceinline__ Split make_split(const PagedParams& p, int b_stop) {
   Split s;
-  s.total = sums[kThreads] * pairs;
-  s.ctas = (int)max(1ll, min((long long)max_ctas, s.total / kMinTiles));
+  s.total = s.before = 0;
+#pragma unroll 4
+  for (int b = threadIdx.x & 31; b < p.B; b += 32) {
+    const int n = tiles_of<KT>(p, b);
+    s.total += n;
+    s.before += b < b_stop ? n : 0;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    s.total += __shfl_xor_sync(kAll, s.total, o);
+    if (b_stop > 0) s.before += __shfl_xor_sync(kAll, s.before, o);
+  }
+  s.total *= (long long)p.h_kv * p.m_tiles;
+  s.part = max((long long)kMinTiles, divide(s.total + PARTS - 1, PARTS));
   return s;
 }
 
-// The sequence that holds tile x (of the list without heads: x < sums[kThreads]), and the
-// tiles before it.
+// The sequence that holds tile x < total of the list, and the tiles of one pair before it.
 template <int KT>
-__device__ __forceinline__ int find_sequence(const PagedParams& p, const long long (&sums)[kThreads + 1], int per,
-                                             long long x, long long& before) {
-  int lo = 0, hi = kThreads - 1;  // the last t with sums[t] <= x
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (sums[mid] <= x)
-      lo = mid;
-    else
-      hi = mid - 1;
+__device__ __forceinline__ int find_sequence(const PagedParams& p, long long x, long long& before) {
+  const long long pairs = (long long)p.h_kv * p.m_tiles;
+  const int lane = threadIdx.x & 31;
+  before = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const uint32_t n = b0 + lane < p.B ? tiles_of<KT>(p, b0 + lane) : 0;  // at most 2^26
+    uint32_t sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(kAll, sum, o);
+      if (lane >= o) sum += y;
+    }
+    const uint32_t past = __ballot_sync(kAll, (before + sum) * pairs > x);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      before += __shfl_sync(kAll, sum - n, at);
+      return b0 + at;
+    }
+    before += __shfl_sync(kAll, sum, 31);
   }
-  before = sums[lo];
-  int b = lo * per;
-  for (int n = tiles_of<KT>(p, b); b + 1 < p.B && before + n <= x; n = tiles_of<KT>(p, b)) before += n, ++b;
-  return b;
 }
 
-// ---------------------------------------------------------------- one pair's tiles
-template <int D, int NT, bool FP8>
-struct Shared {
-  using C = Cfg<D, NT, FP8>;
-  float o[kWarps][C::ROWS][C::O_PITCH];
-  float m[kWarps][C::ROWS], l[kWarps][C::ROWS];
+// A place in the list.
+template <int KT>
+struct Cursor {
+  int b, pair, tile, n;  // tile of n of the pair
+  Visible vis;
+  __device__ __forceinline__ void sequence(const PagedParams& p) {
+    vis = visible_of(p, b);
+    n = (vis.count + KT - 1) / KT;
+  }
+  __device__ __forceinline__ void step(const PagedParams& p) {
+    if (++tile < n) return;
+    tile = 0;
+    if (++pair < p.h_kv * p.m_tiles) return;
+    pair = 0;
+    do {
+      ++b;
+      if (b >= p.B) return;  // past the end of the list: not used
+      sequence(p);
+    } while (n == 0);
+  }
 };
 
-// Cache row of key number x, -1 where there is none.
-__device__ __forceinline__ int cache_row(const PagedParams& p, const Visible& vis, const int32_t* pages, int head,
-                                         int x) {
-  if (x >= vis.count) return -1;
-  const int j = vis.key(x);
+// ---------------------------------------------------------------- one warp's part
+// Cache row of the key that `lane` has of the cursor's tile, -1 where there is none.
+template <int KT>
+__device__ __forceinline__ int cache_row(const PagedParams& p, const Cursor<KT>& c, int lane) {
+  const int x = c.tile * KT + lane;
+  if (lane >= KT || x >= c.vis.count) return -1;
+  const int j = c.vis.key(x);
   const int slot = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
-  const int page = __ldg(pages + slot);
+  const int page = __ldg(p.page_table + (long long)c.b * p.max_pages + slot);
   if (page < 0 || page >= p.n_pages) return -1;  // names no page: its keys count as illegal
-  return (page * p.h_kv + head) * p.page_size + (j - slot * p.page_size);
+  return (page * p.h_kv + c.pair / p.m_tiles) * p.page_size + (j - slot * p.page_size);
 }
 
-// Writes four columns of a finished row.
-template <int D>
-__device__ __forceinline__ void finish(const PagedParams& p, int b, int head, int row, int col, float4 o, float M,
-                                       float L) {
+// Where row `row` of (sequence, head) stands in out and lse.
+__device__ __forceinline__ long long out_row(const PagedParams& p, int b, int head, int row) {
   const int i = row / p.group;
-  const long long at = ((long long)b * p.n_q + i) * p.h_q + head * p.group + (row - i * p.group);
-  const bool none = M == -INFINITY && L == 0.0f;  // no legal key
-  const float inv = none ? 0.0f : 1.0f / L;
-  *reinterpret_cast<uint2*>(p.out + at * D + col) =
-      make_uint2(ptx::pack_bf16x2(o.x * inv, o.y * inv), ptx::pack_bf16x2(o.z * inv, o.w * inv));
-  if (p.lse && col == 0) p.lse[at] = none ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f;
+  return ((long long)b * p.n_q + i) * p.h_q + head * p.group + (row - i * p.group);
 }
 
-// Tiles [t0, t1) of (sequence b, key/value head, row tile mt), joined over the CTA's warps.
-// slot < 0: the pair is complete, write out and lse; else leave (m, l, O) in that slot.
+__device__ __forceinline__ float log_sum(float m, float l) { return (m + log2f(l)) * 0.69314718055994530942f; }
+
+// The rows of one pair as a warp holds them: queries, bounds, running statistics.
 template <int D, int NT, bool FP8>
-__device__ __forceinline__ void attend(const PagedParams& p, Shared<D, NT, FP8>& sh, int b, int head, int mt, int t0,
-                                       int t1, long long slot) {
+struct Rows {
   using C = Cfg<D, NT, FP8>;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t = lane & 3;
-  const Visible vis = visible_of(p, b);
-  const int32_t* pages = p.page_table + (long long)b * p.max_pages;
-  const int rows = min(p.rows - mt * C::ROWS, C::ROWS);
-  constexpr int kElem = FP8 ? 1 : 2;
-  const uint8_t* kp = static_cast<const uint8_t*>(p.k) + 16 * t;
-  const uint8_t* vp = static_cast<const uint8_t*>(p.v) + (FP8 ? D / 8 : 16) * g;
+  uint32_t q[NT][C::S][2];      // B fragments in the order of the K pieces, zeros past the last row
+  float factor[NT][2];          // of rows 2 t, 2 t + 1: scores in log2 units = factor * accumulator
+  int last[NT][2], low[NT][2];  // of the same rows, where rows differ (n_q > 1): keys they may see
+  float o[NT][C::S][4];
+  float m[NT][2], l[NT][2];     // l: this lane's share
 
-  // ---- K and V of a tile; rows_l: the lanes' cache rows
-  uint4 kr[C::KB][2][C::KC];
-  uint32_t vr[C::KB][4][C::VW];
-  auto load_k = [&](int rows_l) {
+  __device__ __forceinline__ void begin(const PagedParams& p, const Cursor<C::KT>& c, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    const int head = c.pair / p.m_tiles, row0 = (c.pair - head * p.m_tiles) * C::ROWS;
 #pragma unroll
-    for (int kb = 0; kb < C::KB; ++kb)
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + nt * 8 + g;
+      const bool real = r < p.rows;
+      const uint16_t* src = p.q + out_row(p, c.b, head, real ? r : 0) * D;
+      if (!FP8) {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int row = __shfl_sync(kAll, rows_l, kb * 16 + hf * 8 + g);
-        const uint8_t* src = kp + (long long)row * (D * kElem);
-#pragma unroll
-        for (int c = 0; c < C::KC; ++c) kr[kb][hf][c] = row >= 0 ? load16(src + 64 * c) : make_uint4(0, 0, 0, 0);
-      }
-  };
-  auto load_v = [&](int rows_l) {  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of each block
-#pragma unroll
-    for (int kb = 0; kb < C::KB; ++kb)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int row = __shfl_sync(kAll, rows_l, kb * 16 + (x >> 1) * 8 + 2 * t + (x & 1));
-        const uint8_t* src = vp + (long long)row * (D * kElem);
-        if (C::VW == 2) {
-          const uint2 w = row >= 0 ? load8(src) : make_uint2(0, 0);
-          vr[kb][x][0] = w.x, vr[kb][x][1] = w.y;
-        } else {
-#pragma unroll
-          for (int c = 0; c < C::VW / 4; ++c) {
-            const uint4 w = row >= 0 ? load16(src + 128 * c) : make_uint4(0, 0, 0, 0);
-            vr[kb][x][4 * c] = w.x, vr[kb][x][4 * c + 1] = w.y, vr[kb][x][4 * c + 2] = w.z, vr[kb][x][4 * c + 3] = w.w;
-          }
+        for (int x = 0; x < C::KC; ++x) {
+          const uint4 w = real ? __ldg(reinterpret_cast<const uint4*>(src + 8 * (t + 4 * x))) : make_uint4(0, 0, 0, 0);
+          q[nt][2 * x][0] = w.x, q[nt][2 * x][1] = w.y;
+          q[nt][2 * x + 1][0] = w.z, q[nt][2 * x + 1][1] = w.w;
         }
+        factor[nt][0] = factor[nt][1] = p.scale_log2;
+      } else {
+        // f16 operands (e4m3 is exact in f16): the row is scaled by the power of two that
+        // brings its largest entry to [1, 2). A bf16 entry above 2^-14 of the largest stays
+        // exact, a smaller one moves by at most 2^-25 of the largest.
+        float top = 0.0f;
+#pragma unroll
+        for (int x = 0; x < C::S; ++x) {
+          const uint2 w = real ? __ldg(reinterpret_cast<const uint2*>(src + 16 * (t + 4 * (x / 4)) + 4 * (x % 4)))
+                               : make_uint2(0, 0);
+          q[nt][x][0] = w.x, q[nt][x][1] = w.y;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(q[nt][x][e] << 16)),
+                                   fabsf(__uint_as_float(q[nt][x][e] & 0xffff0000u))));
+        }
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+        const int ex = min(max((int)(__float_as_uint(top) >> 23), 1), 253);  // 2^(ex - 127) <= top
+        const float down = __uint_as_float((uint32_t)(254 - ex) << 23);       // 2^(127 - ex)
+        const float up = __uint_as_float((uint32_t)ex << 23);
+#pragma unroll
+        for (int x = 0; x < C::S; ++x)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            q[nt][x][e] = pack_f16x2(__uint_as_float(q[nt][x][e] << 16) * down,
+                                     __uint_as_float(q[nt][x][e] & 0xffff0000u) * down);
+        const float mine = p.scale_log2 * __ldg(p.k_scale + head) * up;
+        factor[nt][0] = __shfl_sync(kAll, mine, 8 * t);
+        factor[nt][1] = __shfl_sync(kAll, mine, 8 * t + 4);
       }
-  };
-  auto rows_of = [&](int tile) {
-    return tile < t1 && lane < C::KT ? cache_row(p, vis, pages, head, tile * C::KT + lane) : -1;
-  };
-
-  int tile = t0 + warp;
-  int row_now = rows_of(tile), row_next = rows_of(tile + kWarps);
-  if (tile < t1) {
-    load_k(row_now);
-    load_v(row_now);
-  }
-
-  // ---- queries: B fragments in the order of the K pieces, zeros past the last row
-  uint32_t qf[NT][C::S][2];
-  float factor[NT][2];  // of rows 2 t, 2 t + 1: scores in log2 units = factor * accumulator
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = mt * C::ROWS + nt * 8 + g;
-    const bool real = r < p.rows;
-    const int i = real ? r / p.group : 0, hq = head * p.group + (real ? r - i * p.group : 0);
-    const uint16_t* src = p.q + (((long long)b * p.n_q + i) * p.h_q + hq) * D;
-    if (!FP8) {
-#pragma unroll
-      for (int c = 0; c < C::KC; ++c) {
-        const uint4 w = real ? __ldg(reinterpret_cast<const uint4*>(src + 8 * (t + 4 * c))) : make_uint4(0, 0, 0, 0);
-        qf[nt][2 * c][0] = w.x, qf[nt][2 * c][1] = w.y;
-        qf[nt][2 * c + 1][0] = w.z, qf[nt][2 * c + 1][1] = w.w;
+      for (int e = 0; e < 2; ++e) {
+        if (p.n_q > 1) {
+          last[nt][e] = c.vis.len - p.n_q + min((row0 + nt * 8 + 2 * t + e) / p.group, p.n_q - 1);
+          low[nt][e] = p.window < 0 ? 0 : last[nt][e] - p.window;
+        }
+        m[nt][e] = -INFINITY;
+        l[nt][e] = 0.0f;
       }
-      factor[nt][0] = factor[nt][1] = p.scale_log2;
-    } else {
-      // f16 operands (e4m3 is exact in f16): the row is scaled by the power of two that
-      // brings its largest entry to [1, 2). A bf16 entry above 2^-14 of the largest stays
-      // exact, a smaller one moves by at most 2^-25 of the largest.
-      uint32_t raw[C::S][2];
-      float top = 0.0f;
 #pragma unroll
-      for (int s = 0; s < C::S; ++s) {
-        const uint2 w = real ? __ldg(reinterpret_cast<const uint2*>(src + 16 * (t + 4 * (s / 4)) + 4 * (s % 4)))
-                             : make_uint2(0, 0);
-        raw[s][0] = w.x, raw[s][1] = w.y;
+      for (int x = 0; x < C::S; ++x)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          top = fmaxf(top, fmaxf(fabsf(__uint_as_float(raw[s][e] << 16)),
-                                 fabsf(__uint_as_float(raw[s][e] & 0xffff0000u))));
-      }
-      top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-      const int ex = min(max((int)(__float_as_uint(top) >> 23), 1), 253);  // 2^(ex - 127) <= top
-      const float down = __uint_as_float((uint32_t)(254 - ex) << 23);       // 2^(127 - ex)
-      const float up = __uint_as_float((uint32_t)ex << 23);
-#pragma unroll
-      for (int s = 0; s < C::S; ++s)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          qf[nt][s][e] = pack_f16x2(__uint_as_float(raw[s][e] << 16) * down,
-                                    __uint_as_float(raw[s][e] & 0xffff0000u) * down);
-      const float mine = p.scale_log2 * __ldg(p.k_scale + head) * up;
-      factor[nt][0] = __shfl_sync(kAll, mine, 8 * t);
-      factor[nt][1] = __shfl_sync(kAll, mine, 8 * t + 4);
+        for (int e = 0; e < 4; ++e) o[nt][x][e] = 0.0f;
     }
   }
 
-  // ---- bounds of this lane's rows; `same`: every row sees every key of the range
-  const bool same = p.n_q == 1;
-  int last[NT][2], low[NT][2];
-  int last_min = vis.len - 1, low_max = 0;
-  if (!same) {
+  __device__ __forceinline__ bool legal(const PagedParams& p, int j, int nt, int e) const {
+    return j <= last[nt][e] && (j >= low[nt][e] || j < p.sinks);
+  }
+
+  // Writes the pair's rows: finished (slot < 0), or (m, l, O) into the slot. A lane has 8 (16)
+  // adjacent columns of rows 2 t, 2 t + 1: whole sectors.
+  __device__ __forceinline__ void end(const PagedParams& p, const Cursor<C::KT>& c, int lane, int slot) {
+    const int g = lane >> 2, t = lane & 3;
+    const int head = c.pair / p.m_tiles, row0 = (c.pair - head * p.m_tiles) * C::ROWS;
+    const float v_scale = FP8 ? __ldg(p.v_scale + head) : 1.0f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = mt * C::ROWS + nt * 8 + 2 * t + e;
-        last[nt][e] = vis.len - p.n_q + min(r / p.group, p.n_q - 1);
-        low[nt][e] = p.window < 0 ? 0 : last[nt][e] - p.window;
+        float sum = l[nt][e];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(kAll, sum, x);
+        const int r = nt * 8 + 2 * t + e;
+        if (row0 + r >= p.rows) continue;
+        const bool none = m[nt][e] == -INFINITY && sum == 0.0f;  // no legal key
+        const float f = slot >= 0 ? v_scale : none ? 0.0f : v_scale / sum;
+        const long long at = slot >= 0 ? (long long)slot * C::ROWS + r : out_row(p, c.b, head, row0 + r);
+#pragma unroll
+        for (int x = 0; x < C::S; x += 4) {
+          const int col = FP8 ? (D / 8) * g + 2 * x : 16 * x + 8 * g;
+          float y[8];
+#pragma unroll
+          for (int z = 0; z < 4; ++z) y[2 * z] = o[nt][x + z][e] * f, y[2 * z + 1] = o[nt][x + z][2 + e] * f;
+          if (slot >= 0) {
+            float4* dst = reinterpret_cast<float4*>(p.ws_o + at * D + col);
+            dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+            dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+          } else {
+            *reinterpret_cast<uint4*>(p.out + at * D + col) =
+                make_uint4(ptx::pack_bf16x2(y[0], y[1]), ptx::pack_bf16x2(y[2], y[3]), ptx::pack_bf16x2(y[4], y[5]),
+                           ptx::pack_bf16x2(y[6], y[7]));
+          }
+        }
+        if (g == 0) {
+          if (slot >= 0)
+            *reinterpret_cast<float2*>(p.ws_ml + at * 2) = make_float2(m[nt][e], sum);
+          else if (p.lse)
+            p.lse[at] = none ? -INFINITY : log_sum(m[nt][e], sum);
+        }
       }
-    last_min = vis.len - p.n_q;
-    low_max = p.window < 0 ? 0 : vis.len - 1 - p.window;
   }
-  auto legal = [&](int j, int nt, int e) { return j <= last[nt][e] && (j >= low[nt][e] || j < p.sinks); };
+};
 
-  float o[NT][C::S][4];
-  float m_run[NT][2], l_run[NT][2];
+// `count` tiles from `cur` on. A pair whose tiles are not all among them leaves its (m, l, O) in
+// `slot` (the first one) or slot + 1 (the last).
+template <int D, int NT, bool FP8>
+__device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Cursor<Cfg<D, NT, FP8>::KT> cur,
+                                       long long count, int slot) {
+  using C = Cfg<D, NT, FP8>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+
+  // ---- the ring: stage x holds K at ring + 2 x TILE_BYTES, V behind it. Piece c of row r
+  // stands at place c ^ 4 (r & 1) of the row in K, c ^ 2 (r / 2 & 3) in V (of rows of four
+  // pieces: c, and c ^ 2 (r / 2 & 1)): eight lanes that read together, two keys of K or four
+  // of V, meet different banks.
+  const uint32_t ring = ptx::smem_u32(smem) + warp * C::WARP_BYTES;
+  const int piece = lane % C::PIECES, side = lane / C::PIECES;
+  const uint8_t* kp = static_cast<const uint8_t*>(p.k) + 16 * piece;
+  const uint8_t* vp = static_cast<const uint8_t*>(p.v) + 16 * piece;
+  auto request = [&](int stage, int rows_l) {
+    const uint32_t at = ring + stage * 2 * C::TILE_BYTES;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+    for (int x = 0; x < C::KT / C::SIDE; ++x) {
+      const int r = x * C::SIDE + side;
+      const int row = __shfl_sync(kAll, rows_l, r);
+      const long long off = (long long)max(row, 0) * C::ROW_BYTES;
+      const int k_to = C::PIECES == 4 ? piece : piece ^ (r & 1) << 2;
+      const int v_to = C::PIECES == 4 ? piece ^ (r & 2) : piece ^ (r & 6);
+      copy_async(at + r * C::ROW_BYTES + 16 * k_to, kp + off, row >= 0);
+      copy_async(at + C::TILE_BYTES + r * C::ROW_BYTES + 16 * v_to, vp + off, row >= 0);
+    }
+  };
+  // where this lane reads: key g of K (pieces t + 4 c), keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of V
+  const uint32_t k_lane = g * C::ROW_BYTES + 16 * t + (C::PIECES == 4 ? 0 : 64 * (g & 1));
+  const uint32_t v_lane = C::TILE_BYTES + 2 * t * C::ROW_BYTES +
+                          (C::PIECES == 4 ? 16 * ((g >> 1) ^ (2 * t & 2)) + 8 * (g & 1) : 16 * (g ^ 2 * t));
+  uint32_t there[C::STAGES];  // which keys of the tiles in flight exist; [0]: of the current one
+  Cursor<C::KT> ahead = cur;  // the tile to look up next
+  long long asked = 0;        // tiles looked up
+  auto look_up = [&]() {
+    int row = -1;
+    if (asked < count) {
+      row = cache_row(p, ahead, lane);
+      ahead.step(p);
+    }
+    ++asked;
+    return row;
+  };
 #pragma unroll
-    for (int s = 0; s < C::S; ++s)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[nt][s][e] = 0.0f;
-    m_run[nt][0] = m_run[nt][1] = -INFINITY;
-    l_run[nt][0] = l_run[nt][1] = 0.0f;
+  for (int x = 0; x < C::STAGES; ++x) {
+    const int row = look_up();
+    there[x] = __ballot_sync(kAll, row >= 0);
+    if (x < count) request(x, row);
+    copy_commit();
   }
+  int row_next = look_up();
 
-  for (; tile < t1; tile += kWarps) {
+  Rows<D, NT, FP8> rows;
+  rows.begin(p, cur, lane);
+  int first_tile = cur.tile;  // of this part, of the current pair
+  int later = 0;              // whether that pair is not the part's first
+  int stage = 0;
+  for (long long i = 0; i < count; ++i) {
+    copy_wait<C::STAGES - 1>();
+    __syncwarp();  // every lane's copies are there
+    const uint32_t at = ring + stage * 2 * C::TILE_BYTES;
     // ---- S^T = K Q^T
     float sc[C::KB][NT][4];
 #pragma unroll
@@ -400,15 +473,16 @@ __device__ __forceinline__ void attend(const PagedParams& p, Shared<D, NT, FP8>&
     for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
       for (int c = 0; c < C::KC; ++c) {
-        const uint32_t a0[4] = {kr[kb][0][c].x, kr[kb][0][c].y, kr[kb][0][c].z, kr[kb][0][c].w};
-        const uint32_t a1[4] = {kr[kb][1][c].x, kr[kb][1][c].y, kr[kb][1][c].z, kr[kb][1][c].w};
+        const uint32_t k_at = at + kb * 16 * C::ROW_BYTES + (k_lane ^ (c & 1) * 64) + (c >> 1) * 128;
+        const uint4 k0 = lds128(k_at), k1 = lds128(k_at + 8 * C::ROW_BYTES);
+        const uint32_t a0[4] = {k0.x, k0.y, k0.z, k0.w}, a1[4] = {k1.x, k1.y, k1.z, k1.w};
         if (!FP8) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const uint32_t a[4] = {a0[2 * x], a1[2 * x], a0[2 * x + 1], a1[2 * x + 1]};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma<FP8>(sc[kb][nt], a, qf[nt][2 * c + x][0], qf[nt][2 * c + x][1]);
+              mma<FP8>(sc[kb][nt], a, rows.q[nt][2 * c + x][0], rows.q[nt][2 * c + x][1]);
           }
         } else {
 #pragma unroll
@@ -417,46 +491,39 @@ __device__ __forceinline__ void attend(const PagedParams& p, Shared<D, NT, FP8>&
                                    e4m3_f16x2(a1[x], true)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma<FP8>(sc[kb][nt], a, qf[nt][4 * c + x][0], qf[nt][4 * c + x][1]);
+              mma<FP8>(sc[kb][nt], a, rows.q[nt][4 * c + x][0], rows.q[nt][4 * c + x][1]);
           }
         }
       }
-    const bool more = tile + kWarps < t1;
-    const int row_cur = row_now;
-    row_now = row_next;
-    if (more) {
-      load_k(row_now);
-      row_next = rows_of(tile + 2 * kWarps);
-    }
-
     // ---- masks: keys that are not there, and where rows differ, each row's own bounds
-    const int x0 = tile * C::KT;
-    const bool holes = __any_sync(kAll, lane < C::KT && row_cur < 0);
-    const bool mixed =
-        !same && (vis.key(x0 + C::KT - 1) > last_min || x0 < vis.head || x0 + vis.skip < low_max);
+    const Visible& vis = cur.vis;
+    const int x0 = cur.tile * C::KT;
+    const bool holes = there[0] != (uint32_t)((1ull << C::KT) - 1);
+    const bool mixed = p.n_q > 1 && (vis.key(x0 + C::KT - 1) > vis.len - p.n_q || x0 < vis.head ||
+                                     (p.window >= 0 && x0 + vis.skip < vis.len - 1 - p.window));
 #pragma unroll
     for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[kb][nt][e] *= factor[nt][e & 1];
+        for (int e = 0; e < 4; ++e) sc[kb][nt][e] *= rows.factor[nt][e & 1];
     if (holes || mixed) {
 #pragma unroll
       for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           const int x = kb * 16 + hf * 8 + g;
-          const bool there = __shfl_sync(kAll, row_cur, x) >= 0;
+          const bool is = there[0] >> x & 1;
           const int j = vis.key(x0 + x);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              if (!there || (mixed && !legal(j, nt, e))) sc[kb][nt][2 * hf + e] = -INFINITY;
+              if (!is || (mixed && !rows.legal(p, j, nt, e))) sc[kb][nt][2 * hf + e] = -INFINITY;
         }
     }
 
-    // ---- online softmax; l_run is this lane's share, summed at the end
+    // ---- online softmax; rows.l is this lane's share, summed at the end
     uint32_t pf[C::KB][NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -468,10 +535,10 @@ __device__ __forceinline__ void attend(const PagedParams& p, Shared<D, NT, FP8>&
         for (int kb = 0; kb < C::KB; ++kb) mx = fmaxf(mx, fmaxf(sc[kb][nt][e], sc[kb][nt][2 + e]));
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, x));
-        const float m_new = fmaxf(m_run[nt][e], mx);
+        const float m_new = fmaxf(rows.m[nt][e], mx);
         const float m_use = m_new == -INFINITY ? 0.0f : m_new;  // nothing legal yet
-        alpha[e] = ptx::ex2(m_run[nt][e] - m_use);
-        m_run[nt][e] = m_new;
+        alpha[e] = ptx::ex2(rows.m[nt][e] - m_use);
+        rows.m[nt][e] = m_new;
         float sum = 0.0f;
 #pragma unroll
         for (int kb = 0; kb < C::KB; ++kb)
@@ -480,13 +547,13 @@ __device__ __forceinline__ void attend(const PagedParams& p, Shared<D, NT, FP8>&
             sc[kb][nt][2 * hf + e] = ptx::ex2(sc[kb][nt][2 * hf + e] - m_use);
             sum += sc[kb][nt][2 * hf + e];
           }
-        l_run[nt][e] = fmaf(l_run[nt][e], alpha[e], sum);
+        rows.l[nt][e] = fmaf(rows.l[nt][e], alpha[e], sum);
       }
       if (__any_sync(kAll, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
 #pragma unroll
         for (int s = 0; s < C::S; ++s)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[nt][s][e] *= alpha[e & 1];
+          for (int e = 0; e < 4; ++e) rows.o[nt][s][e] *= alpha[e & 1];
       }
       // P^T as the second product's operand, rounded to the cache's compute type (bf16, or
       // f16 for 8-bit pages): relative 2^-9 (2^-12) per weight, of either sign, below the
@@ -500,6 +567,24 @@ __device__ __forceinline__ void attend(const PagedParams& p, Shared<D, NT, FP8>&
     }
 
     // ---- O^T += V^T P^T
+    uint32_t vr[C::KB][4][C::VW];
+#pragma unroll
+    for (int kb = 0; kb < C::KB; ++kb)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+{
+        const uint32_t v_at = at + v_lane + (kb * 16 + (x >> 1) * 8 + (x & 1)) * C::ROW_BYTES;
+        if (C::VW == 2) {
+          const uint2 w = lds64(v_at);
+          vr[kb][x][0] = w.x, vr[kb][x][1] = w.y;
+        } else {
+#pragma unroll
+          for (int c = 0; c < C::VW / 4; ++c) {
+            const uint4 w = lds128(v_at + 128 * c);
+            vr[kb][x][4 * c] = w.x, vr[kb][x][4 * c + 1] = w.y, vr[kb][x][4 * c + 2] = w.z, vr[kb][x][4 * c + 3] = w.w;
+          }
+        }
+      }
     bool plain = true;
     if (mixed) {
       // a key that some rows may not see: its weight there is 0, and 0 * inf would still
@@ -538,7 +623,7 @@ __device__ __forceinline__ void attend(const PagedParams& p, Shared<D, NT, FP8>&
             }
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma<FP8>(o[nt][s], a, pf[kb][nt][0], pf[kb][nt][1]);
+          for (int nt = 0; nt < NT; ++nt) mma<FP8>(rows.o[nt][s], a, pf[kb][nt][0], pf[kb][nt][1]);
         }
     } else {
 #pragma unroll
@@ -548,14 +633,14 @@ __device__ __forceinline__ void attend(const PagedParams& p, Shared<D, NT, FP8>&
 #pragma unroll 1
           for (int owner = 0; owner < 4; ++owner) {  // key (x >> 1) * 8 + 2 owner + (x & 1) of the block
             const int in8 = 2 * owner + (x & 1), key = kb * 16 + (x >> 1) * 8 + in8;
-            const bool there = __shfl_sync(kAll, row_cur, key) >= 0;
+            const bool is = there[0] >> key & 1;
             const int j = vis.key(x0 + key);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const float w = __shfl_sync(kAll, sc[kb][nt][2 * (x >> 1) + e], in8 * 4 + t);
-                const bool on = there && legal(j, nt, e);
+                const bool on = is && rows.legal(p, j, nt, e);
 #pragma unroll
                 for (int s = 0; s < C::S; ++s) {
                   float v0, v1;
@@ -571,158 +656,152 @@ __device__ __forceinline__ void attend(const PagedParams& p, Shared<D, NT, FP8>&
                         : "r"(y));
                   }
                   if (on) {
-                    o[nt][s][e] = fmaf(w, v0, o[nt][s][e]);
-                    o[nt][s][2 + e] = fmaf(w, v1, o[nt][s][2 + e]);
+                    rows.o[nt][s][e] = fmaf(w, v0, rows.o[nt][s][e]);
+                    rows.o[nt][s][2 + e] = fmaf(w, v1, rows.o[nt][s][2 + e]);
                   }
                 }
               }
           }
     }
-    if (more) load_v(row_now);
-  }
+    __syncwarp();
+    // the stage is read: ask for the tile STAGES further on, and look up the rows of the next
+#pragma unroll
+    for (int x = 0; x + 1 < C::STAGES; ++x) there[x] = there[x + 1];
+    there[C::STAGES - 1] = __ballot_sync(kAll, row_next >= 0);
+    if (i + C::STAGES < count) request(stage, row_next);
+    copy_commit();
+    row_next = look_up();
+    stage = stage + 1 < C::STAGES ? stage + 1 : 0;
 
-  // ---- join the warps
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float l = l_run[nt][e];
-#pragma unroll
-      for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(kAll, l, x);
-      const int r = nt * 8 + 2 * t + e;
-      if (g == 0) {
-        sh.m[warp][r] = m_run[nt][e];
-        sh.l[warp][r] = l;
-      }
-      if (r < rows)
-#pragma unroll
-        for (int s = 0; s < C::S; ++s) {
-          const int col = FP8 ? (D / 8) * g + 2 * s : (s / 4) * 64 + 8 * g + 2 * (s % 4);
-          *reinterpret_cast<float2*>(&sh.o[warp][r][col]) = make_float2(o[nt][s][e], o[nt][s][2 + e]);
-        }
-    }
-  __syncthreads();
-  const float v_scale = FP8 ? __ldg(p.v_scale + head) : 1.0f;
-  for (int x = tid; x < rows * (D / 4); x += kThreads) {
-    const int r = x / (D / 4), col = 4 * (x % (D / 4));
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.m[w][r]);
-    const float base = M == -INFINITY ? 0.0f : M;
-    float L = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = ptx::ex2(sh.m[w][r] - base);
-      const float4 y = *reinterpret_cast<const float4*>(&sh.o[w][r][col]);
-      L = fmaf(f, sh.l[w][r], L);
-      acc.x = fmaf(f, y.x, acc.x), acc.y = fmaf(f, y.y, acc.y);
-      acc.z = fmaf(f, y.z, acc.z), acc.w = fmaf(f, y.w, acc.w);
-    }
-    acc.x *= v_scale, acc.y *= v_scale, acc.z *= v_scale, acc.w *= v_scale;
-    if (slot >= 0) {
-      *reinterpret_cast<float4*>(p.ws_o + (slot * C::ROWS + r) * D + col) = acc;
-      if (col == 0) {
-        p.ws_ml[(slot * C::ROWS + r) * 2] = M;
-        p.ws_ml[(slot * C::ROWS + r) * 2 + 1] = L;
-      }
+    const bool pair_done = cur.tile + 1 == cur.n, part_done = i + 1 == count;
+    if (pair_done || part_done) {
+      const bool complete = pair_done && first_tile == 0;
+      rows.end(p, cur, lane, complete ? -1 : slot + later);
+      if (part_done) break;
+      cur.step(p);
+      first_tile = 0;
+      later = 1;
+      rows.begin(p, cur, lane);
     } else {
-      finish<D>(p, b, head, mt * C::ROWS + r, col, acc, M, L);
+      ++cur.tile;
     }
   }
-  __syncthreads();  // the next pair writes the same shared memory
 }
 
 template <int D, int NT, bool FP8>
 __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FP8>::CTAS_PER_SM) attn_paged_kernel(const PagedParams p) {
   using C = Cfg<D, NT, FP8>;
-  __shared__ __align__(16) Shared<D, NT, FP8> sh;
+  extern __shared__ __align__(16) uint8_t smem[];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int pairs = p.h_kv * p.m_tiles;
+  const long long c = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  Cursor<C::KT> cur;
   if (p.whole) {
-    const int b = blockIdx.x / pairs, pair = blockIdx.x % pairs;
-    attend<D, NT, FP8>(p, sh, b, pair / p.m_tiles, pair % p.m_tiles, 0, tiles_of<C::KT>(p, b), -1);
+    if (c >= (long long)p.B * pairs) return;
+    cur.b = (int)divide(c, pairs), cur.pair = (int)(c - (long long)cur.b * pairs), cur.tile = 0;
+    cur.sequence(p);
+    if (cur.n == 0) {
+      Rows<D, NT, FP8> rows;
+      rows.begin(p, cur, threadIdx.x & 31);
+      rows.end(p, cur, threadIdx.x & 31, -1);
+      return;
+    }
+    stream<D, NT, FP8>(p, smem, cur, cur.n, 0);
     return;
   }
-  __shared__ long long sums[kThreads + 1];
-  int per;
-  const Split s = make_split<C::KT>(p, sums, gridDim.x, per);
-  if ((int)blockIdx.x >= s.ctas) return;
-  const long long begin = s.first(blockIdx.x), end = s.first(blockIdx.x + 1);
+  const Split s = make_split<C::KT, C::PARTS>(p, 0);
+  const long long begin = c * s.part, end = min(begin + s.part, s.total);
   if (begin >= end) return;
   long long before;
-  int b = find_sequence<C::KT>(p, sums, per, begin / pairs, before);
-  for (long long at = begin; at < end;) {
-    int n = tiles_of<C::KT>(p, b);
-    while (n == 0 || at >= (before + n) * pairs) {  // on to the sequence that holds tile `at`
-      before += n;
-      n = tiles_of<C::KT>(p, ++b);
-    }
-    const long long in = at - before * pairs;
-    const int pair = (int)(in / n);
-    const int t0 = (int)(in - (long long)pair * n);
-    const int t1 = (int)min((long long)n, t0 + (end - at));
-    const long long slot = t0 == 0 && t1 == n ? -1 : 2ll * blockIdx.x + (at != begin);
-    attend<D, NT, FP8>(p, sh, b, pair / p.m_tiles, pair % p.m_tiles, t0, t1, slot);
-    at += t1 - t0;
-  }
+  cur.b = find_sequence<C::KT>(p, begin, before);
+  cur.sequence(p);
+  const long long in = begin - before * pairs;
+  cur.pair = (int)divide(in, cur.n);
+  cur.tile = (int)(in - (long long)cur.pair * cur.n);
+  stream<D, NT, FP8>(p, smem, cur, end - begin, 2 * (int)c);
 }
 
 // Joins the parts of a pair that several CTAs share, and writes the rows of pairs without a
-// visible key. Block = pair.
+// visible key. Block (pair, group of `group_rows` rows). A warp takes a slice of a row's
+// parts, a lane four columns; the slices are joined through shared memory.
 template <int D, int NT, bool FP8>
-__global__ void __launch_bounds__(kThreads) attn_paged_merge_kernel(const PagedParams p, int max_ctas) {
+__global__ void __launch_bounds__(kMergeThreads) attn_paged_merge_kernel(const PagedParams p, int group_rows) {
   using C = Cfg<D, NT, FP8>;
-  ptx::grid_dep_wait();
-  ptx::grid_dep_launch();
-  __shared__ long long sums[kThreads + 1];
-  int per;
-  const Split s = make_split<C::KT>(p, sums, max_ctas, per);
+  constexpr int kMergeWarps = kMergeThreads / 32;
+  constexpr int LANES = D / 4;          // lanes of a row of O
+  constexpr int SIDE = 32 / LANES;      // parts side by side in a warp
+  __shared__ float sh_m[kMergeWarps * SIDE], sh_l[kMergeWarps * SIDE];
+  __shared__ __align__(16) float sh_o[kMergeWarps * SIDE][D];
+  // The lengths were there before the decode kernel began, and it let this one start after
+  // it had waited for them itself: the list can be made while it runs.
   const int pairs = p.h_kv * p.m_tiles;
   const int b = blockIdx.x / pairs, pair = blockIdx.x % pairs, head = pair / p.m_tiles, mt = pair % p.m_tiles;
-  long long before = sums[b / per];
-  for (int x = b / per * per; x < b; ++x) before += tiles_of<C::KT>(p, x);
+  const Split s = make_split<C::KT, C::PARTS>(p, b);
   const int n = tiles_of<C::KT>(p, b);
-  const long long begin = before * pairs + (long long)pair * n, end = begin + n;
-  long long c0 = 0, c1 = -1;
-  if (n > 0) {
-    c0 = (begin * s.ctas) / s.total;  // the parts that hold tiles begin and end - 1
-    while (s.first(c0 + 1) <= begin) ++c0;
-    while (s.first(c0) > begin) --c0;
-    c1 = ((end - 1) * s.ctas) / s.total;
-    while (s.first(c1 + 1) <= end - 1) ++c1;
-    while (s.first(c1) > end - 1) --c1;
-    if (c0 == c1) return;  // finished by that CTA
-  }
+  const long long begin = s.before * pairs + (long long)pair * n;
+  int c0 = 0, c1 = -1;  // the parts that hold tiles of the pair
+  if (n > 0) c0 = (int)divide(begin, s.part), c1 = (int)divide(begin + n - 1, s.part);
+  const bool split = c0 < c1 || n == 0;  // else finished by its one warp
+  // part c: slot 2 c if its tiles begin in this pair, else 2 c + 1 (only c0 can begin before it)
+  const int slot0 = 2 * c0 + (c0 * s.part < begin);
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  if (!split) return;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = min(p.rows - mt * C::ROWS, C::ROWS);
-  for (int x = threadIdx.x; x < rows * (D / 4); x += kThreads) {
-    const int r = x / (D / 4), col = 4 * (x % (D / 4));
-    // part c: slot 2 c if its tiles begin in this pair, else 2 c + 1 (only c0 can begin before it)
-    auto ws_row = [&](long long c) { return (2 * c + (s.first(c) < begin)) * C::ROWS + r; };
-    float M = -INFINITY;
-    for (long long c = c0; c <= c1; ++c) M = fmaxf(M, p.ws_ml[ws_row(c) * 2]);
-    const float base = M == -INFINITY ? 0.0f : M;
-    float L = 0.0f;
+  const int r0 = blockIdx.y * group_rows, r1 = min(r0 + group_rows, rows);
+  const int slices = max(1, kMergeWarps / group_rows);  // warps per row
+  const int slice = warp % slices, col = 4 * (lane % LANES), side = lane / LANES;
+  for (int base = r0; base < r1; base += kMergeWarps / slices) {
+    const int r = base + warp / slices;
+    float M = -INFINITY, L = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (r < r1)
 #pragma unroll 4
-    for (long long c = c0; c <= c1; ++c) {
-      const long long w = ws_row(c);
-      const float f = ptx::ex2(p.ws_ml[w * 2] - base);
-      const float4 y = *reinterpret_cast<const float4*>(p.ws_o + w * D + col);
-      L = fmaf(f, p.ws_ml[w * 2 + 1], L);
-      acc.x = fmaf(f, y.x, acc.x), acc.y = fmaf(f, y.y, acc.y);
-      acc.z = fmaf(f, y.z, acc.z), acc.w = fmaf(f, y.w, acc.w);
+      for (int c = c0 + slice * SIDE + side; c <= c1; c += slices * SIDE) {
+        const int w = (c == c0 ? slot0 : 2 * c) * C::ROWS + r;
+        const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + (long long)w * 2);
+        const float4 y = *reinterpret_cast<const float4*>(p.ws_o + (long long)w * D + col);
+        const float m_new = fmaxf(M, ml.x), use = m_new == -INFINITY ? 0.0f : m_new;
+        const float f0 = ptx::ex2(M - use), f1 = ptx::ex2(ml.x - use);
+        M = m_new;
+        L = L * f0 + ml.y * f1;
+        acc.x = acc.x * f0 + y.x * f1, acc.y = acc.y * f0 + y.y * f1;
+        acc.z = acc.z * f0 + y.z * f1, acc.w = acc.w * f0 + y.w * f1;
+      }
+    const int at = warp * SIDE + side;
+    *reinterpret_cast<float4*>(&sh_o[at][col]) = acc;
+    if (col == 0) sh_m[at] = M, sh_l[at] = L;
+    __syncthreads();
+    if (slice == 0 && side == 0 && r < r1) {
+      for (int x = 1; x < slices * SIDE; ++x) {
+        const float4 y = *reinterpret_cast<const float4*>(&sh_o[at + x][col]);
+        const float m_new = fmaxf(M, sh_m[at + x]), use = m_new == -INFINITY ? 0.0f : m_new;
+        const float f0 = ptx::ex2(M - use), f1 = ptx::ex2(sh_m[at + x] - use);
+        M = m_new;
+        L = L * f0 + sh_l[at + x] * f1;
+        acc.x = acc.x * f0 + y.x * f1, acc.y = acc.y * f0 + y.y * f1;
+        acc.z = acc.z * f0 + y.z * f1, acc.w = acc.w * f0 + y.w * f1;
+      }
+      const long long row = out_row(p, b, head, mt * C::ROWS + r);
+      const bool none = M == -INFINITY && L == 0.0f;  // no legal key
+      const float inv = none ? 0.0f : 1.0f / L;
+      *reinterpret_cast<uint2*>(p.out + row * D + col) =
+          make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+      if (p.lse && col == 0) p.lse[row] = none ? -INFINITY : log_sum(M, L);
     }
-    finish<D>(p, b, head, mt * C::ROWS + r, col, acc, M, L);
+    __syncthreads();
   }
 }
 
 template <typename... KArgs, typename... Args>
-int launch_pdl(void (*kernel)(KArgs...), unsigned grid, cudaStream_t stream, Args... args) {
+int launch_pdl(void (*kernel)(KArgs...), dim3 grid, int block, int smem, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -750,17 +829,26 @@ int launch(const PagedArgs& a, float* ws) {
   p.window = a.window < p.max_len ? a.window : p.max_len;
   p.sinks = a.window < 0 ? 0 : a.sinks < p.max_len ? a.sinks : p.max_len;
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634074);
-  const int ctas = C::CTAS_PER_SM * kSMs;
-  p.ws_o = ws, p.ws_ml = ws + (size_t)2 * ctas * C::ROWS * D;
-  // keys that any sequence may have in sight
+  p.ws_o = ws, p.ws_ml = ws + (size_t)2 * C::PARTS * C::ROWS * D;
+  // tiles that any pair may have: a pair is not worth splitting where that is few, nor where
+  // it is no long stretch and there are pairs enough to fill the device twice
   long long most = p.max_len;
   if (p.window >= 0 && (long long)p.window + a.n_q + p.sinks < most) most = (long long)p.window + a.n_q + p.sinks;
-  const long long pairs = (long long)a.B * a.h_kv * p.m_tiles;
+  const long long pairs = (long long)a.B * a.h_kv * p.m_tiles, tiles = (most + C::KT - 1) / C::KT;
   if (pairs > 0x7fffffffLL) return ATTN_ERR_INVALID;
-  p.whole = (most + C::KT - 1) / C::KT <= kWholeTiles;
-  const int st = launch_pdl(attn_paged_kernel<D, NT, FP8>, p.whole ? (unsigned)pairs : (unsigned)ctas, a.stream, p);
+  p.whole = tiles <= kWholeTiles || (tiles <= 4 * kWholeTiles && pairs >= 2 * C::PARTS);
+  if (cudaFuncSetAttribute(attn_paged_kernel<D, NT, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           C::SMEM_BYTES) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  const unsigned ctas = p.whole ? (unsigned)((pairs + kWarps - 1) / kWarps) : C::CTAS_PER_SM * kSMs;
+  const int st = launch_pdl(attn_paged_kernel<D, NT, FP8>, dim3(ctas), kThreads, C::SMEM_BYTES, a.stream, p);
   if (st != ATTN_OK || p.whole) return st;
-  return launch_pdl(attn_paged_merge_kernel<D, NT, FP8>, (unsigned)pairs, a.stream, p, ctas);
+  // few pairs have many parts each: a block per row, all its warps on that row's parts
+  const int rows = p.rows < C::ROWS ? p.rows : C::ROWS;
+  const int group_rows = pairs * rows <= 4 * kSMs ? 1 : C::ROWS;
+  return launch_pdl(attn_paged_merge_kernel<D, NT, FP8>,
+                    dim3((unsigned)pairs, (unsigned)((rows + group_rows - 1) / group_rows)), kMergeThreads, 0, a.stream,
+                    p, group_rows);
 }
 
 template <int D, bool FP8>
@@ -770,10 +858,10 @@ int launch_rows(const PagedArgs& a, float* ws) {
 
 }  // namespace
 
-// Two slots for every CTA that can be resident, whatever the lengths.
+// Two slots for every warp that can be resident, whatever the lengths.
 size_t paged_decode_workspace_bytes(int n_q, int group, int d) {
   const int rows = (long long)n_q * group <= 8 ? 8 : 16;
-  return (size_t)2 * kMaxCtasPerSM * kSMs * rows * (d + 2) * sizeof(float);
+  return (size_t)2 * kMaxParts * rows * (d + 2) * sizeof(float);
 }
 
 int launch_attn_paged_decode(const PagedArgs& a, void* workspace) {
