@@ -158,6 +158,13 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
   return a / b;
 }
 
+// Whether a word of V holds an infinity or NaN (e4m3: NaN is the only special value).
+template <bool FP8>
+__device__ __forceinline__ bool special(uint32_t y) {
+  if (FP8) return __vcmpeq4(y & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+  return (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u;
+}
+
 // ---------------------------------------------------------------- ranges
 // The visible keys of a sequence, numbered 0 .. count - 1: the first `head` are keys 0 ..
 // head - 1 (sinks below the window), number x >= head is key x + skip.
@@ -237,7 +244,7 @@ __device__ __forceinline__ int find_sequence(const PagedParams& p, long long x, 
 // A place in the list.
 template <int KT>
 struct Cursor {
-  int b, pair, tile, n;  // tile of n of the pair
+  int b, head, mt, tile, n;  // tile of n of the pair (head, row tile mt)
   Visible vis;
   __device__ __forceinline__ void sequence(const PagedParams& p) {
     vis = visible_of(p, b);
@@ -246,11 +253,12 @@ struct Cursor {
   __device__ __forceinline__ void step(const PagedParams& p) {
     if (++tile < n) return;
     tile = 0;
-    if (++pair < p.h_kv * p.m_tiles) return;
-    pair = 0;
+    if (++mt < p.m_tiles) return;
+    mt = 0;
+    if (++head < p.h_kv) return;
+    head = 0;
     do {
-      ++b;
-      if (b >= p.B) return;  // past the end of the list: not used
+      if (++b >= p.B) return;  // past the end of the list: not used
       sequence(p);
     } while (n == 0);
   }
@@ -266,13 +274,24 @@ __device__ __forceinline__ int cache_row(const PagedParams& p, const Cursor<KT>&
   const int slot = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
   const int page = __ldg(p.page_table + (long long)c.b * p.max_pages + slot);
   if (page < 0 || page >= p.n_pages) return -1;  // names no page: its keys count as illegal
-  return (page * p.h_kv + c.pair / p.m_tiles) * p.page_size + (j - slot * p.page_size);
+  return (page * p.h_kv + c.head) * p.page_size + (j - slot * p.page_size);
 }
 
 // Where row `row` of (sequence, head) stands in out and lse.
 __device__ __forceinline__ long long out_row(const PagedParams& p, int b, int head, int row) {
   const int i = row / p.group;
   return ((long long)b * p.n_q + i) * p.h_q + head * p.group + (row - i * p.group);
+}
+
+// Rows [r0, r1) of a pair without a visible key, by one warp.
+template <int D>
+__device__ __forceinline__ void empty_rows(const PagedParams& p, int b, int head, int r0, int r1) {
+  const int lane = threadIdx.x & 31;
+  for (int r = r0; r < r1; ++r) {
+    const long long at = out_row(p, b, head, r);
+    if (lane < D / 8) *reinterpret_cast<uint4*>(p.out + at * D + 8 * lane) = make_uint4(0, 0, 0, 0);
+    if (p.lse && lane == 0) p.lse[at] = -INFINITY;
+  }
 }
 
 __device__ __forceinline__ float log_sum(float m, float l) { return (m + log2f(l)) * 0.69314718055994530942f; }
@@ -289,7 +308,7 @@ struct Rows {
 
   __device__ __forceinline__ void begin(const PagedParams& p, const Cursor<C::KT>& c, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const int head = c.pair / p.m_tiles, row0 = (c.pair - head * p.m_tiles) * C::ROWS;
+    const int head = c.head, row0 = c.mt * C::ROWS;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const int r = row0 + nt * 8 + g;
@@ -357,7 +376,7 @@ struct Rows {
   // adjacent columns of rows 2 t, 2 t + 1: whole sectors.
   __device__ __forceinline__ void end(const PagedParams& p, const Cursor<C::KT>& c, int lane, int slot) {
     const int g = lane >> 2, t = lane & 3;
-    const int head = c.pair / p.m_tiles, row0 = (c.pair - head * p.m_tiles) * C::ROWS;
+    const int head = c.head, row0 = c.mt * C::ROWS;
     const float v_scale = FP8 ? __ldg(p.v_scale + head) : 1.0f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -432,258 +451,240 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
   const uint32_t v_lane = C::TILE_BYTES + 2 * t * C::ROW_BYTES +
                           (C::PIECES == 4 ? 16 * ((g >> 1) ^ (2 * t & 2)) + 8 * (g & 1) : 16 * (g ^ 2 * t));
   uint32_t there[C::STAGES];  // which keys of the tiles in flight exist; [0]: of the current one
-  Cursor<C::KT> ahead = cur;  // the tile to look up next
-  long long asked = 0;        // tiles looked up
-  auto look_up = [&]() {
-    int row = -1;
-    if (asked < count) {
-      row = cache_row(p, ahead, lane);
-      ahead.step(p);
-    }
-    ++asked;
-    return row;
-  };
-#pragma unroll
-  for (int x = 0; x < C::STAGES; ++x) {
-    const int row = look_up();
-    there[x] = __ballot_sync(kAll, row >= 0);
-    if (x < count) request(x, row);
-    copy_commit();
-  }
-  int row_next = look_up();
-
+  Cursor<C::KT> ahead = cur;  // the next tile to look up
+  int row_next = -1;          // its rows, one step ahead of the request
   Rows<D, NT, FP8> rows;
-  rows.begin(p, cur, lane);
-  int first_tile = cur.tile;  // of this part, of the current pair
+  bool fresh = true;          // cur's pair has not begun
+  int first_tile = cur.tile;  // of this part, of cur's pair
   int later = 0;              // whether that pair is not the part's first
   int stage = 0;
-  for (long long i = 0; i < count; ++i) {
-    copy_wait<C::STAGES - 1>();
-    __syncwarp();  // every lane's copies are there
-    const uint32_t at = ring + stage * 2 * C::TILE_BYTES;
-    // ---- S^T = K Q^T
-    float sc[C::KB][NT][4];
-#pragma unroll
-    for (int kb = 0; kb < C::KB; ++kb)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[kb][nt][e] = 0.0f;
-#pragma unroll
-    for (int kb = 0; kb < C::KB; ++kb)
-#pragma unroll
-      for (int c = 0; c < C::KC; ++c) {
-        const uint32_t k_at = at + kb * 16 * C::ROW_BYTES + (k_lane ^ (c & 1) * 64) + (c >> 1) * 128;
-        const uint4 k0 = lds128(k_at), k1 = lds128(k_at + 8 * C::ROW_BYTES);
-        const uint32_t a0[4] = {k0.x, k0.y, k0.z, k0.w}, a1[4] = {k1.x, k1.y, k1.z, k1.w};
-        if (!FP8) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t a[4] = {a0[2 * x], a1[2 * x], a0[2 * x + 1], a1[2 * x + 1]};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma<FP8>(sc[kb][nt], a, rows.q[nt][2 * c + x][0], rows.q[nt][2 * c + x][1]);
-          }
-        } else {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t a[4] = {e4m3_f16x2(a0[x], false), e4m3_f16x2(a1[x], false), e4m3_f16x2(a0[x], true),
-                                   e4m3_f16x2(a1[x], true)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma<FP8>(sc[kb][nt], a, rows.q[nt][4 * c + x][0], rows.q[nt][4 * c + x][1]);
-          }
-        }
-      }
-    // ---- masks: keys that are not there, and where rows differ, each row's own bounds
-    const Visible& vis = cur.vis;
-    const int x0 = cur.tile * C::KT;
-    const bool holes = there[0] != (uint32_t)((1ull << C::KT) - 1);
-    const bool mixed = p.n_q > 1 && (vis.key(x0 + C::KT - 1) > vis.len - p.n_q || x0 < vis.head ||
-                                     (p.window >= 0 && x0 + vis.skip < vis.len - 1 - p.window));
-#pragma unroll
-    for (int kb = 0; kb < C::KB; ++kb)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[kb][nt][e] *= rows.factor[nt][e & 1];
-    if (holes || mixed) {
+  // Step i works on tile i and refills its stage; the steps below 0 only fill the ring. (One
+  // copy of the code for both: it has to stay in the instruction caches.)
+  for (long long i = -C::STAGES - 1; i < count; ++i) {
+    if (i >= 0) {
+      if (fresh) rows.begin(p, cur, lane);
+      fresh = false;
+      copy_wait<C::STAGES - 1>();
+      __syncwarp();  // every lane's copies are there
+      const uint32_t at = ring + stage * 2 * C::TILE_BYTES;
+      // ---- S^T = K Q^T
+      float sc[C::KB][NT][4];
 #pragma unroll
       for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int x = kb * 16 + hf * 8 + g;
-          const bool is = there[0] >> x & 1;
-          const int j = vis.key(x0 + x);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int e = 0; e < 4; ++e) sc[kb][nt][e] = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-              if (!is || (mixed && !rows.legal(p, j, nt, e))) sc[kb][nt][2 * hf + e] = -INFINITY;
+      for (int kb = 0; kb < C::KB; ++kb)
+#pragma unroll
+        for (int c = 0; c < C::KC; ++c) {
+          const uint32_t k_at = at + kb * 16 * C::ROW_BYTES + (k_lane ^ (c & 1) * 64) + (c >> 1) * 128;
+          const uint4 k0 = lds128(k_at), k1 = lds128(k_at + 8 * C::ROW_BYTES);
+          const uint32_t a0[4] = {k0.x, k0.y, k0.z, k0.w}, a1[4] = {k1.x, k1.y, k1.z, k1.w};
+          if (!FP8) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t a[4] = {a0[2 * x], a1[2 * x], a0[2 * x + 1], a1[2 * x + 1]};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma<FP8>(sc[kb][nt], a, rows.q[nt][2 * c + x][0], rows.q[nt][2 * c + x][1]);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t a[4] = {e4m3_f16x2(a0[x], false), e4m3_f16x2(a1[x], false), e4m3_f16x2(a0[x], true),
+                                     e4m3_f16x2(a1[x], true)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma<FP8>(sc[kb][nt], a, rows.q[nt][4 * c + x][0], rows.q[nt][4 * c + x][1]);
+            }
+          }
         }
-    }
-
-    // ---- online softmax; rows.l is this lane's share, summed at the end
-    uint32_t pf[C::KB][NT][2];
+      // ---- masks: keys that are not there, and where rows differ, each row's own bounds
+      const Visible& vis = cur.vis;
+      const int x0 = cur.tile * C::KT;
+      const bool holes = there[0] != (uint32_t)((1ull << C::KT) - 1);
+      const bool mixed = p.n_q > 1 && (vis.key(x0 + C::KT - 1) > vis.len - p.n_q || x0 < vis.head ||
+                                       (p.window >= 0 && x0 + vis.skip < vis.len - 1 - p.window));
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float alpha[2];
+      for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float mx = sc[0][nt][e];
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int kb = 0; kb < C::KB; ++kb) mx = fmaxf(mx, fmaxf(sc[kb][nt][e], sc[kb][nt][2 + e]));
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, x));
-        const float m_new = fmaxf(rows.m[nt][e], mx);
-        const float m_use = m_new == -INFINITY ? 0.0f : m_new;  // nothing legal yet
-        alpha[e] = ptx::ex2(rows.m[nt][e] - m_use);
-        rows.m[nt][e] = m_new;
-        float sum = 0.0f;
+          for (int e = 0; e < 4; ++e) sc[kb][nt][e] *= rows.factor[nt][e & 1];
+      if (holes || mixed) {
 #pragma unroll
         for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            sc[kb][nt][2 * hf + e] = ptx::ex2(sc[kb][nt][2 * hf + e] - m_use);
-            sum += sc[kb][nt][2 * hf + e];
+            const int x = kb * 16 + hf * 8 + g;
+            const bool is = there[0] >> x & 1;
+            const int j = vis.key(x0 + x);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (!is || (mixed && !rows.legal(p, j, nt, e))) sc[kb][nt][2 * hf + e] = -INFINITY;
           }
-        rows.l[nt][e] = fmaf(rows.l[nt][e], alpha[e], sum);
       }
-      if (__any_sync(kAll, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
-#pragma unroll
-        for (int s = 0; s < C::S; ++s)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) rows.o[nt][s][e] *= alpha[e & 1];
-      }
-      // P^T as the second product's operand, rounded to the cache's compute type (bf16, or
-      // f16 for 8-bit pages): relative 2^-9 (2^-12) per weight, of either sign, below the
-      // output's own rounding; the sum l keeps the unrounded weights
-#pragma unroll
-      for (int kb = 0; kb < C::KB; ++kb)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-          pf[kb][nt][hf] = transpose8(FP8 ? pack_f16x2(sc[kb][nt][2 * hf], sc[kb][nt][2 * hf + 1])
-                                          : ptx::pack_bf16x2(sc[kb][nt][2 * hf], sc[kb][nt][2 * hf + 1]));
-    }
 
-    // ---- O^T += V^T P^T
-    uint32_t vr[C::KB][4][C::VW];
+      // ---- online softmax; rows.l is this lane's share, summed at the end
+      uint32_t pf[C::KB][NT][2];
 #pragma unroll
-    for (int kb = 0; kb < C::KB; ++kb)
+      for (int nt = 0; nt < NT; ++nt) {
+        float alpha[2];
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-{
-        const uint32_t v_at = at + v_lane + (kb * 16 + (x >> 1) * 8 + (x & 1)) * C::ROW_BYTES;
-        if (C::VW == 2) {
-          const uint2 w = lds64(v_at);
-          vr[kb][x][0] = w.x, vr[kb][x][1] = w.y;
-        } else {
+        for (int e = 0; e < 2; ++e) {
+          float mx = sc[0][nt][e];
 #pragma unroll
-          for (int c = 0; c < C::VW / 4; ++c) {
-            const uint4 w = lds128(v_at + 128 * c);
-            vr[kb][x][4 * c] = w.x, vr[kb][x][4 * c + 1] = w.y, vr[kb][x][4 * c + 2] = w.z, vr[kb][x][4 * c + 3] = w.w;
-          }
+          for (int kb = 0; kb < C::KB; ++kb) mx = fmaxf(mx, fmaxf(sc[kb][nt][e], sc[kb][nt][2 + e]));
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kAll, mx, x));
+          const float m_new = fmaxf(rows.m[nt][e], mx);
+          const float m_use = m_new == -INFINITY ? 0.0f : m_new;  // nothing legal yet
+          alpha[e] = ptx::ex2(rows.m[nt][e] - m_use);
+          rows.m[nt][e] = m_new;
+          float sum = 0.0f;
+#pragma unroll
+          for (int kb = 0; kb < C::KB; ++kb)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              sc[kb][nt][2 * hf + e] = ptx::ex2(sc[kb][nt][2 * hf + e] - m_use);
+              sum += sc[kb][nt][2 * hf + e];
+            }
+          rows.l[nt][e] = fmaf(rows.l[nt][e], alpha[e], sum);
         }
+        if (__any_sync(kAll, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+#pragma unroll
+          for (int s = 0; s < C::S; ++s)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) rows.o[nt][s][e] *= alpha[e & 1];
+        }
+        // P^T as the second product's operand, rounded to the cache's compute type (bf16, or
+        // f16 for 8-bit pages): relative 2^-9 (2^-12) per weight, of either sign, below the
+        // output's own rounding; the sum l keeps the unrounded weights
+#pragma unroll
+        for (int kb = 0; kb < C::KB; ++kb)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+            pf[kb][nt][hf] = transpose8(FP8 ? pack_f16x2(sc[kb][nt][2 * hf], sc[kb][nt][2 * hf + 1])
+                                            : ptx::pack_bf16x2(sc[kb][nt][2 * hf], sc[kb][nt][2 * hf + 1]));
       }
-    bool plain = true;
-    if (mixed) {
-      // a key that some rows may not see: its weight there is 0, and 0 * inf would still
-      // be NaN, so a tile with infinities or NaN among its values goes key by key
+
+      // ---- O^T += V^T P^T
+      uint32_t vr[C::KB][4][C::VW];
       bool bad = false;
 #pragma unroll
       for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t v_at = at + v_lane + (kb * 16 + (x >> 1) * 8 + (x & 1)) * C::ROW_BYTES;
+          if (C::VW == 2) {
+            const uint2 w = lds64(v_at);
+            vr[kb][x][0] = w.x, vr[kb][x][1] = w.y;
+          } else {
 #pragma unroll
-          for (int w = 0; w < C::VW; ++w) {
-            const uint32_t y = vr[kb][x][w];
-            if (FP8)
-              bad |= __vcmpeq4(y & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;  // NaN is the only special value
-            else
-              bad |= (y & 0x7f80u) == 0x7f80u || (y & 0x7f800000u) == 0x7f800000u;
-          }
-      plain = !__any_sync(kAll, bad);
-    }
-    if (plain) {
-#pragma unroll
-      for (int kb = 0; kb < C::KB; ++kb)
-#pragma unroll
-        for (int s = 0; s < C::S; ++s) {
-          uint32_t a[4];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!FP8) {
-              a[2 * x] = __byte_perm(vr[kb][2 * x][s], vr[kb][2 * x + 1][s], 0x5410);
-              a[2 * x + 1] = __byte_perm(vr[kb][2 * x][s], vr[kb][2 * x + 1][s], 0x7632);
-            } else {
-              const uint32_t y =
-                  __byte_perm(vr[kb][2 * x][s / 2], vr[kb][2 * x + 1][s / 2], s % 2 ? 0x7362 : 0x5140);
-              a[2 * x] = e4m3_f16x2(y, false);
-              a[2 * x + 1] = e4m3_f16x2(y, true);
+            for (int c = 0; c < C::VW / 4; ++c) {
+              const uint4 w = lds128(v_at + 128 * c);
+              vr[kb][x][4 * c] = w.x, vr[kb][x][4 * c + 1] = w.y;
+              vr[kb][x][4 * c + 2] = w.z, vr[kb][x][4 * c + 3] = w.w;
             }
           }
+          if (mixed)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma<FP8>(rows.o[nt][s], a, pf[kb][nt][0], pf[kb][nt][1]);
+            for (int w = 0; w < C::VW; ++w) bad |= special<FP8>(vr[kb][x][w]);
         }
-    } else {
+      // In a mixed tile some rows may not see a key: its weight there is 0, and 0 * inf would
+      // still be NaN, so a mixed tile with infinities or NaN among its values goes key by key.
+      const bool plain = !mixed || !__any_sync(kAll, bad);
+      if (plain) {
 #pragma unroll
-      for (int kb = 0; kb < C::KB; ++kb)
+        for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+          for (int s = 0; s < C::S; ++s) {
+            uint32_t a[4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (!FP8) {
+                a[2 * x] = __byte_perm(vr[kb][2 * x][s], vr[kb][2 * x + 1][s], 0x5410);
+                a[2 * x + 1] = __byte_perm(vr[kb][2 * x][s], vr[kb][2 * x + 1][s], 0x7632);
+              } else {
+                const uint32_t y =
+                    __byte_perm(vr[kb][2 * x][s / 2], vr[kb][2 * x + 1][s / 2], s % 2 ? 0x7362 : 0x5140);
+                a[2 * x] = e4m3_f16x2(y, false);
+                a[2 * x + 1] = e4m3_f16x2(y, true);
+              }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma<FP8>(rows.o[nt][s], a, pf[kb][nt][0], pf[kb][nt][1]);
+          }
+      } else {
+        // the weights go where the tile's K was, [key][row]; a lane's columns of V are read anew
+        float* w_sh = reinterpret_cast<float*>(smem + (at - ring) + warp * C::WARP_BYTES);
+#pragma unroll
+        for (int kb = 0; kb < C::KB; ++kb)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w_sh[(kb * 16 + (e >> 1) * 8 + g) * C::ROWS + nt * 8 + 2 * t + (e & 1)] = sc[kb][nt][e];
+        __syncwarp();
 #pragma unroll 1
-          for (int owner = 0; owner < 4; ++owner) {  // key (x >> 1) * 8 + 2 owner + (x & 1) of the block
-            const int in8 = 2 * owner + (x & 1), key = kb * 16 + (x >> 1) * 8 + in8;
-            const bool is = there[0] >> key & 1;
-            const int j = vis.key(x0 + key);
+        for (int key = 0; key < C::KT; ++key) {
+          if (!(there[0] >> key & 1)) continue;
+          const int j = vis.key(x0 + key);
+          const uint32_t v_row = at + C::TILE_BYTES + key * C::ROW_BYTES;
+#pragma unroll
+          for (int x = 0; x < C::S; ++x) {
+            // the word with this lane's columns 2 x, 2 x + 1 (e4m3: two columns of a word)
+            const int byte = FP8 ? (D / 8) * g + 4 * (x / 2) : 128 * (x / 4) + 16 * g + 4 * (x % 4);
+            const int swap = C::PIECES == 4 ? key & 2 : key & 6;
+            uint32_t y;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(y) : "r"(v_row + (byte ^ 16 * swap)) : "memory");
+            float v0, v1;
+            if (!FP8) {
+              v0 = __uint_as_float(y << 16);
+              v1 = __uint_as_float(y & 0xffff0000u);
+            } else {
+              asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}"
+                  : "=f"(v0), "=f"(v1)
+                  : "r"(e4m3_f16x2(y, x % 2)));
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float w = __shfl_sync(kAll, sc[kb][nt][2 * (x >> 1) + e], in8 * 4 + t);
-                const bool on = is && rows.legal(p, j, nt, e);
-#pragma unroll
-                for (int s = 0; s < C::S; ++s) {
-                  float v0, v1;
-                  if (!FP8) {
-                    const uint32_t y = __shfl_sync(kAll, vr[kb][x][s], (lane & ~3) | owner);
-                    v0 = __uint_as_float(y << 16);
-                    v1 = __uint_as_float(y & 0xffff0000u);
-                  } else {
-                    const uint32_t y =
-                        e4m3_f16x2(__shfl_sync(kAll, vr[kb][x][s / 2], (lane & ~3) | owner), s % 2);
-                    asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}"
-                        : "=f"(v0), "=f"(v1)
-                        : "r"(y));
-                  }
-                  if (on) {
-                    rows.o[nt][s][e] = fmaf(w, v0, rows.o[nt][s][e]);
-                    rows.o[nt][s][2 + e] = fmaf(w, v1, rows.o[nt][s][2 + e]);
-                  }
+              for (int e = 0; e < 2; ++e)
+                if (rows.legal(p, j, nt, e)) {
+                  const float w = w_sh[key * C::ROWS + nt * 8 + 2 * t + e];
+                  rows.o[nt][x][e] = fmaf(w, v0, rows.o[nt][x][e]);
+                  rows.o[nt][x][2 + e] = fmaf(w, v1, rows.o[nt][x][2 + e]);
                 }
-              }
           }
+        }
+      }
+      if (cur.tile + 1 == cur.n || i + 1 == count) {
+        const bool complete = cur.tile + 1 == cur.n && first_tile == 0;
+        rows.end(p, cur, lane, complete ? -1 : slot + later);
+        fresh = true;
+        first_tile = 0;
+        later = 1;
+      }
+      if (i + 1 < count) cur.step(p);
+      __syncwarp();  // the stage is read
     }
-    __syncwarp();
-    // the stage is read: ask for the tile STAGES further on, and look up the rows of the next
+    // ask for the tile STAGES further on, and look up the rows of the next
 #pragma unroll
     for (int x = 0; x + 1 < C::STAGES; ++x) there[x] = there[x + 1];
     there[C::STAGES - 1] = __ballot_sync(kAll, row_next >= 0);
-    if (i + C::STAGES < count) request(stage, row_next);
-    copy_commit();
-    row_next = look_up();
-    stage = stage + 1 < C::STAGES ? stage + 1 : 0;
-
-    const bool pair_done = cur.tile + 1 == cur.n, part_done = i + 1 == count;
-    if (pair_done || part_done) {
-      const bool complete = pair_done && first_tile == 0;
-      rows.end(p, cur, lane, complete ? -1 : slot + later);
-      if (part_done) break;
-      cur.step(p);
-      first_tile = 0;
-      later = 1;
-      rows.begin(p, cur, lane);
-    } else {
-      ++cur.tile;
+    if (i >= -C::STAGES) {
+      if (i + C::STAGES < count) request(stage, row_next);
+      copy_commit();
+      stage = stage + 1 < C::STAGES ? stage + 1 : 0;
+    }
+    if (i + C::STAGES + 1 < count) {
+      row_next = cache_row(p, ahead, lane);
+      ahead.step(p);
     }
   }
 }
@@ -697,29 +698,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT, FP8>::CTAS_PER_SM) attn_p
   const int pairs = p.h_kv * p.m_tiles;
   const long long c = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   Cursor<C::KT> cur;
+  long long pair, count = 0;  // pair: of the sequence
+  cur.tile = 0;
   if (p.whole) {
     if (c >= (long long)p.B * pairs) return;
-    cur.b = (int)divide(c, pairs), cur.pair = (int)(c - (long long)cur.b * pairs), cur.tile = 0;
+    cur.b = (int)divide(c, pairs);
     cur.sequence(p);
-    if (cur.n == 0) {
-      Rows<D, NT, FP8> rows;
-      rows.begin(p, cur, threadIdx.x & 31);
-      rows.end(p, cur, threadIdx.x & 31, -1);
-      return;
-    }
-    stream<D, NT, FP8>(p, smem, cur, cur.n, 0);
-    return;
+    pair = c - (long long)cur.b * pairs;
+    count = cur.n;
+  } else {
+    const Split s = make_split<C::KT, C::PARTS>(p, 0);
+    const long long begin = c * s.part;
+    if (begin >= s.total) return;
+    long long before;
+    cur.b = find_sequence<C::KT>(p, begin, before);
+    cur.sequence(p);
+    const long long in = begin - before * pairs;
+    pair = divide(in, cur.n);
+    cur.tile = (int)(in - pair * cur.n);
+    count = min(s.part, s.total - begin);
   }
-  const Split s = make_split<C::KT, C::PARTS>(p, 0);
-  const long long begin = c * s.part, end = min(begin + s.part, s.total);
-  if (begin >= end) return;
-  long long before;
-  cur.b = find_sequence<C::KT>(p, begin, before);
-  cur.sequence(p);
-  const long long in = begin - before * pairs;
-  cur.pair = (int)divide(in, cur.n);
-  cur.tile = (int)(in - (long long)cur.pair * cur.n);
-  stream<D, NT, FP8>(p, smem, cur, end - begin, 2 * (int)c);
+  cur.head = (int)pair / p.m_tiles, cur.mt = (int)pair - cur.head * p.m_tiles;
+  if (count > 0)
+    stream<D, NT, FP8>(p, smem, cur, count, 2 * (int)c);
+  else
+    empty_rows<D>(p, cur.b, cur.head, cur.mt * C::ROWS, min((cur.mt + 1) * C::ROWS, p.rows));
 }
 
 // Joins the parts of a pair that several CTAs share, and writes the rows of pairs without a
