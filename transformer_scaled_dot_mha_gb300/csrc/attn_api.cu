@@ -401,7 +401,8 @@ int attn_paged_append(const void* q, const void* k, const void* v, int64_t q_str
 }
 
 size_t attn_paged_decode_workspace_size(int B, int n_q, int h_q, int h_kv, int d) {
-  if (B <= 0 || n_q < 1 || n_q > 16 || h_q <= 0 || h_kv <= 0 || h_q % h_kv != 0 || (d != 64 && d != 128)) return 0;
+  if (B <= 0 || n_q < 1 || n_q > 16 || h_q <= 0 || h_kv <= 0 || h_q % h_kv != 0) return 0;
+  if (h_q / h_kv > 8192 || (d != 64 && d != 128)) return 0;
   return attn::paged_decode_workspace_bytes(n_q, h_q / h_kv, d);
 }
 
@@ -420,7 +421,7 @@ int attn_paged_decode(const void* q, const void* k_pages, const void* v_pages, v
   const bool e4m3 = (flags & ATTN_CACHE_E4M3) != 0;
   if ((k_scale != nullptr) != e4m3 || (v_scale != nullptr) != e4m3) return ATTN_ERR_INVALID;
   if (e4m3 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))) return ATTN_ERR_INVALID;
-  if (n_q > 16 || (d != 64 && d != 128)) return ATTN_ERR_UNSUPPORTED;
+  if (n_q > 16 || (d != 64 && d != 128) || h_q / h_kv > 8192) return ATTN_ERR_UNSUPPORTED;
   if ((long long)B * n_q > (1LL << 40) / d / h_q) return ATTN_ERR_INVALID;
   if (workspace_bytes < attn::paged_decode_workspace_bytes(n_q, h_q / h_kv, d)) return ATTN_ERR_INVALID;
   attn::PagedArgs a{q, k_pages, v_pages, out, lse, page_table, cache_lens, B, n_q, h_q, h_kv, d, n_pages, page_size,

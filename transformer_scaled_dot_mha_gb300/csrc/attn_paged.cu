@@ -31,11 +31,14 @@
 // are cp.async.wait_group, which ends by itself; no block barrier in the stream.
 //
 // Work split: the tiles (KT keys) of all (sequence, key/value head) pairs form one list,
-// cut into equal parts, one per resident warp, by the lengths on the device -- ragged
-// batches and capacities far above the lengths cost nothing. A warp is on its own: it
+// cut into equal parts by the lengths on the device -- ragged batches and capacities far
+// above the lengths cost nothing. There is a part for every warp that can be resident, and a
+// warp is a CTA (two or three parts for each, to even out the warps' speeds, cost more in
+// starts and joins: 71.2, 71.8, 75.4 us at 16 x 8 heads of d 128 and 4096-8192 keys). It
 // streams its part from one pair into the next without a pause in its copies. A pair that
 // lies within one warp's part is finished there; of one that does not, every part leaves
-// (m, l, O) in the workspace and attn_paged_merge_kernel joins them. When no sequence can be
+// (m, l, O) in the workspace, the warp that has its first tile leaves a note of the parts,
+// and attn_paged_merge_kernel joins them. When no sequence can be
 // longer than a few tiles, each pair gets a warp of its own and there is no second launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -50,9 +53,7 @@ namespace attn {
 namespace {
 
 constexpr int kSMs = 152;
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxParts = 3 * kSMs * kWarps;  // parts of the list of tiles at most, one per resident warp
+constexpr int kMaxParts = 12 * kSMs;  // parts of the list of tiles at most, one per resident warp
 constexpr int kMinTiles = 2;               // tiles per part, at least
 constexpr int kWholeTiles = 8;             // up to here a pair is not worth splitting
 constexpr int kMergeThreads = 256;
@@ -71,11 +72,16 @@ struct Cfg {
   static constexpr int S = D / 16;                         // MMA steps over the columns; column tiles of O
   static constexpr int ROWS = 8 * NT;
   static constexpr int TILE_BYTES = KT * ROW_BYTES;          // of K, and of V
-  static constexpr int CTAS_PER_SM = D == 128 && NT == 2 ? 2 : 3;  // 255 or 168 registers
-  static constexpr int PARTS = CTAS_PER_SM * kSMs * kWarps;
-  static constexpr int STAGES = 49152 / CTAS_PER_SM / (2 * TILE_BYTES);  // tiles in flight per warp: 192 KB per SM
-  static constexpr int WARP_BYTES = STAGES * 2 * TILE_BYTES;
-  static constexpr int SMEM_BYTES = kWarps * WARP_BYTES;
+  static constexpr int CTAS_PER_SM = D == 128 && NT == 2 ? 8 : 12;  // 255 or 168 registers
+  static constexpr int PARTS = CTAS_PER_SM * kSMs;
+  static constexpr int STAGES = 196608 / CTAS_PER_SM / (2 * TILE_BYTES);  // tiles in flight: 192 KB per SM
+  static constexpr int SMEM_BYTES = STAGES * 2 * TILE_BYTES;
+};
+
+// A pair whose tiles several parts share: its first slot, and the slots 2 (first + 1), 2 (first
+// + 2) .. 2 last of the parts behind it; last < 0: nothing to join.
+struct Note {
+  int pair, slot, first, last;
 };
 
 struct PagedParams {
@@ -90,10 +96,14 @@ struct PagedParams {
   const float* v_scale;
   float* ws_o;   // [2 * PARTS][ROWS][D]: slot 2 c for the pair that part c begins in, 2 c + 1 for the one it ends in
   float* ws_ml;  // [2 * PARTS][ROWS][2]
+  Note* notes;   // [PARTS], of pair x where there are at most PARTS pairs, else of the pair that part x begins
   int B, n_q, h_q, h_kv, group, rows, m_tiles;  // rows = n_q * group
-  int n_pages, page_size, page_shift, max_pages, max_len;  // page_shift < 0: not a power of two
+  int n_pages, page_size, max_pages, max_len;
+  uint32_t page_inv, page_shift;  // x / page_size = mulhi(2 x, page_inv) >> page_shift for x < 2^30
+  uint32_t group_inv;             // x / group = mulhi(x, group_inv) for x < 16 group, group <= 8192
   int window, sinks;
   int whole;  // one warp per pair, no split
+  int notes_by_pair;
   float scale_log2;
 };
 
@@ -152,8 +162,10 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   return r;
 }
 
-// a / b; most lists of tiles are numbered in 32 bits, where the division is far shorter.
-__device__ __forceinline__ long long divide(long long a, long long b) {
+// a / b; most lists of tiles are numbered in 32 bits, where the division is far shorter. Not
+// inlined, as little here is that runs once: a warp runs through most of this code a few
+// times only, and what it costs then is the fetch of the instructions.
+__device__ __noinline__ long long divide(long long a, long long b) {
   if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
   return a / b;
 }
@@ -191,51 +203,48 @@ __device__ __forceinline__ int tiles_of(const PagedParams& p, int b) {
 }
 
 // The list of tiles. Sequence b holds its pairs (head, row tile) one after the other, each
-// of tiles_of(b) tiles; part c of the list is [c * part, (c + 1) * part), up to total. Made by
-// every warp for itself; before = tiles of one pair of the sequences below b_stop.
-struct Split {
-  long long total, part, before;
-};
-
-template <int KT, int PARTS>
-__device__ __forceinline__ Split make_split(const PagedParams& p, int b_stop) {
-  Split s;
-  s.total = s.before = 0;
-#pragma unroll 4
-  for (int b = threadIdx.x & 31; b < p.B; b += 32) {
-    const int n = tiles_of<KT>(p, b);
-    s.total += n;
-    s.before += b < b_stop ? n : 0;
-  }
+// of tiles_of(b) tiles; part c of the list is [c * part, (c + 1) * part), up to total.
+// Tiles of one pair of the sequences b0 .. b0 + lane; n: of sequence b0 + lane alone.
+template <int KT>
+__device__ __forceinline__ uint32_t scan_tiles(const PagedParams& p, int b0, uint32_t& n) {
+  const int lane = threadIdx.x;
+  n = b0 + lane < p.B ? tiles_of<KT>(p, b0 + lane) : 0;  // at most 2^26
+  uint32_t sum = n;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    s.total += __shfl_xor_sync(kAll, s.total, o);
-    if (b_stop > 0) s.before += __shfl_xor_sync(kAll, s.before, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(kAll, sum, o);
+    if (lane >= o) sum += y;
   }
-  s.total *= (long long)p.h_kv * p.m_tiles;
-  s.part = max((long long)kMinTiles, divide(s.total + PARTS - 1, PARTS));
-  return s;
+  return sum;
 }
 
-// The sequence that holds tile x < total of the list, and the tiles of one pair before it.
-template <int KT>
-__device__ __forceinline__ int find_sequence(const PagedParams& p, long long x, long long& before) {
+// Where part c begins: its sequence, the tiles of one pair of the sequences before that, and
+// the tiles of a part. False if the list ends before it.
+template <int KT, int PARTS>
+__device__ __forceinline__ bool find_part(const PagedParams& p, int c, int& b, long long& before, long long& begin,
+                                          long long& part, long long& total) {
   const long long pairs = (long long)p.h_kv * p.m_tiles;
-  const int lane = threadIdx.x & 31;
+  uint32_t n, sum;
+  total = 0;
+#pragma unroll 1
+  for (int b0 = (p.B - 1) & ~31; b0 >= 0; b0 -= 32) {  // ends at the first 32, where the search begins
+    sum = scan_tiles<KT>(p, b0, n);
+    total += __shfl_sync(kAll, sum, 31);
+  }
+  total *= pairs;
+  part = max((long long)kMinTiles, divide(total + PARTS - 1, PARTS));
+  begin = c * part;
+  if (begin >= total) return false;
   before = 0;
+#pragma unroll 1
   for (int b0 = 0;; b0 += 32) {
-    const uint32_t n = b0 + lane < p.B ? tiles_of<KT>(p, b0 + lane) : 0;  // at most 2^26
-    uint32_t sum = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(kAll, sum, o);
-      if (lane >= o) sum += y;
-    }
-    const uint32_t past = __ballot_sync(kAll, (before + sum) * pairs > x);
+    if (b0 > 0) sum = scan_tiles<KT>(p, b0, n);
+    const uint32_t past = __ballot_sync(kAll, (before + sum) * pairs > begin);
     if (past) {
       const int at = __ffs(past) - 1;
       before += __shfl_sync(kAll, sum - n, at);
-      return b0 + at;
+      b = b0 + at;
+      return true;
     }
     before += __shfl_sync(kAll, sum, 31);
   }
@@ -271,30 +280,42 @@ __device__ __forceinline__ int cache_row(const PagedParams& p, const Cursor<KT>&
   const int x = c.tile * KT + lane;
   if (lane >= KT || x >= c.vis.count) return -1;
   const int j = c.vis.key(x);
-  const int slot = p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
+  const int slot = (int)(__umulhi(2u * j, p.page_inv) >> p.page_shift);
   const int page = __ldg(p.page_table + (long long)c.b * p.max_pages + slot);
   if (page < 0 || page >= p.n_pages) return -1;  // names no page: its keys count as illegal
   return (page * p.h_kv + c.head) * p.page_size + (j - slot * p.page_size);
 }
 
+// The token that row `row` of a pair belongs to.
+__device__ __forceinline__ int token_of(const PagedParams& p, int row) {
+  return p.group == 1 ? row : (int)__umulhi(row, p.group_inv);
+}
+
 // Where row `row` of (sequence, head) stands in out and lse.
 __device__ __forceinline__ long long out_row(const PagedParams& p, int b, int head, int row) {
-  const int i = row / p.group;
+  const int i = token_of(p, row);
   return ((long long)b * p.n_q + i) * p.h_q + head * p.group + (row - i * p.group);
 }
 
-// Rows [r0, r1) of a pair without a visible key, by one warp.
+// The rows of sequences without a visible key, shared out over the CTAs.
 template <int D>
-__device__ __forceinline__ void empty_rows(const PagedParams& p, int b, int head, int r0, int r1) {
-  const int lane = threadIdx.x & 31;
-  for (int r = r0; r < r1; ++r) {
-    const long long at = out_row(p, b, head, r);
-    if (lane < D / 8) *reinterpret_cast<uint4*>(p.out + at * D + 8 * lane) = make_uint4(0, 0, 0, 0);
-    if (p.lse && lane == 0) p.lse[at] = -INFINITY;
+__device__ __forceinline__ void empty_rows(const PagedParams& p) {
+  const int lane = threadIdx.x;
+#pragma unroll 1
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (visible_of(p, b).count > 0) continue;
+    const long long row0 = (long long)b * p.n_q * p.h_q;
+    for (int r = 0; r < p.n_q * p.h_q; ++r) {
+      if (lane < D / 8) *reinterpret_cast<uint4*>(p.out + (row0 + r) * D + 8 * lane) = make_uint4(0, 0, 0, 0);
+      if (p.lse && lane == 0) p.lse[row0 + r] = -INFINITY;
+    }
+    if (!p.whole && p.notes_by_pair)
+      for (int x = lane; x < p.h_kv * p.m_tiles; x += 32) p.notes[b * p.h_kv * p.m_tiles + x] = Note{0, 0, 0, -1};
   }
 }
 
-__device__ __forceinline__ float log_sum(float m, float l) { return (m + log2f(l)) * 0.69314718055994530942f; }
+// ln of 2^m l; __log2f is within 2^-22, relative (absolute near 1): below lse's own rounding.
+__device__ __forceinline__ float log_sum(float m, float l) { return (m + __log2f(l)) * 0.69314718055994530942f; }
 
 // The rows of one pair as a warp holds them: queries, bounds, running statistics.
 template <int D, int NT, bool FP8>
@@ -355,7 +376,7 @@ struct Rows {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (p.n_q > 1) {
-          last[nt][e] = c.vis.len - p.n_q + min((row0 + nt * 8 + 2 * t + e) / p.group, p.n_q - 1);
+          last[nt][e] = c.vis.len - p.n_q + min(token_of(p, row0 + nt * 8 + 2 * t + e), p.n_q - 1);
           low[nt][e] = p.window < 0 ? 0 : last[nt][e] - p.window;
         }
         m[nt][e] = -INFINITY;
@@ -388,7 +409,7 @@ struct Rows {
         const int r = nt * 8 + 2 * t + e;
         if (row0 + r >= p.rows) continue;
         const bool none = m[nt][e] == -INFINITY && sum == 0.0f;  // no legal key
-        const float f = slot >= 0 ? v_scale : none ? 0.0f : v_scale / sum;
+        const float f = slot >= 0 ? v_scale : none ? 0.0f : __fdividef(v_scale, sum);
         const long long at = slot >= 0 ? (long long)slot * C::ROWS + r : out_row(p, c.b, head, row0 + r);
 #pragma unroll
         for (int x = 0; x < C::S; x += 4) {
@@ -417,19 +438,19 @@ struct Rows {
 };
 
 // `count` tiles from `cur` on. A pair whose tiles are not all among them leaves its (m, l, O) in
-// `slot` (the first one) or slot + 1 (the last).
+// `slot` (the first one) or slot + 1 (the last); part: tiles of a part of the list.
 template <int D, int NT, bool FP8>
 __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Cursor<Cfg<D, NT, FP8>::KT> cur,
-                                       long long count, int slot) {
+                                       int count, int slot, long long part) {
   using C = Cfg<D, NT, FP8>;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x;
   const int g = lane >> 2, t = lane & 3;
 
   // ---- the ring: stage x holds K at ring + 2 x TILE_BYTES, V behind it. Piece c of row r
   // stands at place c ^ 4 (r & 1) of the row in K, c ^ 2 (r / 2 & 3) in V (of rows of four
   // pieces: c, and c ^ 2 (r / 2 & 1)): eight lanes that read together, two keys of K or four
   // of V, meet different banks.
-  const uint32_t ring = ptx::smem_u32(smem) + warp * C::WARP_BYTES;
+  const uint32_t ring = ptx::smem_u32(smem);
   const int piece = lane % C::PIECES, side = lane / C::PIECES;
   const uint8_t* kp = static_cast<const uint8_t*>(p.k) + 16 * piece;
   const uint8_t* vp = static_cast<const uint8_t*>(p.v) + 16 * piece;
@@ -452,7 +473,18 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
                           (C::PIECES == 4 ? 16 * ((g >> 1) ^ (2 * t & 2)) + 8 * (g & 1) : 16 * (g ^ 2 * t));
   uint32_t there[C::STAGES];  // which keys of the tiles in flight exist; [0]: of the current one
   Cursor<C::KT> ahead = cur;  // the next tile to look up
-  int row_next = -1;          // its rows, one step ahead of the request
+  // rows of the next tiles to request: looked up that far ahead, the first ones all at once
+  int rows_ahead[C::STAGES + 1];
+  int looked = 0;
+  auto look_up = [&]() {
+    if (looked >= count) return -1;
+    const int row = cache_row(p, ahead, lane);
+    ahead.step(p);
+    ++looked;
+    return row;
+  };
+#pragma unroll
+  for (int x = 0; x <= C::STAGES; ++x) rows_ahead[x] = look_up();
   Rows<D, NT, FP8> rows;
   bool fresh = true;          // cur's pair has not begun
   int first_tile = cur.tile;  // of this part, of cur's pair
@@ -460,7 +492,7 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
   int stage = 0;
   // Step i works on tile i and refills its stage; the steps below 0 only fill the ring. (One
   // copy of the code for both: it has to stay in the instruction caches.)
-  for (long long i = -C::STAGES - 1; i < count; ++i) {
+  for (int i = -C::STAGES; i < count; ++i) {
     if (i >= 0) {
       if (fresh) rows.begin(p, cur, lane);
       fresh = false;
@@ -621,7 +653,7 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
           }
       } else {
         // the weights go where the tile's K was, [key][row]; a lane's columns of V are read anew
-        float* w_sh = reinterpret_cast<float*>(smem + (at - ring) + warp * C::WARP_BYTES);
+        float* w_sh = reinterpret_cast<float*>(smem + (at - ring));
 #pragma unroll
         for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
@@ -666,6 +698,11 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
       if (cur.tile + 1 == cur.n || i + 1 == count) {
         const bool complete = cur.tile + 1 == cur.n && first_tile == 0;
         rows.end(p, cur, lane, complete ? -1 : slot + later);
+        if (!p.whole && first_tile == 0 && lane == 0 && (p.notes_by_pair || !complete)) {
+          const int c = slot / 2, left = cur.n - 1 - cur.tile, pair = (cur.b * p.h_kv + cur.head) * p.m_tiles + cur.mt;
+          p.notes[p.notes_by_pair ? pair : c] =
+              Note{pair, slot + later, c, complete ? -1 : c + (int)divide(left + part - 1, part)};
+        }
         fresh = true;
         first_tile = 0;
         later = 1;
@@ -673,130 +710,142 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
       if (i + 1 < count) cur.step(p);
       __syncwarp();  // the stage is read
     }
-    // ask for the tile STAGES further on, and look up the rows of the next
+    // ask for the tile STAGES further on, and look up the rows of another
 #pragma unroll
     for (int x = 0; x + 1 < C::STAGES; ++x) there[x] = there[x + 1];
-    there[C::STAGES - 1] = __ballot_sync(kAll, row_next >= 0);
-    if (i >= -C::STAGES) {
-      if (i + C::STAGES < count) request(stage, row_next);
-      copy_commit();
-      stage = stage + 1 < C::STAGES ? stage + 1 : 0;
-    }
-    if (i + C::STAGES + 1 < count) {
-      row_next = cache_row(p, ahead, lane);
-      ahead.step(p);
-    }
+    there[C::STAGES - 1] = __ballot_sync(kAll, rows_ahead[0] >= 0);
+    if (i + C::STAGES < count) request(stage, rows_ahead[0]);
+    copy_commit();
+    stage = stage + 1 < C::STAGES ? stage + 1 : 0;
+#pragma unroll
+    for (int x = 0; x < C::STAGES; ++x) rows_ahead[x] = rows_ahead[x + 1];
+    rows_ahead[C::STAGES] = look_up();
   }
 }
 
 template <int D, int NT, bool FP8>
-__global__ void __launch_bounds__(kThreads, Cfg<D, NT, FP8>::CTAS_PER_SM) attn_paged_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(32, Cfg<D, NT, FP8>::CTAS_PER_SM) attn_paged_kernel(const PagedParams p) {
   using C = Cfg<D, NT, FP8>;
   extern __shared__ __align__(16) uint8_t smem[];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  const int pairs = p.h_kv * p.m_tiles;
-  const long long c = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int pairs = p.h_kv * p.m_tiles, c = blockIdx.x;
+  if (!p.whole && !p.notes_by_pair && threadIdx.x == 0) p.notes[c] = Note{0, 0, 0, -1};
   Cursor<C::KT> cur;
-  long long pair, count = 0;  // pair: of the sequence
+  long long pair = 0, part = 0;  // pair: of the sequence
+  int count = 0;
   cur.tile = 0;
   if (p.whole) {
-    if (c >= (long long)p.B * pairs) return;
-    cur.b = (int)divide(c, pairs);
+    cur.b = c / pairs;
     cur.sequence(p);
-    pair = c - (long long)cur.b * pairs;
+    pair = c - cur.b * pairs;
     count = cur.n;
   } else {
-    const Split s = make_split<C::KT, C::PARTS>(p, 0);
-    const long long begin = c * s.part;
-    if (begin >= s.total) return;
-    long long before;
-    cur.b = find_sequence<C::KT>(p, begin, before);
-    cur.sequence(p);
-    const long long in = begin - before * pairs;
-    pair = divide(in, cur.n);
-    cur.tile = (int)(in - pair * cur.n);
-    count = min(s.part, s.total - begin);
+    long long before, begin, total;
+    if (find_part<C::KT, C::PARTS>(p, c, cur.b, before, begin, part, total)) {
+      cur.sequence(p);
+      const long long in = begin - before * pairs;
+      pair = divide(in, cur.n);
+      cur.tile = (int)(in - pair * cur.n);
+      count = (int)min(part, total - begin);
+    }
   }
-  cur.head = (int)pair / p.m_tiles, cur.mt = (int)pair - cur.head * p.m_tiles;
-  if (count > 0)
-    stream<D, NT, FP8>(p, smem, cur, count, 2 * (int)c);
-  else
-    empty_rows<D>(p, cur.b, cur.head, cur.mt * C::ROWS, min((cur.mt + 1) * C::ROWS, p.rows));
+  if (count > 0) {
+    cur.head = (int)pair / p.m_tiles, cur.mt = (int)pair - cur.head * p.m_tiles;
+    stream<D, NT, FP8>(p, smem, cur, count, 2 * c, part);
+  }
+  empty_rows<D>(p);
 }
 
-// Joins the parts of a pair that several CTAs share, and writes the rows of pairs without a
-// visible key. Block (pair, group of `group_rows` rows). A warp takes a slice of a row's
-// parts, a lane four columns; the slices are joined through shared memory.
+// Joins the parts of a pair that several warps share. Block (note, group of `group_rows`
+// rows). A warp takes a slice of a row's parts, a lane four columns; the slices are joined
+// through shared memory.
 template <int D, int NT, bool FP8>
 __global__ void __launch_bounds__(kMergeThreads) attn_paged_merge_kernel(const PagedParams p, int group_rows) {
   using C = Cfg<D, NT, FP8>;
   constexpr int kMergeWarps = kMergeThreads / 32;
   constexpr int LANES = D / 4;          // lanes of a row of O
   constexpr int SIDE = 32 / LANES;      // parts side by side in a warp
-  __shared__ float sh_m[kMergeWarps * SIDE], sh_l[kMergeWarps * SIDE];
-  __shared__ __align__(16) float sh_o[kMergeWarps * SIDE][D];
-  // The lengths were there before the decode kernel began, and it let this one start after
-  // it had waited for them itself: the list can be made while it runs.
-  const int pairs = p.h_kv * p.m_tiles;
-  const int b = blockIdx.x / pairs, pair = blockIdx.x % pairs, head = pair / p.m_tiles, mt = pair % p.m_tiles;
-  const Split s = make_split<C::KT, C::PARTS>(p, b);
-  const int n = tiles_of<C::KT>(p, b);
-  const long long begin = s.before * pairs + (long long)pair * n;
-  int c0 = 0, c1 = -1;  // the parts that hold tiles of the pair
-  if (n > 0) c0 = (int)divide(begin, s.part), c1 = (int)divide(begin + n - 1, s.part);
-  const bool split = c0 < c1 || n == 0;  // else finished by its one warp
-  // part c: slot 2 c if its tiles begin in this pair, else 2 c + 1 (only c0 can begin before it)
-  const int slot0 = 2 * c0 + (c0 * s.part < begin);
+  __shared__ float sh_m[kMergeWarps], sh_l[kMergeWarps];
+  __shared__ __align__(16) float sh_o[kMergeWarps][D];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  if (!split) return;
+  const Note note = p.notes[blockIdx.x];
+  if (note.last < 0) return;
+  const int bh = note.pair / p.m_tiles, mt = note.pair - bh * p.m_tiles;
+  const int b = bh / p.h_kv, head = bh - b * p.h_kv;
+  const int parts = note.last - note.first + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = min(p.rows - mt * C::ROWS, C::ROWS);
-  const int r0 = blockIdx.y * group_rows, r1 = min(r0 + group_rows, rows);
-  const int slices = max(1, kMergeWarps / group_rows);  // warps per row
-  const int slice = warp % slices, col = 4 * (lane % LANES), side = lane / LANES;
-  for (int base = r0; base < r1; base += kMergeWarps / slices) {
-    const int r = base + warp / slices;
-    float M = -INFINITY, L = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (r < r1)
+  const int slices = kMergeWarps / group_rows;  // warps per row
+  const int slice = warp % slices, r = blockIdx.y * group_rows + warp / slices;
+  const int col = 4 * (lane % LANES), side = lane / LANES;
+  float M = -INFINITY, L = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  // 32 parts of the slice at a time: lane x has the statistics of the x-th
+  if (r < rows)
+#pragma unroll 1
+    for (int c0 = slice; c0 < parts; c0 += 32 * slices) {
+      auto row_of = [&](int c) { return (c == 0 ? note.slot : 2 * (note.first + c)) * C::ROWS + r; };
+      const int mine = c0 + lane * slices;
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (mine < parts) ml = *reinterpret_cast<const float2*>(p.ws_ml + (long long)row_of(mine) * 2);
+      float top = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+      const float m_new = fmaxf(M, top), use = m_new == -INFINITY ? 0.0f : m_new;
+      const float old = ptx::ex2(M - use), f = ptx::ex2(ml.x - use);
+      M = m_new;
+      float l = f * ml.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
+      L = fmaf(L, old, l);
+      acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
+      const int here = min(32, (parts - c0 + slices - 1) / slices);
 #pragma unroll 4
-      for (int c = c0 + slice * SIDE + side; c <= c1; c += slices * SIDE) {
-        const int w = (c == c0 ? slot0 : 2 * c) * C::ROWS + r;
-        const float2 ml = *reinterpret_cast<const float2*>(p.ws_ml + (long long)w * 2);
-        const float4 y = *reinterpret_cast<const float4*>(p.ws_o + (long long)w * D + col);
-        const float m_new = fmaxf(M, ml.x), use = m_new == -INFINITY ? 0.0f : m_new;
-        const float f0 = ptx::ex2(M - use), f1 = ptx::ex2(ml.x - use);
-        M = m_new;
-        L = L * f0 + ml.y * f1;
-        acc.x = acc.x * f0 + y.x * f1, acc.y = acc.y * f0 + y.y * f1;
-        acc.z = acc.z * f0 + y.z * f1, acc.w = acc.w * f0 + y.w * f1;
+      for (int x = 0; x < here; x += SIDE) {
+        const int y = x + side;
+        const float w = __shfl_sync(kAll, f, y & 31);
+        if (y < here) {
+          const float4 v = *reinterpret_cast<const float4*>(p.ws_o + (long long)row_of(c0 + y * slices) * D + col);
+          acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y);
+          acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
+        }
       }
-    const int at = warp * SIDE + side;
-    *reinterpret_cast<float4*>(&sh_o[at][col]) = acc;
-    if (col == 0) sh_m[at] = M, sh_l[at] = L;
-    __syncthreads();
-    if (slice == 0 && side == 0 && r < r1) {
-      for (int x = 1; x < slices * SIDE; ++x) {
-        const float4 y = *reinterpret_cast<const float4*>(&sh_o[at + x][col]);
-        const float m_new = fmaxf(M, sh_m[at + x]), use = m_new == -INFINITY ? 0.0f : m_new;
-        const float f0 = ptx::ex2(M - use), f1 = ptx::ex2(sh_m[at + x] - use);
-        M = m_new;
-        L = L * f0 + sh_l[at + x] * f1;
-        acc.x = acc.x * f0 + y.x * f1, acc.y = acc.y * f0 + y.y * f1;
-        acc.z = acc.z * f0 + y.z * f1, acc.w = acc.w * f0 + y.w * f1;
-      }
-      const long long row = out_row(p, b, head, mt * C::ROWS + r);
-      const bool none = M == -INFINITY && L == 0.0f;  // no legal key
-      const float inv = none ? 0.0f : 1.0f / L;
-      *reinterpret_cast<uint2*>(p.out + row * D + col) =
-          make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
-      if (p.lse && col == 0) p.lse[row] = none ? -INFINITY : log_sum(M, L);
     }
-    __syncthreads();
+  if (SIDE == 2) {
+    acc.x += __shfl_xor_sync(kAll, acc.x, 16), acc.y += __shfl_xor_sync(kAll, acc.y, 16);
+    acc.z += __shfl_xor_sync(kAll, acc.z, 16), acc.w += __shfl_xor_sync(kAll, acc.w, 16);
   }
+  if (slices > 1) {
+    *reinterpret_cast<float4*>(&sh_o[warp][col]) = acc;
+    if (lane == 0) sh_m[warp] = M, sh_l[warp] = L;
+    __syncthreads();
+    if (slice > 0) return;
+    float top = M;
+    for (int x = 1; x < slices; ++x) top = fmaxf(top, sh_m[warp + x]);
+    const float use = top == -INFINITY ? 0.0f : top;
+    const float f = ptx::ex2(M - use);
+    L *= f;
+    acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+#pragma unroll 1
+    for (int x = 1; x < slices; ++x) {
+      const float w = ptx::ex2(sh_m[warp + x] - use);
+      const float4 v = *reinterpret_cast<const float4*>(&sh_o[warp + x][col]);
+      L = fmaf(w, sh_l[warp + x], L);
+      acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y);
+      acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
+    }
+    M = top;
+  }
+  if (r >= rows || side > 0) return;
+  const long long row = out_row(p, b, head, mt * C::ROWS + r);
+  const bool none = M == -INFINITY && L == 0.0f;  // no legal key
+  const float inv = none ? 0.0f : __fdividef(1.0f, L);
+  *reinterpret_cast<uint2*>(p.out + row * D + col) =
+      make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (p.lse && col == 0) p.lse[row] = none ? -INFINITY : log_sum(M, L);
 }
 
 template <typename... KArgs, typename... Args>
@@ -806,11 +855,14 @@ int launch_pdl(void (*kernel)(KArgs...), dim3 grid, int block, int smem, cudaStr
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  // the same division of L1 for both kernels: an SM has to run empty to change it
+  at[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+  at[1].val.sharedMemCarveout = cudaSharedmemCarveoutMaxShared;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -826,13 +878,17 @@ int launch(const PagedArgs& a, float* ws) {
   p.B = a.B, p.n_q = a.n_q, p.h_q = a.h_q, p.h_kv = a.h_kv;
   p.group = a.h_q / a.h_kv, p.rows = a.n_q * p.group, p.m_tiles = (p.rows + C::ROWS - 1) / C::ROWS;
   p.n_pages = a.n_pages, p.page_size = a.page_size, p.max_pages = a.max_pages;
-  p.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz(a.page_size) : -1;
+  p.page_shift = 0;
+  while ((1LL << p.page_shift) < a.page_size) ++p.page_shift;
+  p.page_inv = (uint32_t)(((1ULL << (31 + p.page_shift)) + a.page_size - 1) / a.page_size);
+  p.group_inv = (uint32_t)((0x100000000ULL + p.group - 1) / p.group);  // group 1 does without
   p.max_len = a.max_pages * a.page_size;
   // no key is further back than max_len: wider windows and more sinks say the same
   p.window = a.window < p.max_len ? a.window : p.max_len;
   p.sinks = a.window < 0 ? 0 : a.sinks < p.max_len ? a.sinks : p.max_len;
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634074);
   p.ws_o = ws, p.ws_ml = ws + (size_t)2 * C::PARTS * C::ROWS * D;
+  p.notes = reinterpret_cast<Note*>(p.ws_ml + (size_t)2 * C::PARTS * C::ROWS * 2);
   // tiles that any pair may have: a pair is not worth splitting where that is few, nor where
   // it is no long stretch and there are pairs enough to fill the device twice
   long long most = p.max_len;
@@ -843,15 +899,15 @@ int launch(const PagedArgs& a, float* ws) {
   if (cudaFuncSetAttribute(attn_paged_kernel<D, NT, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            C::SMEM_BYTES) != cudaSuccess)
     return ATTN_ERR_CUDA;
-  const unsigned ctas = p.whole ? (unsigned)((pairs + kWarps - 1) / kWarps) : C::CTAS_PER_SM * kSMs;
-  const int st = launch_pdl(attn_paged_kernel<D, NT, FP8>, dim3(ctas), kThreads, C::SMEM_BYTES, a.stream, p);
+  p.notes_by_pair = pairs <= C::PARTS;
+  const int st = launch_pdl(attn_paged_kernel<D, NT, FP8>, dim3(p.whole ? (unsigned)pairs : C::PARTS), 32,
+                            C::SMEM_BYTES, a.stream, p);
   if (st != ATTN_OK || p.whole) return st;
-  // few pairs have many parts each: a block per row, all its warps on that row's parts
+  // few pairs have many parts each: all warps of a block on one row's
   const int rows = p.rows < C::ROWS ? p.rows : C::ROWS;
-  const int group_rows = pairs * rows <= 4 * kSMs ? 1 : C::ROWS;
-  return launch_pdl(attn_paged_merge_kernel<D, NT, FP8>,
-                    dim3((unsigned)pairs, (unsigned)((rows + group_rows - 1) / group_rows)), kMergeThreads, 0, a.stream,
-                    p, group_rows);
+  const int group_rows = pairs * rows <= 8 * kSMs ? 1 : rows <= 4 ? 4 : 8;
+  const dim3 grid(p.notes_by_pair ? (unsigned)pairs : C::PARTS, (unsigned)((rows + group_rows - 1) / group_rows));
+  return launch_pdl(attn_paged_merge_kernel<D, NT, FP8>, grid, kMergeThreads, 0, a.stream, p, group_rows);
 }
 
 template <int D, bool FP8>
@@ -864,7 +920,7 @@ int launch_rows(const PagedArgs& a, float* ws) {
 // Two slots for every warp that can be resident, whatever the lengths.
 size_t paged_decode_workspace_bytes(int n_q, int group, int d) {
   const int rows = (long long)n_q * group <= 8 ? 8 : 16;
-  return (size_t)2 * kMaxParts * rows * (d + 2) * sizeof(float);
+  return (size_t)kMaxParts * (2 * rows * (d + 2) * sizeof(float) + sizeof(Note));
 }
 
 int launch_attn_paged_decode(const PagedArgs& a, void* workspace) {
