@@ -106,8 +106,8 @@ def status_string(status: int) -> str:
 
 
 def _stream_handle(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the raw handle: a stream object costs 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -454,43 +454,53 @@ def attn_linear(x, w, y, bias=None, stream=None):
     return y
 
 
-def _same_device(first, *others):
-    """The launch goes to the current device: every tensor has to be there."""
-    dev = first.get_device()
+def _device_of(t) -> int:
+    """The device of a call's tensors: the current one, where its launches go."""
+    dev = t.get_device()
     if dev != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on cuda:{dev}, the current device is cuda:{torch.cuda.current_device()}")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("all tensors must be on one device")
+        raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _check_rows(t, name, ndim):
-    """bf16 head rows by token, [..., heads, d]: a token's heads side by side, tokens one stride apart."""
-    if t.dtype != torch.bfloat16 or t.dim() != ndim or not t.is_cuda:
-        raise ValueError(f"{name} must be a {ndim}-D CUDA bfloat16 tensor, got {t.dtype} {tuple(t.shape)}")
-    st, sh = t.stride(), t.shape
-    if (st[-1] != 1 or (sh[-2] != 1 and st[-2] != sh[-1])
-            or (ndim == 4 and sh[0] != 1 and sh[1] != 1 and st[0] != sh[1] * st[1])):
-        raise ValueError(f"{name}: a token's heads must lie side by side and tokens one stride apart, got strides {st}")
+def _need(t, name, dtype, shape, dev):
+    """Data pointer of a contiguous tensor of that type, shape and device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on cuda:{dev}, got "
+                         f"{t.dtype} {list(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
 
 
-def _row_stride(t):
-    """Elements between tokens; of a single token, those of its heads."""
-    if t.dim() == 4 and t.shape[1] == 1:
-        return t.stride(0) if t.shape[0] > 1 else t.shape[2] * t.shape[3]
-    return t.stride(-3) if t.shape[-3] > 1 else t.shape[-2] * t.shape[-1]
+def _need_rows(t, name, shape, dev):
+    """Data pointer and token stride of bf16 head rows by token, ``[..., heads, d]``: a token's
+    heads side by side, tokens one stride apart (a view of a fused projection)."""
+    st = t.stride()
+    if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == dev and st[-1] == 1:
+        n, h, d = shape[-3:]
+        if h == 1 or st[-2] == d:
+            if len(shape) == 3 or shape[0] == 1:
+                return t.data_ptr(), st[-3] if n > 1 else h * d
+            if n == 1:
+                return t.data_ptr(), st[0]
+            if st[0] == n * st[1]:
+                return t.data_ptr(), st[1]
+    raise ValueError(f"{name} must be a bfloat16 tensor of shape {list(shape)} on cuda:{dev}, a token's heads side by "
+                     f"side and tokens one stride apart, got {t.dtype} {list(t.shape)} with strides {st} on {t.device}")
 
 
-def _check_rotation(cos_sin, q_weight, k_weight, d):
-    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _check(t, n, torch.bfloat16, 1)
-            if t.shape[0] != d:
-                raise ValueError(f"{n} must have shape [{d}]")
+def _need_table(cos_sin, dev):
+    """Pointer, positions and columns of a rotation table; none without one."""
     if cos_sin is None:
-        return 0, 0
-    _check(cos_sin, "cos_sin", torch.float32, 2)
-    return cos_sin.shape
+        return None, 0, 0
+    if cos_sin.dim() != 2:
+        raise ValueError(f"cos_sin must be [n_pos, d_rot], got {list(cos_sin.shape)}")
+    shape = cos_sin.shape
+    return _need(cos_sin, "cos_sin", torch.float32, shape, dev), shape[0], shape[1]
+
+
+def _need_workspace(workspace, dev):
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def attn_norm_rope(q, k, q_out, k_out, cos_sin, q_weight=None, k_weight=None, positions=None, eps=1e-6,
@@ -500,24 +510,22 @@ def attn_norm_rope(q, k, q_out, k_out, cos_sin, q_weight=None, k_weight=None, po
     ``q_out [B, h_q, n, d]`` and ``k_out [B, h_kv, n, d]``. ``cos_sin`` is float32
     ``[n_pos, d_rot]`` (cosines, then sines; None: no rotation), ``positions`` int32 ``[B, n]``
     or None for 0 .. n - 1; ``interleaved`` turns adjacent columns instead of the halves."""
-    _check_rows(q, "q", 4)
-    _check_rows(k, "k", 4)
-    _check(q_out, "q_out", torch.bfloat16)
-    _check(k_out, "k_out", torch.bfloat16)
+    dev, bf16 = _device_of(q), torch.bfloat16
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"q, k must be [B, n, heads, d], got {list(q.shape)} {list(k.shape)}")
     B, n, h_q, d = q.shape
     h_kv = k.shape[2]
-    if k.shape != (B, n, h_kv, d) or q_out.shape != (B, h_q, n, d) or k_out.shape != (B, h_kv, n, d):
-        raise ValueError(f"shape mismatch: q{tuple(q.shape)} k{tuple(k.shape)} q_out{tuple(q_out.shape)} "
-                         f"k_out{tuple(k_out.shape)}")
-    n_pos, d_rot = _check_rotation(cos_sin, q_weight, k_weight, d)
-    if positions is not None:
-        _check(positions, "positions", torch.int32, 2)
-        if positions.shape != (B, n):
-            raise ValueError("positions must have shape [B, n]")
-    _same_device(q, k, q_out, k_out, cos_sin, q_weight, k_weight, positions)
-    st = lib().attn_norm_rope(_ptr(q), _ptr(k), _row_stride(q), _row_stride(k), _ptr(q_weight), _ptr(k_weight),
-                              float(eps), _ptr(cos_sin), n_pos, d_rot, _ptr(positions), _ptr(q_out), _ptr(k_out), B, n,
-                              h_q, h_kv, d, ROPE_INTERLEAVED if interleaved else 0, _stream_handle(stream))
+    q_ptr, q_stride = _need_rows(q, "q", (B, n, h_q, d), dev)
+    k_ptr, k_stride = _need_rows(k, "k", (B, n, h_kv, d), dev)
+    table, n_pos, d_rot = _need_table(cos_sin, dev)
+    st = lib().attn_norm_rope(
+        q_ptr, k_ptr, q_stride, k_stride,
+        None if q_weight is None else _need(q_weight, "q_weight", bf16, (d,), dev),
+        None if k_weight is None else _need(k_weight, "k_weight", bf16, (d,), dev),
+        float(eps), table, n_pos, d_rot,
+        None if positions is None else _need(positions, "positions", torch.int32, (B, n), dev),
+        _need(q_out, "q_out", bf16, (B, h_q, n, d), dev), _need(k_out, "k_out", bf16, (B, h_kv, n, d), dev),
+        B, n, h_q, h_kv, d, ROPE_INTERLEAVED if interleaved else 0, _stream_handle(stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_norm_rope")
     return q_out, k_out
@@ -533,56 +541,51 @@ def attn_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, workspace, cos_sin, q_weigh
     ``dq``, ``dk`` (token-major like ``q``, ``k``) and, with a norm, float32 ``dq_weight``,
     ``dk_weight [d]``; ``workspace``: a CUDA tensor of at least
     ``attn_norm_rope_bwd_workspace_size`` bytes (None without a norm)."""
-    for t, m in ((q, "q"), (k, "k"), (dq, "dq"), (dk, "dk")):
-        _check_rows(t, m, 4)
-    _check(dq_out, "dq_out", torch.bfloat16)
-    _check(dk_out, "dk_out", torch.bfloat16)
+    dev, bf16, f32 = _device_of(q), torch.bfloat16, torch.float32
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"q, k must be [B, n, heads, d], got {list(q.shape)} {list(k.shape)}")
     B, n, h_q, d = q.shape
     h_kv = k.shape[2]
-    if (k.shape != (B, n, h_kv, d) or dq_out.shape != (B, h_q, n, d) or dk_out.shape != (B, h_kv, n, d)
-            or dq.shape != q.shape or dk.shape != k.shape):
-        raise ValueError("shape mismatch between q, k, their gradients and the outputs' gradients")
-    n_pos, d_rot = _check_rotation(cos_sin, q_weight, k_weight, d)
-    for t, m in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
-        if t is not None:
-            _check(t, m, torch.float32, 1)
-            if t.shape[0] != d:
-                raise ValueError(f"{m} must have shape [{d}]")
-    if positions is not None:
-        _check(positions, "positions", torch.int32, 2)
-        if positions.shape != (B, n):
-            raise ValueError("positions must have shape [B, n]")
-    if workspace is not None and not (workspace.is_cuda and workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    _same_device(q, k, dq_out, dk_out, dq, dk, workspace, cos_sin, q_weight, k_weight, dq_weight, dk_weight, positions)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = lib().attn_norm_rope_bwd(_ptr(q), _ptr(k), _row_stride(q), _row_stride(k), _ptr(q_weight), _ptr(k_weight),
-                                  float(eps), _ptr(cos_sin), n_pos, d_rot, _ptr(positions), _ptr(dq_out), _ptr(dk_out),
-                                  _ptr(dq), _ptr(dk), _row_stride(dq), _row_stride(dk), _ptr(dq_weight),
-                                  _ptr(dk_weight), B, n, h_q, h_kv, d, ROPE_INTERLEAVED if interleaved else 0,
-                                  _ptr(workspace), nbytes, _stream_handle(stream))
+    q_shape, k_shape = (B, n, h_q, d), (B, n, h_kv, d)
+    q_ptr, q_stride = _need_rows(q, "q", q_shape, dev)
+    k_ptr, k_stride = _need_rows(k, "k", k_shape, dev)
+    dq_ptr, dq_stride = _need_rows(dq, "dq", q_shape, dev)
+    dk_ptr, dk_stride = _need_rows(dk, "dk", k_shape, dev)
+    table, n_pos, d_rot = _need_table(cos_sin, dev)
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else _need_workspace(workspace, dev)
+    st = lib().attn_norm_rope_bwd(
+        q_ptr, k_ptr, q_stride, k_stride,
+        None if q_weight is None else _need(q_weight, "q_weight", bf16, (d,), dev),
+        None if k_weight is None else _need(k_weight, "k_weight", bf16, (d,), dev),
+        float(eps), table, n_pos, d_rot,
+        None if positions is None else _need(positions, "positions", torch.int32, (B, n), dev),
+        _need(dq_out, "dq_out", bf16, (B, h_q, n, d), dev), _need(dk_out, "dk_out", bf16, (B, h_kv, n, d), dev),
+        dq_ptr, dk_ptr, dq_stride, dk_stride,
+        None if dq_weight is None else _need(dq_weight, "dq_weight", f32, (d,), dev),
+        None if dk_weight is None else _need(dk_weight, "dk_weight", f32, (d,), dev),
+        B, n, h_q, h_kv, d, ROPE_INTERLEAVED if interleaved else 0, ws_ptr, ws_bytes, _stream_handle(stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_norm_rope_bwd")
     return dq, dk
 
 
-def _check_pages(k_pages, v_pages, k_scale, v_scale, page_table, h_kv, d):
-    """Flags of a paged cache ``[n_pages, h_kv, page_size, d]`` in bf16 or float8_e4m3fn."""
-    e4m3 = k_pages.dtype == torch.float8_e4m3fn
-    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        _check(t, n, torch.float8_e4m3fn if e4m3 else torch.bfloat16)
-    if k_pages.shape != v_pages.shape or k_pages.shape[1] != h_kv or k_pages.shape[3] != d:
-        raise ValueError(f"k_pages, v_pages must be [n_pages, {h_kv}, page_size, {d}], got {tuple(k_pages.shape)} "
-                         f"{tuple(v_pages.shape)}")
-    _check(page_table, "page_table", torch.int32, 2)
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if (t is not None) != e4m3:
-            raise ValueError(f"{n} is required with an e4m3 cache, and only there")
-        if t is not None:
-            _check(t, n, torch.float32, 1)
-            if t.shape[0] != h_kv:
-                raise ValueError(f"{n} must have shape [{h_kv}]")
-    return CACHE_E4M3 if e4m3 else 0
+def _need_pages(k_pages, v_pages, k_scale, v_scale, h_kv, d, dev):
+    """A paged cache ``[n_pages, h_kv, page_size, d]`` in bf16, or in float8_e4m3fn with its scales:
+    flags, n_pages, page_size, the pages' and scales' pointers."""
+    kind = k_pages.dtype
+    e4m3 = kind is torch.float8_e4m3fn
+    if k_pages.dim() != 4 or not (e4m3 or kind is torch.bfloat16):
+        raise ValueError(f"k_pages must be [n_pages, h_kv, page_size, d] in bfloat16 or float8_e4m3fn, got {kind} "
+                         f"{list(k_pages.shape)}")
+    if (k_scale is not None) != e4m3 or (v_scale is not None) != e4m3:
+        raise ValueError("k_scale and v_scale are required with an e4m3 cache, and only there")
+    n_pages, _, page_size, _ = k_pages.shape
+    shape = (n_pages, h_kv, page_size, d)
+    k_ptr, v_ptr = _need(k_pages, "k_pages", kind, shape, dev), _need(v_pages, "v_pages", kind, shape, dev)
+    if not e4m3:
+        return 0, n_pages, page_size, k_ptr, v_ptr, None, None
+    return (CACHE_E4M3, n_pages, page_size, k_ptr, v_ptr, _need(k_scale, "k_scale", torch.float32, (h_kv,), dev),
+            _need(v_scale, "v_scale", torch.float32, (h_kv,), dev))
 
 
 def attn_paged_append(k, v, k_pages, v_pages, positions, page_table, seq_ids=None, q=None, q_out=None, cos_sin=None,
@@ -594,37 +597,34 @@ def attn_paged_append(k, v, k_pages, v_pages, positions, page_table, seq_ids=Non
     tokens' queries ``q [T, h_q, d]`` into ``q_out`` (contiguous). ``positions`` int32 ``[T]``
     (negative: padding, skipped), ``seq_ids`` int32 ``[T]`` (None: token x is sequence x's),
     ``page_table`` int32 ``[n_seqs, max_pages]``."""
-    _check_rows(k, "k", 3)
-    _check_rows(v, "v", 3)
+    dev, bf16, i32 = _device_of(k), torch.bfloat16, torch.int32
+    if k.dim() != 3 or page_table.dim() != 2:
+        raise ValueError(f"k must be [T, h_kv, d], page_table [n_seqs, max_pages], got {list(k.shape)} "
+                         f"{list(page_table.shape)}")
     T, h_kv, d = k.shape
-    if v.shape != k.shape:
-        raise ValueError(f"shape mismatch: k{tuple(k.shape)} v{tuple(v.shape)}")
-    flags = _check_pages(k_pages, v_pages, k_scale, v_scale, page_table, h_kv, d)
+    k_ptr, k_stride = _need_rows(k, "k", (T, h_kv, d), dev)
+    v_ptr, v_stride = _need_rows(v, "v", (T, h_kv, d), dev)
+    flags, n_pages, page_size, kp, vp, ks, vs = _need_pages(k_pages, v_pages, k_scale, v_scale, h_kv, d, dev)
+    q_ptr = q_to = None
     h_q = q_stride = 0
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None:
-        _check_rows(q, "q", 3)
-        _check(q_out, "q_out", torch.bfloat16, 3)
-        h_q, q_stride = q.shape[1], _row_stride(q)
-        if q.shape != (T, h_q, d) or q_out.shape != q.shape:
-            raise ValueError(f"shape mismatch: q{tuple(q.shape)} q_out{tuple(q_out.shape)} k{tuple(k.shape)}")
-    n_pos, d_rot = _check_rotation(cos_sin, q_weight, k_weight, d)
-    _check(positions, "positions", torch.int32, 1)
-    if positions.shape[0] != T:
-        raise ValueError("positions must have shape [T]")
-    if seq_ids is not None:
-        _check(seq_ids, "seq_ids", torch.int32, 1)
-        if seq_ids.shape[0] != T:
-            raise ValueError("seq_ids must have shape [T]")
-    _same_device(k, v, k_pages, v_pages, positions, page_table, seq_ids, q, q_out, cos_sin, q_weight, k_weight,
-                 k_scale, v_scale)
-    st = lib().attn_paged_append(_ptr(q), _ptr(k), _ptr(v), q_stride, _row_stride(k), _row_stride(v), _ptr(q_weight),
-                                 _ptr(k_weight), float(eps), _ptr(cos_sin), n_pos, d_rot, _ptr(positions),
-                                 _ptr(seq_ids), _ptr(page_table), page_table.shape[0], page_table.shape[1],
-                                 _ptr(q_out), _ptr(k_pages), _ptr(v_pages), k_pages.shape[0], k_pages.shape[2],
-                                 _ptr(k_scale), _ptr(v_scale), T, h_q, h_kv, d,
-                                 flags | (ROPE_INTERLEAVED if interleaved else 0), _stream_handle(stream))
+        if q.dim() != 3:
+            raise ValueError(f"q must be [T, h_q, d], got {list(q.shape)}")
+        h_q = q.shape[1]
+        q_ptr, q_stride = _need_rows(q, "q", (T, h_q, d), dev)
+        q_to = _need(q_out, "q_out", bf16, (T, h_q, d), dev)
+    table, n_pos, d_rot = _need_table(cos_sin, dev)
+    n_seqs, max_pages = page_table.shape
+    st = lib().attn_paged_append(
+        q_ptr, k_ptr, v_ptr, q_stride, k_stride, v_stride,
+        None if q_weight is None else _need(q_weight, "q_weight", bf16, (d,), dev),
+        None if k_weight is None else _need(k_weight, "k_weight", bf16, (d,), dev),
+        float(eps), table, n_pos, d_rot, _need(positions, "positions", i32, (T,), dev),
+        None if seq_ids is None else _need(seq_ids, "seq_ids", i32, (T,), dev),
+        _need(page_table, "page_table", i32, (n_seqs, max_pages), dev), n_seqs, max_pages, q_to, kp, vp, n_pages,
+        page_size, ks, vs, T, h_q, h_kv, d, flags | (ROPE_INTERLEAVED if interleaved else 0), _stream_handle(stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_append")
     return q_out
@@ -641,28 +641,20 @@ def attn_paged_decode(q, k_pages, v_pages, out, page_table, cache_lens, workspac
     included, into ``out`` (like ``q``) and optional float32 ``lse [B, n_q, h_q]``. ``window`` >= 0:
     only keys within that distance and the first ``sinks``. ``workspace``: a CUDA tensor of
     at least ``attn_paged_decode_workspace_size`` bytes."""
-    _check(q, "q", torch.bfloat16)
-    _check(out, "out", torch.bfloat16)
-    B, n_q, h_q, d = q.shape
-    h_kv = k_pages.shape[1] if k_pages.dim() == 4 else 0
-    flags = _check_pages(k_pages, v_pages, k_scale, v_scale, page_table, h_kv, d)
-    _check(cache_lens, "cache_lens", torch.int32, 1)
-    if out.shape != q.shape or page_table.shape[0] != B or cache_lens.shape[0] != B:
-        raise ValueError("shape mismatch between q, out, page_table and cache_lens")
-    if lse is not None:
-        _check(lse, "lse", torch.float32, 3)
-        if lse.shape != (B, n_q, h_q):
-            raise ValueError("lse must have shape [B, n_q, h_q]")
-    if not (workspace.is_cuda and workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous CUDA tensor")
-    _same_device(q, k_pages, v_pages, out, page_table, cache_lens, workspace, lse, k_scale, v_scale)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    st = lib().attn_paged_decode(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(out), _ptr(lse), _ptr(page_table),
-                                 _ptr(cache_lens), B, n_q, h_q, h_kv, d, k_pages.shape[0], k_pages.shape[2],
-                                 page_table.shape[1], float(scale), int(window), int(sinks), _ptr(k_scale),
-                                 _ptr(v_scale), flags, _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                 _stream_handle(stream))
+    dev, i32 = _device_of(q), torch.int32
+    if q.dim() != 4 or k_pages.dim() != 4 or page_table.dim() != 2:
+        raise ValueError(f"q must be [B, n_q, h_q, d], the pages [n_pages, h_kv, page_size, d], page_table "
+                         f"[B, max_pages], got {list(q.shape)} {list(k_pages.shape)} {list(page_table.shape)}")
+    B, n_q, h_q, d = shape = q.shape
+    h_kv, max_pages = k_pages.shape[1], page_table.shape[1]
+    flags, n_pages, page_size, kp, vp, ks, vs = _need_pages(k_pages, v_pages, k_scale, v_scale, h_kv, d, dev)
+    ws_ptr, ws_bytes = _need_workspace(workspace, dev)
+    st = lib().attn_paged_decode(
+        _need(q, "q", torch.bfloat16, shape, dev), kp, vp, _need(out, "out", torch.bfloat16, shape, dev),
+        None if lse is None else _need(lse, "lse", torch.float32, (B, n_q, h_q), dev),
+        _need(page_table, "page_table", i32, (B, max_pages), dev), _need(cache_lens, "cache_lens", i32, (B,), dev),
+        B, n_q, h_q, h_kv, d, n_pages, page_size, max_pages, 1.0 / math.sqrt(d) if scale is None else float(scale),
+        int(window), int(sinks), ks, vs, flags, ws_ptr, ws_bytes, _stream_handle(stream))
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_decode")
     return out

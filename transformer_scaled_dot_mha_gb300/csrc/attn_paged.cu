@@ -896,9 +896,7 @@ int launch(const PagedArgs& a, float* ws) {
   const long long pairs = (long long)a.B * a.h_kv * p.m_tiles, tiles = (most + C::KT - 1) / C::KT;
   if (pairs > 0x7fffffffLL) return ATTN_ERR_INVALID;
   p.whole = tiles <= kWholeTiles || (tiles <= 4 * kWholeTiles && pairs >= 2 * C::PARTS);
-  if (cudaFuncSetAttribute(attn_paged_kernel<D, NT, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           C::SMEM_BYTES) != cudaSuccess)
-    return ATTN_ERR_CUDA;
+  static_assert(C::SMEM_BYTES <= 48 * 1024, "fits without raising the kernel's limit");
   p.notes_by_pair = pairs <= C::PARTS;
   const int st = launch_pdl(attn_paged_kernel<D, NT, FP8>, dim3(p.whole ? (unsigned)pairs : C::PARTS), 32,
                             C::SMEM_BYTES, a.stream, p);

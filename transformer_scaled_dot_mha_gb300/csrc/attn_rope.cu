@@ -37,9 +37,9 @@ namespace {
 constexpr int kSMs = 152;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRows = 4;     // rows in flight per lane group, forward and append
-constexpr int kBwdRows = 2;  // rows in flight per lane group, gradients (two operands each)
-constexpr int kBwdCtasPerSM = 4;
+constexpr int kRows = 4;          // rows in flight per lane group, forward and append
+constexpr int kBwdCtasPerSM = 4;  // gradients: 128 registers a thread
+constexpr int kBwdBytes = 12288;  // of copies in flight per warp
 
 enum Kind { kQuery = 0, kKey = 1, kValue = 2 };
 
@@ -302,26 +302,51 @@ struct RopeBwdParams {
   int n_pos, d_rot;
   const int32_t* positions;
   int n, tokens;
-  int heads[2], units[2], heads_per_unit;
+  int heads[2];
   int ctas[2];      // the first ctas[0] CTAs take the queries, the others the keys
+  int items[2];     // per warp
   float* partials;  // [ctas[0] + ctas[1]][d], sums of the weights' gradients
   float* dw[2];
 };
 
-// A CTA walks over (token tile, heads) tasks of one kind and keeps its share of the
-// weight's gradient in registers; the shares go to the workspace and are summed in a fixed
-// order by attn_rope_dw_kernel: no atomics, the same bits on every run.
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(addr)
+               : "memory");
+  return r;
+}
+
+// An item is one head of the tokens side by side in a warp (32 * 16 / d rows). The items of a
+// kind, heads first, form one list cut into equal runs, a warp each; a warp keeps STAGES items'
+// rows (x and g, whole rows by cp.async: its own ring, its own waits) in flight, so that HBM
+// does not wait for the arithmetic, and its share of the weight's gradient in registers. The
+// shares go to the workspace and are summed in a fixed order by attn_rope_dw_kernel: no
+// atomics, the same bits on every run.
 template <int D, bool PAIRS, bool NORM>
-__global__ void __launch_bounds__(kThreads) attn_rope_bwd_kernel(const RopeBwdParams p) {
+__global__ void __launch_bounds__(kThreads, kBwdCtasPerSM) attn_rope_bwd_kernel(const RopeBwdParams p) {
   using L = Lanes<D>;
+  constexpr int PIECES = D / 8;              // 16-byte pieces of a row
+  constexpr int COPIES = L::GROUPS * PIECES / 32;  // per operand and item
+  constexpr int ITEM = (NORM ? 2 : 1) * 1024;      // bytes of an item: g, then x
+  constexpr int STAGES = kBwdBytes / ITEM;
+  static_assert(L::GROUPS * D * 2 == 1024, "an item's rows");
+  __shared__ __align__(128) uint8_t ring_sh[kWarps][STAGES * ITEM];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int l = lane % L::PER_ROW;
+  const int l = lane % L::PER_ROW, side = lane / L::PER_ROW;
   const int kind = (int)blockIdx.x >= p.ctas[0];
   const int cta = blockIdx.x - (kind ? p.ctas[0] : 0);
-  const int n_units = p.units[kind], H = p.heads[kind];
-  const long long tiles = ((long long)p.tokens + L::TOKENS - 1) / L::TOKENS;
+  const int H = p.heads[kind];
+  const long long total = ((long long)p.tokens + L::GROUPS - 1) / L::GROUPS * H;
+  const long long begin = ((long long)cta * kWarps + warp) * p.items[kind];
+  const int count = (int)max(0ll, min((long long)p.items[kind], total - begin));
+  const uint32_t ring = ptx::smem_u32(ring_sh[warp]);
   int c0, c1;
   bool rot0, rot1;
   chunks_of<D, PAIRS>(l, p.d_rot, c0, c1, rot0, rot1);
@@ -334,75 +359,103 @@ __global__ void __launch_bounds__(kThreads) attn_rope_bwd_kernel(const RopeBwdPa
 #pragma unroll
   for (int e = 0; e < 16; ++e) dw[e] = 0.0f;
 
-  for (long long task = cta; task < tiles * n_units; task += p.ctas[kind]) {
-    const int h0 = (int)(task % n_units) * p.heads_per_unit, h1 = min(h0 + p.heads_per_unit, H);
-    const long long t0 = task / n_units * L::TOKENS + warp * L::GROUPS;
-    if (t0 >= p.tokens) continue;  // whole warps
-    const bool there = t0 + lane / L::PER_ROW < p.tokens;
-    const int t = there ? (int)t0 + lane / L::PER_ROW : p.tokens - 1;
-    const int b = t / p.n, i = t - b * p.n;
-    const int pos = p.positions ? __ldg(p.positions + t) : i;
-    const bool valid = there && pos >= 0 && (p.d_rot == 0 || pos < p.n_pos);
-    Angles a;
-    if (valid) load_angles<PAIRS>(a, p.cos_sin + (long long)pos * p.d_rot, p.d_rot, c0, c1, rot0, rot1);
-    const uint16_t* src = p.x[kind] + t * p.stride[kind];
-    uint16_t* dst = p.dx[kind] + t * p.dstride[kind];
-
-    for (int h = h0; h < h1; h += kBwdRows) {
-      uint4 v[kBwdRows][2], g[kBwdRows][2];
+  // the requests' place in the list, and where their rows start: copy y takes piece
+  // lane % PIECES of row y * 32 / PIECES + lane / PIECES
+  int group_a = (int)(begin / H), h_a = (int)(begin - (long long)group_a * H);
+  const uint16_t* g_src[COPIES];
+  const uint16_t* x_src[COPIES];
+  bool row_there[COPIES];
+  auto rows_of = [&]() {
 #pragma unroll
-      for (int u = 0; u < kBwdRows; ++u) {
-        v[u][0] = v[u][1] = g[u][0] = g[u][1] = make_uint4(0, 0, 0, 0);
-        if (h + u < h1 && valid) {
-          const uint16_t* gs = p.g[kind] + (((long long)b * H + h + u) * p.n + i) * D;
-          if (NORM) {
-            v[u][0] = load_once(src + (h + u) * D + 8 * c0);
-            v[u][1] = load_once(src + (h + u) * D + 8 * c1);
-          }
-          g[u][0] = load_once(gs + 8 * c0);
-          g[u][1] = load_once(gs + 8 * c1);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kBwdRows; ++u) {
-        if (h + u >= h1) break;
-        float gy[16];
-        widen(gy, g[u][0]);
-        widen(gy + 8, g[u][1]);
-        if (valid) rotate<PAIRS, true>(gy, a, rot0, rot1);
-        if (NORM) {
-          float x[16], w[16];
-          widen(x, v[u][0]);
-          widen(x + 8, v[u][1]);
-          widen(w, w0);
-          widen(w + 8, w1);
-          float ss = 0.0f, dot = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            ss = fmaf(x[e], x[e], ss);
-            dot = fmaf(gy[e] * w[e], x[e], dot);
-          }
-          ss = row_sum<D>(ss);
-          dot = row_sum<D>(dot);
-          const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-          const float back = r * r * dot * (1.0f / D);
-          if (valid)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) dw[e] = fmaf(gy[e], x[e] * r, dw[e]);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) gy[e] = r * (gy[e] * w[e] - x[e] * back);
-        }
-        if (there) {  // a padding token's gradient is zero
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(dst + (h + u) * D + 8 * c0) = valid ? narrow(gy) : zero;
-          *reinterpret_cast<uint4*>(dst + (h + u) * D + 8 * c1) = valid ? narrow(gy + 8) : zero;
-        }
-      }
+    for (int y = 0; y < COPIES; ++y) {
+      const long long t = (long long)group_a * L::GROUPS + y * (32 / PIECES) + lane / PIECES;
+      row_there[y] = t < p.tokens;
+      const int tt = row_there[y] ? (int)t : 0, b = tt / p.n, i = tt - b * p.n;
+      g_src[y] = p.g[kind] + ((long long)b * H * p.n + i) * D + 8 * (lane % PIECES);
+      x_src[y] = p.x[kind] + tt * p.stride[kind] + 8 * (lane % PIECES);
     }
+  };
+  if (count > 0) rows_of();
+  auto request = [&](int stage) {
+    const uint32_t at = ring + stage * ITEM + 16 * lane;
+#pragma unroll
+    for (int y = 0; y < COPIES; ++y) {
+      copy_async(at + 512 * y, g_src[y] + (long long)h_a * p.n * D, row_there[y]);
+      if (NORM) copy_async(at + 1024 + 512 * y, x_src[y] + h_a * D, row_there[y]);
+    }
+    if (++h_a == H) {
+      h_a = 0;
+      ++group_a;
+      rows_of();
+    }
+  };
+
+  int group = group_a, h = h_a, stage = 0;
+  bool fresh = true, there = false, valid = false;
+  Angles a;
+  uint16_t* dst = nullptr;
+  // the steps below 0 fill the ring
+  for (int i = -STAGES; i < count; ++i) {
+    if (i >= 0) {
+      if (fresh) {  // the next tokens
+        const long long t_ = (long long)group * L::GROUPS + side;
+        there = t_ < p.tokens;
+        const int t = there ? (int)t_ : p.tokens - 1;
+        const int pos = p.positions ? __ldg(p.positions + t) : t % p.n;
+        valid = there && pos >= 0 && (p.d_rot == 0 || pos < p.n_pos);
+        if (valid) load_angles<PAIRS>(a, p.cos_sin + (long long)pos * p.d_rot, p.d_rot, c0, c1, rot0, rot1);
+        dst = p.dx[kind] + t * p.dstride[kind];
+        fresh = false;
+      }
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+      __syncwarp();
+      const uint32_t at = ring + stage * ITEM + side * (2 * D);
+      float gy[16];
+      widen(gy, lds128(at + 16 * c0));
+      widen(gy + 8, lds128(at + 16 * c1));
+      if (valid) rotate<PAIRS, true>(gy, a, rot0, rot1);
+      if (NORM) {
+        float x[16], w[16];
+        widen(x, lds128(at + 1024 + 16 * c0));
+        widen(x + 8, lds128(at + 1024 + 16 * c1));
+        widen(w, w0);
+        widen(w + 8, w1);
+        float ss = 0.0f, dot = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          ss = fmaf(x[e], x[e], ss);
+          dot = fmaf(gy[e] * w[e], x[e], dot);
+        }
+        ss = row_sum<D>(ss);
+        dot = row_sum<D>(dot);
+        const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+        const float back = r * r * dot * (1.0f / D);
+        if (valid)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) dw[e] = fmaf(gy[e], x[e] * r, dw[e]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) gy[e] = r * (gy[e] * w[e] - x[e] * back);
+      }
+      if (there) {  // a padding token's gradient is zero
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(dst + h * D + 8 * c0) = valid ? narrow(gy) : zero;
+        *reinterpret_cast<uint4*>(dst + h * D + 8 * c1) = valid ? narrow(gy + 8) : zero;
+      }
+      if (++h == H) {
+        h = 0;
+        ++group;
+        fresh = true;
+      }
+      __syncwarp();  // the stage is read
+    }
+    if (i + STAGES < count) request(stage);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    stage = stage + 1 < STAGES ? stage + 1 : 0;
   }
 
   if (NORM) {
-    __shared__ float part[kWarps][D];
+    float(*part)[D] = reinterpret_cast<float(*)[D]>(ring_sh);  // every copy has landed and been read
+    __syncthreads();
 #pragma unroll
     for (int o = L::PER_ROW; o < 32; o <<= 1)
 #pragma unroll
@@ -488,17 +541,22 @@ int launch_rope(RopeParams& p, int d, bool pairs, bool paged, bool e4m3, cudaStr
   return launch_pdl(kernel, dim3((unsigned)(tiles * units)), dim3(kThreads), stream, p);
 }
 
-// CTAs of the gradient kernel: the device filled, shared out by the kinds' heads.
-void bwd_grid(long long tokens, int h_q, int h_kv, int d, int* hp, int* units, int* ctas) {
-  const long long tiles = (tokens + tokens_per_tile(d) - 1) / tokens_per_tile(d);
+// CTAs of the gradient kernel: the device filled, shared out by the kinds' heads; and the
+// items per warp. False where those are too many to count.
+bool bwd_grid(long long tokens, int h_q, int h_kv, int d, int* ctas, int* items) {
+  const int side = 512 / d;  // tokens of an item
   const int heads[2] = {h_q, h_kv};
-  *hp = heads_per_unit(tiles, heads, 2);
   const long long most = (long long)kBwdCtasPerSM * kSMs;
   for (int z = 0; z < 2; ++z) {
-    units[z] = (heads[z] + *hp - 1) / *hp;
+    const long long total = (tokens + side - 1) / side * heads[z];
     const long long share = (most * heads[z] + h_q + h_kv - 1) / ((long long)h_q + h_kv);
-    ctas[z] = (int)(tiles * units[z] < share ? tiles * units[z] : share);
+    const long long need = (total + kWarps - 1) / kWarps;
+    ctas[z] = (int)(need < share ? need : share);
+    const long long per = (total + (long long)ctas[z] * kWarps - 1) / ((long long)ctas[z] * kWarps);
+    if (per > 0x7fffff00LL) return false;
+    items[z] = (int)per;
   }
+  return true;
 }
 
 }  // namespace
@@ -535,8 +593,8 @@ int launch_attn_paged_append(const AppendArgs& a) {
 }
 
 size_t norm_rope_bwd_workspace_bytes(int B, int n, int h_q, int h_kv, int d) {
-  int hp, units[2], ctas[2];
-  bwd_grid((long long)B * n, h_q, h_kv, d, &hp, units, ctas);
+  int ctas[2], items[2];
+  bwd_grid((long long)B * n, h_q, h_kv, d, ctas, items);
   return (size_t)(ctas[0] + ctas[1]) * d * sizeof(float);
 }
 
@@ -552,7 +610,7 @@ int launch_attn_norm_rope_bwd(const RopeBwdArgs& a, void* workspace) {
   p.cos_sin = a.cos_sin, p.n_pos = a.n_pos, p.d_rot = a.d_rot, p.positions = a.positions;
   p.n = a.n, p.tokens = a.B * a.n;
   p.heads[0] = a.h_q, p.heads[1] = a.h_kv;
-  bwd_grid(p.tokens, a.h_q, a.h_kv, a.d, &p.heads_per_unit, p.units, p.ctas);
+  if (!bwd_grid(p.tokens, a.h_q, a.h_kv, a.d, p.ctas, p.items)) return ATTN_ERR_INVALID;
   p.partials = static_cast<float*>(workspace);
   p.dw[0] = a.dq_weight, p.dw[1] = a.dk_weight;
   const bool norm = a.q_weight != nullptr;
