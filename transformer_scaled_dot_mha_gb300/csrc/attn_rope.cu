@@ -38,8 +38,11 @@ constexpr int kSMs = 152;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 4;          // rows in flight per lane group, forward and append
-constexpr int kBwdCtasPerSM = 4;  // gradients: 128 registers a thread
-constexpr int kBwdBytes = 12288;  // of copies in flight per warp
+// Gradients: resident CTAs, and bytes of copies in flight per warp. More of either leaves less
+// L1 for the angles (16384 tokens x 40 heads of 128: 84.8 us; 12 KB per warp 96, 4 CTAs and
+// 12 KB 92.6, 4 KB 88.2).
+constexpr int kBwdCtasPerSM = 3;
+constexpr int kBwdBytes = 6144;
 
 enum Kind { kQuery = 0, kKey = 1, kValue = 2 };
 
@@ -481,8 +484,15 @@ __global__ void __launch_bounds__(1024) attn_rope_dw_kernel(const RopeBwdParams 
   const int kind = blockIdx.y, col = blockIdx.x * 32 + threadIdx.x;
   const int first = kind ? p.ctas[0] : 0, count = p.ctas[kind];
   float sum = 0.0f;
-#pragma unroll 8
-  for (int s = threadIdx.y; s < count; s += 32) sum += p.partials[(long long)(first + s) * D + col];
+  constexpr int kEach = (kBwdCtasPerSM * kSMs + 31) / 32 + 1;  // shares per thread at most: all loads at once
+  float x[kEach];
+#pragma unroll
+  for (int s = 0; s < kEach; ++s) {
+    const int at = threadIdx.y + 32 * s;
+    x[s] = at < count ? p.partials[(long long)(first + at) * D + col] : 0.0f;
+  }
+#pragma unroll
+  for (int s = 0; s < kEach; ++s) sum += x[s];
   __shared__ float part[32][33];
   part[threadIdx.y][threadIdx.x] = sum;
   __syncthreads();
