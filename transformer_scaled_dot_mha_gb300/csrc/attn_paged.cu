@@ -482,7 +482,8 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
       constexpr int LINES = D / 64;
       const int r = ahead.mt * C::ROWS + lane / LINES;
       if (lane < C::ROWS * LINES && r < p.rows)
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.q + out_row(p, ahead.b, ahead.head, r) * D + 64 * (lane % LINES)));
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.q + out_row(p, ahead.b, ahead.head, r) * D +
+                                                      64 * (lane % LINES)));
     }
     const int row = cache_row(p, ahead, lane);
     ahead.step(p);
