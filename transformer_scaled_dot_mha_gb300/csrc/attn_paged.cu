@@ -38,8 +38,8 @@
 // streams its part from one pair into the next without a pause in its copies. A pair that
 // lies within one warp's part is finished there; of one that does not, every part leaves
 // (m, l, O) in the workspace, the warp that has its first tile leaves a note of the parts,
-// and attn_paged_merge_kernel joins them. When no sequence can be
-// longer than a few tiles, each pair gets a warp of its own and there is no second launch.
+// and attn_paged_merge_kernel joins them. When no sequence can be longer than a few tiles,
+// each pair gets a warp of its own and there is no second launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -54,8 +54,8 @@ namespace {
 
 constexpr int kSMs = 152;
 constexpr int kMaxParts = 12 * kSMs;  // parts of the list of tiles at most, one per resident warp
-constexpr int kMinTiles = 2;               // tiles per part, at least
-constexpr int kWholeTiles = 8;             // up to here a pair is not worth splitting
+constexpr int kMinTiles = 2;          // tiles per part, at least
+constexpr int kWholeTiles = 4;        // up to here a pair is not worth splitting
 constexpr int kMergeThreads = 256;
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -224,14 +224,14 @@ template <int KT, int PARTS>
 __device__ __forceinline__ bool find_part(const PagedParams& p, int c, int& b, long long& before, long long& begin,
                                           long long& part, long long& total) {
   const long long pairs = (long long)p.h_kv * p.m_tiles;
-  uint32_t n, sum;
+  uint32_t n, sum = scan_tiles<KT>(p, 0, n);  // the first 32 sequences, where the search begins
   total = 0;
-#pragma unroll 1
-  for (int b0 = (p.B - 1) & ~31; b0 >= 0; b0 -= 32) {  // ends at the first 32, where the search begins
-    sum = scan_tiles<KT>(p, b0, n);
-    total += __shfl_sync(kAll, sum, 31);
-  }
-  total *= pairs;
+#pragma unroll 4
+  for (int b = 32 + threadIdx.x; b < p.B; b += 32) total += tiles_of<KT>(p, b);
+  if (p.B > 32)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+  total = (total + __shfl_sync(kAll, sum, 31)) * pairs;
   part = max((long long)kMinTiles, divide(total + PARTS - 1, PARTS));
   begin = c * part;
   if (begin >= total) return false;
@@ -274,16 +274,25 @@ struct Cursor {
 };
 
 // ---------------------------------------------------------------- one warp's part
-// Cache row of the key that `lane` has of the cursor's tile, -1 where there is none.
+// Looking up the cache row of the key that `lane` has of the cursor's tile, in two steps: the
+// page's number travels while something else is done. page < 0: there is no such key.
+struct Lookup {
+  int page, rest;  // rest: of the row's number, behind the page's first
+};
+
 template <int KT>
-__device__ __forceinline__ int cache_row(const PagedParams& p, const Cursor<KT>& c, int lane) {
+__device__ __forceinline__ Lookup start_lookup(const PagedParams& p, const Cursor<KT>& c, int lane) {
   const int x = c.tile * KT + lane;
-  if (lane >= KT || x >= c.vis.count) return -1;
+  if (lane >= KT || x >= c.vis.count) return Lookup{-1, 0};
   const int j = c.vis.key(x);
   const int slot = (int)(__umulhi(2u * j, p.page_inv) >> p.page_shift);
-  const int page = __ldg(p.page_table + (long long)c.b * p.max_pages + slot);
-  if (page < 0 || page >= p.n_pages) return -1;  // names no page: its keys count as illegal
-  return (page * p.h_kv + c.head) * p.page_size + (j - slot * p.page_size);
+  return Lookup{__ldg(p.page_table + (long long)c.b * p.max_pages + slot),
+                (c.head - slot) * p.page_size + j};  // head rows of whole pages, then the key's place
+}
+
+__device__ __forceinline__ int finish_lookup(const PagedParams& p, const Lookup& l) {
+  if (l.page < 0 || l.page >= p.n_pages) return -1;  // names no page: its keys count as illegal
+  return l.page * p.h_kv * p.page_size + l.rest;
 }
 
 // The token that row `row` of a pair belongs to.
@@ -473,11 +482,11 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
                           (C::PIECES == 4 ? 16 * ((g >> 1) ^ (2 * t & 2)) + 8 * (g & 1) : 16 * (g ^ 2 * t));
   uint32_t there[C::STAGES];  // which keys of the tiles in flight exist; [0]: of the current one
   Cursor<C::KT> ahead = cur;  // the next tile to look up
-  // rows of the next tiles to request: looked up that far ahead, the first ones all at once
-  int rows_ahead[C::STAGES + 1];
+  int rows_ahead[C::STAGES];  // rows of the next tiles to request
+  Lookup pending;             // and of the one behind them
   int looked = 0;
   auto look_up = [&]() {
-    if (looked >= count) return -1;
+    if (looked >= count) return Lookup{-1, 0};
     if (ahead.tile == 0 || looked == 0) {  // a new pair: its queries into L1, a line per lane
       constexpr int LINES = D / 64;
       const int r = ahead.mt * C::ROWS + lane / LINES;
@@ -485,13 +494,19 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
         asm volatile("prefetch.global.L1 [%0];" ::"l"(p.q + out_row(p, ahead.b, ahead.head, r) * D +
                                                       64 * (lane % LINES)));
     }
-    const int row = cache_row(p, ahead, lane);
+    const Lookup l = start_lookup(p, ahead, lane);
     ahead.step(p);
     ++looked;
-    return row;
+    return l;
   };
+  {
+    Lookup first[C::STAGES];
 #pragma unroll
-  for (int x = 0; x <= C::STAGES; ++x) rows_ahead[x] = look_up();
+    for (int x = 0; x < C::STAGES; ++x) first[x] = look_up();
+    pending = look_up();
+#pragma unroll
+    for (int x = 0; x < C::STAGES; ++x) rows_ahead[x] = finish_lookup(p, first[x]);
+  }
   Rows<D, NT, FP8> rows;
   bool fresh = true;          // cur's pair has not begun
   int first_tile = cur.tile;  // of this part, of cur's pair
@@ -725,8 +740,9 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
     copy_commit();
     stage = stage + 1 < C::STAGES ? stage + 1 : 0;
 #pragma unroll
-    for (int x = 0; x < C::STAGES; ++x) rows_ahead[x] = rows_ahead[x + 1];
-    rows_ahead[C::STAGES] = look_up();
+    for (int x = 0; x + 1 < C::STAGES; ++x) rows_ahead[x] = rows_ahead[x + 1];
+    rows_ahead[C::STAGES - 1] = finish_lookup(p, pending);
+    pending = look_up();
   }
 }
 
@@ -897,12 +913,13 @@ int launch(const PagedArgs& a, float* ws) {
   p.ws_o = ws, p.ws_ml = ws + (size_t)2 * C::PARTS * C::ROWS * D;
   p.notes = reinterpret_cast<Note*>(p.ws_ml + (size_t)2 * C::PARTS * C::ROWS * 2);
   // tiles that any pair may have: a pair is not worth splitting where that is few, nor where
-  // it is no long stretch and there are pairs enough to fill the device twice
+  // it is no long stretch and there are pairs enough to keep half the warps busy (200 x 8
+  // heads of d 128, 10-300 keys: 28.5 us, 41.2 split and joined)
   long long most = p.max_len;
   if (p.window >= 0 && (long long)p.window + a.n_q + p.sinks < most) most = (long long)p.window + a.n_q + p.sinks;
   const long long pairs = (long long)a.B * a.h_kv * p.m_tiles, tiles = (most + C::KT - 1) / C::KT;
   if (pairs > 0x7fffffffLL) return ATTN_ERR_INVALID;
-  p.whole = tiles <= kWholeTiles || (tiles <= 4 * kWholeTiles && pairs >= 2 * C::PARTS);
+  p.whole = tiles <= kWholeTiles || (tiles <= 8 * kWholeTiles && 2 * pairs >= C::PARTS);
   static_assert(C::SMEM_BYTES <= 48 * 1024, "fits without raising the kernel's limit");
   p.notes_by_pair = pairs <= C::PARTS;
   const int st = launch_pdl(attn_paged_kernel<D, NT, FP8>, dim3(p.whole ? (unsigned)pairs : C::PARTS), 32,
