@@ -162,14 +162,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   return r;
 }
 
-// a / b; most lists of tiles are numbered in 32 bits, where the division is far shorter. Not
-// inlined, as little here is that runs once: a warp runs through most of this code a few
-// times only, and what it costs then is the fetch of the instructions.
-__device__ __noinline__ long long divide(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
-}
-
 // Whether a word of V holds an infinity or NaN (e4m3: NaN is the only special value).
 template <bool FP8>
 __device__ __forceinline__ bool special(uint32_t y) {
@@ -204,41 +196,42 @@ __device__ __forceinline__ int tiles_of(const PagedParams& p, int b) {
 
 // The list of tiles. Sequence b holds its pairs (head, row tile) one after the other, each
 // of tiles_of(b) tiles; part c of the list is [c * part, (c + 1) * part), up to total.
-// Tiles of one pair of the sequences b0 .. b0 + lane; n: of sequence b0 + lane alone.
+// All of it counts in 32 bits: the launch refuses a list that could be longer.
 template <int KT>
-__device__ __forceinline__ uint32_t scan_tiles(const PagedParams& p, int b0, uint32_t& n) {
-  const int lane = threadIdx.x;
-  n = b0 + lane < p.B ? tiles_of<KT>(p, b0 + lane) : 0;  // at most 2^26
-  uint32_t sum = n;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t y = __shfl_up_sync(kAll, sum, o);
-    if (lane >= o) sum += y;
-  }
-  return sum;
+__device__ __forceinline__ int lane_tiles(const PagedParams& p, int b) {
+  return b < p.B ? tiles_of<KT>(p, b) : 0;
 }
 
-// Where part c begins: its sequence, the tiles of one pair of the sequences before that, and
-// the tiles of a part. False if the list ends before it.
-template <int KT, int PARTS>
-__device__ __forceinline__ bool find_part(const PagedParams& p, int c, int& b, long long& before, long long& begin,
-                                          long long& part, long long& total) {
-  const long long pairs = (long long)p.h_kv * p.m_tiles;
-  uint32_t n, sum = scan_tiles<KT>(p, 0, n);  // the first 32 sequences, where the search begins
-  total = 0;
-#pragma unroll 4
-  for (int b = 32 + threadIdx.x; b < p.B; b += 32) total += tiles_of<KT>(p, b);
-  if (p.B > 32)
+// Sum of n over the lanes up to this one.
+__device__ __forceinline__ int scan(int n) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-  total = (total + __shfl_sync(kAll, sum, 31)) * pairs;
-  part = max((long long)kMinTiles, divide(total + PARTS - 1, PARTS));
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kAll, n, o);
+    if (threadIdx.x >= o) n += y;
+  }
+  return n;
+}
+
+// Where part c begins: tile `begin` of the list, in sequence b; `before`: tiles of one pair of
+// the sequences before that. False if the list ends before it.
+template <int KT, int PARTS>
+__device__ __forceinline__ bool find_part(const PagedParams& p, int c, int& b, int& before, int& begin, int& part,
+                                          int& total) {
+  const int pairs = p.h_kv * p.m_tiles, lane = threadIdx.x;
+  int n = lane_tiles<KT>(p, lane);  // the first 32 sequences, where the search begins
+  int more = 0;
+#pragma unroll 4
+  for (int x = 32 + lane; x < p.B; x += 32) more += tiles_of<KT>(p, x);
+  int sum = scan(n);
+  total = __shfl_sync(kAll, sum, 31);
+  if (p.B > 32) total += __reduce_add_sync(kAll, more);
+  total *= pairs;
+  part = max(kMinTiles, (int)((uint32_t)(total + PARTS - 1) / PARTS));
   begin = c * part;
   if (begin >= total) return false;
   before = 0;
 #pragma unroll 1
-  for (int b0 = 0;; b0 += 32) {
-    if (b0 > 0) sum = scan_tiles<KT>(p, b0, n);
+  for (int b0 = 0;;) {
     const uint32_t past = __ballot_sync(kAll, (before + sum) * pairs > begin);
     if (past) {
       const int at = __ffs(past) - 1;
@@ -247,6 +240,9 @@ __device__ __forceinline__ bool find_part(const PagedParams& p, int c, int& b, l
       return true;
     }
     before += __shfl_sync(kAll, sum, 31);
+    b0 += 32;
+    n = lane_tiles<KT>(p, b0 + lane);
+    sum = scan(n);
   }
 }
 
@@ -450,7 +446,7 @@ struct Rows {
 // `slot` (the first one) or slot + 1 (the last); part: tiles of a part of the list.
 template <int D, int NT, bool FP8>
 __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Cursor<Cfg<D, NT, FP8>::KT> cur,
-                                       int count, int slot, long long part) {
+                                       int count, int slot, int part) {
   using C = Cfg<D, NT, FP8>;
   const int lane = threadIdx.x;
   const int g = lane >> 2, t = lane & 3;
@@ -723,7 +719,7 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
         if (!p.whole && first_tile == 0 && lane == 0 && (p.notes_by_pair || !complete)) {
           const int c = slot / 2, left = cur.n - 1 - cur.tile, pair = (cur.b * p.h_kv + cur.head) * p.m_tiles + cur.mt;
           p.notes[p.notes_by_pair ? pair : c] =
-              Note{pair, slot + later, c, complete ? -1 : c + (int)divide(left + part - 1, part)};
+              Note{pair, slot + later, c, complete ? -1 : c + (left + part - 1) / part};
         }
         fresh = true;
         first_tile = 0;
@@ -755,7 +751,7 @@ __global__ void __launch_bounds__(32, Cfg<D, NT, FP8>::CTAS_PER_SM) attn_paged_k
   const int pairs = p.h_kv * p.m_tiles, c = blockIdx.x;
   if (!p.whole && !p.notes_by_pair && threadIdx.x == 0) p.notes[c] = Note{0, 0, 0, -1};
   Cursor<C::KT> cur;
-  long long pair = 0, part = 0;  // pair: of the sequence
+  int pair = 0, part = 0;  // pair: of the sequence
   int count = 0;
   cur.tile = 0;
   if (p.whole) {
@@ -764,17 +760,17 @@ __global__ void __launch_bounds__(32, Cfg<D, NT, FP8>::CTAS_PER_SM) attn_paged_k
     pair = c - cur.b * pairs;
     count = cur.n;
   } else {
-    long long before, begin, total;
+    int before, begin, total;
     if (find_part<C::KT, C::PARTS>(p, c, cur.b, before, begin, part, total)) {
       cur.sequence(p);
-      const long long in = begin - before * pairs;
-      pair = divide(in, cur.n);
-      cur.tile = (int)(in - pair * cur.n);
-      count = (int)min(part, total - begin);
+      const int in = begin - before * pairs;
+      pair = (uint32_t)in / (uint32_t)cur.n;
+      cur.tile = in - pair * cur.n;
+      count = min(part, total - begin);
     }
   }
   if (count > 0) {
-    cur.head = (int)pair / p.m_tiles, cur.mt = (int)pair - cur.head * p.m_tiles;
+    cur.head = p.m_tiles == 1 ? pair : pair / p.m_tiles, cur.mt = pair - cur.head * p.m_tiles;
     stream<D, NT, FP8>(p, smem, cur, count, 2 * c, part);
   }
   empty_rows<D>(p);
@@ -918,7 +914,7 @@ int launch(const PagedArgs& a, float* ws) {
   long long most = p.max_len;
   if (p.window >= 0 && (long long)p.window + a.n_q + p.sinks < most) most = (long long)p.window + a.n_q + p.sinks;
   const long long pairs = (long long)a.B * a.h_kv * p.m_tiles, tiles = (most + C::KT - 1) / C::KT;
-  if (pairs > 0x7fffffffLL) return ATTN_ERR_INVALID;
+  if (pairs > 0x7ffff000LL / tiles) return ATTN_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
   p.whole = tiles <= kWholeTiles || (tiles <= 8 * kWholeTiles && 2 * pairs >= C::PARTS);
   static_assert(C::SMEM_BYTES <= 48 * 1024, "fits without raising the kernel's limit");
   p.notes_by_pair = pairs <= C::PARTS;
