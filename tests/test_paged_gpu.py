@@ -117,6 +117,39 @@ def test_many_sequences():
     check(*run(q, kp, vp, table, ln, sc), *ref.paged_decode(q, kp, vp, table, ln, 0.125))
 
 
+@pytest.mark.parametrize("B,n_q,h_q,h_kv,d,window", [
+    (400, 1, 8, 8, 64, -1),    # more pairs than parts of the list
+    (130, 1, 32, 8, 128, -1),  # four rows a pair
+    (260, 4, 16, 4, 64, 70),   # two row tiles' worth of rows, short windows
+])
+def test_large_batches_of_short_sequences(B, n_q, h_q, h_kv, d, window):
+    """A capacity far above the lengths: the device cuts up the list, whatever its shape."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 60, (B,), generator=g).tolist()
+    lens[3], lens[B // 2] = 333, 0
+    q, kp, vp, table, ln, sc = make(B, lens, n_q, h_q, h_kv, d, 16, max_pages=100)
+    check(*run(q, kp, vp, table, ln, sc, None, window),
+          *ref.paged_decode(q, kp, vp, table, ln, 1 / math.sqrt(d), window))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own workspace, do not touch each other."""
+    cases = [make(61 + i, [700 + 90 * i, 1200, 3], 1, 8, 2, 64, 16) for i in range(2)]
+    want = [run(*c) for c in cases]
+    dev = [[x.cuda() if torch.is_tensor(x) else x for x in c] for c in cases]
+    outs = [[torch.empty_like(c[0]) for _ in range(20)] for c in dev]
+    size = attn.attn_paged_decode_workspace_size(3, 1, 8, 2, 64)
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for (q, kp, vp, table, ln, _), out, w, st in zip(dev, outs, ws, streams):
+            attn.attn_paged_decode(q, kp, vp, out[i], table, ln, w, stream=st)
+    torch.cuda.synchronize()
+    for (out, _), got in zip(want, outs):
+        assert all(torch.equal(out, x.cpu()) for x in got)
+
+
 def test_lengths_are_clamped_and_scale_used_as_given():
     q, kp, vp, table, _, sc = make(23, [64, 64, 64], 1, 2, 2, 64, 16)
     ln = torch.tensor([-5, 64, 1 << 30], dtype=torch.int32)

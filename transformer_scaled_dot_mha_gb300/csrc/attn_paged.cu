@@ -179,7 +179,7 @@ struct Visible {
 
 __device__ __forceinline__ Visible visible_of(const PagedParams& p, int b) {
   Visible v;
-  v.len = min(max(__ldg(p.cache_lens + b), 0), p.max_len);
+  v.len = min(max(p.cache_lens[b], 0), p.max_len);
   // the first token that stands in the sequence sees furthest back
   const int pos0 = max(v.len - p.n_q, 0);
   const int low = p.window < 0 ? 0 : max(pos0 - p.window, 0);
@@ -282,7 +282,7 @@ __device__ __forceinline__ Lookup start_lookup(const PagedParams& p, const Curso
   if (lane >= KT || x >= c.vis.count) return Lookup{-1, 0};
   const int j = c.vis.key(x);
   const int slot = (int)(__umulhi(2u * j, p.page_inv) >> p.page_shift);
-  return Lookup{__ldg(p.page_table + (long long)c.b * p.max_pages + slot),
+  return Lookup{p.page_table[(long long)c.b * p.max_pages + slot],
                 (c.head - slot) * p.page_size + j};  // head rows of whole pages, then the key's place
 }
 
@@ -343,7 +343,7 @@ struct Rows {
       if (!FP8) {
 #pragma unroll
         for (int x = 0; x < C::KC; ++x) {
-          const uint4 w = real ? __ldg(reinterpret_cast<const uint4*>(src + 8 * (t + 4 * x))) : make_uint4(0, 0, 0, 0);
+          const uint4 w = real ? *reinterpret_cast<const uint4*>(src + 8 * (t + 4 * x)) : make_uint4(0, 0, 0, 0);
           q[nt][2 * x][0] = w.x, q[nt][2 * x][1] = w.y;
           q[nt][2 * x + 1][0] = w.z, q[nt][2 * x + 1][1] = w.w;
         }
@@ -355,7 +355,7 @@ struct Rows {
         float top = 0.0f;
 #pragma unroll
         for (int x = 0; x < C::S; ++x) {
-          const uint2 w = real ? __ldg(reinterpret_cast<const uint2*>(src + 16 * (t + 4 * (x / 4)) + 4 * (x % 4)))
+          const uint2 w = real ? *reinterpret_cast<const uint2*>(src + 16 * (t + 4 * (x / 4)) + 4 * (x % 4))
                                : make_uint2(0, 0);
           q[nt][x][0] = w.x, q[nt][x][1] = w.y;
 #pragma unroll
@@ -374,7 +374,7 @@ struct Rows {
           for (int e = 0; e < 2; ++e)
             q[nt][x][e] = pack_f16x2(__uint_as_float(q[nt][x][e] << 16) * down,
                                      __uint_as_float(q[nt][x][e] & 0xffff0000u) * down);
-        const float mine = p.scale_log2 * __ldg(p.k_scale + head) * up;
+        const float mine = p.scale_log2 * p.k_scale[head] * up;
         factor[nt][0] = __shfl_sync(kAll, mine, 8 * t);
         factor[nt][1] = __shfl_sync(kAll, mine, 8 * t + 4);
       }
@@ -403,7 +403,7 @@ struct Rows {
   __device__ __forceinline__ void end(const PagedParams& p, const Cursor<C::KT>& c, int lane, int slot) {
     const int g = lane >> 2, t = lane & 3;
     const int head = c.head, row0 = c.mt * C::ROWS;
-    const float v_scale = FP8 ? __ldg(p.v_scale + head) : 1.0f;
+    const float v_scale = FP8 ? p.v_scale[head] : 1.0f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll

@@ -75,7 +75,7 @@ __device__ __forceinline__ void chunks_of(int l, int d_rot, int& c0, int& c1, bo
 }
 
 __device__ __forceinline__ void load4(float* dst, const float* src) {
-  const float4 v = __ldg(reinterpret_cast<const float4*>(src));
+  const float4 v = *reinterpret_cast<const float4*>(src);
   dst[0] = v.x, dst[1] = v.y, dst[2] = v.z, dst[3] = v.w;
 }
 
@@ -143,10 +143,12 @@ __device__ __forceinline__ uint2 narrow_e4m3(const float* x, float scale) {
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
-// Inputs are read once: past L1, so that they do not push out the angles.
+// Inputs are read once: past L1, so that they do not push out the angles. (No load here uses
+// the read-only path: a kernel starts before the one that writes its inputs has ended, and
+// such a load could be moved ahead of the wait for it.)
 __device__ __forceinline__ uint4 load_once(const uint16_t* p) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                : "l"(p));
   return r;
@@ -207,14 +209,14 @@ __global__ void __launch_bounds__(kThreads) attn_rope_kernel(const RopeParams p)
   const int b = PAGED ? 0 : t / p.n, i = PAGED ? t : t - b * p.n;
 
   // where the token stands; a position without a table row makes it a padding token
-  const int pos = p.positions ? __ldg(p.positions + t) : i;
+  const int pos = p.positions ? p.positions[t] : i;
   bool valid = there && pos >= 0 && (p.d_rot == 0 || pos < p.n_pos);
   long long page_row = 0;  // cache row of head 0
   if (PAGED) {
-    const int seq = p.seq_ids ? __ldg(p.seq_ids + t) : t;
+    const int seq = p.seq_ids ? p.seq_ids[t] : t;
     const int slot = max(pos, 0) / p.page_size;
     valid = valid && seq >= 0 && seq < p.n_seqs && slot < p.max_pages;
-    const int page = valid ? __ldg(p.page_table + (long long)seq * p.max_pages + slot) : -1;
+    const int page = valid ? p.page_table[(long long)seq * p.max_pages + slot] : -1;
     valid = valid && page >= 0 && page < p.n_pages;
     page_row = (long long)page * p.heads[kKey] * p.page_size + (pos - slot * p.page_size);
   }
@@ -229,8 +231,8 @@ __global__ void __launch_bounds__(kThreads) attn_rope_kernel(const RopeParams p)
     rot0 = rot1 = false;
   } else {
     if (normed) {
-      w0 = __ldg(reinterpret_cast<const uint4*>(p.weight[kind & 1] + 8 * c0));
-      w1 = __ldg(reinterpret_cast<const uint4*>(p.weight[kind & 1] + 8 * c1));
+      w0 = *reinterpret_cast<const uint4*>(p.weight[kind & 1] + 8 * c0);
+      w1 = *reinterpret_cast<const uint4*>(p.weight[kind & 1] + 8 * c1);
     }
     if (valid) load_angles<PAIRS>(a, p.cos_sin + (long long)pos * p.d_rot, p.d_rot, c0, c1, rot0, rot1);
   }
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kThreads) attn_rope_kernel(const RopeParams p)
         } else {
           const long long at = (page_row + (long long)(h + u) * p.page_size) * D;
           if (E4M3) {
-            const float scale = __ldg(p.scale[kind] + h + u);
+            const float scale = p.scale[kind][h + u];
             uint8_t* dst = static_cast<uint8_t*>(p.pages[kind]) + at;
             *reinterpret_cast<uint2*>(dst + 8 * c0) = narrow_e4m3(x, scale);
             *reinterpret_cast<uint2*>(dst + 8 * c1) = narrow_e4m3(x + 8, scale);
@@ -355,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSM) attn_rope_bwd_kernel(
   chunks_of<D, PAIRS>(l, p.d_rot, c0, c1, rot0, rot1);
   uint4 w0{}, w1{};
   if (NORM) {
-    w0 = __ldg(reinterpret_cast<const uint4*>(p.weight[kind] + 8 * c0));
-    w1 = __ldg(reinterpret_cast<const uint4*>(p.weight[kind] + 8 * c1));
+    w0 = *reinterpret_cast<const uint4*>(p.weight[kind] + 8 * c0);
+    w1 = *reinterpret_cast<const uint4*>(p.weight[kind] + 8 * c1);
   }
   float dw[16];
 #pragma unroll
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, kBwdCtasPerSM) attn_rope_bwd_kernel(
         const long long t_ = (long long)group * L::GROUPS + side;
         there = t_ < p.tokens;
         const int t = there ? (int)t_ : p.tokens - 1;
-        const int pos = p.positions ? __ldg(p.positions + t) : t % p.n;
+        const int pos = p.positions ? p.positions[t] : t % p.n;
         valid = there && pos >= 0 && (p.d_rot == 0 || pos < p.n_pos);
         if (valid) load_angles<PAIRS>(a, p.cos_sin + (long long)pos * p.d_rot, p.d_rot, c0, c1, rot0, rot1);
         dst = p.dx[kind] + t * p.dstride[kind];
