@@ -558,10 +558,13 @@ int launch_rope(RopeParams& p, int d, bool pairs, bool paged, bool e4m3, cudaStr
 bool bwd_grid(long long tokens, int h_q, int h_kv, int d, int* ctas, int* items) {
   const int side = 512 / d;  // tokens of an item
   const int heads[2] = {h_q, h_kv};
-  const long long most = (long long)kBwdCtasPerSM * kSMs;
+  const long long most = (long long)kBwdCtasPerSM * kSMs, all = (long long)h_q + h_kv;
+  long long shares[2];  // together no more CTAs than are resident
+  shares[0] = (most * h_q + all / 2) / all;
+  shares[0] = shares[0] < 1 ? 1 : shares[0] > most - 1 ? most - 1 : shares[0];
+  shares[1] = most - shares[0];
   for (int z = 0; z < 2; ++z) {
-    const long long total = (tokens + side - 1) / side * heads[z];
-    const long long share = (most * heads[z] + h_q + h_kv - 1) / ((long long)h_q + h_kv);
+    const long long total = (tokens + side - 1) / side * heads[z], share = shares[z];
     const long long need = (total + kWarps - 1) / kWarps;
     ctas[z] = (int)(need < share ? need : share);
     const long long per = (total + (long long)ctas[z] * kWarps - 1) / ((long long)ctas[z] * kWarps);
