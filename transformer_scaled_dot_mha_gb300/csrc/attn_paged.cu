@@ -802,14 +802,27 @@ __global__ void __launch_bounds__(kMergeThreads) attn_paged_merge_kernel(const P
   const int col = 4 * (lane % LANES), side = lane / LANES;
   float M = -INFINITY, L = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  // 32 parts of the slice at a time: lane x has the statistics of the x-th
+  // 32 parts of the slice at a time: lane x has the statistics of the x-th. The first columns
+  // are asked for together with them.
   if (r < rows)
 #pragma unroll 1
     for (int c0 = slice; c0 < parts; c0 += 32 * slices) {
       auto row_of = [&](int c) { return (c == 0 ? note.slot : 2 * (note.first + c)) * C::ROWS + r; };
-      const int mine = c0 + lane * slices;
+      const int mine = c0 + lane * slices, here = min(32, (parts - c0 + slices - 1) / slices);
       float2 ml = make_float2(-INFINITY, 0.0f);
       if (mine < parts) ml = *reinterpret_cast<const float2*>(p.ws_ml + (long long)row_of(mine) * 2);
+      constexpr int BATCH = 4;
+      float4 v[BATCH];
+      auto load = [&](int x) {
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+          const int y = x + u * SIDE + side;
+          v[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (y < here)
+            v[u] = *reinterpret_cast<const float4*>(p.ws_o + (long long)row_of(c0 + y * slices) * D + col);
+        }
+      };
+      load(0);
       float top = ml.x;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
@@ -821,16 +834,18 @@ __global__ void __launch_bounds__(kMergeThreads) attn_paged_merge_kernel(const P
       for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
       L = fmaf(L, old, l);
       acc.x *= old, acc.y *= old, acc.z *= old, acc.w *= old;
-      const int here = min(32, (parts - c0 + slices - 1) / slices);
-#pragma unroll 4
-      for (int x = 0; x < here; x += SIDE) {
-        const int y = x + side;
-        const float w = __shfl_sync(kAll, f, y & 31);
-        if (y < here) {
-          const float4 v = *reinterpret_cast<const float4*>(p.ws_o + (long long)row_of(c0 + y * slices) * D + col);
-          acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y);
-          acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
+#pragma unroll 1
+      for (int x = 0; x < here;) {
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+          const float w = __shfl_sync(kAll, f, (x + u * SIDE + side) & 31);
+          if (x + u * SIDE + side < here) {
+            acc.x = fmaf(w, v[u].x, acc.x), acc.y = fmaf(w, v[u].y, acc.y);
+            acc.z = fmaf(w, v[u].z, acc.z), acc.w = fmaf(w, v[u].w, acc.w);
+          }
         }
+        x += BATCH * SIDE;
+        if (x < here) load(x);
       }
     }
   if (SIDE == 2) {
