@@ -154,6 +154,10 @@ __device__ __forceinline__ uint4 load_once(const uint16_t* p) {
   return r;
 }
 
+// Outputs are written once and not read here: first to leave L2 (16384 tokens x 40 heads of
+// 128: 52.9 us, 55.0 with plain stores).
+__device__ __forceinline__ void store_once(uint16_t* p, uint4 v) { __stcs(reinterpret_cast<uint4*>(p), v); }
+
 template <int D>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
@@ -270,25 +274,25 @@ __global__ void __launch_bounds__(kThreads) attn_rope_kernel(const RopeParams p)
         if (there) {
           uint16_t* dst = p.out[kind & 1] + (((long long)b * p.heads[kind] + h + u) * p.n + i) * D;
           const uint4 zero = make_uint4(0, 0, 0, 0);  // a padding token
-          *reinterpret_cast<uint4*>(dst + 8 * c0) = valid ? narrow(x) : zero;
-          *reinterpret_cast<uint4*>(dst + 8 * c1) = valid ? narrow(x + 8) : zero;
+          store_once(dst + 8 * c0, valid ? narrow(x) : zero);
+          store_once(dst + 8 * c1, valid ? narrow(x + 8) : zero);
         }
       } else if (valid) {
         if (kind == kQuery) {
           uint16_t* dst = p.out[0] + ((long long)t * p.heads[0] + h + u) * D;
-          *reinterpret_cast<uint4*>(dst + 8 * c0) = narrow(x);
-          *reinterpret_cast<uint4*>(dst + 8 * c1) = narrow(x + 8);
+          store_once(dst + 8 * c0, narrow(x));
+          store_once(dst + 8 * c1, narrow(x + 8));
         } else {
           const long long at = (page_row + (long long)(h + u) * p.page_size) * D;
           if (E4M3) {
             const float scale = p.scale[kind][h + u];
             uint8_t* dst = static_cast<uint8_t*>(p.pages[kind]) + at;
-            *reinterpret_cast<uint2*>(dst + 8 * c0) = narrow_e4m3(x, scale);
-            *reinterpret_cast<uint2*>(dst + 8 * c1) = narrow_e4m3(x + 8, scale);
+            __stcs(reinterpret_cast<uint2*>(dst + 8 * c0), narrow_e4m3(x, scale));
+            __stcs(reinterpret_cast<uint2*>(dst + 8 * c1), narrow_e4m3(x + 8, scale));
           } else {
             uint16_t* dst = static_cast<uint16_t*>(p.pages[kind]) + at;
-            *reinterpret_cast<uint4*>(dst + 8 * c0) = narrow(x);
-            *reinterpret_cast<uint4*>(dst + 8 * c1) = narrow(x + 8);
+            store_once(dst + 8 * c0, narrow(x));
+            store_once(dst + 8 * c1, narrow(x + 8));
           }
         }
       }
