@@ -457,9 +457,13 @@ def attn_linear(x, w, y, bias=None, stream=None):
 def _device_of(t) -> int:
     """The device of a call's tensors: the current one, where its launches go."""
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
     return dev
+
+
+def _raw_stream(stream, dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
 
 
 def _need(t, name, dtype, shape, dev):
@@ -525,7 +529,7 @@ def attn_norm_rope(q, k, q_out, k_out, cos_sin, q_weight=None, k_weight=None, po
         float(eps), table, n_pos, d_rot,
         None if positions is None else _need(positions, "positions", torch.int32, (B, n), dev),
         _need(q_out, "q_out", bf16, (B, h_q, n, d), dev), _need(k_out, "k_out", bf16, (B, h_kv, n, d), dev),
-        B, n, h_q, h_kv, d, ROPE_INTERLEAVED if interleaved else 0, _stream_handle(stream))
+        B, n, h_q, h_kv, d, ROPE_INTERLEAVED if interleaved else 0, _raw_stream(stream, dev))
     if st != ATTN_OK:
         raise AttnError(st, "attn_norm_rope")
     return q_out, k_out
@@ -563,7 +567,7 @@ def attn_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, workspace, cos_sin, q_weigh
         dq_ptr, dk_ptr, dq_stride, dk_stride,
         None if dq_weight is None else _need(dq_weight, "dq_weight", f32, (d,), dev),
         None if dk_weight is None else _need(dk_weight, "dk_weight", f32, (d,), dev),
-        B, n, h_q, h_kv, d, ROPE_INTERLEAVED if interleaved else 0, ws_ptr, ws_bytes, _stream_handle(stream))
+        B, n, h_q, h_kv, d, ROPE_INTERLEAVED if interleaved else 0, ws_ptr, ws_bytes, _raw_stream(stream, dev))
     if st != ATTN_OK:
         raise AttnError(st, "attn_norm_rope_bwd")
     return dq, dk
@@ -624,7 +628,7 @@ def attn_paged_append(k, v, k_pages, v_pages, positions, page_table, seq_ids=Non
         float(eps), table, n_pos, d_rot, _need(positions, "positions", i32, (T,), dev),
         None if seq_ids is None else _need(seq_ids, "seq_ids", i32, (T,), dev),
         _need(page_table, "page_table", i32, (n_seqs, max_pages), dev), n_seqs, max_pages, q_to, kp, vp, n_pages,
-        page_size, ks, vs, T, h_q, h_kv, d, flags | (ROPE_INTERLEAVED if interleaved else 0), _stream_handle(stream))
+        page_size, ks, vs, T, h_q, h_kv, d, flags | (ROPE_INTERLEAVED if interleaved else 0), _raw_stream(stream, dev))
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_append")
     return q_out
@@ -654,7 +658,7 @@ def attn_paged_decode(q, k_pages, v_pages, out, page_table, cache_lens, workspac
         None if lse is None else _need(lse, "lse", torch.float32, (B, n_q, h_q), dev),
         _need(page_table, "page_table", i32, (B, max_pages), dev), _need(cache_lens, "cache_lens", i32, (B,), dev),
         B, n_q, h_q, h_kv, d, n_pages, page_size, max_pages, 1.0 / math.sqrt(d) if scale is None else float(scale),
-        int(window), int(sinks), ks, vs, flags, ws_ptr, ws_bytes, _stream_handle(stream))
+        int(window), int(sinks), ks, vs, flags, ws_ptr, ws_bytes, _raw_stream(stream, dev))
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_decode")
     return out
