@@ -497,7 +497,7 @@ size_t attn_paged_decode_workspace_size(int B, int n_q, int h_q, int h_kv, int d
  * Supported: 1 <= n_q <= 16, d in {64, 128}, h_q a multiple of h_kv (of at most 8192
  * h_kv), any page size (limits as in attn_paged_append), and with `keys` the most that a
  * sequence may see (max_pages * page_size, or window + n_q + sinks),
- * B * h_kv * ceil(n_q * h_q / h_kv / 8) * ceil(keys / 16) < 2^30.
+ * B * h_kv * ceil(n_q * h_q / h_kv / 8) * (ceil(keys / 16) + 2) < 2^30.
  * Numerics: the products accumulate in fp32 on the tensor cores,
  * softmax statistics in fp32; the weights are rounded to bf16 (8-bit cache: to f16) before
  * the second product, the output once to bf16. One or two launches on `stream`.

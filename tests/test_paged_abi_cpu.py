@@ -87,7 +87,8 @@ def test_paged_decode_invalid_arguments(L, bad):
 
 
 def test_paged_unsupported_shapes_and_workspace(L):
-    for bad in (dict(n_q=17), dict(d=96), dict(d=256)):
+    for bad in (dict(n_q=17), dict(d=96), dict(d=256), dict(h_q=2 * 8193),
+                dict(B=1 << 20, max_pages=1 << 26)):  # more tiles than 32 bits count
         assert L.attn_paged_decode(*dict(DECODE, **bad).values()) == attn.ATTN_ERR_UNSUPPORTED
     assert L.attn_paged_append(*dict(APPEND, d=96, q_stride=512, k_stride=512, v_stride=512).values()) == \
         attn.ATTN_ERR_UNSUPPORTED
@@ -97,4 +98,4 @@ def test_paged_unsupported_shapes_and_workspace(L):
     assert need > 0 and need == size(3000, 2, 4, 2, 64)
     assert L.attn_paged_decode(*dict(DECODE, nbytes=need - 1).values()) == attn.ATTN_ERR_INVALID
     assert size(0, 1, 1, 1, 64) == 0 and size(1, 17, 1, 1, 64) == 0 and size(1, 1, 3, 2, 64) == 0
-    assert size(1, 1, 1, 1, 96) == 0
+    assert size(1, 1, 1, 1, 96) == 0 and size(1, 1, 8193, 1, 64) == 0

@@ -55,6 +55,7 @@ namespace {
 constexpr int kSMs = 152;
 constexpr int kMaxParts = 12 * kSMs;  // parts of the list of tiles at most, one per resident warp
 constexpr int kMinTiles = 2;          // tiles per part, at least
+constexpr int kPairCost = 2;          // tiles that a pair's queries and results cost
 constexpr int kWholeTiles = 4;        // up to here a pair is not worth splitting
 constexpr int kMergeThreads = 256;
 constexpr uint32_t kAll = 0xffffffffu;
@@ -194,56 +195,89 @@ __device__ __forceinline__ int tiles_of(const PagedParams& p, int b) {
   return (visible_of(p, b).count + KT - 1) / KT;
 }
 
-// The list of tiles. Sequence b holds its pairs (head, row tile) one after the other, each
-// of tiles_of(b) tiles; part c of the list is [c * part, (c + 1) * part), up to total.
-// All of it counts in 32 bits: the launch refuses a list that could be longer.
+// The list of tiles. Sequence b holds its pairs (head, row tile) one after the other, each of
+// n = tiles_of(b) tiles. A pair costs kPairCost tiles more (its queries, its results): in the
+// count that parts are cut from it has kPairCost units, if it has tiles at all, and then one
+// per tile; part c is units [c * part, (c + 1) * part). (64 sequences of 3 to 8191 keys, windows
+// of 1024: 20.9 us, 27.0 without.) All of it counts in 32 bits: the launch refuses a list
+// that could be longer.
+struct Scan {
+  int b0;            // the first of the 32 sequences that the lanes stand for
+  int n, units;      // tiles of the lane's, units up to and with it
+  uint32_t some;     // which have tiles
+  int tiles, before;  // tiles and units of the sequences below b0 (of one pair each)
+};
+
 template <int KT>
 __device__ __forceinline__ int lane_tiles(const PagedParams& p, int b) {
   return b < p.B ? tiles_of<KT>(p, b) : 0;
 }
 
-// Sum of n over the lanes up to this one.
-__device__ __forceinline__ int scan(int n) {
+__device__ __forceinline__ void scan(Scan& s, int n) {
+  s.n = n;
+  s.some = __ballot_sync(kAll, n > 0);
+  s.units = n > 0 ? n + kPairCost : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kAll, n, o);
-    if (threadIdx.x >= o) n += y;
+    const int y = __shfl_up_sync(kAll, s.units, o);
+    if (threadIdx.x >= o) s.units += y;
   }
-  return n;
 }
 
-// Where part c begins: tile `begin` of the list, in sequence b; `before`: tiles of one pair of
-// the sequences before that. False if the list ends before it.
-template <int KT, int PARTS>
-__device__ __forceinline__ bool find_part(const PagedParams& p, int c, int& b, int& before, int& begin, int& part,
-                                          int& total) {
-  const int pairs = p.h_kv * p.m_tiles, lane = threadIdx.x;
-  int n = lane_tiles<KT>(p, lane);  // the first 32 sequences, where the search begins
-  int more = 0;
-#pragma unroll 4
-  for (int x = 32 + lane; x < p.B; x += 32) more += tiles_of<KT>(p, x);
-  int sum = scan(n);
-  total = __shfl_sync(kAll, sum, 31);
-  if (p.B > 32) total += __reduce_add_sync(kAll, more);
-  total *= pairs;
-  part = max(kMinTiles, (int)((uint32_t)(total + PARTS - 1) / PARTS));
-  begin = c * part;
-  if (begin >= total) return false;
-  before = 0;
-#pragma unroll 1
-  for (int b0 = 0;;) {
-    const uint32_t past = __ballot_sync(kAll, (before + sum) * pairs > begin);
+// The sequence, pair of it and tile at which unit x stands (the first tile, if x is among the
+// pair's own units), searching on from s; returns the list's tiles before that one.
+template <int KT>
+__device__ __forceinline__ int locate(const PagedParams& p, Scan& s, int pairs, int x, int& b, int& pair, int& tile) {
+  for (;;) {
+    const uint32_t past = __ballot_sync(kAll, (s.before + s.units) * pairs > x);
+    const int last = past ? __ffs(past) - 1 : 32;  // the sequence that holds x
+    const int skipped = __popc(s.some & (uint32_t)((1ull << last) - 1));
+    const int at = __shfl_sync(kAll, s.units, (last - 1) & 31), units = last > 0 ? at : 0;
     if (past) {
-      const int at = __ffs(past) - 1;
-      before += __shfl_sync(kAll, sum - n, at);
-      b = b0 + at;
-      return true;
+      const int n = __shfl_sync(kAll, s.n, last);
+      const int in = x - (s.before + units) * pairs;
+      b = s.b0 + last;
+      pair = (uint32_t)in / (uint32_t)(n + kPairCost);
+      tile = max(in - pair * (n + kPairCost) - kPairCost, 0);
+      return (s.tiles + units - kPairCost * skipped) * pairs + pair * n + tile;
     }
-    before += __shfl_sync(kAll, sum, 31);
-    b0 += 32;
-    n = lane_tiles<KT>(p, b0 + lane);
-    sum = scan(n);
+    s.before += units;
+    s.tiles += units - kPairCost * skipped;
+    s.b0 += 32;
+    scan(s, lane_tiles<KT>(p, s.b0 + threadIdx.x));
   }
+}
+
+// Part c: its first sequence, pair and tile, and how many tiles (0: the list ends before it, or
+// it has a pair's units only).
+template <int KT, int PARTS>
+__device__ __forceinline__ int find_part(const PagedParams& p, int c, int& part, int& b, int& pair, int& tile) {
+  const int pairs = p.h_kv * p.m_tiles, lane = threadIdx.x;
+  const int n0 = lane_tiles<KT>(p, lane);  // the first 32 sequences, where the search begins
+  int more = 0, more_some = 0;
+#pragma unroll 4
+  for (int x = 32 + lane; x < p.B; x += 32) {
+    const int n = tiles_of<KT>(p, x);
+    more += n;
+    more_some += n > 0;
+  }
+  Scan s;
+  s.b0 = s.tiles = s.before = 0;
+  scan(s, n0);
+  int units = __shfl_sync(kAll, s.units, 31), tiles = units - kPairCost * __popc(s.some);
+  if (p.B > 32) {
+    more = __reduce_add_sync(kAll, more);
+    tiles += more;
+    units += more + kPairCost * __reduce_add_sync(kAll, more_some);
+  }
+  units *= pairs;
+  part = max(kMinTiles, (int)((uint32_t)(units + PARTS - 1) / PARTS));
+  const int begin = c * part, end = begin + part;
+  if (begin >= units) return 0;
+  const int first = locate<KT>(p, s, pairs, begin, b, pair, tile);
+  int b2, pair2, tile2;
+  const int last = end < units ? locate<KT>(p, s, pairs, end, b2, pair2, tile2) : tiles * pairs;
+  return last - first;
 }
 
 // A place in the list.
@@ -270,6 +304,7 @@ struct Cursor {
 };
 
 // ---------------------------------------------------------------- one warp's part
+
 // Looking up the cache row of the key that `lane` has of the cursor's tile, in two steps: the
 // page's number travels while something else is done. page < 0: there is no such key.
 struct Lookup {
@@ -612,8 +647,9 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
             for (int e = 0; e < 4; ++e) rows.o[nt][s][e] *= alpha[e & 1];
         }
         // P^T as the second product's operand, rounded to the cache's compute type (bf16, or
-        // f16 for 8-bit pages): relative 2^-9 (2^-12) per weight, of either sign, below the
-        // output's own rounding; the sum l keeps the unrounded weights
+        // f16 for 8-bit pages): at most 2^-8 (2^-11) of a weight, of either sign (1.9e-3
+        // relative in norm against 64 bits at 17 to 8192 keys, where rounding the output alone gives
+        // 1.7e-3); the sum l keeps the unrounded weights
 #pragma unroll
         for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
@@ -760,14 +796,8 @@ __global__ void __launch_bounds__(32, Cfg<D, NT, FP8>::CTAS_PER_SM) attn_paged_k
     pair = c - cur.b * pairs;
     count = cur.n;
   } else {
-    int before, begin, total;
-    if (find_part<C::KT, C::PARTS>(p, c, cur.b, before, begin, part, total)) {
-      cur.sequence(p);
-      const int in = begin - before * pairs;
-      pair = (uint32_t)in / (uint32_t)cur.n;
-      cur.tile = in - pair * cur.n;
-      count = min(part, total - begin);
-    }
+    count = find_part<C::KT, C::PARTS>(p, c, part, cur.b, pair, cur.tile);
+    if (count > 0) cur.sequence(p);
   }
   if (count > 0) {
     cur.head = p.m_tiles == 1 ? pair : pair / p.m_tiles, cur.mt = pair - cur.head * p.m_tiles;
@@ -923,14 +953,17 @@ int launch(const PagedArgs& a, float* ws) {
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634074);
   p.ws_o = ws, p.ws_ml = ws + (size_t)2 * C::PARTS * C::ROWS * D;
   p.notes = reinterpret_cast<Note*>(p.ws_ml + (size_t)2 * C::PARTS * C::ROWS * 2);
-  // tiles that any pair may have: a pair is not worth splitting where that is few, nor where
-  // it is no long stretch and there are pairs enough to keep half the warps busy (200 x 8
-  // heads of d 128, 10-300 keys: 28.5 us, 41.2 split and joined)
+  // Tiles that any pair may have decide whether pairs are split. They are not where that is
+  // few; nor up to 24 tiles with pairs for half the warps (200 x 8 heads of d 128, 10-300 keys:
+  // 27.0 us, 33.4 split; but 256 x 8 heads of 64 with 1000 keys, 32 tiles: 99.9 and 92.3), nor,
+  // from 1.5 pairs per warp on, up to 22 times as many tiles as pairs per warp: the longest
+  // pair is then no long tail (1000 x 8 heads, 500-2000 keys: 373.8 us, 398.4 split).
   long long most = p.max_len;
   if (p.window >= 0 && (long long)p.window + a.n_q + p.sinks < most) most = (long long)p.window + a.n_q + p.sinks;
   const long long pairs = (long long)a.B * a.h_kv * p.m_tiles, tiles = (most + C::KT - 1) / C::KT;
-  if (pairs > 0x7ffff000LL / tiles) return ATTN_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
-  p.whole = tiles <= kWholeTiles || (tiles <= 8 * kWholeTiles && 2 * pairs >= C::PARTS);
+  if (pairs > 0x7ffff000LL / (tiles + kPairCost)) return ATTN_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
+  p.whole = tiles <= kWholeTiles || (tiles <= 6 * kWholeTiles && 2 * pairs >= C::PARTS) ||
+            (2 * pairs >= 3 * C::PARTS && tiles * C::PARTS <= 22 * pairs);
   static_assert(C::SMEM_BYTES <= 48 * 1024, "fits without raising the kernel's limit");
   p.notes_by_pair = pairs <= C::PARTS;
   const int st = launch_pdl(attn_paged_kernel<D, NT, FP8>, dim3(p.whole ? (unsigned)pairs : C::PARTS), 32,
