@@ -94,6 +94,8 @@ CASES = [  # lens, n_q, h_q, h_kv, d, page, window, sinks, e4m3, max_pages
     ([1900, 300], 7, 2, 2, 128, 64, 1200, 37, True, 0),              # window over several tiles, split
     ([64, 200], 2, 64, 1, 64, 16, -1, 0, False, 0),                  # one key head for 64
     ([300, 70], 1, 4, 4, 64, 16, 50, 1000, False, 0),                # more sinks than keys
+    ([60001], 1, 2, 1, 64, 64, -1, 0, False, 0),                     # hundreds of parts of one pair
+    ([70003, 5], 3, 4, 1, 128, 256, -1, 0, True, 0),
 ]
 
 
