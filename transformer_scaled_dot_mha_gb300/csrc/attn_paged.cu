@@ -54,9 +54,9 @@ namespace {
 
 constexpr int kSMs = 152;
 constexpr int kMaxParts = 12 * kSMs;  // parts of the list of tiles at most, one per resident warp
-constexpr int kMinTiles = 2;          // tiles per part, at least
+constexpr int kMinTiles = 2;          // tiles per part, at least (8 heads, 500 keys: 8.5 us; 10.1 from three)
 constexpr int kPairCost = 2;          // tiles that a pair's queries and results cost
-constexpr int kWholeTiles = 4;        // up to here a pair is not worth splitting
+constexpr int kWholeTiles = 4;        // up to here no pair is split (8 heads, 250 keys: 7.9 us; 10.1 up to eight)
 constexpr int kMergeThreads = 256;
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -969,7 +969,8 @@ int launch(const PagedArgs& a, float* ws) {
   const int st = launch_pdl(attn_paged_kernel<D, NT, FP8>, dim3(p.whole ? (unsigned)pairs : C::PARTS), 32,
                             C::SMEM_BYTES, a.stream, p);
   if (st != ATTN_OK || p.whole) return st;
-  // few pairs have many parts each: all warps of a block on one row's
+  // Few pairs have many parts each: all warps of a block on one row's. Many pairs' blocks take
+  // several rows (256 pairs of 16 rows: 29.4 us, 39.6 with a block for each row).
   const int rows = p.rows < C::ROWS ? p.rows : C::ROWS;
   const int group_rows = pairs * rows <= 8 * kSMs ? 1 : rows <= 4 ? 4 : 8;
   const dim3 grid(p.notes_by_pair ? (unsigned)pairs : C::PARTS, (unsigned)((rows + group_rows - 1) / group_rows));

@@ -524,13 +524,15 @@ int launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t str
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
-// Heads a lane group walks over: as many as leave the device filled. More heads per group
-// read the token's angles fewer times; fewer give short batches more CTAs.
+// Heads a lane group walks over: as many, up to 8, as leave two CTAs per SM. More heads per
+// group read the token's angles fewer times; fewer give short batches more CTAs. (8192 tokens x
+// 16 heads of 64: 8.1 us, 8.8 from eight CTAs per SM, 12.2 from sixteen; 16384 x 40 heads of
+// 128 with plain stores: 55.0 with up to 8 heads, 59.9 with 4, 59.6 with 32.)
 int heads_per_unit(long long token_tiles, const int* heads, int kinds) {
   for (int hp = 8; hp > 1; hp /= 2) {
     long long units = 0;
     for (int z = 0; z < kinds; ++z) units += (heads[z] + hp - 1) / hp;
-    if (token_tiles * units >= 8LL * kSMs) return hp;
+    if (token_tiles * units >= 2LL * kSMs) return hp;
   }
   return 1;
 }
