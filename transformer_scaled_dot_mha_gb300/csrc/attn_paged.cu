@@ -57,7 +57,7 @@ constexpr int kMaxParts = 12 * kSMs;  // parts of the list of tiles at most, one
 constexpr int kMinTiles = 2;          // tiles per part, at least (8 heads, 500 keys: 8.5 us; 10.1 from three)
 constexpr int kPairCost = 2;          // tiles that a pair's queries and results cost
 constexpr int kWholeTiles = 4;        // up to here no pair is split (8 heads, 250 keys: 7.9 us; 10.1 up to eight)
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 1024;   // at most
 constexpr uint32_t kAll = 0xffffffffu;
 
 // D columns, NT tiles of 8 query rows, FP8: e4m3 pages.
@@ -812,11 +812,10 @@ __global__ void __launch_bounds__(32, Cfg<D, NT, FP8>::CTAS_PER_SM) attn_paged_k
 template <int D, int NT, bool FP8>
 __global__ void __launch_bounds__(kMergeThreads) attn_paged_merge_kernel(const PagedParams p, int group_rows) {
   using C = Cfg<D, NT, FP8>;
-  constexpr int kMergeWarps = kMergeThreads / 32;
   constexpr int LANES = D / 4;          // lanes of a row of O
   constexpr int SIDE = 32 / LANES;      // parts side by side in a warp
-  __shared__ float sh_m[kMergeWarps], sh_l[kMergeWarps];
-  __shared__ __align__(16) float sh_o[kMergeWarps][D];
+  __shared__ float sh_m[kMergeThreads / 32], sh_l[kMergeThreads / 32];
+  __shared__ __align__(16) float sh_o[kMergeThreads / 32][D];
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const Note note = p.notes[blockIdx.x];
@@ -827,7 +826,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_paged_merge_kernel(const P
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = min(p.rows - mt * C::ROWS, C::ROWS);
-  const int slices = kMergeWarps / group_rows;  // warps per row
+  const int slices = blockDim.x / 32 / group_rows;  // warps per row
   const int slice = warp % slices, r = blockIdx.y * group_rows + warp / slices;
   const int col = 4 * (lane % LANES), side = lane / LANES;
   float M = -INFINITY, L = 0.0f;
@@ -973,8 +972,13 @@ int launch(const PagedArgs& a, float* ws) {
   // several rows (256 pairs of 16 rows: 29.4 us, 39.6 with a block for each row).
   const int rows = p.rows < C::ROWS ? p.rows : C::ROWS;
   const int group_rows = pairs * rows <= 8 * kSMs ? 1 : rows <= 4 ? 4 : 8;
+  // More than 160 parts to a pair are worth blocks of 32 warps (8 heads of d 128: 32000 keys
+  // 34.1 -> 30.4 us, 128000 91.2 -> 86.6); fewer are joined later by them (256 pairs of 7: 23.3
+  // -> 27.2; 8 heads of 64, 8000 keys, 125 parts: 8.6 -> 9.7).
+  const bool many = 160 * pairs < C::PARTS && tiles > 160 * kMinTiles && pairs * rows <= 2 * kSMs;
+  const int threads = many ? kMergeThreads : 256;
   const dim3 grid(p.notes_by_pair ? (unsigned)pairs : C::PARTS, (unsigned)((rows + group_rows - 1) / group_rows));
-  return launch_pdl(attn_paged_merge_kernel<D, NT, FP8>, grid, kMergeThreads, 0, a.stream, p, group_rows);
+  return launch_pdl(attn_paged_merge_kernel<D, NT, FP8>, grid, threads, 0, a.stream, p, group_rows);
 }
 
 template <int D, bool FP8>
