@@ -499,7 +499,7 @@ size_t attn_paged_decode_workspace_size(int B, int n_q, int h_q, int h_kv, int d
  * sequence may see (max_pages * page_size, or window + n_q + sinks),
  * B * h_kv * ceil(n_q * h_q / h_kv / 8) * (ceil(keys / 16) + 2) < 2^30.
  * Numerics: the products accumulate in fp32 on the tensor cores,
- * softmax statistics in fp32; the weights are rounded to bf16 (8-bit cache: to f16) before
+ * softmax statistics in fp32; the weights are rounded to bf16 (8-bit cache: times 2^15 to f16) before
  * the second product, the output once to bf16. One or two launches on `stream`.
  */
 int attn_paged_decode(const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,

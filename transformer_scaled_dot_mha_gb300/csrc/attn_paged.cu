@@ -6,6 +6,7 @@
 // For row r (token i, query head) of a sequence of `len` tokens, pos = len - n_q + i:
 //   legal keys: j <= pos and (no window, or j >= pos - window, or j < sinks)
 //   out = sum_j p_j v_j / sum_j p_j,   p_j = 2^(s_j - m),  s_j = scale log2(e) q . k_j,  m = max_j s_j
+// (8-bit pages: all p_j times 2^15, see Cfg::SHIFT, which the quotient takes back).
 //
 // What bounds it: each visible K and V row is read once, 4 (8-bit: 2) bytes per column pair
 // against 4 x group operations, so HBM. The arithmetic has only to stay out of the way,
@@ -72,6 +73,11 @@ struct Cfg {
   static constexpr int SIDE = 32 / PIECES;                 // rows that one copy instruction covers
   static constexpr int S = D / 16;                         // MMA steps over the columns; column tiles of O
   static constexpr int ROWS = 8 * NT;
+  // e4m3: the weights go through f16, which ends at 2^16 and has all its bits from 2^-14 up only.
+  // As 2^15 p they keep them down to 2^-29 of the largest, and none above 2^-40 of it vanishes.
+  // (An early token that takes nearly all the weight and has no value leaves an output made of
+  // such weights.) O and l carry the factor; it leaves with their quotient, and in lse.
+  static constexpr float SHIFT = FP8 ? 15.0f : 0.0f;
   static constexpr int TILE_BYTES = KT * ROW_BYTES;          // of K, and of V
   static constexpr int CTAS_PER_SM = D == 128 && NT == 2 ? 8 : 12;  // 255 or 168 registers
   static constexpr int PARTS = CTAS_PER_SM * kSMs;
@@ -354,8 +360,11 @@ __device__ __forceinline__ void empty_rows(const PagedParams& p) {
   }
 }
 
-// ln of 2^m l; __log2f is within 2^-22, relative (absolute near 1): below lse's own rounding.
-__device__ __forceinline__ float log_sum(float m, float l) { return (m + __log2f(l)) * 0.69314718055994530942f; }
+// ln of 2^m l, where l is 2^shift times the sum; __log2f is within 2^-22, relative (absolute near
+// 1): below lse's own rounding.
+__device__ __forceinline__ float log_sum(float m, float l, float shift) {
+  return (m + (__log2f(l) - shift)) * 0.69314718055994530942f;
+}
 
 // The rows of one pair as a warp holds them: queries, bounds, running statistics.
 template <int D, int NT, bool FP8>
@@ -471,7 +480,7 @@ struct Rows {
           if (slot >= 0)
             *reinterpret_cast<float2*>(p.ws_ml + at * 2) = make_float2(m[nt][e], sum);
           else if (p.lse)
-            p.lse[at] = none ? -INFINITY : log_sum(m[nt][e], sum);
+            p.lse[at] = none ? -INFINITY : log_sum(m[nt][e], sum, C::SHIFT);
         }
       }
   }
@@ -635,7 +644,9 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
           for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-              sc[kb][nt][2 * hf + e] = ptx::ex2(sc[kb][nt][2 * hf + e] - m_use);
+              // at most SHIFT, however large m: the difference is at most 0 before it is shifted
+              const float x = sc[kb][nt][2 * hf + e] - m_use;
+              sc[kb][nt][2 * hf + e] = ptx::ex2(FP8 ? x + C::SHIFT : x);
               sum += sc[kb][nt][2 * hf + e];
             }
           rows.l[nt][e] = fmaf(rows.l[nt][e], alpha[e], sum);
@@ -647,9 +658,9 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
             for (int e = 0; e < 4; ++e) rows.o[nt][s][e] *= alpha[e & 1];
         }
         // P^T as the second product's operand, rounded to the cache's compute type (bf16, or
-        // f16 for 8-bit pages): at most 2^-8 (2^-11) of a weight, of either sign (1.9e-3
-        // relative in norm against 64 bits at 17 to 8192 keys, where rounding the output alone gives
-        // 1.7e-3); the sum l keeps the unrounded weights
+        // f16 for 8-bit pages): at most 2^-8 (2^-11, or 2^-40 of the largest) of a weight, of either
+        // sign (1.9e-3 relative in norm against 64 bits at 17 to 8192 keys, where rounding the
+        // output alone gives 1.7e-3); the sum l keeps the unrounded weights
 #pragma unroll
         for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
@@ -908,7 +919,7 @@ __global__ void __launch_bounds__(kMergeThreads) attn_paged_merge_kernel(const P
   const float inv = none ? 0.0f : __fdividef(1.0f, L);
   *reinterpret_cast<uint2*>(p.out + row * D + col) =
       make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (p.lse && col == 0) p.lse[row] = none ? -INFINITY : log_sum(M, L);
+  if (p.lse && col == 0) p.lse[row] = none ? -INFINITY : log_sum(M, L, C::SHIFT);
 }
 
 template <typename... KArgs, typename... Args>
