@@ -498,9 +498,12 @@ size_t attn_paged_decode_workspace_size(int B, int n_q, int h_q, int h_kv, int d
  * h_kv), any page size (limits as in attn_paged_append), and with `keys` the most that a
  * sequence may see (max_pages * page_size, or window + n_q + sinks),
  * B * h_kv * ceil(n_q * h_q / h_kv / 8) * (ceil(keys / 16) + 2) < 2^30.
- * Numerics: the products accumulate in fp32 on the tensor cores,
- * softmax statistics in fp32; the weights are rounded to bf16 (8-bit cache: times 2^15 to f16) before
- * the second product, the output once to bf16. One or two launches on `stream`.
+ * Numerics: the products accumulate in fp32 on the tensor cores, softmax statistics in fp32;
+ * the weights enter the second product as two bf16 parts, within 2^-15 of each (8-bit
+ * cache: two f16 parts, 2^-21, or 2^-40 of the largest), and the output is rounded once to
+ * bf16. With an 8-bit cache the queries enter the first product as f16, scaled by a power of
+ * two: exact but for entries below 2^-14 of the row's largest, which move by at most 2^-25
+ * of it. One or two launches on `stream`.
  */
 int attn_paged_decode(const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,
                       const int32_t* page_table, const int32_t* cache_lens, int B, int n_q, int h_q, int h_kv, int d,

@@ -146,6 +146,14 @@ __device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t x, bool high) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(h));
   return r;
 }
+// The leading bits of a weight, exact in the compute type (f16: from 2^-14 up, below it the rest
+// is what the pair loses). bf16: of the next number below it, so that the rest of a weight above
+// zero is above zero too: 0 times an infinite value would be NaN. (e4m3 has no infinity.)
+template <bool FP8>
+__device__ __forceinline__ float leading(float w) {
+  const int bits = __float_as_int(w);
+  return __int_as_float(FP8 ? bits & 0xffffe000 : max(bits - 1, 0) & 0xffff0000);
+}
 // 16 bytes to shared memory, zeros where `there` is false (then nothing is read).
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -624,7 +632,7 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
       }
 
       // ---- online softmax; rows.l is this lane's share, summed at the end
-      uint32_t pf[C::KB][NT][2];
+      uint32_t pf[C::KB][NT][2][2];  // [.][.][half of the keys][leading bits, rest]
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float alpha[2];
@@ -657,16 +665,19 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
 #pragma unroll
             for (int e = 0; e < 4; ++e) rows.o[nt][s][e] *= alpha[e & 1];
         }
-        // P^T as the second product's operand, rounded to the cache's compute type (bf16, or
-        // f16 for 8-bit pages): at most 2^-8 (2^-11, or 2^-40 of the largest) of a weight, of either
-        // sign (1.9e-3 relative in norm against 64 bits at 17 to 8192 keys, where rounding the
-        // output alone gives 1.7e-3); the sum l keeps the unrounded weights
+        // P^T as the second product's operand, in two parts of the cache's compute type (bf16, or
+        // f16 for 8-bit pages): the leading bits of a weight and what they leave, so that no more
+        // is lost than 2^-15 (f16: 2^-21, or 2^-40 of the largest) of it.
 #pragma unroll
         for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-            pf[kb][nt][hf] = transpose8(FP8 ? pack_f16x2(sc[kb][nt][2 * hf], sc[kb][nt][2 * hf + 1])
-                                            : ptx::pack_bf16x2(sc[kb][nt][2 * hf], sc[kb][nt][2 * hf + 1]));
+          for (int hf = 0; hf < 2; ++hf) {
+            const float p0 = sc[kb][nt][2 * hf], p1 = sc[kb][nt][2 * hf + 1];
+            const float h0 = leading<FP8>(p0), h1 = leading<FP8>(p1);
+            pf[kb][nt][hf][0] = transpose8(FP8 ? pack_f16x2(h0, h1)
+                                               : __byte_perm(__float_as_uint(h0), __float_as_uint(h1), 0x7632));
+            pf[kb][nt][hf][1] = transpose8(FP8 ? pack_f16x2(p0 - h0, p1 - h1) : ptx::pack_bf16x2(p0 - h0, p1 - h1));
+          }
       }
 
       // ---- O^T += V^T P^T
@@ -714,7 +725,9 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
               }
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma<FP8>(rows.o[nt][s], a, pf[kb][nt][0], pf[kb][nt][1]);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int x = 0; x < 2; ++x) mma<FP8>(rows.o[nt][s], a, pf[kb][nt][0][x], pf[kb][nt][1][x]);
           }
       } else {
         // the weights go where the tile's K was, [key][row]; a lane's columns of V are read anew
