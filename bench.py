@@ -87,18 +87,18 @@ KERNEL_SOURCES = {
     "attn_bwd_tc_kernel": ("attn_bwd.cu", "ptx_sm103.cuh"),
 }
 NCU_TRAFFIC = {
-    ("long_causal_b2_h16_n8192_d64", "attn_fwd_tc_kernel", "dd287655676f270e"): 153654016,
-    ("long_none_b2_h16_n8192_d64", "attn_fwd_tc_kernel", "dd287655676f270e"): 114852352,
-    ("long_causal_b2_h16_n8192_d128", "attn_fwd_tc_kernel", "dd287655676f270e"): 572768256,
-    ("long_none_b2_h16_n8192_d128", "attn_fwd_tc_kernel", "dd287655676f270e"): 1066685952,
-    ("long_cross_pad_b2_h16_q4096_k8192_d64", "attn_fwd_tc_kernel", "dd287655676f270e"): 76273152,
-    ("long_cross_pad_b2_h16_q4096_k8192_d128", "attn_fwd_tc_kernel", "dd287655676f270e"): 529536512,
-    ("local_causal_b2_h16_n8192_d64_w511", "attn_fwd_tc_kernel", "dd287655676f270e"): 110697472,
+    ("long_causal_b2_h16_n8192_d64", "attn_fwd_tc_kernel", "84f411279cd9898e"): 153654016,
+    ("long_none_b2_h16_n8192_d64", "attn_fwd_tc_kernel", "84f411279cd9898e"): 114852352,
+    ("long_causal_b2_h16_n8192_d128", "attn_fwd_tc_kernel", "84f411279cd9898e"): 572768256,
+    ("long_none_b2_h16_n8192_d128", "attn_fwd_tc_kernel", "84f411279cd9898e"): 1066685952,
+    ("long_cross_pad_b2_h16_q4096_k8192_d64", "attn_fwd_tc_kernel", "84f411279cd9898e"): 76273152,
+    ("long_cross_pad_b2_h16_q4096_k8192_d128", "attn_fwd_tc_kernel", "84f411279cd9898e"): 529536512,
+    ("local_causal_b2_h16_n8192_d64_w511", "attn_fwd_tc_kernel", "84f411279cd9898e"): 110697472,
     # the warp kernel only (the merge kernel is not counted)
-    ("decode_b16_h16_q1_k8192_d64", "attn_decode_warp_kernel", "15a9265a513b2001"): 424486400,
+    ("decode_b16_h16_q1_k8192_d64", "attn_decode_warp_kernel", "873cae2d608ca4d8"): 424486400,
     # the fused d = 64 kernel (the local-window workload: its LOCAL instantiation)
-    ("long_causal_b2_h16_n8192_d64", "attn_bwd_tc_kernel", "0aab31e7fb26f9cd"): 291646464,
-    ("local_causal_b2_h16_n8192_d64_w511", "attn_bwd_tc_kernel", "0aab31e7fb26f9cd"): 290630656,
+    ("long_causal_b2_h16_n8192_d64", "attn_bwd_tc_kernel", "d65231bf0af9d267"): 291646464,
+    ("local_causal_b2_h16_n8192_d64_w511", "attn_bwd_tc_kernel", "d65231bf0af9d267"): 290630656,
 }
 
 

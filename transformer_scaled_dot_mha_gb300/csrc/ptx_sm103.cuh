@@ -109,18 +109,6 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, uint
       : "memory");
 }
 
-// As tma_load_2d, multicast: the box lands at the same shared-memory offset in every
-// CTA of the cluster named in cta_mask, and completes bytes on the mbarrier at the
-// same offset in each of them.
-__device__ __forceinline__ void tma_load_2d_mc(uint32_t dst, const void* tmap, uint32_t bar, int x, int y,
-                                               uint16_t cta_mask, uint64_t cache_hint) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-      ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5, %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "h"(cta_mask), "l"(cache_hint)
-      : "memory");
-}
-
 // 3-D tiled reduce-add shared -> global (element type of the tensor map), tracked
 // by the bulk async-group of the issuing thread. Elements outside the tensor are
 // skipped. Coordinates as in tma_load_3d; they must not be negative.
