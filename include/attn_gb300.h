@@ -397,8 +397,8 @@ enum { ATTN_ROPE_INTERLEAVED = 1, ATTN_CACHE_E4M3 = 2 };
  *           A token whose position is negative or, with d_rot > 0, not below n_pos, is
  *           padding: its outputs are zero.
  *   flags   0 or ATTN_ROPE_INTERLEAVED
- * Supported: d in {64, 128}, d_rot a multiple of 16 in [0, d]; data pointers 16-byte
- * aligned. fp32 arithmetic, one rounding to bf16. One launch on `stream`.
+ * Supported: d in {64, 128}, d_rot a multiple of 16 in [0, d]; heads * d < 2^31; data
+ * pointers 16-byte aligned. fp32 arithmetic, one rounding to bf16. One launch on `stream`.
  */
 int attn_norm_rope(const void* q, const void* k, int64_t q_stride, int64_t k_stride, const void* q_weight,
                    const void* k_weight, float eps, const float* cos_sin, int n_pos, int d_rot,
@@ -454,8 +454,8 @@ int attn_norm_rope_bwd(const void* q, const void* k, int64_t q_stride, int64_t k
  * outside [0, n_seqs), or when its page table entry is outside [0, n_pages): a batch padded
  * to a fixed size marks its padding with position -1. Cache rows of no token stay as they
  * were. Two tokens with the same sequence and position leave either's values, column by
- * column. Supported: d in {64, 128}, d_rot a multiple of 16, any page size (n_pages * h_kv
- * * page_size < 2^31, max_pages * page_size <= 2^30). One launch on `stream`.
+ * column. Supported: d in {64, 128}, d_rot a multiple of 16, heads * d < 2^31, any page size
+ * (n_pages * h_kv * page_size < 2^31, max_pages * page_size <= 2^30). One launch on `stream`.
  */
 int attn_paged_append(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
                       int64_t v_stride, const void* q_weight, const void* k_weight, float eps, const float* cos_sin,

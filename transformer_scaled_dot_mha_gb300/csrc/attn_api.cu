@@ -44,9 +44,12 @@ int check_common(const void* q, const void* k, const void* v, const void* out, c
   return ATTN_OK;
 }
 
+// The kernels count a token's columns in 32 bits.
+bool too_wide(int h, int d) { return (long long)h * d > 0x7fffffffLL; }
+
 // Heads' rows laid out by token: `tokens` rows of h * d columns, `stride` elements apart.
 bool bad_rows(const void* x, long long tokens, int64_t stride, int h, int d) {
-  return !x || !aligned(x, 16) || stride < (long long)h * d || stride % 8 != 0 || stride > (1LL << 40) / tokens;
+  return !x || too_wide(h, d) || !aligned(x, 16) || stride < (long long)h * d || stride % 8 != 0 || stride > (1LL << 40) / tokens;
 }
 
 // The norm and rotation arguments that attn_norm_rope, its gradients and attn_paged_append
@@ -341,6 +344,7 @@ size_t attn_norm_rope_bwd_workspace_size(int B, int n, int h_q, int h_kv, int d)
   if (B <= 0 || n <= 0 || h_q <= 0 || h_kv <= 0 || (d != 64 && d != 128)) return 0;
   const long long tokens = (long long)B * n;
   if (tokens > 0x7fffff00LL || (long long)h_q + h_kv > (1LL << 40) / d / tokens) return 0;
+  if (too_wide(h_q, d) || too_wide(h_kv, d)) return 0;
   return attn::norm_rope_bwd_workspace_bytes(B, n, h_q, h_kv, d);
 }
 
