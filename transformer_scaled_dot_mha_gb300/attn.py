@@ -457,7 +457,9 @@ def attn_linear(x, w, y, bias=None, stream=None):
 def _device_of(t) -> int:
     """The device of a call's tensors: the current one, where its launches go."""
     dev = t.get_device()
-    if dev < 0 or dev != torch._C._cuda_getDevice():
+    if dev < 0:
+        raise ValueError(f"the tensors must be on a CUDA device, got {t.device}")
+    if dev != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
     return dev
 
