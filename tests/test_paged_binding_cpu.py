@@ -23,3 +23,17 @@ def test_host_tensors_are_refused_as_values():
     for call in calls:
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+@pytest.mark.parametrize("short_way", [True, False])
+def test_current_stream_with_and_without_the_private_name(monkeypatch, short_way):
+    """Every entry point asks for the current stream: it has to be found by public names too."""
+    if short_way:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 70 + dev, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: type("S", (), {"cuda_stream": 70 + dev}))
+    assert attn._stream_handle(None) == 73
+    assert attn._raw_stream(None, 2) == 72
+    assert attn._raw_stream(5, 2) == attn._stream_handle(5) == 5

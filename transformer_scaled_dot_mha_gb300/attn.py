@@ -105,9 +105,16 @@ def status_string(status: int) -> str:
     return lib().attn_status_string(int(status)).decode()
 
 
+def _current_stream(dev) -> int:
+    """Handle of the device's current stream. torch's short way to it saves 3 us a call, but is not
+    a public name: without it, the stream object's."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(dev).cuda_stream if raw is None else raw(dev)
+
+
 def _stream_handle(stream) -> int:
-    if stream is None:  # the raw handle: a stream object costs 3 us a call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        return _current_stream(torch.cuda.current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -465,7 +472,7 @@ def _device_of(t) -> int:
 
 
 def _raw_stream(stream, dev) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(stream)
+    return _current_stream(dev) if stream is None else _stream_handle(stream)
 
 
 def _need(t, name, dtype, shape, dev):
