@@ -37,3 +37,10 @@ def test_current_stream_with_and_without_the_private_name(monkeypatch, short_way
     assert attn._stream_handle(None) == 73
     assert attn._raw_stream(None, 2) == 72
     assert attn._raw_stream(5, 2) == attn._stream_handle(5) == 5
+
+
+def test_numbers_beyond_a_c_int_keep_their_side():
+    """A window of 2^32 + 1 once became 1, one of 2^32 0, and -2^32 - 1 became -1 (no window)."""
+    for x, want in ((2 ** 32 + 1, 2 ** 31 - 1), (2 ** 63, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31 - 1),
+                    (-2 ** 32 - 1, -2 ** 31), (-1, -1), (0, 0), (1023, 1023)):
+        assert attn._int32(x) == want

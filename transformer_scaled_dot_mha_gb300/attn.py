@@ -471,6 +471,11 @@ def _device_of(t) -> int:
     return dev
 
 
+def _int32(x) -> int:
+    """The nearest number that a C int holds (ctypes would drop the upper bits)."""
+    return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
+
+
 def _raw_stream(stream, dev) -> int:
     return _current_stream(dev) if stream is None else _stream_handle(stream)
 
@@ -636,8 +641,9 @@ def attn_paged_append(k, v, k_pages, v_pages, positions, page_table, seq_ids=Non
         None if k_weight is None else _need(k_weight, "k_weight", bf16, (d,), dev),
         float(eps), table, n_pos, d_rot, _need(positions, "positions", i32, (T,), dev),
         None if seq_ids is None else _need(seq_ids, "seq_ids", i32, (T,), dev),
-        _need(page_table, "page_table", i32, (n_seqs, max_pages), dev), n_seqs, max_pages, q_to, kp, vp, n_pages,
-        page_size, ks, vs, T, h_q, h_kv, d, flags | (ROPE_INTERLEAVED if interleaved else 0), _raw_stream(stream, dev))
+        _need(page_table, "page_table", i32, (n_seqs, max_pages), dev), _int32(n_seqs), _int32(max_pages), q_to, kp, vp,
+        n_pages, page_size, ks, vs, T, h_q, h_kv, d, flags | (ROPE_INTERLEAVED if interleaved else 0),
+        _raw_stream(stream, dev))
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_append")
     return q_out
@@ -666,8 +672,9 @@ def attn_paged_decode(q, k_pages, v_pages, out, page_table, cache_lens, workspac
         _need(q, "q", torch.bfloat16, shape, dev), kp, vp, _need(out, "out", torch.bfloat16, shape, dev),
         None if lse is None else _need(lse, "lse", torch.float32, (B, n_q, h_q), dev),
         _need(page_table, "page_table", i32, (B, max_pages), dev), _need(cache_lens, "cache_lens", i32, (B,), dev),
-        B, n_q, h_q, h_kv, d, n_pages, page_size, max_pages, 1.0 / math.sqrt(d) if scale is None else float(scale),
-        int(window), int(sinks), ks, vs, flags, ws_ptr, ws_bytes, _raw_stream(stream, dev))
+        B, n_q, h_q, h_kv, d, n_pages, page_size, _int32(max_pages),
+        1.0 / math.sqrt(d) if scale is None else float(scale), _int32(window), _int32(sinks), ks, vs, flags, ws_ptr,
+        ws_bytes, _raw_stream(stream, dev))
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_decode")
     return out
