@@ -500,7 +500,7 @@ size_t attn_paged_decode_workspace_size(int B, int n_q, int h_q, int h_kv, int d
  * B * h_kv * ceil(n_q * h_q / h_kv / 8) * (ceil(keys / 16) + 2) < 2^30.
  * Numerics: the products accumulate in fp32 on the tensor cores, softmax statistics in fp32;
  * the weights enter the second product as two bf16 parts, within 2^-15 of each (8-bit
- * cache: two f16 parts, 2^-21, or 2^-40 of the largest), and the output is rounded once to
+ * cache: as f16, within 2^-11, or 2^-40 of the largest), and the output is rounded once to
  * bf16. With an 8-bit cache the queries enter the first product as f16, scaled by a power of
  * two: exact but for entries below 2^-14 of the row's largest, which move by at most 2^-25
  * of it. One or two launches on `stream`.

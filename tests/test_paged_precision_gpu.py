@@ -27,7 +27,8 @@ WHOLE = torch.randint(400, 750, (60,), generator=torch.Generator().manual_seed(7
 
 
 @pytest.mark.parametrize("lens,h_kv,d,group,e4m3", [
-    (WHOLE, 16, 64, 1, True), (WHOLE, 16, 64, 1, False), ([700, 64, 33], 2, 128, 1, True), ([700, 64], 2, 128, 12, True)])
+    (WHOLE, 16, 64, 1, True), (WHOLE, 16, 64, 1, False), ([700, 64, 33], 2, 128, 1, True),
+    ([700, 64], 2, 128, 12, True)])
 @pytest.mark.parametrize("first", [1.5, 2.0, 2.25])
 def test_dominant_first_token_without_a_value(lens, h_kv, d, group, e4m3, first):
     """The first key scores 12, 16 or 18 above the others' mean and its value is zero: the other
@@ -59,8 +60,8 @@ def test_weights_keep_their_precision(lens, h_kv, d, group, e4m3):
     exact in fp32. What remains: the factor scale log2(e) and its product (2^-23 of the score,
     in log2 units below 7, eight standard deviations: 2^-20), the exponential, its argument and
     the sums (2^-20 together): weights within 2^-18 of themselves, one way for all at the
-    worst; the second product takes them in 16 bits (2^-15), independently; the output is
-    rounded once (u / 2 in root mean square)."""
+    worst; the second product takes them in two bf16 parts (2^-15; e4m3 pages: rounded to f16,
+    2^-11), independently; the output is rounded once (u / 2 in root mean square)."""
     g = torch.Generator().manual_seed(72)
     q, kp, vp, table, ln, _ = make(73, lens, 1, group * h_kv, h_kv, d, 64, False)
     B, one = len(lens), torch.ones(h_kv) if e4m3 else None
@@ -89,7 +90,8 @@ def test_weights_keep_their_precision(lens, h_kv, d, group, e4m3):
         p = torch.softmax(scale * torch.einsum("nhd,hd->nh", k, per_head[b, 0, :, 0].double()), 0)[..., None]
         all_ways, each_way = (p * v.abs()).sum(0), (p * v).square().sum(0).sqrt()
         w = want[b, 0].view(h_kv, group, d)
-        bound = ((ref.U_BF16 / 2 * w) ** 2 + ((2.0 ** -18 * all_ways) ** 2 + (2.0 ** -15 * each_way) ** 2)[:, None]).sqrt()
+        fixed = (2.0 ** -18 * all_ways) ** 2 + ((ref.U_F16 if e4m3 else 2.0 ** -15) * each_way) ** 2
+        bound = ((ref.U_BF16 / 2 * w) ** 2 + fixed[:, None]).sqrt()
         err = (out[b, 0].double().view(h_kv, group, d) - w).abs()
         assert err.norm() <= bound.norm(), f"{(err.norm() / bound.norm()).item():.2f} of the bound"
 

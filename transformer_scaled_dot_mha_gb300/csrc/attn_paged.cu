@@ -73,6 +73,7 @@ struct Cfg {
   static constexpr int SIDE = 32 / PIECES;                 // rows that one copy instruction covers
   static constexpr int S = D / 16;                         // MMA steps over the columns; column tiles of O
   static constexpr int ROWS = 8 * NT;
+  static constexpr int PARTS_P = FP8 ? 1 : 2;  // of a weight, in the second product
   // e4m3: the weights go through f16, which ends at 2^16 and has all its bits from 2^-14 up only.
   // As 2^15 p they keep them down to 2^-29 of the largest, and none above 2^-40 of it vanishes.
   // (An early token that takes nearly all the weight and has no value leaves an output made of
@@ -146,14 +147,9 @@ __device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t x, bool high) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(h));
   return r;
 }
-// The leading bits of a weight, exact in the compute type (f16: from 2^-14 up, below it the rest
-// is what the pair loses). bf16: of the next number below it, so that the rest of a weight above
-// zero is above zero too: 0 times an infinite value would be NaN. (e4m3 has no infinity.)
-template <bool FP8>
-__device__ __forceinline__ float leading(float w) {
-  const int bits = __float_as_int(w);
-  return __int_as_float(FP8 ? bits & 0xffffe000 : max(bits - 1, 0) & 0xffff0000);
-}
+// The bits of bf16's leading part of a weight: of the next number below it, so that the rest of a
+// weight above zero is above zero too (0 times an infinite value would be NaN).
+__device__ __forceinline__ uint32_t leading(float w) { return max(__float_as_int(w) - 1, 0) & 0xffff0000; }
 // 16 bytes to shared memory, zeros where `there` is false (then nothing is read).
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -632,7 +628,7 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
       }
 
       // ---- online softmax; rows.l is this lane's share, summed at the end
-      uint32_t pf[C::KB][NT][2][2];  // [.][.][half of the keys][leading bits, rest]
+      uint32_t pf[C::KB][NT][2][C::PARTS_P];  // [.][.][half of the keys][part]
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float alpha[2];
@@ -665,18 +661,26 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
 #pragma unroll
             for (int e = 0; e < 4; ++e) rows.o[nt][s][e] *= alpha[e & 1];
         }
-        // P^T as the second product's operand, in two parts of the cache's compute type (bf16, or
-        // f16 for 8-bit pages): the leading bits of a weight and what they leave, so that no more
-        // is lost than 2^-15 (f16: 2^-21, or 2^-40 of the largest) of it.
+        // P^T as the second product's operand. bf16 pages: in two parts, the leading bits of a
+        // weight and what they leave, so that at most 2^-15 of it is lost; one part alone loses
+        // up to 2^-8 of every term, as much as the output's own rounding (16 x 8 heads of d 128
+        // 68.9 us, 68.4 with one part; 64 sequences x 64 rows and windows of 1024, bound by the
+        // MMAs, 53.4 and 48.3). 8-bit pages: one part in f16, which loses 2^-11 of a weight
+        // (2^-40 of the largest), an eighth of the output's rounding; two would take 125.7 us
+        // instead of 112.7 (8 x 8 heads of 16 rows, 9001-65521 keys).
 #pragma unroll
         for (int kb = 0; kb < C::KB; ++kb)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const float p0 = sc[kb][nt][2 * hf], p1 = sc[kb][nt][2 * hf + 1];
-            const float h0 = leading<FP8>(p0), h1 = leading<FP8>(p1);
-            pf[kb][nt][hf][0] = transpose8(FP8 ? pack_f16x2(h0, h1)
-                                               : __byte_perm(__float_as_uint(h0), __float_as_uint(h1), 0x7632));
-            pf[kb][nt][hf][1] = transpose8(FP8 ? pack_f16x2(p0 - h0, p1 - h1) : ptx::pack_bf16x2(p0 - h0, p1 - h1));
+            if (FP8) {
+              pf[kb][nt][hf][0] = transpose8(pack_f16x2(p0, p1));
+            } else {
+              const uint32_t h0 = leading(p0), h1 = leading(p1);
+              pf[kb][nt][hf][0] = transpose8(__byte_perm(h0, h1, 0x7632));
+              pf[kb][nt][hf][C::PARTS_P - 1] =
+                  transpose8(ptx::pack_bf16x2(p0 - __uint_as_float(h0), p1 - __uint_as_float(h1)));
+            }
           }
       }
 
@@ -727,7 +731,7 @@ __device__ __forceinline__ void stream(const PagedParams& p, uint8_t* smem, Curs
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int x = 0; x < 2; ++x) mma<FP8>(rows.o[nt][s], a, pf[kb][nt][0][x], pf[kb][nt][1][x]);
+              for (int x = 0; x < C::PARTS_P; ++x) mma<FP8>(rows.o[nt][s], a, pf[kb][nt][0][x], pf[kb][nt][1][x]);
           }
       } else {
         // the weights go where the tile's K was, [key][row]; a lane's columns of V are read anew
