@@ -25,15 +25,20 @@ def test_host_tensors_are_refused_as_values():
             call()
 
 
-@pytest.mark.parametrize("short_way", [True, False])
-def test_current_stream_with_and_without_the_private_name(monkeypatch, short_way):
+@pytest.mark.parametrize("short_ways", [True, False])
+def test_current_device_and_stream_with_and_without_private_names(monkeypatch, short_ways):
     """Every entry point asks for the current stream: it has to be found by public names too."""
-    if short_way:
-        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 70 + dev, raising=False)
-    else:
-        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    for name, short in (("_cuda_getDevice", lambda: 3), ("_cuda_getCurrentRawStream", lambda dev: 70 + dev)):
+        if short_ways:
+            monkeypatch.setattr(torch._C, name, short, raising=False)
+        else:
+            monkeypatch.delattr(torch._C, name, raising=False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: type("S", (), {"cuda_stream": 70 + dev}))
+    device, stream = attn._short_ways()
+    assert device() == 3 and stream(2) == 72
+    monkeypatch.setattr(attn, "_current_device", device)
+    monkeypatch.setattr(attn, "_current_stream", stream)
     assert attn._stream_handle(None) == 73
     assert attn._raw_stream(None, 2) == 72
     assert attn._raw_stream(5, 2) == attn._stream_handle(5) == 5
@@ -42,5 +47,5 @@ def test_current_stream_with_and_without_the_private_name(monkeypatch, short_way
 def test_numbers_beyond_a_c_int_keep_their_side():
     """A window of 2^32 + 1 once became 1, one of 2^32 0, and -2^32 - 1 became -1 (no window)."""
     for x, want in ((2 ** 32 + 1, 2 ** 31 - 1), (2 ** 63, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31 - 1),
-                    (-2 ** 32 - 1, -2 ** 31), (-1, -1), (0, 0), (1023, 1023)):
+                    (-2 ** 32 - 1, 1 - 2 ** 31), (-1, -1), (0, 0), (1023, 1023)):
         assert attn._int32(x) == want
