@@ -197,3 +197,36 @@ def test_append_walks_over_heads(toks, h_q, h_kv, d, d_rot, norm, inter, page, e
     raw = torch.int8 if e4m3 else torch.int16
     for got in (gk, gv):
         assert torch.all((got.cpu().view(raw) == before.view(raw)).all(-1).all(1) | touched)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_padding_tokens_may_hold_anything(d):
+    """Infinities and NaN in padding tokens reach nothing: zeros there, all else bit for bit as with
+    zeros in their place."""
+    B, n, h_q, h_kv = 2, 700, 3, 2
+    gen, qkv, w, table, pos, real, _ = inputs(84, B, n, h_q, h_kv, d, d, True, True)
+    grads = [rand(gen, B, h, n, d) for h in (h_q, h_kv)]
+    assert 0 < (~real).sum() < B * n
+    got = []
+    for fill in (0.0, NAN, float("inf")):
+        x, gr = qkv.clone(), [t.clone() for t in grads]
+        x.view(B * n, -1)[~real] = fill
+        for t in gr:
+            t.transpose(1, 2)[~real.view(B, n)] = fill
+        q, k = split(x.cuda(), h_q, h_kv, d)
+        outs = [torch.full((B, h, n, d), NAN, dtype=torch.bfloat16, device="cuda") for h in (h_q, h_kv)]
+        back = [torch.full((B, n, h, d), NAN, dtype=torch.bfloat16, device="cuda") for h in (h_q, h_kv)]
+        dw = [torch.full((d,), NAN, device="cuda") for _ in range(2)]
+        ws = torch.empty(attn.attn_norm_rope_bwd_workspace_size(B, n, h_q, h_kv, d), dtype=torch.uint8, device="cuda")
+        at = pos.int().cuda()
+        attn.attn_norm_rope(q, k, *outs, dev(table), *map(dev, w), positions=at, eps=EPS)
+        attn.attn_norm_rope_bwd(q, k, *map(dev, gr), *back, ws, dev(table), *map(dev, w), *dw, positions=at, eps=EPS)
+        torch.cuda.synchronize()
+        got.append([t.cpu() for t in outs + back + dw])
+        for t in got[-1][:2]:
+            assert torch.all(t.transpose(1, 2)[~real.view(B, n)] == 0)
+        for t in got[-1][2:4]:
+            assert torch.all(t[~real.view(B, n)] == 0)
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+    assert all(torch.isfinite(t).all() for t in got[0])
