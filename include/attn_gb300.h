@@ -388,8 +388,9 @@ enum { ATTN_ROPE_INTERLEAVED = 1, ATTN_CACHE_E4M3 = 2 };
  *   q, k    bf16, token-major: head h of token x (of B * n) starts at q + x * q_stride + h * d
  *           (strides in elements, multiples of 8, at least heads * d): slices of one fused
  *           projection, for instance
- *   q_out [B, h_q, n, d], k_out [B, h_kv, n, d]: bf16, the layout attn_fwd reads; they must
- *           not overlap q or k
+ *   q_out [B, h_q, n, d], k_out [B, h_kv, n, d]: bf16, the layout attn_fwd reads (which has
+ *           one h: for h_kv < h_q the caller repeats each key head for its h_q / h_kv query
+ *           heads); they must not overlap q or k
  *   q_weight, k_weight [d]: bf16, or both NULL for no norm;   eps >= 0, finite
  *   cos_sin [n_pos, d_rot]: float32, row = position: d_rot / 2 cosines, then their sines
  *           (any scaling of the angles is in the table); not read when d_rot is 0
@@ -438,7 +439,8 @@ int attn_norm_rope_bwd(const void* q, const void* k, int64_t q_stride, int64_t k
  * normalises and rotates the tokens' queries: the step before attn_paged_decode, or a
  * packed batch of prompts of different lengths. (An addition of this library.)
  *   q [T, h_q, d], k, v [T, h_kv, d]: bf16, token-major with strides as in attn_norm_rope
- *   q_out [T, h_q, d]: bf16, contiguous; NULL exactly when q is (then q_weight is NULL too)
+ *   q_out [T, h_q, d]: bf16, contiguous; NULL exactly when q is (then q_weight is NULL too);
+ *           it and the pages must not overlap q, k or v
  *   q_weight, k_weight, eps, cos_sin, n_pos, d_rot: as in attn_norm_rope (values are neither
  *           normalised nor turned)
  *   positions [T]: int32, the token's place in its sequence: its angle and its cache row

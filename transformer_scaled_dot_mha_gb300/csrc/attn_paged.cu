@@ -8,12 +8,16 @@
 //   out = sum_j p_j v_j / sum_j p_j,   p_j = 2^(s_j - m),  s_j = scale log2(e) q . k_j,  m = max_j s_j
 // (8-bit pages: all p_j times 2^15, see Cfg::SHIFT, which the quotient takes back).
 //
-// What bounds it: each visible K and V row is read once, 4 (8-bit: 2) bytes per column pair
-// against 4 x group operations, so HBM. The arithmetic has only to stay out of the way,
-// which CUDA cores cannot at group 8 (54 TFLOP/s at the full HBM rate): both products run
-// on the warp-level matrix instruction m16n8k16, whose operands are registers. A tcgen05
-// MMA would need 128 rows and its operands in shared memory; one key/value head offers 1 to
-// 16 rows, and the cache would pass through shared memory for nothing.
+// What bounds it, up to 16 rows (n_q x group) per key/value head: each visible K and V row is
+// read once, 4 (8-bit: 2) bytes per column pair against 4 x rows operations, so HBM. The
+// arithmetic has only to stay out of the way, which CUDA cores cannot at group 8 (54 TFLOP/s at
+// the full HBM rate): both products run on the warp-level matrix instruction m16n8k16, whose
+// operands are registers. A tcgen05 MMA would need 128 rows and its operands in shared
+// memory; for 1 to 16 rows the cache would pass through shared memory for nothing.
+// More rows (several tokens of a large group) are tiles of 16, each a pair of its own in the
+// list below that reads the keys again: the matrix pipe and the reads from L2 bound those calls
+// (16 x 64/8 heads of d 128, 4096-8192 keys, floor 60 us: 8 rows 72 us, 16 76, 32 120, 128 437;
+// e4m3, 8 x 64/8 heads, 9001-65521 keys, floor 90 us: 104, 113, 207, 777).
 //
 // The products are formed transposed, S^T = K Q^T and O^T = V^T P^T, so that the keys (then
 // the columns) are the 16 rows of an MMA and the query rows its 8 columns (NT column tiles
@@ -31,16 +35,20 @@
 // a row are swapped by its number so that the fragment reads meet no bank conflict. Waits
 // are cp.async.wait_group, which ends by itself; no block barrier in the stream.
 //
-// Work split: the tiles (KT keys) of all (sequence, key/value head) pairs form one list,
-// cut into equal parts by the lengths on the device -- ragged batches and capacities far
-// above the lengths cost nothing. There is a part for every warp that can be resident, and a
-// warp is a CTA (two or three parts for each, to even out the warps' speeds, cost more in
-// starts and joins: 71.2, 71.8, 75.4 us at 16 x 8 heads of d 128 and 4096-8192 keys). It
+// Work split: the tiles (KT keys) of all (sequence, key/value head, row tile) pairs form one
+// list, cut into equal parts by the lengths on the device, so that ragged batches leave no
+// warp idle and what a capacity holds above the lengths is not read. There is a part for
+// every warp that can be resident, and a warp is a CTA (two or three parts for each, to even out
+// the warps' speeds, cost more in starts and joins: 71.2, 71.8, 75.4 us at 16 x 8 heads of d 128
+// and 4096-8192 keys when that was tried, with the weights in one part). It
 // streams its part from one pair into the next without a pause in its copies. A pair that
 // lies within one warp's part is finished there; of one that does not, every part leaves
 // (m, l, O) in the workspace, the warp that has its first tile leaves a note of the parts,
 // and attn_paged_merge_kernel joins them. When no sequence can be longer than a few tiles,
-// each pair gets a warp of its own and there is no second launch.
+// each pair gets a warp of its own and there is no second launch. The host chooses between the
+// two and knows the capacity alone, not the lengths: short sequences under a wide page table
+// are cut up and joined (200 x 8 heads of d 128, 10-300 keys: 33.1 us, 27.6 under a table of
+// 300 keys).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -55,9 +63,9 @@ namespace {
 
 constexpr int kSMs = 152;
 constexpr int kMaxParts = 12 * kSMs;  // parts of the list of tiles at most, one per resident warp
-constexpr int kMinTiles = 2;          // tiles per part, at least (8 heads, 500 keys: 8.5 us; 10.1 from three)
+constexpr int kMinTiles = 2;          // tiles per part, at least (8 heads, 500 keys: 7.3 us; 8.0 from three)
 constexpr int kPairCost = 2;          // tiles that a pair's queries and results cost
-constexpr int kWholeTiles = 4;        // up to here no pair is split (8 heads, 250 keys: 7.9 us; 10.1 up to eight)
+constexpr int kWholeTiles = 4;        // up to here no pair is split (8 heads, 250 keys: 7.3 us; 9.0 up to eight)
 constexpr int kMergeThreads = 1024;   // at most
 constexpr uint32_t kAll = 0xffffffffu;
 
@@ -209,7 +217,7 @@ __device__ __forceinline__ int tiles_of(const PagedParams& p, int b) {
 // n = tiles_of(b) tiles. A pair costs kPairCost tiles more (its queries, its results): in the
 // count that parts are cut from it has kPairCost units, if it has tiles at all, and then one
 // per tile; part c is units [c * part, (c + 1) * part). (64 sequences of 3 to 8191 keys, windows
-// of 1024: 20.9 us, 27.0 without.) All of it counts in 32 bits: the launch refuses a list
+// of 1024: 21.7 us, 28.0 without.) All of it counts in 32 bits: the launch refuses a list
 // that could be longer.
 struct Scan {
   int b0;            // the first of the 32 sequences that the lanes stand for
@@ -982,9 +990,9 @@ int launch(const PagedArgs& a, float* ws) {
   p.notes = reinterpret_cast<Note*>(p.ws_ml + (size_t)2 * C::PARTS * C::ROWS * 2);
   // Tiles that any pair may have decide whether pairs are split. They are not where that is
   // few; nor up to 24 tiles with pairs for half the warps (200 x 8 heads of d 128, 10-300 keys:
-  // 27.0 us, 33.4 split; but 256 x 8 heads of 64 with 1000 keys, 32 tiles: 99.9 and 92.3), nor,
+  // 27.6 us, 33.1 split; but 256 x 8 heads of 64 with 1000 keys, 32 tiles: 102.6 and 92.0), nor,
   // from 1.5 pairs per warp on, up to 22 times as many tiles as pairs per warp: the longest
-  // pair is then no long tail (1000 x 8 heads, 500-2000 keys: 373.8 us, 398.4 split).
+  // pair is then no long tail (1000 x 8 heads, 500-2000 keys: 373.8 us, 398.9 split).
   long long most = p.max_len;
   if (p.window >= 0 && (long long)p.window + a.n_q + p.sinks < most) most = (long long)p.window + a.n_q + p.sinks;
   const long long pairs = (long long)a.B * a.h_kv * p.m_tiles, tiles = (most + C::KT - 1) / C::KT;
@@ -997,12 +1005,12 @@ int launch(const PagedArgs& a, float* ws) {
                             C::SMEM_BYTES, a.stream, p);
   if (st != ATTN_OK || p.whole) return st;
   // Few pairs have many parts each: all warps of a block on one row's. Many pairs' blocks take
-  // several rows (256 pairs of 16 rows: 29.4 us, 39.6 with a block for each row).
+  // several rows (256 pairs of 16 rows: 21.7 us, 34.8 with a block for each row).
   const int rows = p.rows < C::ROWS ? p.rows : C::ROWS;
   const int group_rows = pairs * rows <= 8 * kSMs ? 1 : rows <= 4 ? 4 : 8;
   // More than 160 parts to a pair are worth blocks of 32 warps (8 heads of d 128: 32000 keys
-  // 34.1 -> 30.4 us, 128000 91.2 -> 86.6); fewer are joined later by them (256 pairs of 7: 23.3
-  // -> 27.2; 8 heads of 64, 8000 keys, 125 parts: 8.6 -> 9.7).
+  // 33.7 -> 30.5 us, 128000 91.6 -> 87.8); fewer are joined later by them (256 pairs of 7: 23.5
+  // -> 27.5; 8 heads of 64, 8000 keys, 125 parts: 8.7 -> 9.9).
   const bool many = 160 * pairs < C::PARTS && tiles > 160 * kMinTiles && pairs * rows <= 2 * kSMs;
   const int threads = many ? kMergeThreads : 256;
   const dim3 grid(p.notes_by_pair ? (unsigned)pairs : C::PARTS, (unsigned)((rows + group_rows - 1) / group_rows));
