@@ -514,6 +514,86 @@ int attn_paged_decode(const void* q, const void* k_pages, const void* v_pages, v
                       void* stream);
 
 /*
+ * attn_packed_fwd_workspace_size -- bytes of device workspace attn_packed_fwd needs: its work
+ * list, and partial results whose size does not depend on T_q or n_seqs. Returns 0 for an
+ * invalid or unsupported shape.
+ */
+size_t attn_packed_fwd_workspace_size(int T_q, int n_seqs, int h_q, int h_kv, int d);
+
+/*
+ * attn_packed_fwd -- attn_fwd for sequences of different lengths packed one after the other,
+ * without padding between them, whose query heads share key/value heads. (An addition of this
+ * library.) Query head h uses key/value head h / (h_q / h_kv).
+ *   q, out  bf16 [T_q, h_q, d], k, v bf16 [T_k, h_kv, d]: element (x, h, c) at x * stride +
+ *           h * head_stride + c. Strides are multiples of 8, and tokens or heads are the
+ *           outer side (slices of one fused projection [T, (h_q + 2 h_kv) d], or what
+ *           attn_norm_rope returns for B = 1); the stride of a single token or head is not
+ *           read. out must not overlap the others.
+ *   lse     float32 [T_q, h_q], contiguous, or NULL
+ *   q_starts, k_starts [n_seqs + 1]: int32, not decreasing: sequence b's queries are rows
+ *           q_starts[b] .. q_starts[b + 1] - 1, its keys rows k_starts[b] .. of k and v.
+ *           k_starts NULL: the queries' rows. Rows of no sequence (before the first, behind the
+ *           last) are not used, and left as they were in out and lse. Offsets outside the
+ *           arrays are clamped to them; a sequence that ends before it starts is empty.
+ *   mask_mode  ATTN_MASK_NONE or ATTN_MASK_CAUSAL. Query i of a sequence of n_q queries and n_k
+ *           keys stands at position x = n_k - n_q + i (the last query at the last key); causal:
+ *           key j is legal for j <= x only.
+ *   window  -1, or the radius of attn_fwd_local: key j is legal for |x - j| <= window only
+ *   workspace: device scratch of at least attn_packed_fwd_workspace_size(...) bytes, 256-byte
+ *           aligned, owned by the caller, contents undefined on return; concurrent calls must
+ *           not share it.
+ * A query without a legal key gets out = 0, lse = -inf. What other sequences' rows and rows of
+ * no sequence hold, infinities and NaN included, does not reach a sequence; within a sequence a
+ * value row's infinities and NaN may reach every query whose 128-key tile holds it, masked or not.
+ * Supported: d in {64, 128}, h_q a multiple of h_kv (of at most 128 h_kv), scale > 0, T_q and
+ * T_k below 2^28, n_seqs h_kv and the numbers of 128-row tiles below 2^30 together.
+ * Numerics as attn_fwd: fp32 accumulation on the tensor cores, weights rounded to bf16 for the
+ * second product, one rounding of the output. Two or three launches on `stream`; no atomics on
+ * results: the same bits on every run.
+ */
+int attn_packed_fwd(const void* q, const void* k, const void* v, void* out, float* lse, int64_t q_stride,
+                    int64_t q_head_stride, int64_t k_stride, int64_t k_head_stride, int64_t v_stride,
+                    int64_t v_head_stride, int64_t out_stride, int64_t out_head_stride, const int32_t* q_starts,
+                    const int32_t* k_starts, int n_seqs, int T_q, int T_k, int h_q, int h_kv, int d, float scale,
+                    int mask_mode, int window, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * attn_paged_chunk_workspace_size -- bytes of device workspace attn_paged_chunk needs, for
+ * either cache type. Returns 0 for an invalid or unsupported shape.
+ */
+size_t attn_paged_chunk_workspace_size(int T, int n_seqs, int h_q, int h_kv, int d);
+
+/*
+ * attn_paged_chunk -- attn_paged_decode for any number of new tokens in every sequence, from none
+ * to a whole prompt: the step after attn_paged_append for prompts, pieces of prompts, and
+ * batches in which some sequences bring a piece and others one token. (An addition of this
+ * library.)
+ *   q, out  bf16 [T, h_q, d], contiguous: what attn_paged_append returns
+ *   lse     float32 [T, h_q], or NULL
+ *   q_starts [n_seqs + 1]: int32, as in attn_packed_fwd: sequence b's new tokens are rows
+ *           q_starts[b] .. q_starts[b + 1] - 1, the newest last. Rows of no sequence are left as
+ *           they were.
+ *   k_pages, v_pages, page_table, n_pages, page_size, max_pages, k_scale, v_scale, flags: the
+ *           cache, as in attn_paged_append, one page table row per sequence
+ *   cache_lens [n_seqs]: int32, tokens in the cache including the new ones, clamped to [0,
+ *           max_pages * page_size]. New token i of n stands at position cache_lens[b] - n + i; one
+ *           whose position is negative has no legal key: out = 0, lse = -inf.
+ *   window, sinks: as in attn_paged_decode
+ *   workspace: as in attn_packed_fwd, of at least attn_paged_chunk_workspace_size(...) bytes
+ * A page table entry outside [0, n_pages) names no page: its keys count as illegal. Cache rows
+ * behind the length are never used, whatever they hold.
+ * Supported: d in {64, 128}, h_q a multiple of h_kv (of at most 128 h_kv), scale > 0, any page size
+ * (limits as in attn_paged_append; copies are of gcd(page_size, 128) rows, so page sizes that are
+ * multiples of 16 or more are the fast ones), T below 2^28. Numerics as attn_packed_fwd; an 8-bit
+ * cache's numbers enter the products exactly, as bf16. Two or three launches on `stream`.
+ */
+int attn_paged_chunk(const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,
+                     const int32_t* q_starts, const int32_t* page_table, const int32_t* cache_lens, int n_seqs, int T,
+                     int h_q, int h_kv, int d, int n_pages, int page_size, int max_pages, float scale, int window,
+                     int sinks, const float* k_scale, const float* v_scale, int flags, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
  * attn_fault_status -- synchronises `stream`, then reports whether any kernel of
  * this library on the current device gave up waiting on one of its internal
  * barriers since the last clear (each such wait is bounded in time; a kernel that
@@ -523,7 +603,7 @@ int attn_paged_decode(const void* q, const void* k_pages, const void* v_pages, v
  * issuer, bit 2 softmax, bit 3 epilogue (attn_fwd), bit 4 decode copy (attn_decode),
  * bit 5 gradient kernels (attn_bwd), bit 6 attn_fwd found its shared memory not
  * 1024-byte aligned (it then writes nothing), bit 7 projection kernel (attn_linear,
- * attn_mha_fwd), bit 8 attn_weights.
+ * attn_mha_fwd), bit 8 attn_weights, bit 9 attn_packed_fwd and attn_paged_chunk.
  */
 int attn_fault_status(void* stream, int clear, uint32_t* fault_code);
 

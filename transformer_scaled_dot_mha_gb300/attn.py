@@ -91,6 +91,14 @@ def lib() -> ctypes.CDLL:
         L.attn_paged_decode_workspace_size.restype = sz
         L.attn_paged_decode.argtypes = [vp] * 7 + [i] * 8 + [f, i, i, vp, vp, i, vp, sz, vp]
         L.attn_paged_decode.restype = i
+        L.attn_packed_fwd_workspace_size.argtypes = [i, i, i, i, i]
+        L.attn_packed_fwd_workspace_size.restype = sz
+        L.attn_packed_fwd.argtypes = [vp] * 5 + [i64] * 8 + [vp, vp] + [i] * 6 + [f, i, i, vp, sz, vp]
+        L.attn_packed_fwd.restype = i
+        L.attn_paged_chunk_workspace_size.argtypes = [i, i, i, i, i]
+        L.attn_paged_chunk_workspace_size.restype = sz
+        L.attn_paged_chunk.argtypes = [vp] * 8 + [i] * 8 + [f, i, i, vp, vp, i, vp, sz, vp]
+        L.attn_paged_chunk.restype = i
         L.attn_fault_status.argtypes = [vp, i, ctypes.POINTER(ctypes.c_uint32)]
         L.attn_fault_status.restype = i
         L.attn_status_string.argtypes = [i]
@@ -684,6 +692,92 @@ def attn_paged_decode(q, k_pages, v_pages, out, page_table, cache_lens, workspac
         ws_bytes, _raw_stream(stream, dev))
     if st != ATTN_OK:
         raise AttnError(st, "attn_paged_decode")
+    return out
+
+
+def _need_heads(t, name, shape, dev):
+    """Data pointer, token stride and head stride of a bf16 ``[tokens, heads, d]`` tensor, tokens or
+    heads outermost."""
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev or t.stride(2) != 1:
+        raise ValueError(f"{name} must be a bfloat16 tensor of shape {list(shape)} on cuda:{dev} with d side by side, got "
+                         f"{t.dtype} {list(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _need_starts(starts, name, dev):
+    """Data pointer and number of sequences of int32 offsets ``[n_seqs + 1]``."""
+    if starts.dim() != 1 or starts.shape[0] < 2:
+        raise ValueError(f"{name} must be [n_seqs + 1], got {list(starts.shape)}")
+    return _need(starts, name, torch.int32, starts.shape, dev), starts.shape[0] - 1
+
+
+def attn_packed_fwd_workspace_size(T_q, n_seqs, h_q, h_kv, d) -> int:
+    return int(lib().attn_packed_fwd_workspace_size(_int32(T_q), _int32(n_seqs), _int32(h_q), _int32(h_kv), _int32(d)))
+
+
+def attn_packed_fwd(q, k, v, out, q_starts, workspace, k_starts=None, lse=None, scale=None, mask_mode=MASK_NONE,
+                    window=-1, stream=None):
+    """Attention of packed sequences with shared key/value heads, bf16: ``q [T_q, h_q, d]`` and
+    ``k, v [T_k, h_kv, d]`` (views with tokens or heads outermost) into ``out`` (shaped like ``q``) and
+    optional float32 ``lse [T_q, h_q]``. Sequence b's queries are rows ``q_starts[b]`` to
+    ``q_starts[b + 1] - 1`` (int32 ``[n_seqs + 1]``), its keys likewise by ``k_starts`` (None: the same
+    rows). ``mask_mode`` MASK_NONE or MASK_CAUSAL, the last query at the last key's position;
+    ``window`` >= 0: only keys within that distance. ``workspace``: a CUDA tensor of at least
+    ``attn_packed_fwd_workspace_size`` bytes."""
+    dev = _device_of(q)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError(f"q must be [T_q, h_q, d], k [T_k, h_kv, d], got {list(q.shape)} {list(k.shape)}")
+    T_q, h_q, d = q_shape = q.shape
+    T_k, h_kv, _ = k.shape
+    k_shape = (T_k, h_kv, d)
+    q_ptr, *q_st = _need_heads(q, "q", q_shape, dev)
+    k_ptr, *k_st = _need_heads(k, "k", k_shape, dev)
+    v_ptr, *v_st = _need_heads(v, "v", k_shape, dev)
+    o_ptr, *o_st = _need_heads(out, "out", q_shape, dev)
+    starts, n_seqs = _need_starts(q_starts, "q_starts", dev)
+    ws_ptr, ws_bytes = _need_workspace(workspace, dev)
+    st = lib().attn_packed_fwd(
+        q_ptr, k_ptr, v_ptr, o_ptr, None if lse is None else _need(lse, "lse", torch.float32, (T_q, h_q), dev), *q_st,
+        *k_st, *v_st, *o_st, starts,
+        None if k_starts is None else _need(k_starts, "k_starts", torch.int32, (n_seqs + 1,), dev), _int32(n_seqs),
+        _int32(T_q), _int32(T_k), h_q, h_kv, d, 1.0 / math.sqrt(d) if scale is None else float(scale), int(mask_mode),
+        _int32(window), ws_ptr, ws_bytes, _raw_stream(stream, dev))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_packed_fwd")
+    return out
+
+
+def attn_paged_chunk_workspace_size(T, n_seqs, h_q, h_kv, d) -> int:
+    return int(lib().attn_paged_chunk_workspace_size(_int32(T), _int32(n_seqs), _int32(h_q), _int32(h_kv), _int32(d)))
+
+
+def attn_paged_chunk(q, k_pages, v_pages, out, q_starts, page_table, cache_lens, workspace, lse=None, scale=None,
+                     window=-1, sinks=0, k_scale=None, v_scale=None, stream=None):
+    """New tokens of every sequence, any number of them, attend over the paged cache (see
+    attn_paged_append) that holds them already: ``q [T, h_q, d]`` bf16 into ``out`` (like ``q``) and
+    optional float32 ``lse [T, h_q]``. Sequence b's new tokens are rows ``q_starts[b]`` to
+    ``q_starts[b + 1] - 1`` (int32 ``[n_seqs + 1]``), the last of its ``cache_lens[b]`` cached ones (int32
+    ``[n_seqs]``); ``page_table`` int32 ``[n_seqs, max_pages]``. ``window`` >= 0: only keys within that
+    distance and the first ``sinks``. ``workspace``: a CUDA tensor of at least
+    ``attn_paged_chunk_workspace_size`` bytes."""
+    dev, i32 = _device_of(q), torch.int32
+    if q.dim() != 3 or k_pages.dim() != 4 or page_table.dim() != 2:
+        raise ValueError(f"q must be [T, h_q, d], the pages [n_pages, h_kv, page_size, d], page_table [n_seqs, max_pages], "
+                         f"got {list(q.shape)} {list(k_pages.shape)} {list(page_table.shape)}")
+    T, h_q, d = shape = q.shape
+    h_kv, max_pages = k_pages.shape[1], page_table.shape[1]
+    starts, n_seqs = _need_starts(q_starts, "q_starts", dev)
+    flags, n_pages, page_size, kp, vp, ks, vs = _need_pages(k_pages, v_pages, k_scale, v_scale, h_kv, d, dev)
+    ws_ptr, ws_bytes = _need_workspace(workspace, dev)
+    st = lib().attn_paged_chunk(
+        _need(q, "q", torch.bfloat16, shape, dev), kp, vp, _need(out, "out", torch.bfloat16, shape, dev),
+        None if lse is None else _need(lse, "lse", torch.float32, (T, h_q), dev), starts,
+        _need(page_table, "page_table", i32, (n_seqs, max_pages), dev),
+        _need(cache_lens, "cache_lens", i32, (n_seqs,), dev), _int32(n_seqs), _int32(T), h_q, h_kv, d, n_pages, page_size,
+        _int32(max_pages), 1.0 / math.sqrt(d) if scale is None else float(scale), _int32(window), _int32(sinks), ks, vs,
+        flags, ws_ptr, ws_bytes, _raw_stream(stream, dev))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_paged_chunk")
     return out
 
 

@@ -90,6 +90,34 @@ bool bad_cache(const void* k_pages, const void* v_pages, int n_pages, int page_s
   return (long long)max_pages * page_size > (1LL << 30);
 }
 
+// One packed operand [tokens, heads, d] with strides between tokens and heads, either of them the
+// outer one; the stride of a single token or head does not matter and is replaced.
+bool bad_packed(const void* x, long long tokens, int heads, int d, int64_t& ts, int64_t& hs) {
+  if (!x || !aligned(x, 16)) return true;
+  if (heads == 1) hs = tokens == 1 || ts >= d ? d : ts;
+  if (tokens == 1) ts = heads == 1 || hs >= d ? d : hs;
+  if (ts < d || hs < d || ts % 8 != 0 || hs % 8 != 0 || ts > (1LL << 38) || hs > (1LL << 38)) return true;
+  if (tokens == 1 || heads == 1) return (tokens - 1) * ts > (1LL << 40) || (heads - 1) * hs > (1LL << 40);
+  if (ts > (1LL << 40) / tokens || hs > (1LL << 40) / heads) return true;
+  return ts < (heads - 1) * hs + d && hs < (tokens - 1) * ts + d;  // neither token-major nor head-major: rows overlap
+}
+
+constexpr int kMaxPacked = 1 << 28;  // tokens of a packed array
+
+// Sizes of a ragged batch: an error status, or ATTN_OK.
+int check_ragged(int n_seqs, long long T_q, long long T_k, int h_q, int h_kv, int d) {
+  if (n_seqs <= 0 || T_q <= 0 || T_k <= 0 || h_q <= 0 || h_kv <= 0 || d <= 0 || h_q % h_kv != 0) return ATTN_ERR_INVALID;
+  if (T_q >= kMaxPacked || T_k >= kMaxPacked || n_seqs >= kMaxPacked) return ATTN_ERR_INVALID;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  const int group = h_q / h_kv;
+  if (group > 128) return ATTN_ERR_UNSUPPORTED;
+  // the work list is counted in 32 bits
+  const long long tok = 128 / group;
+  if ((T_q / tok + T_k / 128 + 2LL * n_seqs + 2) * h_kv > (1LL << 30)) return ATTN_ERR_UNSUPPORTED;
+  if ((T_q > T_k ? T_q : T_k) > (1LL << 40) / d / h_q) return ATTN_ERR_INVALID;
+  return ATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -433,13 +461,75 @@ int attn_paged_decode(const void* q, const void* k_pages, const void* v_pages, v
   return attn::launch_attn_paged_decode(a, workspace);
 }
 
+size_t attn_packed_fwd_workspace_size(int T_q, int n_seqs, int h_q, int h_kv, int d) {
+  if (check_ragged(n_seqs, T_q, 1, h_q, h_kv, d) != ATTN_OK) return 0;
+  return attn::packed_fwd_workspace_bytes(T_q, n_seqs, h_q, h_kv, d);
+}
+
+int attn_packed_fwd(const void* q, const void* k, const void* v, void* out, float* lse, int64_t q_stride,
+                    int64_t q_head_stride, int64_t k_stride, int64_t k_head_stride, int64_t v_stride,
+                    int64_t v_head_stride, int64_t out_stride, int64_t out_head_stride, const int32_t* q_starts,
+                    const int32_t* k_starts, int n_seqs, int T_q, int T_k, int h_q, int h_kv, int d, float scale,
+                    int mask_mode, int window, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q_starts || !aligned(q_starts, 4) || (k_starts && !aligned(k_starts, 4))) return ATTN_ERR_INVALID;
+  if (!std::isfinite(scale) || scale <= 0.0f || window < -1 || (mask_mode & ~ATTN_MASK_CAUSAL)) return ATTN_ERR_INVALID;
+  if (!workspace || !aligned(workspace, 256) || (lse && !aligned(lse, 4))) return ATTN_ERR_INVALID;
+  const int st = check_ragged(n_seqs, T_q, T_k, h_q, h_kv, d);
+  if (st != ATTN_OK) return st;
+  if (bad_packed(q, T_q, h_q, d, q_stride, q_head_stride) || bad_packed(k, T_k, h_kv, d, k_stride, k_head_stride) ||
+      bad_packed(v, T_k, h_kv, d, v_stride, v_head_stride) || bad_packed(out, T_q, h_q, d, out_stride, out_head_stride))
+    return ATTN_ERR_INVALID;
+  if (workspace_bytes < attn::packed_fwd_workspace_bytes(T_q, n_seqs, h_q, h_kv, d)) return ATTN_ERR_INVALID;
+  attn::PFN_encodeTiled enc = tensor_map_encoder();
+  if (!enc) return ATTN_ERR_CUDA;
+  // no two positions are further apart than two arrays are long
+  const int w = window < (1 << 29) ? window : (1 << 29);
+  attn::PackedArgs a{q, k, v, out, lse, q_stride, q_head_stride, k_stride, k_head_stride, v_stride, v_head_stride,
+                     out_stride, out_head_stride, q_starts, k_starts, n_seqs, T_q, T_k, h_q, h_kv, d, scale,
+                     (mask_mode & ATTN_MASK_CAUSAL) != 0, w, 0, static_cast<cudaStream_t>(stream)};
+  return attn::launch_attn_packed(a, enc, workspace);
+}
+
+size_t attn_paged_chunk_workspace_size(int T, int n_seqs, int h_q, int h_kv, int d) {
+  if (check_ragged(n_seqs, T, 1, h_q, h_kv, d) != ATTN_OK) return 0;
+  return attn::paged_chunk_workspace_bytes(T, n_seqs, h_q, h_kv, d);
+}
+
+int attn_paged_chunk(const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,
+                     const int32_t* q_starts, const int32_t* page_table, const int32_t* cache_lens, int n_seqs, int T,
+                     int h_q, int h_kv, int d, int n_pages, int page_size, int max_pages, float scale, int window,
+                     int sinks, const float* k_scale, const float* v_scale, int flags, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4))) return ATTN_ERR_INVALID;
+  if (!q_starts || !cache_lens || !aligned(q_starts, 4) || !aligned(cache_lens, 4)) return ATTN_ERR_INVALID;
+  if (!std::isfinite(scale) || scale <= 0.0f || window < -1 || sinks < 0 || (flags & ~ATTN_CACHE_E4M3))
+    return ATTN_ERR_INVALID;
+  if (!workspace || !aligned(workspace, 256)) return ATTN_ERR_INVALID;
+  if (bad_cache(k_pages, v_pages, n_pages, page_size, max_pages, h_kv, page_table)) return ATTN_ERR_INVALID;
+  const bool e4m3 = (flags & ATTN_CACHE_E4M3) != 0;
+  if ((k_scale != nullptr) != e4m3 || (v_scale != nullptr) != e4m3) return ATTN_ERR_INVALID;
+  if (e4m3 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))) return ATTN_ERR_INVALID;
+  const int st = check_ragged(n_seqs, T, 1, h_q, h_kv, d);
+  if (st != ATTN_OK) return st;
+  if (workspace_bytes < attn::paged_chunk_workspace_bytes(T, n_seqs, h_q, h_kv, d)) return ATTN_ERR_INVALID;
+  attn::PFN_encodeTiled enc = tensor_map_encoder();
+  if (!enc) return ATTN_ERR_CUDA;
+  const int w = window < (1 << 30) ? window : (1 << 30);  // no sequence is longer
+  const long long row = (long long)h_q * d;
+  attn::PackedArgs a{q, k_pages, v_pages, out, lse, row, d, 0, 0, 0, 0, row, d, q_starts, nullptr, n_seqs, T, 0,
+                     h_q, h_kv, d, scale, 1, w, sinks, static_cast<cudaStream_t>(stream),
+                     page_table, cache_lens, n_pages, page_size, max_pages, k_scale, v_scale};
+  return attn::launch_attn_packed(a, enc, workspace);
+}
+
 int attn_fault_status(void* stream, int clear, uint32_t* fault_code) {
-  uint32_t w = 0, wb = 0, wl = 0, ww = 0;
+  uint32_t w = 0, wb = 0, wl = 0, ww = 0, wp = 0;
   const int st = attn::read_fault_word(static_cast<cudaStream_t>(stream), clear, &w);
   if (st == ATTN_ERR_CUDA || attn::read_bwd_fault_word(clear, &wb) != ATTN_OK ||
-      attn::read_linear_fault_word(clear, &wl) != ATTN_OK || attn::read_weights_fault_word(clear, &ww) != ATTN_OK)
+      attn::read_linear_fault_word(clear, &wl) != ATTN_OK || attn::read_weights_fault_word(clear, &ww) != ATTN_OK ||
+      attn::read_packed_fault_word(clear, &wp) != ATTN_OK)
     return ATTN_ERR_CUDA;
-  w |= wb | wl | ww;
+  w |= wb | wl | ww | wp;
   if (fault_code) *fault_code = w;
   return w ? ATTN_ERR_TIMEOUT : ATTN_OK;
 }

@@ -205,6 +205,29 @@ struct PagedArgs {
   cudaStream_t stream;
 };
 
+// Validated arguments of one attn_packed_fwd or attn_paged_chunk call. Strides: elements between
+// tokens (ts) and heads (hs).
+struct PackedArgs {
+  const void* q;
+  const void* k;  // pages, with a page table
+  const void* v;
+  void* out;
+  float* lse;
+  long long q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, out_ts, out_hs;
+  const int32_t* q_starts;
+  const int32_t* k_starts;  // nullptr: as the queries'
+  int B, T_q, T_k, h_q, h_kv, d;
+  float scale;
+  int causal, window, sinks;  // window -1: none
+  cudaStream_t stream;
+  // pages
+  const int32_t* page_table = nullptr;
+  const int32_t* cache_lens = nullptr;
+  int n_pages = 0, page_size = 0, max_pages = 0;
+  const float* k_scale = nullptr;  // 8-bit pages
+  const float* v_scale = nullptr;
+};
+
 int launch_attn_tc(const TcArgs& a, PFN_encodeTiled enc);   // attn_fwd_tc.cu
 int launch_attn_f32(const F32Args& a);                       // attn_fwd_f32.cu
 int read_fault_word(cudaStream_t stream, int clear, uint32_t* out);  // attn_fwd_tc.cu
@@ -231,6 +254,10 @@ int launch_attn_norm_rope_bwd(const RopeBwdArgs& a, void* workspace);    // attn
 int launch_attn_paged_append(const AppendArgs& a);                       // attn_rope.cu
 size_t paged_decode_workspace_bytes(int n_q, int group, int d);          // attn_paged.cu
 int launch_attn_paged_decode(const PagedArgs& a, void* workspace);       // attn_paged.cu
+size_t packed_fwd_workspace_bytes(int T_q, int B, int h_q, int h_kv, int d);   // attn_packed.cu
+size_t paged_chunk_workspace_bytes(int T_q, int B, int h_q, int h_kv, int d);  // attn_packed.cu
+int launch_attn_packed(const PackedArgs& a, PFN_encodeTiled enc, void* workspace);  // attn_packed.cu
+int read_packed_fault_word(int clear, uint32_t* out);                    // attn_packed.cu
 size_t mha_workspace_bytes(int B, int n_q, int n_k, int H, int d);         // attn_mha.cu
 int launch_attn_mha(const MhaArgs& a, PFN_encodeTiled enc, void* workspace);  // attn_mha.cu
 // Host-operand pipelines (attn_host.cu, attn_bwd_host.cu): chunks of the flattened

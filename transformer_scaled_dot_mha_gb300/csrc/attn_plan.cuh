@@ -1,0 +1,369 @@
+// attn_plan.cuh -- the work list of attention over ragged batches.
+//
+// The lengths of packed sequences live in device memory, so the host cannot say which CTA
+// does what. One CTA writes the list: an item is a block of own rows of one sequence (query
+// tokens, or keys), a unit is an item for one key/value head, and a unit's cost is the number
+// of tiles that it streams. Two ways to hand the units out:
+//   whole    heaviest first, dealt to the CTAs in snake order (0 .. G-1, G-1 .. 0, ..); no unit
+//            is cut. Taken when there are many units for every CTA.
+//   cut      the units' tiles one after the other, in equal shares of consecutive tiles, so a
+//            CTA's first and last units may be pieces, whose partial results a second kernel
+//            joins. Taken when the units are few for every CTA, or one of them is longer than
+//            a CTA's even share.
+// Everything about a unit is in its entry, so a CTA needs one load to know its work.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace attn {
+namespace plan {
+
+constexpr int TILE = 128;      // streamed keys per tile, own rows per tile
+constexpr int THREADS = 1024;  // of the planning CTA
+constexpr int SMEM_SEQS = 4095;
+constexpr int BINS = 512;
+
+struct Entry {        // 64 bytes
+  int own_row;        // first own row (token or key) in the packed array
+  int own_n;          // own tokens or keys of the block
+  int str_row;        // first row of the sequence's streamed side (paged: the sequence)
+  int str_len;        // its rows (keys; or query tokens where keys are the own rows)
+  int pos;            // queries own: position of the first own token; keys own: index of the first own key
+  int off;            // keys minus queries of the sequence: position of its first query
+  int n_first, skip;  // list entry j is tile j, from n_first on tile j + skip
+  int j0, n;          // this unit's list entries [j0, j0 + n)
+  int lo0, hi0;       // of these, those that own tile 0 needs, counted from j0
+  int lo1, hi1;       // and own tile 1
+  int slot;           // place of the partial result, or -1: the unit is whole
+  int hk;             // key/value head
+};
+static_assert(sizeof(Entry) == 64, "read as four 16-byte words");
+
+struct Join {  // 32 bytes: a unit that was cut
+  int own_row, own_n, hk;
+  int slot;      // of the first piece
+  int next;      // of the second; the further ones two apart
+  int pieces;
+  int pad[2];
+};
+
+struct Header {
+  int cut;      // 1: CTA a takes entries [range[a].x, range[a].y); 0: snake order over n_units
+  int n_units;
+  int n_join;
+  int pad;
+};
+
+struct Args {
+  const int32_t* q_starts;
+  const int32_t* k_starts;    // null: as the queries'
+  const int32_t* cache_lens;  // paged: keys per sequence (then k_starts is null)
+  int B, T_q, T_k, max_keys;  // max_keys: paged, the page table's reach
+  int own_keys;               // 1: own rows are keys (tiles of TILE), streamed rows query tokens
+  int own_tiles;              // own tiles per unit: 1, or 2 (queries own)
+  int tok;                    // query tokens per tile of rows
+  int h_kv, causal, window, sinks;  // window -1: none
+  int ctas;                   // CTAs of the kernel that works the list off
+  int min_share;              // least tiles of a CTA's share when units are cut
+  int max_deal;               // units per CTA from which on they are dealt whole
+  int may_cut;
+  Header* head;
+  int2* range;   // [ctas]
+  Join* joins;   // [ctas]
+  int* first;    // [B + 1]: items before each sequence
+  Entry* list;   // [items * h_kv + ctas]
+};
+
+// Bytes of the plan part of a workspace; items: an upper bound.
+inline size_t bytes(long long items, int h_kv, int B, int ctas) {
+  const size_t lists = ((size_t)items * h_kv + ctas) * sizeof(Entry) + (size_t)ctas * (sizeof(Join) + sizeof(int2));
+  return (sizeof(Header) + lists + ((size_t)B + 1) * sizeof(int) + 255) & ~size_t(255);
+}
+
+inline void place(Args& a, void* base, long long items) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  a.head = reinterpret_cast<Header*>(p);
+  p += sizeof(Header);
+  a.list = reinterpret_cast<Entry*>(p);
+  p += ((size_t)items * a.h_kv + a.ctas) * sizeof(Entry);
+  a.joins = reinterpret_cast<Join*>(p);
+  p += (size_t)a.ctas * sizeof(Join);
+  a.range = reinterpret_cast<int2*>(p);
+  p += (size_t)a.ctas * sizeof(int2);
+  a.first = reinterpret_cast<int*>(p);
+}
+
+struct Seq {
+  int q0, n_q, k0, n_k;  // n_k: keys
+};
+
+// Offsets that decrease or leave the array give empty or shortened sequences, never rows outside it.
+__device__ __forceinline__ Seq sequence(const Args& a, int b) {
+  Seq s;
+  s.q0 = min(max(a.q_starts[b], 0), a.T_q);
+  s.n_q = max(min(a.q_starts[b + 1], a.T_q) - s.q0, 0);
+  if (a.cache_lens) {
+    s.k0 = b;
+    s.n_k = min(max(a.cache_lens[b], 0), a.max_keys);
+  } else if (a.k_starts) {
+    s.k0 = min(max(a.k_starts[b], 0), a.T_k);
+    s.n_k = max(min(a.k_starts[b + 1], a.T_k) - s.k0, 0);
+  } else {
+    s.k0 = min(s.q0, a.T_k);
+    s.n_k = min(s.n_q, a.T_k - s.k0);
+  }
+  return s;
+}
+
+__device__ __forceinline__ int blocks_of(const Args& a, const Seq& s) {
+  const int rows = a.own_keys ? s.n_k : s.n_q, per = a.own_keys ? TILE : a.tok * a.own_tiles;
+  return rows / per + (rows % per != 0);
+}
+
+// Keys [lo, hi) that some query at positions [p0, p1] may use, in tiles, and the tiles of the first
+// keys before them; empty: hi <= lo.
+__device__ __forceinline__ void key_tiles(const Args& a, int n_k, int p0, int p1, int& first, int& lo, int& hi) {
+  int top = n_k, bottom = 0;
+  if (a.causal) top = min(top, p1 + 1);
+  if (a.window >= 0) {
+    if (!a.causal) top = min(top, p1 + a.window + 1);
+    bottom = max(0, p0 - a.window);
+  }
+  first = lo = hi = 0;
+  if (top <= 0) return;
+  bottom = min(bottom, top);
+  lo = bottom / TILE;
+  hi = (top + TILE - 1) / TILE;
+  if (a.window >= 0) first = min((min(a.sinks, top) + TILE - 1) / TILE, lo);
+}
+
+// Block `own` of a sequence: everything but the head, the piece and its slot.
+__device__ __forceinline__ Entry item(const Args& a, const Seq& s, int own) {
+  Entry e;
+  e.off = s.n_k - s.n_q;
+  e.j0 = 0;
+  e.slot = -1;
+  e.hk = 0;
+  e.lo1 = e.hi1 = 0;
+  if (a.own_keys) {
+    const int key = own * TILE, n = min(TILE, s.n_k - key);
+    e.own_row = s.k0 + key;
+    e.own_n = n;
+    e.str_row = s.q0;
+    e.str_len = s.n_q;
+    e.pos = key;
+    // query tokens [t0, t1) that may use one of the keys
+    int t0 = a.causal ? key - e.off : 0, t1 = s.n_q;
+    if (a.window >= 0) {
+      if (!a.causal) t0 = key - a.window - e.off;
+      t1 = min(t1, key + n + a.window - e.off);
+    }
+    t0 = max(t0, 0);
+    const bool none = t1 <= t0;
+    e.n_first = 0;
+    e.skip = none ? 0 : t0 / a.tok;
+    e.n = none ? 0 : (t1 + a.tok - 1) / a.tok - e.skip;
+    e.lo0 = 0;
+    e.hi0 = e.n;
+    return e;
+  }
+  const int t0 = own * a.tok * a.own_tiles, n = min(a.tok * a.own_tiles, s.n_q - t0);
+  e.own_row = s.q0 + t0;
+  e.own_n = n;
+  e.str_row = s.k0;
+  e.str_len = s.n_k;
+  e.pos = e.off + t0;
+  int first, lo, hi;
+  key_tiles(a, s.n_k, e.pos, e.pos + n - 1, first, lo, hi);
+  e.n_first = first;
+  e.skip = lo - first;
+  e.n = first + hi - lo;
+  e.lo0 = 0;
+  e.hi0 = e.n;
+  if (a.own_tiles == 2) {
+    // each tile of rows: its own end of the list, and without first keys its own start
+    const int n0 = min(n, a.tok);
+    int f, l, h;
+    key_tiles(a, s.n_k, e.pos, e.pos + n0 - 1, f, l, h);
+    e.hi0 = h > l || f > 0 ? e.n - (hi - h) : 0;
+    if (n > a.tok) {
+      key_tiles(a, s.n_k, e.pos + a.tok, e.pos + n - 1, f, l, h);
+      e.lo1 = f > 0 || first > 0 ? 0 : l - lo;
+      e.hi1 = e.n;
+    }
+  }
+  return e;
+}
+
+__device__ __forceinline__ void put(Entry* to, const Entry& e) {
+  int4* d = reinterpret_cast<int4*>(to);
+  d[0] = make_int4(e.own_row, e.own_n, e.str_row, e.str_len);
+  d[1] = make_int4(e.pos, e.off, e.n_first, e.skip);
+  d[2] = make_int4(e.j0, e.n, e.lo0, e.hi0);
+  d[3] = make_int4(e.lo1, e.hi1, e.slot, e.hk);
+}
+
+// Sum of v over the threads before this one, and over all of them.
+__device__ __forceinline__ long long scan(long long v, long long* warps, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // `warps` may still be read from the call before
+  if (lane == 31) warps[warp] = x;
+  __syncthreads();
+  long long w = lane < THREADS / 32 ? warps[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  return x - v + (warp ? before : 0);
+}
+
+// One CTA of THREADS threads.
+static __global__ void __launch_bounds__(THREADS, 1) attn_plan_kernel(const Args a) {
+  __shared__ long long warps[THREADS / 32];
+  __shared__ int s_first[SMEM_SEQS + 1];
+  __shared__ int s_bin[BINS];
+  __shared__ int s_max, s_joins;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int t = threadIdx.x;
+  if (t == 0) {
+    s_max = 0;
+    s_joins = 0;
+  }
+  if (t < BINS) s_bin[t] = 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // items before each sequence
+  int* first = a.B <= SMEM_SEQS ? s_first : a.first;
+  long long items = 0;
+  for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+    const int b = b0 + t;
+    const int mine = b < a.B ? blocks_of(a, sequence(a, b)) : 0;
+    long long total;
+    const long long at = scan(mine, warps, total);
+    if (b < a.B) first[b] = (int)(items + at);
+    items += total;
+  }
+  if (t == 0) first[a.B] = (int)items;
+  __syncthreads();
+  const int N = (int)items;
+  auto find = [&](int i) -> Entry {  // item i: the last sequence that starts at or before it and has items
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= i) lo = mid;
+      else hi = mid - 1;
+    }
+    return item(a, sequence(a, lo), i - first[lo]);
+  };
+  // costs: their sum over the items, and the largest
+  long long sum = 0;
+  int top = 0;
+  for (int i = t; i < N; i += THREADS) {
+    const int n = max(find(i).n, 1);
+    sum += n;
+    top = max(top, n);
+  }
+  long long total;
+  scan(sum, warps, total);
+  atomicMax(&s_max, top);
+  __syncthreads();
+  top = s_max;
+  const long long units = (long long)N * a.h_kv, work = total * a.h_kv;
+  const long long share = max((work + a.ctas - 1) / a.ctas, (long long)a.min_share);
+  const bool cut = a.may_cut && (units <= (long long)a.max_deal * a.ctas || top > share);
+  if (t == 0) {
+    a.head->cut = cut;
+    a.head->n_units = (int)units;
+  }
+  if (cut) {
+    for (int i = t; i < a.ctas; i += THREADS) a.range[i] = make_int2(0, 0);
+    __syncthreads();
+    long long base = 0;  // cost of the items before this round's
+    for (int i0 = 0; i0 < N; i0 += THREADS) {
+      const int i = i0 + t;
+      Entry e;
+      int cost = 0;
+      if (i < N) {
+        e = find(i);
+        cost = max(e.n, 1);
+      }
+      long long round;
+      const long long at = base + scan(cost, warps, round);
+      base += round;
+      if (i >= N) continue;
+      const int n = e.n;
+      const int lo0 = e.lo0, hi0 = e.hi0, lo1 = e.lo1, hi1 = e.hi1;
+      for (int hk = 0; hk < a.h_kv; ++hk) {
+        const long long w0 = at * a.h_kv + (long long)hk * cost, w1 = w0 + cost;
+        const int u = i * a.h_kv + hk;
+        const int c0 = (int)(w0 / share), c1 = (int)((w1 - 1) / share);
+        e.hk = hk;
+        for (int c = c0; c <= c1; ++c) {
+          // entry u + c: units and CTAs both only go up along the tiles, so it is this piece's alone
+          const long long r0 = c * share, r1 = r0 + share;
+          const int j0 = (int)(max(r0, w0) - w0), j1 = (int)(min(r1, w1) - w0);
+          e.j0 = j0;
+          e.n = n == 0 ? 0 : j1 - j0;
+          auto clip = [&](int x) { return min(max(x - j0, 0), e.n); };
+          e.lo0 = clip(lo0);
+          e.hi0 = clip(hi0);
+          e.lo1 = clip(lo1);
+          e.hi1 = clip(hi1);
+          e.slot = c0 == c1 ? -1 : (r0 >= w0 ? 2 * c : 2 * c + 1);
+          put(a.list + u + c, e);
+          if (r0 >= w0) a.range[c].x = u + c;               // the CTA's share starts here
+          if (r1 <= w1 || w1 == work) a.range[c].y = u + c + 1;  // and ends here
+        }
+        if (c0 != c1) {
+          Join& j = a.joins[atomicAdd(&s_joins, 1)];
+          j.own_row = e.own_row;
+          j.own_n = e.own_n;
+          j.hk = hk;
+          j.slot = (long long)c0 * share >= w0 ? 2 * c0 : 2 * c0 + 1;
+          j.next = 2 * (c0 + 1);
+          j.pieces = c1 - c0 + 1;
+        }
+      }
+    }
+    __syncthreads();
+    if (t == 0) a.head->n_join = s_joins;
+    return;
+  }
+  if (t == 0) a.head->n_join = 0;
+  // heaviest first: a counting sort by cost (the order within a bin does not matter to any result)
+  auto bin_of = [&](int n) { return (int)((long long)(top - max(n, 1)) * (BINS - 1) / max(top, 1)); };
+  for (int i = t; i < N; i += THREADS) atomicAdd(&s_bin[bin_of(find(i).n)], 1);
+  __syncthreads();
+  long long all;
+  const long long at = scan(t < BINS ? s_bin[t] : 0, warps, all);
+  __syncthreads();
+  if (t < BINS) s_bin[t] = (int)at;
+  __syncthreads();
+  for (int i = t; i < N; i += THREADS) {
+    Entry e = find(i);
+    Entry* to = a.list + (size_t)atomicAdd(&s_bin[bin_of(e.n)], 1) * a.h_kv;
+    for (int hk = 0; hk < a.h_kv; ++hk) {
+      e.hk = hk;
+      put(to + hk, e);
+    }
+  }
+}
+
+// Index in the list of CTA `cta`'s k-th unit, or -1.
+__device__ __forceinline__ int unit_of(const Header& h, int2 range, int cta, int ctas, int k) {
+  if (h.cut) return range.x + k < range.y ? range.x + k : -1;
+  const long long at = (long long)k * ctas + ((k & 1) ? ctas - 1 - cta : cta);
+  return at < h.n_units ? (int)at : -1;
+}
+
+}  // namespace plan
+}  // namespace attn
