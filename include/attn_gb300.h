@@ -558,6 +558,34 @@ int attn_packed_fwd(const void* q, const void* k, const void* v, void* out, floa
                     int mask_mode, int window, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * attn_packed_bwd_workspace_size -- bytes of device workspace attn_packed_bwd needs: its work
+ * lists, two floats per query row, and partial results of fixed size. Returns 0 for an invalid
+ * or unsupported shape.
+ */
+size_t attn_packed_bwd_workspace_size(int T_q, int T_k, int n_seqs, int h_q, int h_kv, int d);
+
+/*
+ * attn_packed_bwd -- gradients of attn_packed_fwd, with the definitions of attn_bwd; the
+ * gradients of a key/value head are the sums over the query heads that share it.
+ *   q, k, v, q_starts .. window: as in the forward call; out and lse are what it returned
+ *   dout, dq  bf16 [T_q, h_q, d], dk, dv  bf16 [T_k, h_kv, d]
+ *   strides  HOST array of 16: token stride and head stride of q, k, v, out, dout, dq, dk, dv, with
+ *           the forward's rules. The gradients must not overlap one another or the inputs
+ *           (slices of one array are fine).
+ *   workspace: as in attn_packed_fwd, of at least attn_packed_bwd_workspace_size(...) bytes
+ * Written for every row of every sequence: a key that no query may see gets dk = dv = 0, a query
+ * with no legal key dq = 0. Rows of no sequence are not used and left as they were. What other
+ * sequences' rows hold, infinities and NaN included, does not reach a sequence.
+ * Supported: as attn_packed_fwd. Numerics as attn_bwd: fp32 accumulation on the tensor cores, P and dS
+ * rounded to bf16, results rounded to bf16 once; no atomics: the same bits on every run. Three or
+ * four launches on `stream`.
+ */
+int attn_packed_bwd(const void* q, const void* k, const void* v, const void* out, const void* dout, const float* lse,
+                    void* dq, void* dk, void* dv, const int64_t* strides, const int32_t* q_starts,
+                    const int32_t* k_starts, int n_seqs, int T_q, int T_k, int h_q, int h_kv, int d, float scale,
+                    int mask_mode, int window, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * attn_paged_chunk_workspace_size -- bytes of device workspace attn_paged_chunk needs, for
  * either cache type. Returns 0 for an invalid or unsupported shape.
  */
@@ -603,7 +631,8 @@ int attn_paged_chunk(const void* q, const void* k_pages, const void* v_pages, vo
  * issuer, bit 2 softmax, bit 3 epilogue (attn_fwd), bit 4 decode copy (attn_decode),
  * bit 5 gradient kernels (attn_bwd), bit 6 attn_fwd found its shared memory not
  * 1024-byte aligned (it then writes nothing), bit 7 projection kernel (attn_linear,
- * attn_mha_fwd), bit 8 attn_weights, bit 9 attn_packed_fwd and attn_paged_chunk.
+ * attn_mha_fwd), bit 8 attn_weights, bit 9 attn_packed_fwd and attn_paged_chunk,
+ * bit 10 attn_packed_bwd.
  */
 int attn_fault_status(void* stream, int clear, uint32_t* fault_code);
 

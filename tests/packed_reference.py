@@ -83,6 +83,72 @@ def chunk(q, q_at, k_pages, v_pages, table, lens, scale, window=-1, sinks=0, k_s
     return out, lse, qb, lb
 
 
+def attend_bwd(q, k, v, out, lse, dout, scale, legal):
+    """One sequence's dq, dk, dv from the definition (P from lse, D from out), each with its qbound.
+
+    P, dS and the results are rounded to bf16: independent roundings of root mean square at most 2^-9,
+    so a sum of products of theirs moves by 2^-9 sqrt(sum of squared terms), the result by 2^-9 of itself.
+    Scores and dP are d products summed in fp32 (relative d 2^-23 of the terms' sizes); exp2, its argument
+    and the differences dP - D: 2^-16 of |dP| + |D| (D from bf16 rows in fp32: d 2^-23 of its terms).
+    """
+    n_q, h_q, d = q.shape
+    n_k, h_kv, _ = k.shape
+    group = h_q // h_kv
+    f64 = dict(dtype=torch.float64, device=q.device)
+    dq, qq = torch.zeros(n_q, h_q, d, **f64), torch.zeros(n_q, h_q, d, **f64)
+    dk, qk, dv, qv = (torch.zeros(n_k, h_kv, d, **f64) for _ in range(4))
+    some, used = legal.any(1), legal.any(0)
+    if n_k == 0 or not some.any():
+        return dq, dk, dv, qq, qk, qv
+    legal = legal[some][:, used]
+    u2 = (U_BF16 / 2) ** 2
+    small_k, small_v = torch.zeros_like(qk), torch.zeros_like(qv)
+    for h in range(h_q):
+        z = h // group
+        x, g, o = (t[some, h].double() for t in (q, dout, out))
+        kk, vv = k[used, z].double(), v[used, z].double()
+        p = (scale * (x @ kk.T) - lse[some, h].double()[:, None]).exp().masked_fill(~legal, 0)
+        dp, dd = g @ vv.T, (g * o).sum(-1, keepdim=True)
+        ds = p * (dp - dd)
+        # fp32 errors of P (relative) and of dS
+        es = 2 * scale * d * 2.0 ** -23 * (x.abs() @ kk.abs().T) + 2.0 ** -16
+        eds = ds.abs() * es + p * (d * 2.0 ** -22 * (g.abs() @ vv.abs().T + (g * o).abs().sum(-1, keepdim=True)))
+        dq[some, h] = scale * (ds @ kk)
+        dv[used, z] += p.T @ g
+        dk[used, z] += scale * (ds.T @ x)
+        qq[some, h] = scale ** 2 * u2 * (ds ** 2 @ kk ** 2) + (scale * (eds @ kk.abs())) ** 2
+        qv[used, z] += u2 * ((p ** 2).T @ g ** 2)
+        qk[used, z] += scale ** 2 * u2 * ((ds ** 2).T @ x ** 2)
+        small_v[used, z] += (p * es).T @ g.abs()
+        small_k[used, z] += scale * (eds.T @ x.abs())
+    return (dq, dk, dv, (qq + u2 * dq ** 2).sqrt(), (qk + small_k ** 2 + u2 * dk ** 2).sqrt(),
+            (qv + small_v ** 2 + u2 * dv ** 2).sqrt())
+
+
+def packed_bwd(q, k, v, out, lse, dout, q_at, k_at, scale, causal, window=-1):
+    """-> dq, dk, dv and their qbounds over all rows; rows of no sequence hold 7."""
+    got = [torch.full(x.shape, 7.0, dtype=torch.float64, device=q.device) for x in (q, k, v)]
+    bounds = [torch.zeros_like(x) for x in got]
+    for b in range(len(q_at) - 1):
+        r, s = slice(q_at[b], q_at[b + 1]), slice(k_at[b], k_at[b + 1])
+        legal = legal_pairs(r.stop - r.start, s.stop - s.start, causal, window, 0, q.device)
+        g = attend_bwd(q[r], k[s], v[s], out[r], lse[r], dout[r], scale, legal)
+        for x, to, rows in zip(g, got + bounds, (r, s, s, r, s, s)):
+            to[rows] = x
+    return got, bounds
+
+
+def check_grads(got, want, bounds):
+    """Per element 6 qbound, over a tensor 2 ||qbound||: where softmax leaves one key almost all the weight, one
+    rounding decides the norm, and it may be at its largest, 2^-8 of the term, twice the mean that
+    qbound counts. With e_ij the roundings of dS: ||sum_i e_ij q_i||^2 summed over j is sum_ij e_ij^2 |q_i|^2
+    plus products of independent roundings (zero in the mean), and e_ij^2 <= (2^-8 ds_ij)^2 = 4 (2^-9 ds_ij)^2."""
+    for name, x, y, qb in zip(("dq", "dk", "dv"), got, want, bounds):
+        err = (x.double() - y).abs()
+        assert torch.all(err <= 6 * qb + 1e-30), f"{name}: {(err / qb.clamp_min(1e-30)).max():.2f} of qbound"
+        assert err.norm() <= 2 * qb.norm() + 1e-30, f"{name}: {(err.norm() / qb.norm()):.2f} of the norm's bound"
+
+
 def check(got, lse, want, want_lse, qb, lb):
     """Per element 6 qbound, over the tensor ||qbound||; each lse within its bound; NaN where the formula is."""
     fin = torch.isfinite(want)

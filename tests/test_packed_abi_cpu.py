@@ -1,6 +1,8 @@
 """The entry points for packed sequences and chunks over a paged cache reject bad arguments with the
 documented status codes, without a GPU (argument validation returns before any CUDA call; the
 placeholder pointers are never read)."""
+import ctypes
+
 import pytest
 import torch
 
@@ -35,6 +37,43 @@ def test_packed_fwd_invalid_arguments(L, bad):
 def test_packed_fwd_unsupported_shapes(L):
     for bad in (dict(d=96), dict(d=256), dict(h_q=129, h_kv=1), dict(n_seqs=1 << 27, h_q=16, h_kv=8)):
         assert L.attn_packed_fwd(*dict(PACKED, **bad).values()) == attn.ATTN_ERR_UNSUPPORTED, bad
+
+
+BWD = dict(q=16, k=32, v=48, out=64, dout=80, lse=96, dq=112, dk=128, dv=144, strides=[512, 64] * 8, q_starts=160,
+           k_starts=None, n_seqs=3, T_q=40, T_k=40, h_q=4, h_kv=2, d=64, scale=0.125, mask_mode=1, window=-1, ws=256,
+           nbytes=BIG, stream=None)
+
+
+def bwd(L, **bad):
+    a = dict(BWD, **bad)
+    if a["strides"] is not None:
+        a["strides"] = (ctypes.c_int64 * 16)(*a["strides"])
+    return L.attn_packed_bwd(*a.values())
+
+
+@pytest.mark.parametrize("bad", [
+    *[{x: None} for x in ("q", "k", "v", "out", "dout", "lse", "dq", "dk", "dv", "strides", "q_starts", "ws")],
+    *[{x: 24} for x in ("q", "k", "v", "out", "dout", "dq", "dk", "dv", "ws")],
+    *[dict(strides=[512, 64] * i + [128, 64] + [512, 64] * (7 - i)) for i in (0, 3, 4, 5)],  # 4 heads in 128 columns
+    *[dict(strides=[512, 64] * i + [64, 64] + [512, 64] * (7 - i)) for i in (1, 2, 6, 7)],
+    dict(strides=[512, 60] + [512, 64] * 7), dict(lse=97), dict(q_starts=161), dict(k_starts=2), dict(n_seqs=0),
+    dict(T_q=0), dict(T_k=1 << 28), dict(h_q=3), dict(scale=0.0), dict(scale=float("nan")), dict(mask_mode=2),
+    dict(window=-5), dict(nbytes=1 << 20),
+])
+def test_packed_bwd_invalid_arguments(L, bad):
+    assert bwd(L, **bad) == attn.ATTN_ERR_INVALID
+
+
+def test_packed_bwd_unsupported_shapes(L):
+    for bad in (dict(d=96), dict(h_q=129, h_kv=1)):
+        assert bwd(L, **bad) == attn.ATTN_ERR_UNSUPPORTED, bad
+
+
+def test_packed_bwd_workspace_size():
+    size = attn.attn_packed_bwd_workspace_size
+    assert size(0, 1, 1, 1, 1, 64) == 0 and size(1, 0, 1, 1, 1, 64) == 0 and size(1, 1, 0, 1, 1, 64) == 0
+    assert size(1, 1, 1, 3, 2, 64) == 0 and size(1, 1, 1, 1, 1, 32) == 0
+    assert 0 < size(1, 1, 1, 8, 8, 128) < size(1 << 20, 1 << 20, 100, 8, 8, 128)
 
 
 def test_workspace_sizes(L):

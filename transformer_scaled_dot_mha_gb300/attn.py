@@ -95,6 +95,10 @@ def lib() -> ctypes.CDLL:
         L.attn_packed_fwd_workspace_size.restype = sz
         L.attn_packed_fwd.argtypes = [vp] * 5 + [i64] * 8 + [vp, vp] + [i] * 6 + [f, i, i, vp, sz, vp]
         L.attn_packed_fwd.restype = i
+        L.attn_packed_bwd_workspace_size.argtypes = [i, i, i, i, i, i]
+        L.attn_packed_bwd_workspace_size.restype = sz
+        L.attn_packed_bwd.argtypes = [vp] * 9 + [ctypes.POINTER(i64), vp, vp] + [i] * 6 + [f, i, i, vp, sz, vp]
+        L.attn_packed_bwd.restype = i
         L.attn_paged_chunk_workspace_size.argtypes = [i, i, i, i, i]
         L.attn_paged_chunk_workspace_size.restype = sz
         L.attn_paged_chunk.argtypes = [vp] * 8 + [i] * 8 + [f, i, i, vp, vp, i, vp, sz, vp]
@@ -745,6 +749,43 @@ def attn_packed_fwd(q, k, v, out, q_starts, workspace, k_starts=None, lse=None, 
     if st != ATTN_OK:
         raise AttnError(st, "attn_packed_fwd")
     return out
+
+
+def attn_packed_bwd_workspace_size(T_q, T_k, n_seqs, h_q, h_kv, d) -> int:
+    return int(lib().attn_packed_bwd_workspace_size(_int32(T_q), _int32(T_k), _int32(n_seqs), _int32(h_q), _int32(h_kv),
+                                                    _int32(d)))
+
+
+_SixteenStrides = ctypes.c_int64 * 16
+
+
+def attn_packed_bwd(q, k, v, out, dout, lse, dq, dk, dv, q_starts, workspace, k_starts=None, scale=None,
+                    mask_mode=MASK_NONE, window=-1, stream=None):
+    """Gradients of attn_packed_fwd into ``dq`` (shaped like ``q``), ``dk`` and ``dv`` (like ``k``, ``v``), given
+    ``dout`` and the forward's ``out`` and float32 ``lse``; views as there. ``workspace``: a CUDA tensor of
+    at least ``attn_packed_bwd_workspace_size`` bytes."""
+    dev = _device_of(q)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError(f"q must be [T_q, h_q, d], k [T_k, h_kv, d], got {list(q.shape)} {list(k.shape)}")
+    T_q, h_q, d = q_shape = q.shape
+    T_k, h_kv, _ = k.shape
+    k_shape = (T_k, h_kv, d)
+    ptrs, strides = [], []
+    for t, name, shape in ((q, "q", q_shape), (k, "k", k_shape), (v, "v", k_shape), (out, "out", q_shape),
+                           (dout, "dout", q_shape), (dq, "dq", q_shape), (dk, "dk", k_shape), (dv, "dv", k_shape)):
+        ptr, ts, hs = _need_heads(t, name, shape, dev)
+        ptrs.append(ptr)
+        strides += (ts, hs)
+    starts, n_seqs = _need_starts(q_starts, "q_starts", dev)
+    ws_ptr, ws_bytes = _need_workspace(workspace, dev)
+    st = lib().attn_packed_bwd(
+        *ptrs[:5], _need(lse, "lse", torch.float32, (T_q, h_q), dev), *ptrs[5:], _SixteenStrides(*strides), starts,
+        None if k_starts is None else _need(k_starts, "k_starts", torch.int32, (n_seqs + 1,), dev), _int32(n_seqs),
+        _int32(T_q), _int32(T_k), h_q, h_kv, d, 1.0 / math.sqrt(d) if scale is None else float(scale), int(mask_mode),
+        _int32(window), ws_ptr, ws_bytes, _raw_stream(stream, dev))
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_packed_bwd")
+    return dq, dk, dv
 
 
 def attn_paged_chunk_workspace_size(T, n_seqs, h_q, h_kv, d) -> int:

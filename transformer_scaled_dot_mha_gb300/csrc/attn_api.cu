@@ -490,6 +490,38 @@ int attn_packed_fwd(const void* q, const void* k, const void* v, void* out, floa
   return attn::launch_attn_packed(a, enc, workspace);
 }
 
+size_t attn_packed_bwd_workspace_size(int T_q, int T_k, int n_seqs, int h_q, int h_kv, int d) {
+  if (check_ragged(n_seqs, T_q, T_k, h_q, h_kv, d) != ATTN_OK) return 0;
+  return attn::packed_bwd_workspace_bytes(T_q, T_k, n_seqs, h_q, h_kv, d);
+}
+
+int attn_packed_bwd(const void* q, const void* k, const void* v, const void* out, const void* dout, const float* lse,
+                    void* dq, void* dk, void* dv, const int64_t* strides, const int32_t* q_starts,
+                    const int32_t* k_starts, int n_seqs, int T_q, int T_k, int h_q, int h_kv, int d, float scale,
+                    int mask_mode, int window, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!strides || !q_starts || !aligned(q_starts, 4) || (k_starts && !aligned(k_starts, 4))) return ATTN_ERR_INVALID;
+  if (!std::isfinite(scale) || scale <= 0.0f || window < -1 || (mask_mode & ~ATTN_MASK_CAUSAL)) return ATTN_ERR_INVALID;
+  if (!workspace || !aligned(workspace, 256) || !lse || !aligned(lse, 4)) return ATTN_ERR_INVALID;
+  const int st = check_ragged(n_seqs, T_q, T_k, h_q, h_kv, d);
+  if (st != ATTN_OK) return st;
+  const void* ptrs[8] = {q, k, v, out, dout, dq, dk, dv};
+  int64_t ts[8], hs[8];
+  for (int i = 0; i < 8; ++i) {
+    const bool keys = i == 1 || i == 2 || i >= 6;
+    ts[i] = strides[2 * i];
+    hs[i] = strides[2 * i + 1];
+    if (bad_packed(ptrs[i], keys ? T_k : T_q, keys ? h_kv : h_q, d, ts[i], hs[i])) return ATTN_ERR_INVALID;
+  }
+  if (workspace_bytes < attn::packed_bwd_workspace_bytes(T_q, T_k, n_seqs, h_q, h_kv, d)) return ATTN_ERR_INVALID;
+  attn::PFN_encodeTiled enc = tensor_map_encoder();
+  if (!enc) return ATTN_ERR_CUDA;
+  const int w = window < (1 << 29) ? window : (1 << 29);  // as in attn_packed_fwd
+  attn::PackedBwdArgs a{q, k, v, out, dout, lse, dq, dk, dv, ts[0], hs[0], ts[1], hs[1], ts[2], hs[2], ts[3], hs[3],
+                        ts[4], hs[4], ts[5], hs[5], ts[6], hs[6], ts[7], hs[7], q_starts, k_starts, n_seqs, T_q, T_k,
+                        h_q, h_kv, d, scale, (mask_mode & ATTN_MASK_CAUSAL) != 0, w, static_cast<cudaStream_t>(stream)};
+  return attn::launch_attn_packed_bwd(a, enc, workspace);
+}
+
 size_t attn_paged_chunk_workspace_size(int T, int n_seqs, int h_q, int h_kv, int d) {
   if (check_ragged(n_seqs, T, 1, h_q, h_kv, d) != ATTN_OK) return 0;
   return attn::paged_chunk_workspace_bytes(T, n_seqs, h_q, h_kv, d);
@@ -523,13 +555,13 @@ int attn_paged_chunk(const void* q, const void* k_pages, const void* v_pages, vo
 }
 
 int attn_fault_status(void* stream, int clear, uint32_t* fault_code) {
-  uint32_t w = 0, wb = 0, wl = 0, ww = 0, wp = 0;
+  uint32_t w = 0, wb = 0, wl = 0, ww = 0, wp = 0, wg = 0;
   const int st = attn::read_fault_word(static_cast<cudaStream_t>(stream), clear, &w);
   if (st == ATTN_ERR_CUDA || attn::read_bwd_fault_word(clear, &wb) != ATTN_OK ||
       attn::read_linear_fault_word(clear, &wl) != ATTN_OK || attn::read_weights_fault_word(clear, &ww) != ATTN_OK ||
-      attn::read_packed_fault_word(clear, &wp) != ATTN_OK)
+      attn::read_packed_fault_word(clear, &wp) != ATTN_OK || attn::read_packed_bwd_fault_word(clear, &wg) != ATTN_OK)
     return ATTN_ERR_CUDA;
-  w |= wb | wl | ww | wp;
+  w |= wb | wl | ww | wp | wg;
   if (fault_code) *fault_code = w;
   return w ? ATTN_ERR_TIMEOUT : ATTN_OK;
 }

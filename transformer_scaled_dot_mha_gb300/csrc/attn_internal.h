@@ -228,6 +228,26 @@ struct PackedArgs {
   const float* v_scale = nullptr;
 };
 
+// Validated arguments of one attn_packed_bwd call.
+struct PackedBwdArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* out;
+  const void* dout;
+  const float* lse;
+  void* dq;
+  void* dk;
+  void* dv;
+  long long q_ts, q_hs, k_ts, k_hs, v_ts, v_hs, out_ts, out_hs, dout_ts, dout_hs, dq_ts, dq_hs, dk_ts, dk_hs, dv_ts, dv_hs;
+  const int32_t* q_starts;
+  const int32_t* k_starts;  // nullptr: as the queries'
+  int B, T_q, T_k, h_q, h_kv, d;
+  float scale;
+  int causal, window;  // window -1: none
+  cudaStream_t stream;
+};
+
 int launch_attn_tc(const TcArgs& a, PFN_encodeTiled enc);   // attn_fwd_tc.cu
 int launch_attn_f32(const F32Args& a);                       // attn_fwd_f32.cu
 int read_fault_word(cudaStream_t stream, int clear, uint32_t* out);  // attn_fwd_tc.cu
@@ -258,6 +278,9 @@ size_t packed_fwd_workspace_bytes(int T_q, int B, int h_q, int h_kv, int d);   /
 size_t paged_chunk_workspace_bytes(int T_q, int B, int h_q, int h_kv, int d);  // attn_packed.cu
 int launch_attn_packed(const PackedArgs& a, PFN_encodeTiled enc, void* workspace);  // attn_packed.cu
 int read_packed_fault_word(int clear, uint32_t* out);                    // attn_packed.cu
+size_t packed_bwd_workspace_bytes(int T_q, int T_k, int B, int h_q, int h_kv, int d);      // attn_packed_bwd.cu
+int launch_attn_packed_bwd(const PackedBwdArgs& a, PFN_encodeTiled enc, void* workspace);  // attn_packed_bwd.cu
+int read_packed_bwd_fault_word(int clear, uint32_t* out);                // attn_packed_bwd.cu
 size_t mha_workspace_bytes(int B, int n_q, int n_k, int H, int d);         // attn_mha.cu
 int launch_attn_mha(const MhaArgs& a, PFN_encodeTiled enc, void* workspace);  // attn_mha.cu
 // Host-operand pipelines (attn_host.cu, attn_bwd_host.cu): chunks of the flattened

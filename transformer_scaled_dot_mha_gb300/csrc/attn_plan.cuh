@@ -227,13 +227,19 @@ __device__ __forceinline__ long long scan(long long v, long long* warps, long lo
   return x - v + (warp ? before : 0);
 }
 
-// One CTA of THREADS threads.
-static __global__ void __launch_bounds__(THREADS, 1) attn_plan_kernel(const Args a) {
-  __shared__ long long warps[THREADS / 32];
-  __shared__ int s_first[SMEM_SEQS + 1];
-  __shared__ int s_bin[BINS];
-  __shared__ int s_max, s_joins;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+struct Scratch {  // shared memory
+  long long warps[THREADS / 32];
+  int first[SMEM_SEQS + 1];
+  int bin[BINS];
+  int max, joins;
+};
+
+// Writes the list: one CTA of THREADS threads.
+__device__ __forceinline__ void write(const Args& a, Scratch& sh) {
+  long long* warps = sh.warps;
+  int* s_first = sh.first;
+  int* s_bin = sh.bin;
+  int &s_max = sh.max, &s_joins = sh.joins;
   const int t = threadIdx.x;
   if (t == 0) {
     s_max = 0;
@@ -356,6 +362,12 @@ static __global__ void __launch_bounds__(THREADS, 1) attn_plan_kernel(const Args
       put(to + hk, e);
     }
   }
+}
+
+static __global__ void __launch_bounds__(THREADS, 1) attn_plan_kernel(const Args a) {
+  __shared__ Scratch scratch;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  write(a, scratch);
 }
 
 // Index in the list of CTA `cta`'s k-th unit, or -1.
