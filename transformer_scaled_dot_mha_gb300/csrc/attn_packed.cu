@@ -29,10 +29,11 @@
 //           page or a tile; a lane of the copy warp looks up the page of its boxes and issues
 //           them. Rows of no page (a bad entry, or behind the length) are boxes outside the
 //           tensor: zeros. Bad entries' keys are masked by bits that go with the tile.
-//   8 bits  the boxes land in a raw tile, and four more warps turn it into the bf16 tile that the
-//           products read: exact, as bf16 holds every e4m3 number (the scales are folded
-//           into the exponent's factor and the last division). Two row tiles at either d, so that
-//           a tile is converted once for 256 rows.
+//   8 bits  the boxes land in a raw tile, and four more warps turn it into the f16 tile that the
+//           products read: exact, as f16 holds every e4m3 number (the scales are folded into the
+//           exponent's factor and the last division). An MMA's operands are of one type, so Q
+//           becomes f16 too, each row times a power of two, and P is f16. Two row tiles at either
+//           d, so that a tile is converted once for 256 rows.
 // Values behind the sequence's end (the next sequence's rows, a page's stale rows) would meet
 // P = 0 in the product, and 0 times infinity or NaN is NaN: a spare warp zeroes them in shared
 // memory when the issuer of that product has seen the tile land and asks for it.
@@ -62,11 +63,18 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 200000000ull;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 constexpr uint32_t FAULT_PACKED = 512;
+constexpr int UNITS = 4;    // units whose entries a CTA holds at a time
 constexpr int FLAGS = 8;    // tiles whose page bits are held: more than the roles are apart
 constexpr int kMinShare = 2;   // tiles
-constexpr int kMaxDeal = 4;    // units per CTA from which on they are not cut
+constexpr int kMaxDeal = 2;    // units per CTA above which they are not cut
+constexpr float kBias = 7.0f;  // P in f16 is 2^7 times the weight
 
 enum { DENSE = 0, PAGED = 1, PAGED8 = 2 };
+
+// As ptx::idesc_bf16_f32, for f16 operands (format 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
 
 template <int D, int KIND>
 struct Cfg {
@@ -77,23 +85,21 @@ struct Cfg {
   static constexpr int CHUNKS = D / 64;
   static constexpr int CHUNK_BYTES = BM * 128;
   static constexpr int TILE_BYTES = BM * D * 2;
-  static constexpr int STAGES = SINGLE ? 3 : 2;
+  static constexpr int Q_BUFS = SINGLE ? 2 : 1;  // SINGLE: the next unit's Q is there when the last S is issued
+  static constexpr int SLOTS = SINGLE ? 5 : 4;   // K and V tiles in turn
   static constexpr int RAW_BYTES = KIND == PAGED8 ? BN * 128 : 0;  // 128-byte row pitch for single rows at d = 64
-  static constexpr int BATCH = SINGLE ? 8 : 16;  // units whose entries a CTA holds at a time
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = OFF_Q + Q_TILES * TILE_BYTES;
-  static constexpr int OFF_V = OFF_K + STAGES * TILE_BYTES;
-  static constexpr int OFF_RAW = OFF_V + STAGES * TILE_BYTES;  // [K, V]
-  static constexpr int OFF_UNITS = OFF_RAW + 2 * RAW_BYTES;    // Entry [BATCH]
-  static constexpr int OFF_FLAGS = OFF_UNITS + BATCH * 64;     // uint32 [FLAGS][8]: any, four words of key bits
+  static constexpr int OFF_KV = OFF_Q + Q_BUFS * Q_TILES * TILE_BYTES;
+  static constexpr int OFF_RAW = OFF_KV + SLOTS * TILE_BYTES;  // [K, V]
+  static constexpr int OFF_UNITS = OFF_RAW + 2 * RAW_BYTES;    // Entry [UNITS]
+  static constexpr int OFF_FLAGS = OFF_UNITS + UNITS * 64;     // uint32 [FLAGS][8]: any, four words of key bits
   static constexpr int OFF_BAR = OFF_FLAGS + (KIND == DENSE ? 0 : FLAGS * 32);
-  static constexpr int B_QFULL = 0;
-  static constexpr int B_QEMPTY = 1;
-  static constexpr int B_KFULL = 2;
-  static constexpr int B_KEMPTY = B_KFULL + STAGES;
-  static constexpr int B_VFULL = B_KEMPTY + STAGES;
-  static constexpr int B_VEMPTY = B_VFULL + STAGES;
-  static constexpr int B_SFULL = B_VEMPTY + STAGES;  // [2] S_t computed
+  static constexpr int B_QFULL = 0;                  // [Q_BUFS]
+  static constexpr int B_QEMPTY = B_QFULL + 2;       // [Q_BUFS]
+  static constexpr int B_QREADY = B_QEMPTY + 2;      // PAGED8: Q in f16
+  static constexpr int B_FULL = B_QREADY + 1;        // [SLOTS]
+  static constexpr int B_EMPTY = B_FULL + SLOTS;     // [SLOTS]
+  static constexpr int B_SFULL = B_EMPTY + SLOTS;    // [2] S_t computed
   static constexpr int B_SFREE = B_SFULL + 2;        // S loaded by the softmax (SINGLE)
   static constexpr int B_PFULL = B_SFREE + 1;        // [2] P_t stored
   static constexpr int B_ODONE = B_PFULL + 2;        // [2] PV_t completed
@@ -102,7 +108,9 @@ struct Cfg {
   static constexpr int B_RAWFULL = B_TAIL + 1;       // [K, V]
   static constexpr int B_RAWEMPTY = B_RAWFULL + 2;
   static constexpr int B_DRAIN = B_RAWEMPTY + 2;     // [2] MMAs after an abort, one per issuer
-  static constexpr int NUM_BARS = B_DRAIN + 2;
+  static constexpr int B_UNITFULL = B_DRAIN + 2;     // [UNITS]
+  static constexpr int B_UNITEMPTY = B_UNITFULL + UNITS;
+  static constexpr int NUM_BARS = B_UNITEMPTY + UNITS;
   static constexpr int OFF_SLOT = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_ABORT = OFF_SLOT + 4;
   static constexpr int SMEM_BYTES = OFF_ABORT + 4;
@@ -113,24 +121,39 @@ struct Cfg {
   static constexpr int WARP_LOAD = SOFTMAX_WARPS, WARP_MMA = SOFTMAX_WARPS + 1, WARP_TAIL = SOFTMAX_WARPS + 2,
                        WARP_PV = SOFTMAX_WARPS + 3, WARP_CVT = SOFTMAX_WARPS + 4;
   static constexpr int THREADS = 32 * (SOFTMAX_WARPS + 4 + (KIND == PAGED8 ? 4 : 0));
-  static constexpr int REGS_CONTROL = SINGLE || KIND == PAGED8 ? 40 : 72;
+  // readers of a unit's entry: softmax warps, MMA issuers, tail warp or converting warps
+  static constexpr int UNIT_READERS = SOFTMAX_WARPS + (SINGLE ? 2 : 1) + (KIND == PAGED8 ? 4 : 1);
+  static constexpr int REGS_CONTROL = SINGLE ? 48 : KIND == PAGED8 ? 56 : 80;
   static constexpr int REGS_CVT = 40;
-  static constexpr int REGS_SOFTMAX = 216;
+  static constexpr int REGS_SOFTMAX = 208;
   static constexpr int LAUNCH_REGS = (65536 / (THREADS * CTAS_PER_SM)) & ~7;
   static_assert(128 * REGS_CONTROL + (KIND == PAGED8 ? 128 * REGS_CVT : 0) + 32 * SOFTMAX_WARPS * REGS_SOFTMAX <=
                     THREADS * LAUNCH_REGS,
                 "register split");
   static constexpr uint32_t TMEM_P = SINGLE ? BN : 0;  // else P_t over S_t
   static constexpr uint32_t TMEM_O = SINGLE ? BN + BN / 2 : 2 * BN;
-  static constexpr uint32_t IDESC_S = ptx::idesc_bf16_f32(BM, BN, false);
-  static constexpr uint32_t IDESC_PV = ptx::idesc_bf16_f32(BM, D, true);
+  static constexpr uint32_t IDESC_S = KIND == PAGED8 ? idesc_f16_f32(BM, BN, false) : ptx::idesc_bf16_f32(BM, BN, false);
+  static constexpr uint32_t IDESC_PV = KIND == PAGED8 ? idesc_f16_f32(BM, D, true) : ptx::idesc_bf16_f32(BM, D, true);
   static_assert(TMEM_O + Q_TILES * D <= TMEM_COLS, "TMEM budget");
   static_assert(OFF_UNITS % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
   static_assert(CTAS_PER_SM * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory budget");
 };
 
+// A place in the ring of key and value tiles and the parity of its phase.
+template <int N>
+struct RingPos {
+  uint32_t s = 0, ph = 0;
+  __device__ __forceinline__ void step(uint32_t by) {
+    s += by;
+    if (s >= N) {
+      s -= N;
+      ph ^= 1;
+    }
+  }
+};
+
 struct Params {
-  const plan::Header* head;
+  plan::Header* head;
   const int2* range;
   const plan::Entry* list;
   uint16_t* out;
@@ -187,15 +210,22 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   return v;
 }
 
-// Two e4m3 numbers, in bits 15:8 and 31:24 of x (the other bits zero), as two bf16: the exponent and
-// mantissa fields moved to their places read 2^-120 times the value, subnormal ones included, and
-// the product with 2^120 is exact. 0x7f, NaN, would read 480: the caller looks for it.
+// Two e4m3 numbers, in bits 7:0 and 15:8 of x, as two f16: exact, NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3_pair(uint32_t x) {
-  const uint32_t y = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x7b807b80u));  // 2^120
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)x));
   return r;
 }
+
+// Two floats -> packed f16x2 (nearest even); `lo` lands in bits 15:0.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A word with its lowest n bits set; none for n <= 0, all from 32 on.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
 // The key tile of list entry j.
 __device__ __forceinline__ int tile_of(const plan::Entry& e, int j) {
@@ -209,14 +239,16 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
                        const __grid_constant__ CUtensorMap tm_v, const Params p) {
   using C = Cfg<D, KIND>;
   constexpr bool SINGLE = C::SINGLE;
-  constexpr int STAGES = C::STAGES;
+  constexpr bool RAW = KIND == PAGED8;
+  using Pos = RingPos<C::SLOTS>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((ptx::smem_u32(smem) & 1023u) != 0) {
     if (threadIdx.x == 0) atomicOr(&g_packed_fault_word, FAULT_PACKED);
     return;
   }
   const uint32_t s_base = ptx::smem_u32(smem);
-  const uint32_t s_q = s_base + C::OFF_Q, s_k = s_base + C::OFF_K, s_v = s_base + C::OFF_V;
+  auto s_q = [&](uint32_t b) -> uint32_t { return s_base + C::OFF_Q + b * (C::Q_TILES * C::TILE_BYTES); };
+  auto s_kv = [&](uint32_t slot) -> uint32_t { return s_base + C::OFF_KV + slot * C::TILE_BYTES; };
   auto bar = [&](int i) -> uint32_t { return s_base + C::OFF_BAR + 8u * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_ABORT);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
@@ -225,13 +257,14 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    ptx::mbar_init(bar(C::B_QFULL), 1);
-    ptx::mbar_init(bar(C::B_QEMPTY), 1);
-    for (int s = 0; s < STAGES; ++s) {
-      ptx::mbar_init(bar(C::B_KFULL + s), KIND == PAGED8 ? 4 : 1);  // converting warps, or the copies' bytes
-      ptx::mbar_init(bar(C::B_KEMPTY + s), 1);
-      ptx::mbar_init(bar(C::B_VFULL + s), KIND == PAGED8 ? 4 : 1);
-      ptx::mbar_init(bar(C::B_VEMPTY + s), 1);
+    for (int b = 0; b < C::Q_BUFS; ++b) {
+      ptx::mbar_init(bar(C::B_QFULL + b), 1);
+      ptx::mbar_init(bar(C::B_QEMPTY + b), 1);
+    }
+    ptx::mbar_init(bar(C::B_QREADY), 2 * BM);
+    for (int s = 0; s < C::SLOTS; ++s) {
+      ptx::mbar_init(bar(C::B_FULL + s), RAW ? 4 : 1);  // converting warps, or the copies' bytes
+      ptx::mbar_init(bar(C::B_EMPTY + s), 1);
     }
     for (int t = 0; t < 2; ++t) {
       // pages: the issuer arrives besides its commit, so that the page bits, written before the
@@ -246,6 +279,10 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
     ptx::mbar_init(bar(C::B_SFREE), BM);
     ptx::mbar_init(bar(C::B_TAILREQ), 1);
     ptx::mbar_init(bar(C::B_TAIL), 1);
+    for (int u = 0; u < UNITS; ++u) {
+      ptx::mbar_init(bar(C::B_UNITFULL + u), 1);
+      ptx::mbar_init(bar(C::B_UNITEMPTY + u), C::UNIT_READERS);
+    }
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -265,242 +302,268 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
   ptx::grid_dep_wait();  // the plan is written
   ptx::grid_dep_launch();
 
-  const plan::Header head = *p.head;
-  const int2 range = p.range[blockIdx.x];
-
-  // The entries of this CTA's next units, up to BATCH, into shared memory; their number. Every warp
-  // calls it, from its role's own loop (the register split forbids one loop around the roles).
-  auto next_batch = [&](int batch) -> int {
-    __syncwarp();  // the barrier counts whole warps
-    ptx::named_bar_sync(1, C::THREADS);  // every role is through with the batch before
-    if (*abort_flag) return 0;
-    int n_b = 0;
-    while (n_b < C::BATCH && plan::unit_of(head, range, blockIdx.x, gridDim.x, batch * C::BATCH + n_b) >= 0) ++n_b;
-    for (int x = threadIdx.x; x < n_b * 4; x += C::THREADS) {
-      const int u = plan::unit_of(head, range, blockIdx.x, gridDim.x, batch * C::BATCH + (x >> 2));
-      reinterpret_cast<int4*>(smem + C::OFF_UNITS)[x] = reinterpret_cast<const int4*>(p.list + u)[x & 3];
-    }
-    __syncwarp();
-    ptx::named_bar_sync(1, C::THREADS);
-    return n_b;
-  };
-
-  // Counters that run through all units, each kept by the roles that need it.
-  uint32_t ring = 0;   // key tiles so far
-  uint32_t tails = 0;  // tails zeroed so far: asked for and answered one at a time
+  // The copy warp passes the units' entries on through a ring of UNITS places; every other warp
+  // runs through them in that order, each at its own pace. n < 0: no more units.
+  auto unit_wait = [&](uint32_t un) -> bool { return wait_bar(bar(C::B_UNITFULL + un % UNITS), (un / UNITS) & 1, abort_flag, SINGLE); };
+  auto unit_done = [&](uint32_t un) { ptx::mbar_arrive(bar(C::B_UNITEMPTY + un % UNITS)); };
   bool ok = true;
 
   if (warp < C::SOFTMAX_WARPS) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
-      // ================================================================ softmax
-      const int t = warp >> 2;               // row tile
-      const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
-      const int rt = r / p.group;            // its token
-      const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t t_s = tmem + lane_off + t * BN;
-      const uint32_t t_p = tmem + lane_off + C::TMEM_P + t * BN;
-      const uint32_t t_o = tmem + lane_off + C::TMEM_O + t * D;
-      uint32_t cnt0 = 0;  // key tiles of this row tile so far
-      for (int batch = 0, n_b; (n_b = next_batch(batch)) > 0; ++batch) {
-      for (int b = 0; b < n_b && ok; ++b) {
-        // the entry is read from shared memory where it is used: the score tile and P leave no
-        // registers to hold it
-        const plan::Entry& e = units[b];
-        const int lo = t ? e.lo1 : e.lo0, n_tiles = (t ? e.hi1 : e.hi0) - lo;
-        const float c = KIND == PAGED8 ? p.scale_log2 * p.k_scale[e.hk] : p.scale_log2;
-        float m_ref = -INFINITY;  // reference maximum, log2 units
-        float l = 0.0f;           // sum of 2^(c s - m_ref)
-        for (int j = 0; j < n_tiles; ++j) {
-          const uint32_t cnt = cnt0 + j;
-          ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_SFULL + t), cnt & 1, abort_flag));
+    // ================================================================ softmax
+    const int t = warp >> 2;               // row tile
+    const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
+    const int rt = r / p.group;            // its token
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lane_off + t * BN;
+    const uint32_t t_p = tmem + lane_off + C::TMEM_P + t * BN;
+    const uint32_t t_o = tmem + lane_off + C::TMEM_O + t * D;
+    uint32_t cnt0 = 0;   // key tiles of this row tile so far
+    uint32_t tiles = 0;  // key tiles of the units so far (pages: their bits' place)
+    uint32_t n_q = 0;    // units with keys so far
+    for (uint32_t un = 0;; ++un) {
+      ok = __all_sync(0xffffffffu, unit_wait(un));
+      if (!ok) break;
+      // the entry is read from shared memory where it is used: the score tile and P leave no
+      // registers to hold it
+      const plan::Entry& e = units[un % UNITS];
+      if (e.n < 0) break;
+      const int lo = t ? e.lo1 : e.lo0, n_tiles = (t ? e.hi1 : e.hi0) - lo;
+      float c = p.scale_log2;
+      if constexpr (RAW) {
+        c *= p.k_scale[e.hk];
+        if (e.n > 0) {
+          // this row of Q as f16, times the power of two that brings its largest entry to 2^14:
+          // bf16's eight bits fit, and entries below 2^-28 of the largest are rounded to 2^-39 of it
+          ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_QFULL), n_q & 1, abort_flag));
           if (!ok) break;
-          ptx::tc_fence_after();
-          uint32_t sr[4][32];
+          if (t * p.tok < e.own_n) {
+            const uint32_t row = s_q(0) + t * C::TILE_BYTES + r * 128;
+            float top = 0.0f;
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) ptx::tmem_ld32(t_s + q4 * 32, sr[q4]);
-          ptx::tmem_wait_ld();
-          if constexpr (KIND != DENSE) {
-            volatile const uint32_t* fl = flags + ((ring + lo + j) % FLAGS) * 8;
-            if (fl[0]) {  // keys of pages that are not there
+            for (int u = 0; u < D / 8; ++u) {
+              const uint4 w = ld_shared_v4(row + (u >> 3) * C::CHUNK_BYTES + (((u & 7) ^ (r & 7)) << 4));
+              const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-              for (int q4 = 0; q4 < 4; ++q4) {
-                const uint32_t bad = fl[1 + q4];
-#pragma unroll
-                for (int x = 0; x < 32; ++x)
-                  if ((bad >> x) & 1u) sr[q4][x] = __float_as_uint(-INFINITY);
-              }
+              for (int i = 0; i < 4; ++i)
+                top = ptx::max3(top, fabsf(__uint_as_float(in[i] << 16)), fabsf(__uint_as_float(in[i] & 0xffff0000u)));
             }
-          }
-          if constexpr (SINGLE) {  // S is in registers, the page bits are read
-            ptx::tc_fence_before();
-            ptx::mbar_arrive_after(bar(C::B_SFREE), __uint_as_float(sr[3][31]));
-          }
-          const int key0 = tile_of(e, lo + j) * BN;
-          const int pos_lo = e.pos + t * p.tok;
-          const bool edge =
-              key0 + BN > e.str_len || (p.causal && key0 + BN - 1 > pos_lo) ||
-              (p.window >= 0 && (key0 < pos_lo + min(e.own_n - t * p.tok, p.tok) - 1 - p.window ||
-                                 (!p.causal && key0 + BN - 1 > pos_lo + p.window)));
-          if (edge) {
-            const int pos = pos_lo + rt;
-            int lim = e.str_len - key0;  // columns [first, lim) are legal, and those below `sink`
-            if (p.causal) lim = min(lim, pos + 1 - key0);
-            int first = 0, sink = 0;
-            if (p.window >= 0) {
-              if (!p.causal) lim = min(lim, pos + p.window + 1 - key0);
-              first = pos - p.window - key0;
-              sink = p.sinks - key0;
-            }
-            if (first <= 0) sink = BN;
+            // exponents of two normal numbers; zero, subnormal, infinite rows stay as they are
+            const int field = (int)(__float_as_uint(top) >> 23);
+            const int up = field == 0 || field >= 255 ? 0 : min(max(127 + 14 - field, -126), 126);
+            const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
+            c *= __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4)
+            for (int u = 0; u < D / 8; ++u) {
+              const uint32_t at = row + (u >> 3) * C::CHUNK_BYTES + (((u & 7) ^ (r & 7)) << 4);
+              const uint4 w = ld_shared_v4(at);
+              const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+              uint32_t o[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                o[i] = pack_f16x2(__uint_as_float(in[i] << 16) * mul, __uint_as_float(in[i] & 0xffff0000u) * mul);
+              ptx::st_shared_v4(at, o[0], o[1], o[2], o[3]);
+            }
+            ptx::fence_proxy_async_smem();
+          }
+          ptx::mbar_arrive(bar(C::B_QREADY));
+          ++n_q;
+        }
+      }
+      float m_ref = -INFINITY;  // reference maximum, log2 units
+      float l = 0.0f;           // sum of 2^(c s - m_ref + kBias)
+      for (int j = 0; j < n_tiles; ++j) {
+        const uint32_t cnt = cnt0 + j;
+        ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_SFULL + t), cnt & 1, abort_flag));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        uint32_t sr[4][32];
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) ptx::tmem_ld32(t_s + q4 * 32, sr[q4]);
+        ptx::tmem_wait_ld();
+        if constexpr (KIND != DENSE) {
+          volatile const uint32_t* fl = flags + ((tiles + lo + j) % FLAGS) * 8;
+          if (fl[0]) {  // keys of pages that are not there
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              const uint32_t bad = fl[1 + q4];
 #pragma unroll
               for (int x = 0; x < 32; ++x)
-                if (q4 * 32 + x >= lim || (q4 * 32 + x < first && q4 * 32 + x >= sink))
-                  sr[q4][x] = __float_as_uint(-INFINITY);
+                if ((bad >> x) & 1u) sr[q4][x] = __float_as_uint(-INFINITY);
+            }
           }
-          uint32_t pk[2][32];
-          auto col = [&](int a, int x) { return __uint_as_float(sr[a >> 1][(a & 1) * 16 + x]); };
-          // row maximum: eight independent chains of three-way maxima
-          auto row_max = [&]() -> float {
-            float mc[8];
-#pragma unroll
-            for (int a = 0; a < 8; ++a) {
-              mc[a] = fmaxf(col(a, 0), col(a, 1));
-#pragma unroll
-              for (int x = 2; x < 16; x += 2) mc[a] = ptx::max3(mc[a], col(a, x), col(a, x + 1));
-            }
-            return ptx::max3(ptx::max3(mc[0], mc[1], mc[2]), ptx::max3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7])) * c;
-          };
-          // P, rounded to bf16 for the tensor cores (the row sum takes it unrounded): each weight moves
-          // by at most 2^-9 of itself, independently, less than the output's own rounding in the mean
-          auto exps = [&](float m_now) -> float {
-            const float m_use = (m_now == -INFINITY) ? 0.0f : m_now;
-            const uint64_t c2 = ptx::f2_pack(c, c);
-            const uint64_t negm2 = ptx::f2_pack(-m_use, -m_use);
-            uint64_t part[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4)
-#pragma unroll
-              for (int x = 0; x < 32; x += 2) {
-                const uint64_t sx = ptx::f2_pack(__uint_as_float(sr[q4][x]), __uint_as_float(sr[q4][x + 1]));
-                float a0, a1;
-                ptx::f2_unpack(ptx::f2_fma(sx, c2, negm2), a0, a1);
-                const float p0 = ptx::ex2(a0), p1 = ptx::ex2(a1);
-                part[q4] = ptx::f2_add(part[q4], ptx::f2_pack(p0, p1));
-                pk[q4 >> 1][(q4 & 1) * 16 + (x >> 1)] = ptx::pack_bf16x2(p0, p1);
-              }
-            float l0, l1;
-            ptx::f2_unpack(ptx::f2_add(ptx::f2_add(part[0], part[1]), ptx::f2_add(part[2], part[3])), l0, l1);
-            return l0 + l1;
-          };
-          bool pv_done = j == 0;  // the PV before this tile is known to be complete
-          // O, holding the PVs so far, to the reference that the rows which grew now have
-          auto rescale = [&](float alpha) -> bool {
-            if (!__all_sync(0xffffffffu, wait_bar(bar(C::B_ODONE + t), (cnt - 1) & 1, abort_flag))) return false;
-            pv_done = true;
-            ptx::tc_fence_after();
-#pragma unroll
-            for (int q4 = 0; q4 < D / 32; ++q4) {
-              uint32_t o[32];
-              ptx::tmem_ld32(t_o + q4 * 32, o);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-              ptx::tmem_st32(t_o + q4 * 32, o);
-            }
-            return true;
-          };
-          if constexpr (SINGLE) {
-            // after the first tile, exponentials against the current reference, before the tile's
-            // maximum is known: a sum of at most 2^7 shows that no score exceeds the reference by
-            // the threshold; only a larger one (or NaN, or a reference still at -inf) needs the maximum
-            if (j == 0) {
-              m_ref = row_max();
-              l = exps(m_ref);
-            } else {
-              float l_tile = exps(m_ref);
-              float m_tile = m_ref;
-              bool grow = false;
-              if (__any_sync(0xffffffffu, !(l_tile <= 128.0f) || m_ref == -INFINITY)) {
-                m_tile = row_max();
-                grow = m_tile > m_ref + kRescaleThreshold;
-              }
-              if (__any_sync(0xffffffffu, grow)) {
-                float alpha = 1.0f;
-                if (grow) {
-                  alpha = ptx::ex2(m_ref - m_tile);
-                  l *= alpha;
-                  m_ref = m_tile;
-                }
-                if (!(ok = rescale(alpha))) break;
-                l_tile = exps(m_ref);
-              }
-              l += l_tile;
-            }
-          } else {
-            const float m_tile = row_max();
-            const bool grow = m_tile > m_ref + kRescaleThreshold;
-            float alpha = 1.0f;
-            if (grow) {
-              alpha = ptx::ex2(m_ref - m_tile);  // 0 when m_ref is still -inf
-              l *= alpha;
-              m_ref = m_tile;
-            }
-            if (j > 0 && __any_sync(0xffffffffu, grow) && !(ok = rescale(alpha))) break;
-            l += exps(m_ref);
-          }
-          if (SINGLE && !pv_done) {
-            // P is still the A operand of the PV before until that completes
-            ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_ODONE + t), (cnt - 1) & 1, abort_flag));
-            if (!ok) break;
-            ptx::tc_fence_after();
-          }
-          ptx::tmem_st32(t_p, pk[0]);
-          ptx::tmem_st32(t_p + 32, pk[1]);
-          ptx::tmem_wait_st();
+        }
+        if constexpr (SINGLE) {  // S is in registers, the page bits are read
           ptx::tc_fence_before();
-          ptx::mbar_arrive(bar(C::B_PFULL + t));
+          ptx::mbar_arrive_after(bar(C::B_SFREE), __uint_as_float(sr[3][31]));
         }
-        if (!ok) break;
-
-        // ---------------------------------------------------------------- this unit's rows
-        const bool row_valid = rt < min(e.own_n - t * p.tok, p.tok);
-        if (n_tiles > 0) {
-          ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_ODONE + t), (cnt0 + n_tiles - 1) & 1, abort_flag));
-          if (!ok) break;
+        const int key0 = tile_of(e, lo + j) * BN;
+        const int pos_lo = e.pos + t * p.tok;
+        const bool edge =
+            key0 + BN > e.str_len || (p.causal && key0 + BN - 1 > pos_lo) ||
+            (p.window >= 0 && (key0 < pos_lo + min(e.own_n - t * p.tok, p.tok) - 1 - p.window ||
+                               (!p.causal && key0 + BN - 1 > pos_lo + p.window)));
+        if (edge) {
+          const int pos = pos_lo + rt;
+          int lim = e.str_len - key0;  // columns [first, lim) are legal, and those below `sink`
+          if (p.causal) lim = min(lim, pos + 1 - key0);
+          int first = 0, sink = 0;
+          if (p.window >= 0) {
+            if (!p.causal) lim = min(lim, pos + p.window + 1 - key0);
+            first = pos - p.window - key0;
+            sink = p.sinks - key0;
+          }
+          // as bits, a word for 32 columns
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            const uint32_t legal = bits_below(lim - q4 * 32) & (~bits_below(first - q4 * 32) | bits_below(sink - q4 * 32));
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!((legal >> x) & 1u)) sr[q4][x] = __float_as_uint(-INFINITY);
+          }
+        }
+        uint32_t pk[2][32];
+        auto col = [&](int a, int x) { return __uint_as_float(sr[a >> 1][(a & 1) * 16 + x]); };
+        // row maximum: eight independent chains of three-way maxima
+        auto row_max = [&]() -> float {
+          float mc[8];
+#pragma unroll
+          for (int a = 0; a < 8; ++a) {
+            mc[a] = fmaxf(col(a, 0), col(a, 1));
+#pragma unroll
+            for (int x = 2; x < 16; x += 2) mc[a] = ptx::max3(mc[a], col(a, x), col(a, x + 1));
+          }
+          return ptx::max3(ptx::max3(mc[0], mc[1], mc[2]), ptx::max3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7])) * c;
+        };
+        // P, rounded for the tensor cores (the row sum takes it unrounded). bf16: each weight moves by at
+        // most 2^-8 of itself, independently, less than the output's own rounding in the mean. f16, with
+        // 8-bit pages: 2^-11, and P is 2^7 times the weight, so that 2^-32 of the largest still counts
+        auto exps = [&](float m_now) -> float {
+          const float m_use = ((m_now == -INFINITY) ? 0.0f : m_now) - (RAW ? kBias : 0.0f);
+          const uint64_t c2 = ptx::f2_pack(c, c);
+          const uint64_t negm2 = ptx::f2_pack(-m_use, -m_use);
+          uint64_t part[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4)
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              const uint64_t sx = ptx::f2_pack(__uint_as_float(sr[q4][x]), __uint_as_float(sr[q4][x + 1]));
+              float a0, a1;
+              ptx::f2_unpack(ptx::f2_fma(sx, c2, negm2), a0, a1);
+              const float p0 = ptx::ex2(a0), p1 = ptx::ex2(a1);
+              part[q4] = ptx::f2_add(part[q4], ptx::f2_pack(p0, p1));
+              pk[q4 >> 1][(q4 & 1) * 16 + (x >> 1)] = RAW ? pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1);
+            }
+          float l0, l1;
+          ptx::f2_unpack(ptx::f2_add(ptx::f2_add(part[0], part[1]), ptx::f2_add(part[2], part[3])), l0, l1);
+          return l0 + l1;
+        };
+        bool pv_done = j == 0;  // the PV before this tile is known to be complete
+        // O, holding the PVs so far, to the reference that the rows which grew now have
+        auto rescale = [&](float alpha) -> bool {
+          if (!__all_sync(0xffffffffu, wait_bar(bar(C::B_ODONE + t), (cnt - 1) & 1, abort_flag))) return false;
+          pv_done = true;
           ptx::tc_fence_after();
-        }
-        cnt0 += n_tiles;
-        ring += e.n;
-        if (e.slot >= 0) {
-          // a piece: unnormalised sums, their reference, the row sum
-          float* part = p.part + (size_t)e.slot * (C::ROWS * (D + 2)) + (size_t)(t * BM + r) * D;
-          float* stat = p.part + (size_t)e.slot * (C::ROWS * (D + 2)) + (size_t)C::ROWS * D + t * BM + r;
 #pragma unroll
           for (int q4 = 0; q4 < D / 32; ++q4) {
             uint32_t o[32];
-            if (n_tiles > 0) {
-              ptx::tmem_ld32(t_o + q4 * 32, o);
-              ptx::tmem_wait_ld();
-            } else {
+            ptx::tmem_ld32(t_o + q4 * 32, o);
+            ptx::tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] = 0u;
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+            ptx::tmem_st32(t_o + q4 * 32, o);
+          }
+          return true;
+        };
+        if constexpr (SINGLE) {
+          // after the first tile, exponentials against the current reference, before the tile's
+          // maximum is known: a sum of at most 2^7 shows that no score exceeds the reference by
+          // the threshold; only a larger one (or NaN, or a reference still at -inf) needs the maximum
+          if (j == 0) {
+            m_ref = row_max();
+            l = exps(m_ref);
+          } else {
+            float l_tile = exps(m_ref);
+            float m_tile = m_ref;
+            bool grow = false;
+            if (__any_sync(0xffffffffu, !(l_tile <= 128.0f) || m_ref == -INFINITY)) {
+              m_tile = row_max();
+              grow = m_tile > m_ref + kRescaleThreshold;
             }
-            if (row_valid) {
+            if (__any_sync(0xffffffffu, grow)) {
+              float alpha = 1.0f;
+              if (grow) {
+                alpha = ptx::ex2(m_ref - m_tile);
+                l *= alpha;
+                m_ref = m_tile;
+              }
+              if (!(ok = rescale(alpha))) break;
+              l_tile = exps(m_ref);
+            }
+            l += l_tile;
+          }
+        } else {
+          const float m_tile = row_max();
+          const bool grow = m_tile > m_ref + kRescaleThreshold;
+          float alpha = 1.0f;
+          if (grow) {
+            alpha = ptx::ex2(m_ref - m_tile);  // 0 when m_ref is still -inf
+            l *= alpha;
+            m_ref = m_tile;
+          }
+          if (j > 0 && __any_sync(0xffffffffu, grow) && !(ok = rescale(alpha))) break;
+          l += exps(m_ref);
+        }
+        if (SINGLE && !pv_done) {
+          // P is still the A operand of the PV before until that completes
+          ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_ODONE + t), (cnt - 1) & 1, abort_flag));
+          if (!ok) break;
+          ptx::tc_fence_after();
+        }
+        ptx::tmem_st32(t_p, pk[0]);
+        ptx::tmem_st32(t_p + 32, pk[1]);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(C::B_PFULL + t));
+      }
+      if (!ok) break;
+
+      // ---------------------------------------------------------------- this unit's rows
+      const bool row_valid = rt < min(e.own_n - t * p.tok, p.tok);
+      if (n_tiles > 0) {
+        ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_ODONE + t), (cnt0 + n_tiles - 1) & 1, abort_flag));
+        if (!ok) break;
+        ptx::tc_fence_after();
+      }
+      cnt0 += n_tiles;
+      tiles += e.n;
+      if (e.slot >= 0) {
+        // a piece: unnormalised sums, their reference, the row sum
+        float* part = p.part + (size_t)e.slot * (C::ROWS * (D + 2)) + (size_t)(t * BM + r) * D;
+        float* stat = p.part + (size_t)e.slot * (C::ROWS * (D + 2)) + (size_t)C::ROWS * D + t * BM + r;
 #pragma unroll
-              for (int x = 0; x < 8; ++x)
-                reinterpret_cast<uint4*>(part + q4 * 32)[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-            }
-            __syncwarp();
+        for (int q4 = 0; q4 < D / 32; ++q4) {
+          uint32_t o[32];
+          if (n_tiles > 0) {
+            ptx::tmem_ld32(t_o + q4 * 32, o);
+            ptx::tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) o[x] = 0u;
           }
           if (row_valid) {
-            stat[0] = m_ref;
-            stat[C::ROWS] = l;
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              reinterpret_cast<uint4*>(part + q4 * 32)[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
           }
-          continue;
+          __syncwarp();
         }
-        const float v_mul = KIND == PAGED8 ? p.v_scale[e.hk] : 1.0f;
+        if (row_valid) {
+          stat[0] = m_ref - (RAW ? kBias : 0.0f);
+          stat[C::ROWS] = l;
+        }
+      } else {
+        const float v_mul = RAW ? p.v_scale[e.hk] : 1.0f;
         const float inv = l == 0.0f ? 0.0f : v_mul / l;  // no legal key: zeros
         const long long row = (long long)e.own_row + t * p.tok + rt;
         const int head_q = e.hk * p.group + r - rt * p.group;
@@ -528,240 +591,249 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         }
         if (row_valid && p.lse)
           p.lse[row * p.h_q + head_q] =
-              l == 0.0f ? -INFINITY : (m_ref + __log2f(l)) * 0.69314718055994530942f;
+              l == 0.0f ? -INFINITY : (m_ref - (RAW ? kBias : 0.0f) + __log2f(l)) * 0.69314718055994530942f;
       }
-      }
-  } else if (KIND == PAGED8 && warp >= C::WARP_CVT) {
+      __syncwarp();
+      if (lane == 0) unit_done(un);
+    }
+  } else if (RAW && warp >= C::WARP_CVT) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CVT));
-      // ================================================================ 8 bits to bf16
-      // Sixteen numbers per thread and step: D / 16 lanes a row. Rows behind the end become zero.
-      const int id = threadIdx.x - 32 * C::WARP_CVT;
-      constexpr int LPR = D / 16, STEP = 128 / LPR;  // lanes per row, rows per step
-      const uint32_t raw_pitch = p.box == 1 ? 128u : (uint32_t)D;
-      for (int batch = 0, n_b; (n_b = next_batch(batch)) > 0; ++batch) {
-      for (int b = 0; b < n_b && ok; ++b) {
-        const plan::Entry& e = units[b];
-        const int n = e.n, len = e.str_len;
-        for (int j = 0; j < n && ok; ++j, ++ring) {
-          const int s = ring % STAGES;
-          const int there = len - tile_of(e, j) * BN;
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_RAWFULL + kv), ring & 1, abort_flag, true) &&
-                                             wait_bar(bar((kv ? C::B_VEMPTY : C::B_KEMPTY) + s), ((ring / STAGES) & 1) ^ 1,
-                                                      abort_flag, true));
-            if (!ok) break;
-            const uint32_t src = s_base + C::OFF_RAW + kv * C::RAW_BYTES + (id / LPR) * raw_pitch + (id % LPR) * 16;
-            const uint32_t tile = (kv ? s_v : s_k) + s * C::TILE_BYTES;
-            const uint32_t slab = tile + ((id % LPR) >> 2) * C::CHUNK_BYTES;
-            const int unit = ((id % LPR) & 3) * 2;
-#pragma unroll 4
-            for (int r0 = 0; r0 < BN; r0 += STEP) {
-              const int r = r0 + id / LPR;
-              const uint4 w = ld_shared_v4(src + r0 * raw_pitch);
-              const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-              uint32_t o[8];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                o[2 * i] = e4m3_pair(__byte_perm(in[i], 0, 0x1404));
-                o[2 * i + 1] = e4m3_pair(__byte_perm(in[i], 0, 0x3424));
-                if ((((in[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0) {  // a NaN among the four
-#pragma unroll
-                  for (int y = 0; y < 4; ++y)
-                    if (((in[i] >> (8 * y)) & 0x7f) == 0x7f) o[2 * i + (y >> 1)] |= 0x7fffu << (16 * (y & 1));
-                }
-              }
-              if (r >= there) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = 0;
-              }
-              const uint32_t row = slab + r * 128;
-              ptx::st_shared_v4(row + ((unit ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-              ptx::st_shared_v4(row + (((unit + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
-            }
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              ptx::mbar_arrive(bar(C::B_RAWEMPTY + kv));
-              ptx::mbar_arrive(bar((kv ? C::B_VFULL : C::B_KFULL) + s));
-            }
-          }
+    // ================================================================ 8 bits to f16
+    // Sixteen numbers per thread and step: D / 16 lanes a row. Rows behind the end become zero.
+    const int id = threadIdx.x - 32 * C::WARP_CVT;
+    constexpr int LPR = D / 16, STEP = 128 / LPR;  // lanes per row, rows per step
+    const uint32_t raw_pitch = p.box == 1 ? 128u : (uint32_t)D;
+    const int unit = ((id % LPR) & 3) * 2;
+    uint32_t n_raw = 0;
+    Pos pos;
+    for (uint32_t un = 0;; ++un) {
+      ok = __all_sync(0xffffffffu, unit_wait(un));
+      if (!ok) break;
+      const plan::Entry& e = units[un % UNITS];
+      const int n = e.n, len = e.str_len;
+      if (n < 0) break;
+      for (int j = 0; j < n && ok; ++j, ++n_raw) {
+        const int there = len - tile_of(e, j) * BN;
+        for (int kv = 0; kv < 2; ++kv, pos.step(1)) {
+          ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_RAWFULL + kv), n_raw & 1, abort_flag, true) &&
+                                           wait_bar(bar(C::B_EMPTY + pos.s), pos.ph ^ 1, abort_flag, true));
           if (!ok) break;
+          const uint32_t src = s_base + C::OFF_RAW + kv * C::RAW_BYTES + (id / LPR) * raw_pitch + (id % LPR) * 16;
+          const uint32_t slab = s_kv(pos.s) + ((id % LPR) >> 2) * C::CHUNK_BYTES;
+#pragma unroll 4
+          for (int r0 = 0; r0 < BN; r0 += STEP) {
+            const int r = r0 + id / LPR;
+            uint4 w = ld_shared_v4(src + r0 * raw_pitch);
+            if (r >= there) w = make_uint4(0, 0, 0, 0);
+            const uint32_t row = slab + r * 128;
+            ptx::st_shared_v4(row + ((unit ^ (r & 7)) << 4), e4m3_pair(w.x), e4m3_pair(w.x >> 16), e4m3_pair(w.y),
+                              e4m3_pair(w.y >> 16));
+            ptx::st_shared_v4(row + (((unit + 1) ^ (r & 7)) << 4), e4m3_pair(w.z), e4m3_pair(w.z >> 16), e4m3_pair(w.w),
+                              e4m3_pair(w.w >> 16));
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            ptx::mbar_arrive(bar(C::B_RAWEMPTY + kv));
+            ptx::mbar_arrive(bar(C::B_FULL + pos.s));
+          }
+          __syncwarp();
         }
       }
-      }
+      if (!ok) break;
+      if (lane == 0) unit_done(un);
+      __syncwarp();
+    }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONTROL));
     if (warp == C::WARP_LOAD) {
-      // ================================================================ copies
+      // ================================================================ units and copies
       const uint64_t pol_q = ptx::policy_evict_first();
       const uint64_t pol_kv = ptx::policy_evict_last();
-      uint32_t n_q = 0;  // units with keys so far
-      for (int batch = 0, n_b; (n_b = next_batch(batch)) > 0; ++batch) {
-      for (int b = 0; b < n_b && ok; ++b) {
-        const plan::Entry& e = units[b];
-        const int n = e.n;
-        if (n == 0) continue;
-        ok = __all_sync(0xffffffffu,
-                        n_q == 0 || wait_bar(bar(C::B_QEMPTY), (n_q - 1) & 1, abort_flag, SINGLE));
-        if (!ok) break;
-        if (lane == 0) {
-          const int n_qt = e.own_n > p.tok ? 2 : 1;
-          const int bytes = p.tok * p.group * 128 * C::CHUNKS;
-          ptx::mbar_arrive_expect_tx(bar(C::B_QFULL), n_qt * bytes);
-          for (int t = 0; t < n_qt; ++t)
-            for (int c = 0; c < C::CHUNKS; ++c)
-              tma_load_4d(s_q + t * C::TILE_BYTES + c * C::CHUNK_BYTES, &tm_q, bar(C::B_QFULL), c * 64, 0,
-                          e.own_row + t * p.tok, e.hk, pol_q);
+      const plan::Header head = *p.head;
+      plan::Turn turn(head, p.range);
+      auto next_unit = [&]() -> int { return __shfl_sync(0xffffffffu, lane == 0 ? turn.next(p.head) : 0, 0); };
+      auto word_of = [&](int u) -> int { return u < 0 ? -1 : lane < 16 ? reinterpret_cast<const int*>(p.list + u)[lane] : 0; };
+      int word = word_of(next_unit());  // lane x: word x of the entry; all -1: no more units
+      uint32_t n_q = 0;   // units with keys so far
+      uint32_t n_kv = 0;  // tiles so far
+      Pos pos;
+      // pages cut into boxes of 4 rows or more: the page table is looked up for 32 boxes at a time, ahead
+      const int boxes = KIND == DENSE ? 1 : BN / p.box;
+      const bool ahead = boxes <= 32;
+      const int per = ahead ? 32 / boxes : 1;  // tiles per look-up
+      // box `lane % boxes` of list entry l of a unit; l at or behind `end`: none
+      struct Box {
+        int row, z;  // in the page; which page and head
+        bool bad;    // a key there, but no page
+      };
+      auto look = [&](int key, int seq, int len, int hk) -> Box {
+        Box b{0, p.n_pages * p.h_kv, false};  // outside the tensor: zeros
+        if (key < len) {
+          const int page = key / p.page_size;
+          const int id = p.page_table[(size_t)seq * p.max_pages + page];
+          b.bad = id < 0 || id >= p.n_pages;
+          if (!b.bad) {
+            b.row = key - page * p.page_size;
+            b.z = id * p.h_kv + hk;
+          }
         }
-        ++n_q;
-        for (int j = 0; j < n && ok; ++j) {
-          const uint32_t x = ring;
-          const int s = x % STAGES;
-          const uint32_t ph = (x / STAGES) & 1;
+        return b;
+      };
+      auto field = [&](int w, int x) { return __shfl_sync(0xffffffffu, w, x); };
+      auto look_ahead = [&](int w, int j) -> Box {  // boxes of tiles j .. j + per - 1 of the unit whose words are w
+        const int seq = field(w, 2), len = field(w, 3), n_first = field(w, 6), skip = field(w, 7), j0 = field(w, 8),
+                  n = field(w, 9), hk = field(w, 15);
+        const int at = j + lane / boxes, l = j0 + at;
+        if (at >= n) return Box{0, p.n_pages * p.h_kv, false};
+        return look((l + (l >= n_first ? skip : 0)) * BN + lane % boxes * p.box, seq, len, hk);
+      };
+      Box box{0, 0, false}, next_box{0, 0, false};
+      if (KIND != DENSE && ahead) box = look_ahead(word, 0);
+      for (uint32_t un = 0;; ++un) {
+        ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_UNITEMPTY + un % UNITS), ((un / UNITS) & 1) ^ 1, abort_flag, SINGLE));
+        if (!ok) break;
+        if (lane < 16) reinterpret_cast<int*>(smem + C::OFF_UNITS)[(un % UNITS) * 16 + lane] = word;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_UNITFULL + un % UNITS));
+        const int n = field(word, 9);
+        if (n < 0) break;
+        const int next_word = word_of(next_unit());
+        const plan::Entry& e = units[un % UNITS];  // stays: this warp alone replaces it
+        if (n > 0) {
+          const uint32_t qb = n_q % C::Q_BUFS;
+          ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_QEMPTY + qb), ((n_q / C::Q_BUFS) & 1) ^ 1, abort_flag, SINGLE));
+          if (!ok) break;
+          if (lane == 0) {
+            const int n_qt = e.own_n > p.tok ? 2 : 1;
+            ptx::mbar_arrive_expect_tx(bar(C::B_QFULL + qb), n_qt * p.tok * p.group * 128 * C::CHUNKS);
+            for (int t = 0; t < n_qt; ++t)
+              for (int c = 0; c < C::CHUNKS; ++c)
+                tma_load_4d(s_q(qb) + t * C::TILE_BYTES + c * C::CHUNK_BYTES, &tm_q, bar(C::B_QFULL + qb), c * 64, 0,
+                            e.own_row + t * p.tok, e.hk, pol_q);
+          }
+          ++n_q;
+        }
+        for (int j = 0; j < n && ok; ++j, ++n_kv) {
           const int key0 = tile_of(e, j) * BN;
           if constexpr (KIND == DENSE) {
-            ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_KEMPTY + s), ph ^ 1, abort_flag, SINGLE));
-            if (!ok) break;
-            if (lane == 0) {
-              ptx::mbar_arrive_expect_tx(bar(C::B_KFULL + s), C::TILE_BYTES);
-              for (int c = 0; c < C::CHUNKS; ++c)
-                ptx::tma_load_3d(s_k + s * C::TILE_BYTES + c * C::CHUNK_BYTES, &tm_k, bar(C::B_KFULL + s), c * 64,
-                                 e.str_row + key0, e.hk, pol_kv);
-            }
-            ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_VEMPTY + s), ph ^ 1, abort_flag, SINGLE));
-            if (!ok) {
-              // K of this tile is in flight, V is not
-              if (lane == 0) drain_wait(bar(C::B_KFULL + s), ph);
-              break;
-            }
-            if (lane == 0) {
-              ptx::mbar_arrive_expect_tx(bar(C::B_VFULL + s), C::TILE_BYTES);
-              for (int c = 0; c < C::CHUNKS; ++c)
-                ptx::tma_load_3d(s_v + s * C::TILE_BYTES + c * C::CHUNK_BYTES, &tm_v, bar(C::B_VFULL + s), c * 64,
-                                 e.str_row + key0, e.hk, pol_kv);
+            for (int kv = 0; kv < 2; ++kv) {
+              ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_EMPTY + pos.s), pos.ph ^ 1, abort_flag, SINGLE));
+              if (!ok) break;
+              if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(bar(C::B_FULL + pos.s), C::TILE_BYTES);
+                for (int c = 0; c < C::CHUNKS; ++c)
+                  ptx::tma_load_3d(s_kv(pos.s) + c * C::CHUNK_BYTES, kv ? &tm_v : &tm_k, bar(C::B_FULL + pos.s), c * 64,
+                                   e.str_row + key0, e.hk, pol_kv);
+              }
+              pos.step(1);
             }
           } else {
-            // boxes of p.box rows, lane by lane; a row behind the length or of a page that is
-            // not there comes from outside the tensor
-            constexpr bool RAW = KIND == PAGED8;
-            const int boxes = BN / p.box;
-            const int32_t* pages = p.page_table + (size_t)e.str_row * p.max_pages;
-            const uint32_t full_k = bar(RAW ? C::B_RAWFULL : C::B_KFULL + s), full_v = bar(RAW ? C::B_RAWFULL + 1 : C::B_VFULL + s);
-            const uint32_t empty_k = bar(RAW ? C::B_RAWEMPTY : C::B_KEMPTY + s),
-                           empty_v = bar(RAW ? C::B_RAWEMPTY + 1 : C::B_VEMPTY + s);
-            const uint32_t eph = RAW ? (x & 1) ^ 1 : ph ^ 1, fph = RAW ? x & 1 : ph;
-            const uint32_t bytes = RAW ? BN * D : C::TILE_BYTES;
-            const uint32_t pitch = RAW ? max(p.box * D, 128) : p.box * 128;
-            volatile uint32_t* fl = flags + (x % FLAGS) * 8;
-            auto lookup = [&](int i, int& row, int& z) -> bool {  // false: a key there whose page is bad
-              const int key = key0 + i * p.box;
-              z = p.n_pages * p.h_kv;
-              row = 0;
-              if (key >= e.str_len) return true;
-              const int page = key / p.page_size;
-              const int id = pages[page];
-              if (id < 0 || id >= p.n_pages) return false;
-              row = key - page * p.page_size;
-              z = id * p.h_kv + e.hk;
-              return true;
-            };
-            int row0, z0;  // this lane's first box, the only one unless pages are cut finer than 4 rows
-            const bool good = lane >= boxes || lookup(lane, row0, z0);
-            ok = __all_sync(0xffffffffu, wait_bar(empty_k, eph, abort_flag, SINGLE));
-            if (!ok) break;
-            bool bad = !good;
-            for (int i = lane + 32; i < boxes; i += 32) {
-              int row, z;
-              bad |= !lookup(i, row, z);
+            // this tile's boxes: lane i has box i
+            Box mine{0, 0, false};
+            if (ahead) {
+              const int k = j % per, from = k * boxes + lane % boxes;
+              mine.row = __shfl_sync(0xffffffffu, box.row, from);
+              mine.z = __shfl_sync(0xffffffffu, box.z, from);
+              mine.bad = __shfl_sync(0xffffffffu, (int)box.bad, from) != 0;
+              if (k == 0) next_box = j + per < n ? look_ahead(word, j + per) : look_ahead(next_word, 0);
+              if (k == per - 1 || j == n - 1) box = next_box;
             }
+            const uint32_t fph = RAW ? n_kv & 1 : pos.ph;
+            ok = __all_sync(0xffffffffu, wait_bar(bar(RAW ? (int)C::B_RAWEMPTY : C::B_EMPTY + (int)pos.s), fph ^ 1, abort_flag, SINGLE));
+            if (!ok) break;
+            volatile uint32_t* fl = flags + (n_kv % FLAGS) * 8;
+            bool bad = ahead && lane < boxes && mine.bad;
+            if (!ahead)
+              for (int i = lane; i < boxes; i += 32) bad |= look(key0 + i * p.box, e.str_row, e.str_len, e.hk).bad;
             const bool any = __any_sync(0xffffffffu, bad);
-            if (lane < 5) fl[lane] = lane == 0 ? (any ? 1u : 0u) : 0u;
+            if (lane < 5) fl[lane] = lane == 0 && any ? 1u : 0u;
             __syncwarp();
             if (any) {
               for (int i = lane; i < boxes; i += 32) {
-                int row, z;
-                if (lookup(i, row, z)) continue;
+                if (ahead ? !mine.bad : !look(key0 + i * p.box, e.str_row, e.str_len, e.hk).bad) continue;
                 for (int key = i * p.box; key < (i + 1) * p.box; ++key)
                   atomicOr(const_cast<uint32_t*>(fl) + 1 + (key >> 5), 1u << (key & 31));
               }
               __syncwarp();
             }
-            if (lane == 0) ptx::mbar_arrive_expect_tx(full_k, bytes);
-            __syncwarp();
-            auto copy = [&](const CUtensorMap* map, uint32_t dst, uint32_t full) {
+            const uint32_t pitch = RAW ? max(p.box * D, 128) : p.box * 128;
+            for (int kv = 0; kv < 2; ++kv) {
+              const int full_i = RAW ? C::B_RAWFULL + kv : C::B_FULL + (int)pos.s;
+              const uint32_t full = bar(full_i), dst = RAW ? s_base + C::OFF_RAW + kv * C::RAW_BYTES : s_kv(pos.s);
+              if (kv) {
+                ok = __all_sync(0xffffffffu, wait_bar(bar(RAW ? C::B_RAWEMPTY + 1 : C::B_EMPTY + (int)pos.s),
+                                                      (RAW ? n_kv & 1 : pos.ph) ^ 1, abort_flag, SINGLE));
+                if (!ok) break;
+              }
+              if (lane == 0) ptx::mbar_arrive_expect_tx(full, RAW ? BN * D : C::TILE_BYTES);
+              __syncwarp();
               for (int i = lane; i < boxes; i += 32) {
-                int row = row0, z = z0;
-                if (i != lane) lookup(i, row, z);
-                else if (!good) {
-                  row = 0;
-                  z = p.n_pages * p.h_kv;
-                }
+                const Box b = ahead ? mine : look(key0 + i * p.box, e.str_row, e.str_len, e.hk);
                 if constexpr (RAW) {
-                  ptx::tma_load_3d(dst + i * pitch, map, full, 0, row, z, pol_kv);
+                  ptx::tma_load_3d(dst + i * pitch, kv ? &tm_v : &tm_k, full, 0, b.row, b.z, pol_kv);
                 } else {
                   for (int c = 0; c < C::CHUNKS; ++c)
-                    ptx::tma_load_3d(dst + c * C::CHUNK_BYTES + i * pitch, map, full, c * 64, row, z, pol_kv);
+                    ptx::tma_load_3d(dst + c * C::CHUNK_BYTES + i * pitch, kv ? &tm_v : &tm_k, full, c * 64, b.row, b.z, pol_kv);
                 }
               }
-            };
-            copy(&tm_k, RAW ? s_base + C::OFF_RAW : s_k + s * C::TILE_BYTES, full_k);
-            ok = __all_sync(0xffffffffu, wait_bar(empty_v, eph, abort_flag, SINGLE));
-            if (!ok) {
-              if (lane == 0) drain_wait(full_k, fph);
-              break;
+              __syncwarp();
+              pos.step(1);
             }
-            if (lane == 0) ptx::mbar_arrive_expect_tx(full_v, bytes);
-            __syncwarp();
-            copy(&tm_v, RAW ? s_base + C::OFF_RAW + C::RAW_BYTES : s_v + s * C::TILE_BYTES, full_v);
           }
-          ++ring;
         }
+        if (!ok) break;
+        if (KIND != DENSE && ahead && n == 0) box = look_ahead(next_word, 0);
+        word = next_word;
       }
       if (!ok && lane == 0) {
-        // copies in flight must land before this CTA's shared memory goes away
-        if (n_q > 0) drain_wait(bar(C::B_QFULL), (n_q - 1) & 1);
-        for (uint32_t x = ring > STAGES ? ring - STAGES : 0; x < ring; ++x) {
-          if (KIND == PAGED8) {
-            drain_wait(bar(C::B_RAWFULL), x & 1);
-            drain_wait(bar(C::B_RAWFULL + 1), x & 1);
-          } else {
-            drain_wait(bar(C::B_KFULL + x % STAGES), (x / STAGES) & 1);
-            drain_wait(bar(C::B_VFULL + x % STAGES), (x / STAGES) & 1);
+        // copies in flight must land before this CTA's shared memory goes away: every barrier's last
+        // phase that was armed, told by its parity after the last use of the slot
+        for (int b = 0; b < C::Q_BUFS; ++b)
+          if (n_q > (uint32_t)b) drain_wait(bar(C::B_QFULL + b), ((n_q - 1 - b) / C::Q_BUFS) & 1);
+        if (RAW) {
+          for (int kv = 0; kv < 2; ++kv) {
+            if (n_kv > 0) drain_wait(bar(C::B_RAWFULL + kv), (n_kv - 1) & 1);
+            drain_wait(bar(C::B_RAWFULL + kv), n_kv & 1);
           }
+        } else {
+          for (int s = 0; s < C::SLOTS; ++s) drain_wait(bar(C::B_FULL + s), s < (int)pos.s ? pos.ph : pos.ph ^ 1);
         }
       }
       __syncwarp();
-      }
     } else if (SINGLE && warp == C::WARP_MMA) {
-      uint32_t n_q = 0;  // units with keys so far
-      for (int batch = 0, n_b; (n_b = next_batch(batch)) > 0; ++batch) {
       // ================================================================ S = Q K^T (one row tile)
       if (lane == 0) {
-        for (int b = 0; b < n_b && ok; ++b) {
-          const int n = units[b].n;
+        uint32_t n_q = 0, tiles = 0;
+        Pos pos;
+        for (uint32_t un = 0;; ++un) {
+          if (!(ok = unit_wait(un))) break;
+          const int n = units[un % UNITS].n;
+          unit_done(un);
+          if (n < 0) break;
           if (n == 0) continue;
-          ok = wait_bar(bar(C::B_QFULL), n_q & 1, abort_flag, true);
+          const uint32_t qb = n_q % C::Q_BUFS, q_tile = s_q(qb);
+          ok = wait_bar(bar(C::B_QFULL + qb), (n_q / C::Q_BUFS) & 1, abort_flag, true);
           ++n_q;
-          for (int j = 0; j < n && ok; ++j) {
-            const int s = ring % STAGES;
-            ok = wait_bar(bar(C::B_KFULL + s), (ring / STAGES) & 1, abort_flag, true) &&
-                 (ring == 0 || wait_bar(bar(C::B_SFREE), (ring - 1) & 1, abort_flag, true));
+          for (int j = 0; j < n && ok; ++j, ++tiles) {
+            ok = wait_bar(bar(C::B_FULL + pos.s), pos.ph, abort_flag, true) &&
+                 (tiles == 0 || wait_bar(bar(C::B_SFREE), (tiles - 1) & 1, abort_flag, true));
             if (!ok) break;
             ptx::tc_fence_after();
-            const uint32_t k_stage = s_k + s * C::TILE_BYTES;
+            const uint32_t k_tile = s_kv(pos.s);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t koff = (kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32;
-              ptx::mma_ss(tmem, ptx::sdesc_sw128(s_q + koff, 16, 1024), ptx::sdesc_sw128(k_stage + koff, 16, 1024),
+              ptx::mma_ss(tmem, ptx::sdesc_sw128(q_tile + koff, 16, 1024), ptx::sdesc_sw128(k_tile + koff, 16, 1024),
                           C::IDESC_S, kk > 0 ? 1u : 0u);
             }
             ptx::mma_commit(bar(C::B_SFULL));
             if (KIND != DENSE) ptx::mbar_arrive(bar(C::B_SFULL));
-            ptx::mma_commit(bar(C::B_KEMPTY + s));
-            ++ring;
+            ptx::mma_commit(bar(C::B_EMPTY + pos.s));
+            pos.step(2);
           }
-          if (ok) ptx::mma_commit(bar(C::B_QEMPTY));
+          if (!ok) break;
+          ptx::mma_commit(bar(C::B_QEMPTY + qb));
         }
         if (!ok) {
           ptx::mma_commit(bar(C::B_DRAIN));
@@ -769,35 +841,39 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         }
       }
       __syncwarp();
-      }
     } else if (SINGLE && warp == C::WARP_PV) {
-      for (int batch = 0, n_b; (n_b = next_batch(batch)) > 0; ++batch) {
       // ================================================================ O += P V (one row tile)
       if (lane == 0) {
-        for (int b = 0; b < n_b && ok; ++b) {
-          const plan::Entry& e = units[b];
+        uint32_t tiles = 0, tails = 0;
+        Pos pos;
+        pos.step(1);
+        for (uint32_t un = 0;; ++un) {
+          if (!(ok = unit_wait(un))) break;
+          const plan::Entry& e = units[un % UNITS];
           const int n = e.n, len = e.str_len;
-          for (int j = 0; j < n && ok; ++j) {
-            const int s = ring % STAGES;
+          if (n < 0) break;
+          for (int j = 0; j < n && ok; ++j, ++tiles) {
             const bool tail = (tile_of(e, j) + 1) * BN > len;
-            ok = wait_bar(bar(C::B_VFULL + s), (ring / STAGES) & 1, abort_flag, true);
+            ok = wait_bar(bar(C::B_FULL + pos.s), pos.ph, abort_flag, true);
             if (!ok) break;
             if (tail) ptx::mbar_arrive(bar(C::B_TAILREQ));
-            ok = wait_bar(bar(C::B_PFULL), ring & 1, abort_flag, true) &&
+            ok = wait_bar(bar(C::B_PFULL), tiles & 1, abort_flag, true) &&
                  (!tail || wait_bar(bar(C::B_TAIL), tails & 1, abort_flag, true));
             if (!ok) break;
             tails += tail;
             ptx::tc_fence_after();
-            const uint32_t v_stage = s_v + s * C::TILE_BYTES;
+            const uint32_t v_tile = s_kv(pos.s);
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk)
               ptx::mma_ts(tmem + C::TMEM_O, tmem + C::TMEM_P + kk * 8,
-                          ptx::sdesc_sw128(v_stage + kk * 2048, C::CHUNK_BYTES, 1024), C::IDESC_PV,
+                          ptx::sdesc_sw128(v_tile + kk * 2048, C::CHUNK_BYTES, 1024), C::IDESC_PV,
                           (j > 0 || kk > 0) ? 1u : 0u);
             ptx::mma_commit(bar(C::B_ODONE));
-            ptx::mma_commit(bar(C::B_VEMPTY + s));
-            ++ring;
+            ptx::mma_commit(bar(C::B_EMPTY + pos.s));
+            pos.step(2);
           }
+          if (!ok) break;
+          unit_done(un);
         }
         if (!ok) {
           ptx::mma_commit(bar(C::B_DRAIN + 1));
@@ -805,45 +881,44 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         }
       }
       __syncwarp();
-      }
     } else if (!SINGLE && warp == C::WARP_MMA) {
-      uint32_t n_q = 0;             // units with keys so far
-      uint32_t cnt0 = 0, cnt1 = 0;  // key tiles of row tile 0 and 1 so far
-      bool pend = false, pend0 = false, pend1 = false, acc0 = false, acc1 = false, pend_tail = false;  // PVs not yet issued
-      for (int batch = 0, n_b; (n_b = next_batch(batch)) > 0; ++batch) {
       // ================================================================ both products of two row tiles
       // P_t lies in S_t, so S_t(j) follows PV_t(j - 1). In order PV0(j - 1), S0(j), PV1(j - 1), S1(j),
       // over all units as one stream: a unit's last PV waits for the softmax while the next one's
       // keys are on their way. Only where a unit starts do both PVs come first, since S needs
       // the new Q.
       if (lane == 0) {
+        uint32_t n_q = 0, tails = 0;
+        uint32_t cnt0 = 0, cnt1 = 0;  // key tiles of row tile 0 and 1 so far
+        bool pend = false, pend0 = false, pend1 = false, acc0 = false, acc1 = false, pend_tail = false;  // PVs not yet issued
+        Pos kpos, vpos;  // this tile's keys; the values of the PVs not yet issued
+        vpos.step(1);
         auto issue_pv = [&](int t, uint32_t cnt, bool acc) -> bool {
           if (!wait_bar(bar(C::B_PFULL + t), (cnt - 1) & 1, abort_flag)) return false;
           ptx::tc_fence_after();
-          const uint32_t v_stage = s_v + ((ring - 1) % STAGES) * C::TILE_BYTES;
+          const uint32_t v_tile = s_kv(vpos.s);
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
             ptx::mma_ts(tmem + C::TMEM_O + t * D, tmem + t * BN + kk * 8,
-                        ptx::sdesc_sw128(v_stage + kk * 2048, C::CHUNK_BYTES, 1024), C::IDESC_PV,
+                        ptx::sdesc_sw128(v_tile + kk * 2048, C::CHUNK_BYTES, 1024), C::IDESC_PV,
                         (acc || kk > 0) ? 1u : 0u);
           ptx::mma_commit(bar(C::B_ODONE + t));
           return true;
         };
         auto issue_s = [&](int t) {
-          const uint32_t q_tile = s_q + t * C::TILE_BYTES, k_stage = s_k + (ring % STAGES) * C::TILE_BYTES;
+          const uint32_t q_tile = s_q(0) + t * C::TILE_BYTES, k_tile = s_kv(kpos.s);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t koff = (kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32;
             ptx::mma_ss(tmem + t * BN, ptx::sdesc_sw128(q_tile + koff, 16, 1024),
-                        ptx::sdesc_sw128(k_stage + koff, 16, 1024), C::IDESC_S, kk > 0 ? 1u : 0u);
+                        ptx::sdesc_sw128(k_tile + koff, 16, 1024), C::IDESC_S, kk > 0 ? 1u : 0u);
           }
           ptx::mma_commit(bar(C::B_SFULL + t));
           if (KIND != DENSE) ptx::mbar_arrive(bar(C::B_SFULL + t));
         };
-        // the values of the ring use before this one, for the PVs still to come
+        // the values for the PVs still to come have landed
         auto values = [&]() -> bool {
-          const uint32_t s = (ring - 1) % STAGES;
-          if (!wait_bar(bar(C::B_VFULL + s), ((ring - 1) / STAGES) & 1, abort_flag)) return false;
+          if (!wait_bar(bar(C::B_FULL + vpos.s), vpos.ph, abort_flag)) return false;
           if (!pend_tail) return true;
           ptx::mbar_arrive(bar(C::B_TAILREQ));
           pend_tail = false;
@@ -853,20 +928,24 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           if (!values()) return false;
           if (pend0 && !issue_pv(0, cnt0, acc0)) return false;
           if (pend1 && !issue_pv(1, cnt1, acc1)) return false;
-          ptx::mma_commit(bar(C::B_VEMPTY + (ring - 1) % STAGES));
+          ptx::mma_commit(bar(C::B_EMPTY + vpos.s));
+          vpos.step(2);
           pend = false;
           return true;
         };
-        for (int b = 0; b < n_b && ok; ++b) {
-          const plan::Entry& e = units[b];
+        for (uint32_t un = 0;; ++un) {
+          if (pend && !(ok = flush())) break;
+          if (!(ok = unit_wait(un))) break;
+          const plan::Entry& e = units[un % UNITS];
           const int n = e.n, len = e.str_len;
-          if (n == 0) continue;
+          if (n < 0) break;
           const int lo0 = e.lo0, hi0 = e.hi0, lo1 = e.lo1, hi1 = e.hi1;
-          if (pend) ok = flush();
-          ok = ok && wait_bar(bar(C::B_QFULL), n_q & 1, abort_flag);
-          ++n_q;
+          if (n > 0) {
+            ok = wait_bar(bar(RAW ? C::B_QREADY : C::B_QFULL), n_q & 1, abort_flag);
+            ++n_q;
+          }
           for (int j = 0; j < n && ok; ++j) {
-            ok = wait_bar(bar(C::B_KFULL + ring % STAGES), (ring / STAGES) & 1, abort_flag) && (!pend || values());
+            ok = wait_bar(bar(C::B_FULL + kpos.s), kpos.ph, abort_flag) && (!pend || values());
             if (!ok) break;
             ptx::tc_fence_after();
             if (pend && pend0 && !(ok = issue_pv(0, cnt0, acc0))) break;
@@ -880,49 +959,56 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
               issue_s(1);
               ++cnt1;
             }
-            ptx::mma_commit(bar(C::B_KEMPTY + ring % STAGES));
-            if (pend) ptx::mma_commit(bar(C::B_VEMPTY + (ring - 1) % STAGES));
+            ptx::mma_commit(bar(C::B_EMPTY + kpos.s));
+            kpos.step(2);
+            if (pend) {
+              ptx::mma_commit(bar(C::B_EMPTY + vpos.s));
+              vpos.step(2);
+            }
             pend = true;
             pend0 = in0;
             pend1 = in1;
             acc0 = j > lo0;
             acc1 = j > lo1;
-            pend_tail = KIND != PAGED8 && (tile_of(e, j) + 1) * BN > len;
-            ++ring;
+            pend_tail = !RAW && (tile_of(e, j) + 1) * BN > len;
           }
-          if (ok) ptx::mma_commit(bar(C::B_QEMPTY));
+          if (!ok) break;
+          if (n > 0) ptx::mma_commit(bar(C::B_QEMPTY));
+          unit_done(un);
         }
-        if (ok && pend) ok = flush();
         if (!ok) {
           ptx::mma_commit(bar(C::B_DRAIN));
           drain_wait(bar(C::B_DRAIN), 0);
         }
       }
       __syncwarp();
-      }
-    } else if (KIND != PAGED8 && warp == C::WARP_TAIL) {
-      for (int batch = 0, n_b; (n_b = next_batch(batch)) > 0; ++batch) {
+    } else if (!RAW && warp == C::WARP_TAIL) {
       // ================================================================ values behind the end: zero
-      for (int b = 0; b < n_b && ok; ++b) {
-        const plan::Entry& e = units[b];
+      uint32_t tails = 0;
+      Pos pos;
+      pos.step(1);
+      for (uint32_t un = 0;; ++un) {
+        ok = __all_sync(0xffffffffu, unit_wait(un));
+        if (!ok) break;
+        const plan::Entry& e = units[un % UNITS];
         const int n = e.n, len = e.str_len;
-        for (int j = 0; j < n && ok; ++j, ++ring) {
+        if (n < 0) break;
+        for (int j = 0; j < n; ++j, pos.step(2)) {
           const int there = len - tile_of(e, j) * BN;
           if (there >= BN) continue;
-          const int s = ring % STAGES;
           ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_TAILREQ), tails++ & 1, abort_flag, true));
           if (!ok) break;
           for (int c = 0; c < C::CHUNKS; ++c)
             for (int x = there * 8 + lane; x < BN * 8; x += 32)
-              ptx::st_shared_v4(s_v + s * C::TILE_BYTES + c * C::CHUNK_BYTES + x * 16, 0, 0, 0, 0);
+              ptx::st_shared_v4(s_kv(pos.s) + c * C::CHUNK_BYTES + x * 16, 0, 0, 0, 0);
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar(C::B_TAIL));
+          __syncwarp();
         }
-      }
-      }
-    } else {  // no role
-      for (int batch = 0; next_batch(batch) > 0; ++batch) {
+        if (!ok) break;
+        if (lane == 0) unit_done(un);
+        __syncwarp();
       }
     }
   }
@@ -937,7 +1023,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
 }
 
 // Rows of the units that were cut: out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i over the pieces, in
-// their order. A warp per row, D / 32 columns per lane.
+// their order. A block takes 32 rows of one unit, a warp four of them at once, D / 32 columns per
+// lane: a row's loads do not wait for another's.
 struct JoinParams {
   const plan::Header* head;
   const plan::Join* joins;
@@ -951,44 +1038,77 @@ struct JoinParams {
 
 template <int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const JoinParams p) {
-  constexpr int W = D / 32;
+  constexpr int W = D / 32, R = 4;
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  const int n_join = p.head->n_join;
+  if ((int)blockIdx.x >= p.head->n_join) return;
+  const plan::Join j = p.joins[blockIdx.x];
   const int lane = threadIdx.x & 31;
-  const long long warps = (long long)gridDim.x * 8;
   const size_t slot_floats = (size_t)p.rows * (D + 2);
-  for (long long x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); x < (long long)n_join * p.rows; x += warps) {
-    const plan::Join j = p.joins[x / p.rows];
-    const int row = (int)(x % p.rows), t = row / BM, r = row % BM;
-    const int rt = r / p.group, tok = t * p.tok + rt;
-    if (rt >= p.tok || tok >= j.own_n) continue;
-    auto slot = [&](int i) { return p.part + (size_t)(i == 0 ? j.slot : j.next + 2 * (i - 1)) * slot_floats; };
-    float m = -INFINITY;
-    for (int i = lane; i < j.pieces; i += 32) m = fmaxf(m, slot(i)[(size_t)p.rows * D + row]);
+  int row[R], token[R];
+  bool valid[R], some = false;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float sum = 0.0f, o[W] = {};
-#pragma unroll 4
-    for (int i = 0; i < j.pieces; ++i) {
-      const float* s = slot(i);
-      const float mi = s[(size_t)p.rows * D + row], li = s[(size_t)p.rows * (D + 1) + row];
-      const float w = mi == -INFINITY ? 0.0f : exp2f(mi - m);
-      sum += w * li;
-      const float* v = s + (size_t)row * D + lane * W;
-      if (w != 0.0f) {
+  for (int y = 0; y < R; ++y) {
+    row[y] = (int)blockIdx.y * 32 + (threadIdx.x >> 5) * R + y;
+    const int t = row[y] / BM, rt = row[y] % BM / p.group;
+    token[y] = t * p.tok + rt;
+    valid[y] = rt < p.tok && token[y] < j.own_n;
+    some |= valid[y];
+  }
+  if (!some) return;
+  auto slot = [&](int i) { return p.part + (size_t)(i == 0 ? j.slot : j.next + 2 * (i - 1)) * slot_floats; };
+  float m[R], sum[R], o[R][W];
 #pragma unroll
-        for (int y = 0; y < W; ++y) o[y] += w * v[y];
+  for (int y = 0; y < R; ++y) {
+    m[y] = -INFINITY;
+    sum[y] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) o[y][w] = 0.0f;
+    if (!valid[y]) row[y] = row[0] - row[0] % R;  // a row whose statistics may be read; not used
+  }
+  for (int i = lane; i < j.pieces; i += 32) {
+    const float* s = slot(i) + (size_t)p.rows * D;
+#pragma unroll
+    for (int y = 0; y < R; ++y)
+      if (valid[y]) m[y] = fmaxf(m[y], s[row[y]]);
+  }
+#pragma unroll
+  for (int y = 0; y < R; ++y)
+#pragma unroll
+    for (int off = 16; off; off >>= 1) m[y] = fmaxf(m[y], __shfl_xor_sync(0xffffffffu, m[y], off));
+#pragma unroll 2
+  for (int i = 0; i < j.pieces; ++i) {
+    const float* s = slot(i);
+#pragma unroll
+    for (int y = 0; y < R; ++y) {
+      if (!valid[y]) continue;
+      const float mi = s[(size_t)p.rows * D + row[y]], li = s[(size_t)p.rows * (D + 1) + row[y]];
+      float v[W];
+      const float* at = s + (size_t)row[y] * D + lane * W;
+      if constexpr (W == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(at);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(at);
+        v[0] = x.x, v[1] = x.y;
       }
+      const float w = mi == -INFINITY ? 0.0f : exp2f(mi - m[y]);
+      sum[y] += w * li;
+#pragma unroll
+      for (int z = 0; z < W; ++z) o[y][z] = w == 0.0f ? o[y][z] : o[y][z] + w * v[z];
     }
-    const int head_q = j.hk * p.group + (r - rt * p.group);
-    const long long at = (long long)j.own_row + tok;
-    const float inv = sum == 0.0f ? 0.0f : (p.v_scale ? p.v_scale[j.hk] : 1.0f) / sum;
+  }
+#pragma unroll
+  for (int y = 0; y < R; ++y) {
+    if (!valid[y]) continue;
+    const int head_q = j.hk * p.group + row[y] % BM % p.group;
+    const long long at = (long long)j.own_row + token[y];
+    const float inv = sum[y] == 0.0f ? 0.0f : (p.v_scale ? p.v_scale[j.hk] : 1.0f) / sum[y];
     uint32_t* to = reinterpret_cast<uint32_t*>(p.out + at * p.out_ts + head_q * p.out_hs) + lane * (W / 2);
 #pragma unroll
-    for (int y = 0; y < W; y += 2) to[y / 2] = ptx::pack_bf16x2(o[y] * inv, o[y + 1] * inv);
+    for (int z = 0; z < W; z += 2) to[z / 2] = ptx::pack_bf16x2(o[y][z] * inv, o[y][z + 1] * inv);
     if (lane == 0 && p.lse)
-      p.lse[at * p.h_q + head_q] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.69314718055994530942f;
+      p.lse[at * p.h_q + head_q] = sum[y] == 0.0f ? -INFINITY : (m[y] + log2f(sum[y])) * 0.69314718055994530942f;
   }
 }
 
@@ -1047,9 +1167,9 @@ Geometry geometry_of(int T_q, int B, int h_q, int h_kv) {
 }
 
 template <typename Kernel, typename... A>
-bool launch(Kernel* kernel, unsigned grid, unsigned threads, size_t smem, cudaStream_t stream, const A&... args) {
+bool launch(Kernel* kernel, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -1139,7 +1259,7 @@ int run(const PackedArgs& a, PFN_encodeTiled enc, void* workspace) {
   if (may_cut) {
     const JoinParams j = {pa.head, pa.joins, p.part, p.out,  p.lse,  p.out_ts,
                           p.out_hs, p.h_q,    p.group, p.tok, C::ROWS, KIND == PAGED8 ? p.v_scale : nullptr};
-    if (!launch(attn_join_kernel<D>, kSms * 4, 256, 0, a.stream, j)) return ATTN_ERR_CUDA;
+    if (!launch(attn_join_kernel<D>, dim3((unsigned)g.ctas, C::ROWS / 32), 256, 0, a.stream, j)) return ATTN_ERR_CUDA;
   }
   return cudaPeekAtLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

@@ -51,9 +51,9 @@ constexpr int kSms = 152;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr uint64_t kDrainLimitNs = 200000000ull;
 constexpr uint32_t FAULT_PACKED_BWD = 1024;
-constexpr int BATCH = 16;
+constexpr int UNITS = 4;      // units whose entries a CTA holds at a time
 constexpr int kMinShare = 2;  // tiles
-constexpr int kMaxDeal = 4;   // units per CTA from which on they are not cut
+constexpr int kMaxDeal = 2;   // units per CTA above which they are not cut
 
 template <int D>
 struct BCfg {
@@ -67,10 +67,11 @@ struct BCfg {
   static constexpr int OFF_R1 = OFF_R0 + STAGES * TILE_BYTES;  // ring: dO, or V
   static constexpr int OFF_VEC = OFF_R1 + STAGES * TILE_BYTES;  // float [STAGES][-lse log2(e)[T], -D[T]]
   static constexpr int OFF_UNITS = OFF_VEC + STAGES * 2 * T * 4;
-  static constexpr int OFF_BAR = OFF_UNITS + BATCH * 64;
+  static constexpr int OFF_BAR = OFF_UNITS + UNITS * 64;
   static constexpr int B_AFULL = 0, B_AEMPTY = 1, B_FULL = 2, B_EMPTY = B_FULL + STAGES, B_MMFULL = B_EMPTY + STAGES;
   static constexpr int B_PFULL = B_MMFULL + 2, B_ACC = B_PFULL + 2, B_TAILREQ = B_ACC + 1, B_TAIL = B_TAILREQ + 2;
-  static constexpr int B_DRAIN = B_TAIL + 2, NUM_BARS = B_DRAIN + 2;
+  static constexpr int B_DRAIN = B_TAIL + 2, B_UNITFULL = B_DRAIN + 2, B_UNITEMPTY = B_UNITFULL + UNITS,
+                       NUM_BARS = B_UNITEMPTY + UNITS;
   static constexpr int OFF_SLOT = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_ABORT = OFF_SLOT + 4;
   static constexpr int SMEM_BYTES = OFF_ABORT + 4;
@@ -84,7 +85,7 @@ struct BCfg {
 };
 
 struct BwdParams {
-  const plan::Header* head;
+  plan::Header* head;
   const int2* range;
   const plan::Entry* list;
   const float* stats;  // [2][h_kv][T_q g]: -lse log2(e), then -D, by packed row
@@ -254,6 +255,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       ptx::mbar_init(bar(C::B_DRAIN + h), 1);
     }
     ptx::mbar_init(bar(C::B_ACC), SPLIT ? 2 : 1);
+    for (int u = 0; u < UNITS; ++u) {
+      ptx::mbar_init(bar(C::B_UNITFULL + u), 1);
+      ptx::mbar_init(bar(C::B_UNITEMPTY + u), 8 + (SPLIT ? 2 : 1) + 1);  // elementwise, issuing and tail warps
+    }
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -283,24 +288,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
 
-  const plan::Header head = *p.head;
-  const int2 range = p.range[blockIdx.x];
-
-  // The entries of this CTA's next units into shared memory; every warp calls it.
-  auto next_batch = [&](int batch) -> int {
-    __syncwarp();  // the barrier counts whole warps
-    ptx::named_bar_sync(1, THREADS);
-    if (*abort_flag) return 0;
-    int n_b = 0;
-    while (n_b < BATCH && plan::unit_of(head, range, blockIdx.x, gridDim.x, batch * BATCH + n_b) >= 0) ++n_b;
-    for (int x = threadIdx.x; x < n_b * 4; x += THREADS) {
-      const int u = plan::unit_of(head, range, blockIdx.x, gridDim.x, batch * BATCH + (x >> 2));
-      reinterpret_cast<int4*>(smem + C::OFF_UNITS)[x] = reinterpret_cast<const int4*>(p.list + u)[x & 3];
-    }
-    __syncwarp();
-    ptx::named_bar_sync(1, THREADS);
-    return n_b;
-  };
+  // The copy warp passes the units' entries on through a ring of UNITS places; every other warp
+  // runs through them in that order, each at its own pace. n < 0: no more units.
+  auto unit_wait = [&](uint32_t un) -> bool { return wait_bar(bar(C::B_UNITFULL + un % UNITS), (un / UNITS) & 1, abort_flag); };
+  auto unit_done = [&](uint32_t un) { ptx::mbar_arrive(bar(C::B_UNITEMPTY + un % UNITS)); };
   // Rows of streamed tile j that belong to the sequence, when they are not all (else T or more).
   auto there = [&](const plan::Entry& e, int j) -> int {
     const int left = e.str_len - (e.j0 + j + e.skip) * (DKDV ? p.tok : T);
@@ -313,10 +304,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp == WARP_LOAD) {
     // ================================================================ copies
     uint32_t n_a = 0;  // units with tiles so far
-    for (int batch = 0, n_b; (n_b = next_batch(batch)) > 0; ++batch) {
-      for (int b = 0; b < n_b && ok; ++b) {
-        const plan::Entry& e = units[b];
-        const int n = e.n;
+    const plan::Header head = *p.head;
+    plan::Turn turn(head, p.range);
+    auto next_unit = [&]() -> int { return __shfl_sync(0xffffffffu, lane == 0 ? turn.next(p.head) : 0, 0); };
+    auto word_of = [&](int u) -> int { return u < 0 ? -1 : lane < 16 ? reinterpret_cast<const int*>(p.list + u)[lane] : 0; };
+    int word = word_of(next_unit());  // lane x: word x of the entry; all -1: no more units
+    {
+      for (uint32_t un = 0;; ++un) {
+        ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_UNITEMPTY + un % UNITS), ((un / UNITS) & 1) ^ 1, abort_flag));
+        if (!ok) break;
+        if (lane < 16) reinterpret_cast<int*>(smem + C::OFF_UNITS)[(un % UNITS) * 16 + lane] = word;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(C::B_UNITFULL + un % UNITS));
+        const int n = __shfl_sync(0xffffffffu, word, 9);
+        if (n < 0) break;
+        word = word_of(next_unit());
+        const plan::Entry& e = units[un % UNITS];  // stays: this warp alone replaces it
         if (n == 0) continue;
         ok = __all_sync(0xffffffffu, n_a == 0 || wait_bar(bar(C::B_AEMPTY), (n_a - 1) & 1, abort_flag));
         if (!ok) break;
@@ -367,6 +370,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           ++ring;
         }
+        if (!ok) break;
       }
       if (!ok && lane == 0) {
         if (n_a > 0) drain_wait(bar(C::B_AFULL), (n_a - 1) & 1);
@@ -435,13 +439,18 @@ __global__ void __launch_bounds__(THREADS, 1)
       pend = false;
       return true;
     };
-    for (int batch = 0, n_b; (n_b = next_batch(batch)) > 0; ++batch) {
+    {
       if (lane == 0 && (SPLIT || hs == 0)) {
-        for (int b = 0; b < n_b && ok; ++b) {
-          const plan::Entry& e = units[b];
-          const int n = e.n;
-          if (n == 0) continue;
+        for (uint32_t un = 0;; ++un) {
           if (pend && !(ok = flush())) break;
+          if (!(ok = unit_wait(un))) break;
+          const plan::Entry& e = units[un % UNITS];
+          const int n = e.n;
+          if (n < 0) break;
+          if (n == 0) {
+            unit_done(un);
+            continue;
+          }
           if (!(ok = wait_bar(bar(C::B_AFULL), n_a & 1, abort_flag))) break;
           ++n_a;
           for (int j = 0; j < n; ++j) {
@@ -465,9 +474,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (pend_tail) ptx::mbar_arrive(bar(C::B_TAILREQ + (SPLIT ? hs : 0)));
             ++ring;
           }
-          if (ok) ptx::mma_commit(bar(C::B_AEMPTY));
+          if (!ok) break;
+          ptx::mma_commit(bar(C::B_AEMPTY));
+          unit_done(un);
         }
-        if (ok && pend) ok = flush();
         if (!ok) {
           ptx::mma_commit(bar(C::B_DRAIN + hs));
           drain_wait(bar(C::B_DRAIN + hs), 0);
@@ -478,10 +488,13 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == WARP_TAIL) {
     // ================================================================ rows of other sequences: zero
     uint32_t tails = 0;
-    for (int batch = 0, n_b; (n_b = next_batch(batch)) > 0; ++batch) {
-      for (int b = 0; b < n_b && ok; ++b) {
-        const plan::Entry& e = units[b];
+    {
+      for (uint32_t un = 0;; ++un) {
+        ok = __all_sync(0xffffffffu, unit_wait(un));
+        if (!ok) break;
+        const plan::Entry& e = units[un % UNITS];
         const int n = e.n;
+        if (n < 0) break;
         for (int j = 0; j < n && ok; ++j, ++ring) {
           const int from = there(e, j);
           if (from >= T) continue;
@@ -502,6 +515,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           ++tails;
         }
+        if (!ok) break;
+        if (lane == 0) unit_done(un);
+        __syncwarp();
       }
     }
   } else {
@@ -513,10 +529,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint64_t c2 = ptx::f2_pack(p.scale_log2, p.scale_log2);
     const int rt = r / p.group;  // rows own: this row's token
     uint32_t n_a = 0;
-    for (int batch = 0, n_b; (n_b = next_batch(batch)) > 0; ++batch) {
-      for (int b = 0; b < n_b && ok; ++b) {
-        const plan::Entry& e = units[b];
+    {
+      for (uint32_t un = 0;; ++un) {
+        ok = __all_sync(0xffffffffu, unit_wait(un));
+        if (!ok) break;
+        const plan::Entry& e = units[un % UNITS];
         const int n = e.n;
+        if (n < 0) break;
         const bool row_valid = DKDV ? r < e.own_n : rt < min(e.own_n, p.tok);
         // the streamed side's rows that this row pairs with: [my_lo, my_hi), query tokens or keys
         int my_lo = 0, my_hi = 0;
@@ -669,6 +688,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           __syncwarp();
         }
+        if (lane == 0) unit_done(un);
+        __syncwarp();
       }
     }
   }

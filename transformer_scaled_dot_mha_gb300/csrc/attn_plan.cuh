@@ -4,8 +4,8 @@
 // does what. One CTA writes the list: an item is a block of own rows of one sequence (query
 // tokens, or keys), a unit is an item for one key/value head, and a unit's cost is the number
 // of tiles that it streams. Two ways to hand the units out:
-//   whole    heaviest first, dealt to the CTAs in snake order (0 .. G-1, G-1 .. 0, ..); no unit
-//            is cut. Taken when there are many units for every CTA.
+//   whole    heaviest first, to the CTA that asks next; no unit is cut. Taken when there are many
+//            units for every CTA. (Who computes a unit does not change its result.)
 //   cut      the units' tiles one after the other, in equal shares of consecutive tiles, so a
 //            CTA's first and last units may be pieces, whose partial results a second kernel
 //            joins. Taken when the units are few for every CTA, or one of them is longer than
@@ -21,8 +21,8 @@ namespace plan {
 
 constexpr int TILE = 128;      // streamed keys per tile, own rows per tile
 constexpr int THREADS = 1024;  // of the planning CTA
-constexpr int SMEM_SEQS = 4095;
-constexpr int BINS = 512;
+constexpr int SMEM_SEQS = 2047, SMEM_ITEMS = 2048;  // with more, these lists are in the workspace
+constexpr int BINS = 640;
 
 struct Entry {        // 64 bytes
   int own_row;        // first own row (token or key) in the packed array
@@ -49,10 +49,10 @@ struct Join {  // 32 bytes: a unit that was cut
 };
 
 struct Header {
-  int cut;      // 1: CTA a takes entries [range[a].x, range[a].y); 0: snake order over n_units
+  int cut;      // 1: CTA a takes entries [range[a].x, range[a].y); 0: the next of n_units, as CTAs ask
   int n_units;
   int n_join;
-  int pad;
+  int next;     // units handed out so far, when they are whole
 };
 
 struct Args {
@@ -72,13 +72,16 @@ struct Args {
   int2* range;   // [ctas]
   Join* joins;   // [ctas]
   int* first;    // [B + 1]: items before each sequence
+  long long* at;  // [items]: cost before each item
+  int* rank;     // [items]: place among the items of like cost
   Entry* list;   // [items * h_kv + ctas]
 };
 
 // Bytes of the plan part of a workspace; items: an upper bound.
 inline size_t bytes(long long items, int h_kv, int B, int ctas) {
   const size_t lists = ((size_t)items * h_kv + ctas) * sizeof(Entry) + (size_t)ctas * (sizeof(Join) + sizeof(int2));
-  return (sizeof(Header) + lists + ((size_t)B + 1) * sizeof(int) + 255) & ~size_t(255);
+  const size_t scratch = (size_t)items * (sizeof(long long) + sizeof(int)) + ((size_t)B + 1) * sizeof(int);
+  return (sizeof(Header) + lists + scratch + 255) & ~size_t(255);
 }
 
 inline void place(Args& a, void* base, long long items) {
@@ -91,6 +94,10 @@ inline void place(Args& a, void* base, long long items) {
   p += (size_t)a.ctas * sizeof(Join);
   a.range = reinterpret_cast<int2*>(p);
   p += (size_t)a.ctas * sizeof(int2);
+  a.at = reinterpret_cast<long long*>(p);
+  p += (size_t)items * sizeof(long long);
+  a.rank = reinterpret_cast<int*>(p);
+  p += (size_t)items * sizeof(int);
   a.first = reinterpret_cast<int*>(p);
 }
 
@@ -230,37 +237,76 @@ __device__ __forceinline__ long long scan(long long v, long long* warps, long lo
 struct Scratch {  // shared memory
   long long warps[THREADS / 32];
   int first[SMEM_SEQS + 1];
+  long long at[SMEM_ITEMS];  // cost of the items before each
+  int rank[SMEM_ITEMS];      // its place among the items of its bin
   int bin[BINS];
   int max, joins;
 };
 
-// Writes the list: one CTA of THREADS threads.
+// Bins of the counting sort, heaviest first: exact costs below 256, sixteen bins per doubling above.
+__device__ __forceinline__ int bin_of(int n) {
+  if (n < 256) return BINS - 1 - n;
+  const int e = 31 - __clz(n);  // 8 ..
+  return max(BINS - 256 - ((e - 8) * 16 + ((n >> (e - 4)) & 15)) - 1, 0);
+}
+
+// Units [w0, w0 + cost) of the cut list; I: a type that holds the whole work.
+template <typename I>
+__device__ __forceinline__ void cut_unit(const Args& a, Scratch& sh, Entry e, int u, I w0, I cost, I share, I work) {
+  const I w1 = w0 + cost;
+  const int c0 = (int)(w0 / share), c1 = (int)((w1 - 1) / share);
+  const int n = e.n, lo0 = e.lo0, hi0 = e.hi0, lo1 = e.lo1, hi1 = e.hi1;
+  for (int c = c0; c <= c1; ++c) {
+    // entry u + c: units and CTAs both only go up along the tiles, so it is this piece's alone
+    const I r0 = (I)c * share, r1 = r0 + share;
+    const int j0 = (int)((r0 > w0 ? r0 : w0) - w0), j1 = (int)((r1 < w1 ? r1 : w1) - w0);
+    e.j0 = j0;
+    e.n = n == 0 ? 0 : j1 - j0;
+    auto clip = [&](int x) { return min(max(x - j0, 0), e.n); };
+    e.lo0 = clip(lo0);
+    e.hi0 = clip(hi0);
+    e.lo1 = clip(lo1);
+    e.hi1 = clip(hi1);
+    e.slot = c0 == c1 ? -1 : (r0 >= w0 ? 2 * c : 2 * c + 1);
+    put(a.list + u + c, e);
+    if (r0 >= w0) a.range[c].x = u + c;                    // the CTA's share starts here
+    if (r1 <= w1 || w1 == work) a.range[c].y = u + c + 1;  // and ends here
+  }
+  if (c0 == c1) return;
+  Join& j = a.joins[atomicAdd(&sh.joins, 1)];
+  j.own_row = e.own_row;
+  j.own_n = e.own_n;
+  j.hk = e.hk;
+  j.slot = (I)c0 * share >= w0 ? 2 * c0 : 2 * c0 + 1;
+  j.next = 2 * (c0 + 1);
+  j.pieces = c1 - c0 + 1;
+}
+
+// Writes the list: one CTA of THREADS threads. A thread takes an item to count, a unit to write.
 __device__ __forceinline__ void write(const Args& a, Scratch& sh) {
-  long long* warps = sh.warps;
-  int* s_first = sh.first;
-  int* s_bin = sh.bin;
-  int &s_max = sh.max, &s_joins = sh.joins;
   const int t = threadIdx.x;
   if (t == 0) {
-    s_max = 0;
-    s_joins = 0;
+    sh.max = 0;
+    sh.joins = 0;
   }
-  if (t < BINS) s_bin[t] = 0;
+  for (int x = t; x < BINS; x += THREADS) sh.bin[x] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // items before each sequence
-  int* first = a.B <= SMEM_SEQS ? s_first : a.first;
+  int* first = a.B <= SMEM_SEQS ? sh.first : a.first;
   long long items = 0;
   for (int b0 = 0; b0 < a.B; b0 += THREADS) {
     const int b = b0 + t;
     const int mine = b < a.B ? blocks_of(a, sequence(a, b)) : 0;
     long long total;
-    const long long at = scan(mine, warps, total);
+    const long long at = scan(mine, sh.warps, total);
     if (b < a.B) first[b] = (int)(items + at);
     items += total;
   }
   if (t == 0) first[a.B] = (int)items;
   __syncthreads();
   const int N = (int)items;
+  long long* at = N <= SMEM_ITEMS ? sh.at : a.at;
+  int* rank = N <= SMEM_ITEMS ? sh.rank : a.rank;
   auto find = [&](int i) -> Entry {  // item i: the last sequence that starts at or before it and has items
     int lo = 0, hi = a.B - 1;
     while (lo < hi) {
@@ -270,98 +316,66 @@ __device__ __forceinline__ void write(const Args& a, Scratch& sh) {
     }
     return item(a, sequence(a, lo), i - first[lo]);
   };
-  // costs: their sum over the items, and the largest
+  // costs: the sum before every item, the largest, and how many there are of each
   long long sum = 0;
-  int top = 0;
-  for (int i = t; i < N; i += THREADS) {
-    const int n = max(find(i).n, 1);
-    sum += n;
-    top = max(top, n);
+  Entry mine;  // item t
+  for (int i0 = 0; i0 < N; i0 += THREADS) {
+    const int i = i0 + t;
+    int cost = 0;
+    if (i < N) {
+      const Entry e = find(i);
+      if (i0 == 0) mine = e;
+      cost = max(e.n, 1);
+      rank[i] = atomicAdd(&sh.bin[bin_of(cost)], 1);
+    }
+    long long total;
+    const long long before = scan(cost, sh.warps, total);
+    if (i < N) at[i] = sum + before;
+    sum += total;
+    const int top = __reduce_max_sync(0xffffffffu, cost);
+    if ((t & 31) == 0 && top > 0) atomicMax(&sh.max, top);
   }
-  long long total;
-  scan(sum, warps, total);
-  atomicMax(&s_max, top);
   __syncthreads();
-  top = s_max;
-  const long long units = (long long)N * a.h_kv, work = total * a.h_kv;
+  const int top = sh.max;
+  const long long units = (long long)N * a.h_kv, work = sum * a.h_kv;
   const long long share = max((work + a.ctas - 1) / a.ctas, (long long)a.min_share);
-  const bool cut = a.may_cut && (units <= (long long)a.max_deal * a.ctas || top > share);
+  // cut: few units for every CTA, or one that is far longer than an even share. A piece costs its CTA
+  // some tiles' time (its sums go through memory), so a little unevenness is the better choice.
+  const bool cut = a.may_cut && (units <= (long long)a.max_deal * a.ctas || top > share + share / 2);
   if (t == 0) {
     a.head->cut = cut;
     a.head->n_units = (int)units;
+    a.head->next = a.ctas;
   }
   if (cut) {
     for (int i = t; i < a.ctas; i += THREADS) a.range[i] = make_int2(0, 0);
-    __syncthreads();
-    long long base = 0;  // cost of the items before this round's
-    for (int i0 = 0; i0 < N; i0 += THREADS) {
-      const int i = i0 + t;
-      Entry e;
-      int cost = 0;
-      if (i < N) {
-        e = find(i);
-        cost = max(e.n, 1);
-      }
-      long long round;
-      const long long at = base + scan(cost, warps, round);
-      base += round;
-      if (i >= N) continue;
-      const int n = e.n;
-      const int lo0 = e.lo0, hi0 = e.hi0, lo1 = e.lo1, hi1 = e.hi1;
-      for (int hk = 0; hk < a.h_kv; ++hk) {
-        const long long w0 = at * a.h_kv + (long long)hk * cost, w1 = w0 + cost;
-        const int u = i * a.h_kv + hk;
-        const int c0 = (int)(w0 / share), c1 = (int)((w1 - 1) / share);
-        e.hk = hk;
-        for (int c = c0; c <= c1; ++c) {
-          // entry u + c: units and CTAs both only go up along the tiles, so it is this piece's alone
-          const long long r0 = c * share, r1 = r0 + share;
-          const int j0 = (int)(max(r0, w0) - w0), j1 = (int)(min(r1, w1) - w0);
-          e.j0 = j0;
-          e.n = n == 0 ? 0 : j1 - j0;
-          auto clip = [&](int x) { return min(max(x - j0, 0), e.n); };
-          e.lo0 = clip(lo0);
-          e.hi0 = clip(hi0);
-          e.lo1 = clip(lo1);
-          e.hi1 = clip(hi1);
-          e.slot = c0 == c1 ? -1 : (r0 >= w0 ? 2 * c : 2 * c + 1);
-          put(a.list + u + c, e);
-          if (r0 >= w0) a.range[c].x = u + c;               // the CTA's share starts here
-          if (r1 <= w1 || w1 == work) a.range[c].y = u + c + 1;  // and ends here
-        }
-        if (c0 != c1) {
-          Join& j = a.joins[atomicAdd(&s_joins, 1)];
-          j.own_row = e.own_row;
-          j.own_n = e.own_n;
-          j.hk = hk;
-          j.slot = (long long)c0 * share >= w0 ? 2 * c0 : 2 * c0 + 1;
-          j.next = 2 * (c0 + 1);
-          j.pieces = c1 - c0 + 1;
-        }
-      }
-    }
-    __syncthreads();
-    if (t == 0) a.head->n_join = s_joins;
-    return;
+  } else {
+    // places of the bins: a scan over BINS = THREADS counts
+    long long all;
+    const int count = t < BINS ? sh.bin[t] : 0;
+    const long long before = scan(count, sh.warps, all);
+    if (t < BINS) sh.bin[t] = (int)before;
   }
-  if (t == 0) a.head->n_join = 0;
-  // heaviest first: a counting sort by cost (the order within a bin does not matter to any result)
-  auto bin_of = [&](int n) { return (int)((long long)(top - max(n, 1)) * (BINS - 1) / max(top, 1)); };
-  for (int i = t; i < N; i += THREADS) atomicAdd(&s_bin[bin_of(find(i).n)], 1);
   __syncthreads();
-  long long all;
-  const long long at = scan(t < BINS ? s_bin[t] : 0, warps, all);
-  __syncthreads();
-  if (t < BINS) s_bin[t] = (int)at;
-  __syncthreads();
-  for (int i = t; i < N; i += THREADS) {
-    Entry e = find(i);
-    Entry* to = a.list + (size_t)atomicAdd(&s_bin[bin_of(e.n)], 1) * a.h_kv;
-    for (int hk = 0; hk < a.h_kv; ++hk) {
-      e.hk = hk;
-      put(to + hk, e);
+  const bool narrow = work < (1LL << 30);
+  for (long long u0 = 0; u0 < units; u0 += THREADS) {
+    const long long u = u0 + t;
+    if (u >= units) break;
+    // by head, then by item: a thread's first unit is the item that it has counted
+    const int hk = (int)((unsigned)u / (unsigned)N), i = (int)((unsigned)u - (unsigned)hk * (unsigned)N);
+    Entry e = u == t && t < N ? mine : find(i);
+    const int cost = max(e.n, 1);
+    e.hk = hk;
+    if (!cut) {
+      put(a.list + ((size_t)sh.bin[bin_of(cost)] + rank[i]) * a.h_kv + hk, e);
+    } else {
+      const long long w0 = at[i] * a.h_kv + (long long)hk * cost;
+      if (narrow) cut_unit<unsigned>(a, sh, e, i * a.h_kv + hk, (unsigned)w0, (unsigned)cost, (unsigned)share, (unsigned)work);
+      else cut_unit<long long>(a, sh, e, i * a.h_kv + hk, w0, cost, share, work);
     }
   }
+  __syncthreads();
+  if (t == 0) a.head->n_join = sh.joins;
 }
 
 static __global__ void __launch_bounds__(THREADS, 1) attn_plan_kernel(const Args a) {
@@ -370,12 +384,24 @@ static __global__ void __launch_bounds__(THREADS, 1) attn_plan_kernel(const Args
   write(a, scratch);
 }
 
-// Index in the list of CTA `cta`'s k-th unit, or -1.
-__device__ __forceinline__ int unit_of(const Header& h, int2 range, int cta, int ctas, int k) {
-  if (h.cut) return range.x + k < range.y ? range.x + k : -1;
-  const long long at = (long long)k * ctas + ((k & 1) ? ctas - 1 - cta : cta);
-  return at < h.n_units ? (int)at : -1;
-}
+// The copy warp's way through the list: the number of its CTA's next unit, or -1. Lane 0 asks.
+struct Turn {
+  int at, end;  // cut: the rest of this CTA's range
+  bool cut;
+  __device__ __forceinline__ Turn(const Header& h, const int2* range) : cut(h.cut != 0) {
+    at = cut ? range[blockIdx.x].x : (int)blockIdx.x;
+    end = cut ? range[blockIdx.x].y : h.n_units;
+  }
+  __device__ __forceinline__ int next(Header* head) {  // one past: the unit after the one returned is asked for
+    const int u = at < end ? at : -1;
+    if (cut) {
+      ++at;
+    } else if (u >= 0) {
+      at = atomicAdd(&head->next, 1);
+    }
+    return u;
+  }
+};
 
 }  // namespace plan
 }  // namespace attn
