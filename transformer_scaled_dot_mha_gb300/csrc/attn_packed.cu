@@ -93,7 +93,11 @@ struct Cfg {
   static constexpr int OFF_RAW = OFF_KV + SLOTS * TILE_BYTES;  // [K, V]
   static constexpr int OFF_UNITS = OFF_RAW + 2 * RAW_BYTES;    // Entry [UNITS]
   static constexpr int OFF_FLAGS = OFF_UNITS + UNITS * 64;     // uint32 [FLAGS][8]: any, four words of key bits
-  static constexpr int OFF_BAR = OFF_FLAGS + (KIND == DENSE ? 0 : FLAGS * 32);
+  // rows on their way out, 32 rows x 64 columns per softmax warp: a place of their own, or the unit's Q
+  // (SINGLE), or none (8-bit pages at d = 128: shared memory is full, rows are stored as they lie)
+  static constexpr bool STAGED = KIND != PAGED8 || D == 64, OWN_STAGE = STAGED && !SINGLE;
+  static constexpr int OFF_STAGE = (OFF_FLAGS + (KIND == DENSE ? 0 : FLAGS * 32) + 127) & ~127;
+  static constexpr int OFF_BAR = OWN_STAGE ? OFF_STAGE + 4 * Q_TILES * 4096 : OFF_FLAGS + (KIND == DENSE ? 0 : FLAGS * 32);
   static constexpr int B_QFULL = 0;                  // [Q_BUFS]
   static constexpr int B_QEMPTY = B_QFULL + 2;       // [Q_BUFS]
   static constexpr int B_QREADY = B_QEMPTY + 2;      // PAGED8: Q in f16
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
   if (threadIdx.x == 0) {
     for (int b = 0; b < C::Q_BUFS; ++b) {
       ptx::mbar_init(bar(C::B_QFULL + b), 1);
-      ptx::mbar_init(bar(C::B_QEMPTY + b), 1);
+      ptx::mbar_init(bar(C::B_QEMPTY + b), SINGLE ? 4 : 1);  // the softmax warps, or the last S
     }
     ptx::mbar_init(bar(C::B_QREADY), 2 * BM);
     for (int s = 0; s < C::SLOTS; ++s) {
@@ -367,8 +371,22 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
             ptx::fence_proxy_async_smem();
           }
           ptx::mbar_arrive(bar(C::B_QREADY));
-          ++n_q;
         }
+      }
+      if (e.n > 0) ++n_q;
+      // list entries [inner, outer) of this row tile are legal for all of its rows; the others need the mask
+      int inner = 0, outer;
+      {
+        const int pos_lo = e.pos + t * p.tok, pos_hi = pos_lo + min(e.own_n - t * p.tok, p.tok) - 1;
+        int end = e.str_len;
+        if (p.causal) end = min(end, pos_lo + 1);
+        if (p.window >= 0) {
+          if (!p.causal) end = min(end, pos_lo + p.window + 1);
+          inner = max(pos_hi - p.window + BN - 1, 0) / BN - e.skip;
+          if (e.skip > 0) inner = max(inner, e.n_first);  // the first keys' tiles are masked
+        }
+        outer = max(end, 0) / BN - e.skip - e.j0 - lo;
+        inner -= p.window >= 0 ? e.j0 + lo : 0;
       }
       float m_ref = -INFINITY;  // reference maximum, log2 units
       float l = 0.0f;           // sum of 2^(c s - m_ref + kBias)
@@ -397,14 +415,9 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           ptx::tc_fence_before();
           ptx::mbar_arrive_after(bar(C::B_SFREE), __uint_as_float(sr[3][31]));
         }
-        const int key0 = tile_of(e, lo + j) * BN;
-        const int pos_lo = e.pos + t * p.tok;
-        const bool edge =
-            key0 + BN > e.str_len || (p.causal && key0 + BN - 1 > pos_lo) ||
-            (p.window >= 0 && (key0 < pos_lo + min(e.own_n - t * p.tok, p.tok) - 1 - p.window ||
-                               (!p.causal && key0 + BN - 1 > pos_lo + p.window)));
-        if (edge) {
-          const int pos = pos_lo + rt;
+        if (j < inner || j >= outer) {
+          const int key0 = tile_of(e, lo + j) * BN;
+          const int pos = e.pos + t * p.tok + rt;
           int lim = e.str_len - key0;  // columns [first, lim) are legal, and those below `sink`
           if (p.causal) lim = min(lim, pos + 1 - key0);
           int first = 0, sink = 0;
@@ -567,34 +580,59 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         const float inv = l == 0.0f ? 0.0f : v_mul / l;  // no legal key: zeros
         const long long row = (long long)e.own_row + t * p.tok + rt;
         const int head_q = e.hk * p.group + r - rt * p.group;
-        uint16_t* orow = p.out + (row_valid ? row * p.out_ts + head_q * p.out_hs : 0);
+        const long long at = row_valid ? row * p.out_ts + head_q * p.out_hs : -1;
+        const uint32_t stage = SINGLE ? s_q((n_q - 1) % C::Q_BUFS) + (warp & 3) * 4096 : s_base + C::OFF_STAGE + warp * 4096;
 #pragma unroll
-        for (int q4 = 0; q4 < D / 32; ++q4) {
-          uint32_t o[32];
-          if (n_tiles > 0) {
-            ptx::tmem_ld32(t_o + q4 * 32, o);
-            ptx::tmem_wait_ld();
+        for (int c64 = 0; c64 < D / 64; ++c64) {
+          uint32_t w[32];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t o[32];
+            if (n_tiles > 0) {
+              ptx::tmem_ld32(t_o + c64 * 64 + half * 32, o);
+              ptx::tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = 0u;
+            }
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+              w[half * 16 + x] = ptx::pack_bf16x2(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
+          }
+          if (C::STAGED && (!SINGLE || e.n > 0)) {
+            // through shared memory (16-byte units swizzled by the row), so that eight lanes store one row's
+            // 128 bytes: a lane's own row would be 16 bytes of 32 lines in every store
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              ptx::st_shared_v4(stage + lane * 128 + ((u ^ (lane & 7)) << 4), w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int from = i * 4 + (lane >> 3);
+              const long long to = __shfl_sync(0xffffffffu, at, from);
+              const uint4 v = ld_shared_v4(stage + from * 128 + (((lane & 7) ^ (from & 7)) << 4));
+              if (to >= 0) *reinterpret_cast<uint4*>(p.out + to + c64 * 64 + (lane & 7) * 8) = v;
+            }
           } else {
+            if (row_valid) {
+              uint4* dst = reinterpret_cast<uint4*>(p.out + at + c64 * 64);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = 0u;
+              for (int x = 0; x < 8; ++x) dst[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+            }
+            __syncwarp();
           }
-          uint32_t w[16];
-#pragma unroll
-          for (int x = 0; x < 16; ++x)
-            w[x] = ptx::pack_bf16x2(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
-          if (row_valid) {
-            uint4* dst = reinterpret_cast<uint4*>(orow + q4 * 32);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) dst[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
-          }
-          __syncwarp();
         }
         if (row_valid && p.lse)
           p.lse[row * p.h_q + head_q] =
               l == 0.0f ? -INFINITY : (m_ref - (RAW ? kBias : 0.0f) + __log2f(l)) * 0.69314718055994530942f;
       }
+      if (SINGLE && e.n > 0) ptx::fence_proxy_async_smem();  // Q's place: before the copies of another Q
       __syncwarp();
-      if (lane == 0) unit_done(un);
+      if (lane == 0) {
+        if (SINGLE && e.n > 0) ptx::mbar_arrive(bar(C::B_QEMPTY + (n_q - 1) % C::Q_BUFS));
+        unit_done(un);
+      }
     }
   } else if (RAW && warp >= C::WARP_CVT) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CVT));
@@ -651,9 +689,9 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
       const uint64_t pol_q = ptx::policy_evict_first();
       const uint64_t pol_kv = ptx::policy_evict_last();
       const plan::Header head = *p.head;
-      plan::Turn turn(head, p.range);
+      plan::Turn turn(head, p.range, p.h_kv);
       auto next_unit = [&]() -> int { return __shfl_sync(0xffffffffu, lane == 0 ? turn.next(p.head) : 0, 0); };
-      auto word_of = [&](int u) -> int { return u < 0 ? -1 : lane < 16 ? reinterpret_cast<const int*>(p.list + u)[lane] : 0; };
+      auto word_of = [&](int u) -> int { return turn.word(p.list, u, lane & 15); };
       int word = word_of(next_unit());  // lane x: word x of the entry; all -1: no more units
       uint32_t n_q = 0;   // units with keys so far
       uint32_t n_kv = 0;  // tiles so far
@@ -833,7 +871,6 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
             pos.step(2);
           }
           if (!ok) break;
-          ptx::mma_commit(bar(C::B_QEMPTY + qb));
         }
         if (!ok) {
           ptx::mma_commit(bar(C::B_DRAIN));

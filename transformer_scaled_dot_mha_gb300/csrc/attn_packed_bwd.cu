@@ -94,7 +94,7 @@ struct BwdParams {
   uint16_t* g0;        // dK, or dQ
   uint16_t* g1;        // dV
   long long g0_ts, g0_hs, g1_ts, g1_hs;
-  int group, tok, T_q;
+  int group, tok, T_q, h_kv;
   int causal, window;
   float scale, scale_log2;
   float* part;  // [slots][T][accumulator columns]
@@ -305,9 +305,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     // ================================================================ copies
     uint32_t n_a = 0;  // units with tiles so far
     const plan::Header head = *p.head;
-    plan::Turn turn(head, p.range);
+    plan::Turn turn(head, p.range, p.h_kv);
     auto next_unit = [&]() -> int { return __shfl_sync(0xffffffffu, lane == 0 ? turn.next(p.head) : 0, 0); };
-    auto word_of = [&](int u) -> int { return u < 0 ? -1 : lane < 16 ? reinterpret_cast<const int*>(p.list + u)[lane] : 0; };
+    auto word_of = [&](int u) -> int { return turn.word(p.list, u, lane & 15); };
     int word = word_of(next_unit());  // lane x: word x of the entry; all -1: no more units
     {
       for (uint32_t un = 0;; ++un) {
@@ -886,6 +886,7 @@ int run(const PackedBwdArgs& a, PFN_encodeTiled enc, void* workspace) {
   p.group = s.group;
   p.tok = s.tok;
   p.T_q = a.T_q;
+  p.h_kv = a.h_kv;
   p.causal = a.causal;
   p.window = a.window;
   p.scale = a.scale;

@@ -50,7 +50,7 @@ struct Join {  // 32 bytes: a unit that was cut
 
 struct Header {
   int cut;      // 1: CTA a takes entries [range[a].x, range[a].y); 0: the next of n_units, as CTAs ask
-  int n_units;
+  int n_units;  // whole: unit u is the list's entry u / h_kv, head u % h_kv
   int n_join;
   int next;     // units handed out so far, when they are whole
 };
@@ -357,6 +357,14 @@ __device__ __forceinline__ void write(const Args& a, Scratch& sh) {
     if (t < BINS) sh.bin[t] = (int)before;
   }
   __syncthreads();
+  if (!cut) {
+    for (int i = t; i < N; i += THREADS) {
+      const Entry e = i == t ? mine : find(i);
+      put(a.list + sh.bin[bin_of(max(e.n, 1))] + rank[i], e);
+    }
+    if (t == 0) a.head->n_join = 0;
+    return;
+  }
   const bool narrow = work < (1LL << 30);
   for (long long u0 = 0; u0 < units; u0 += THREADS) {
     const long long u = u0 + t;
@@ -366,13 +374,9 @@ __device__ __forceinline__ void write(const Args& a, Scratch& sh) {
     Entry e = u == t && t < N ? mine : find(i);
     const int cost = max(e.n, 1);
     e.hk = hk;
-    if (!cut) {
-      put(a.list + ((size_t)sh.bin[bin_of(cost)] + rank[i]) * a.h_kv + hk, e);
-    } else {
-      const long long w0 = at[i] * a.h_kv + (long long)hk * cost;
-      if (narrow) cut_unit<unsigned>(a, sh, e, i * a.h_kv + hk, (unsigned)w0, (unsigned)cost, (unsigned)share, (unsigned)work);
-      else cut_unit<long long>(a, sh, e, i * a.h_kv + hk, w0, cost, share, work);
-    }
+    const long long w0 = at[i] * a.h_kv + (long long)hk * cost;
+    if (narrow) cut_unit<unsigned>(a, sh, e, i * a.h_kv + hk, (unsigned)w0, (unsigned)cost, (unsigned)share, (unsigned)work);
+    else cut_unit<long long>(a, sh, e, i * a.h_kv + hk, w0, cost, share, work);
   }
   __syncthreads();
   if (t == 0) a.head->n_join = sh.joins;
@@ -388,7 +392,8 @@ static __global__ void __launch_bounds__(THREADS, 1) attn_plan_kernel(const Args
 struct Turn {
   int at, end;  // cut: the rest of this CTA's range
   bool cut;
-  __device__ __forceinline__ Turn(const Header& h, const int2* range) : cut(h.cut != 0) {
+  int h_kv;
+  __device__ __forceinline__ Turn(const Header& h, const int2* range, int h_kv_) : cut(h.cut != 0), h_kv(h_kv_) {
     at = cut ? range[blockIdx.x].x : (int)blockIdx.x;
     end = cut ? range[blockIdx.x].y : h.n_units;
   }
@@ -400,6 +405,13 @@ struct Turn {
       at = atomicAdd(&head->next, 1);
     }
     return u;
+  }
+  // Word x of unit u's entry, x < 16; all are -1 for no unit.
+  __device__ __forceinline__ int word(const Entry* list, int u, int x) const {
+    if (u < 0) return -1;
+    const int i = cut ? u : u / h_kv;
+    if (!cut && x == 15) return u - i * h_kv;
+    return reinterpret_cast<const int*>(list + i)[x];
   }
 };
 
