@@ -22,19 +22,18 @@
 // adds the pieces up.
 //
 // Tiles. As in attn_fwd_tc.cu: at d = 64 a CTA has one row tile, two CTAs share an SM, and P has
-// TMEM columns of its own; at d = 128 a CTA has two row tiles, P written over S. Keys come as
+// TMEM columns of its own; at d = 128, and with pages, whose copies cost more, a CTA has two row
+// tiles, P written over S. Keys come as
 // 128-row tiles through a shared-memory ring:
 //   dense   one TMA box per 64 columns;
-//   pages   a tile is 128 / r boxes of r rows, r = gcd(page size, 128), so that no box crosses a
-//           page or a tile; a lane of the copy warp looks up the page of its boxes and issues
-//           them. Rows of no page (a bad entry, or behind the length) are boxes outside the
-//           tensor: zeros. Bad entries' keys are masked by bits that go with the tile.
-//   8 bits  the boxes land in a raw tile, and four more warps turn it into the f16 tile that the
+//   pages   warps for K and warps for V copy a tile row by row with cp.async, page numbers looked
+//           up ahead. Rows of no page (a bad entry, or behind the length) are zeros. Bad entries'
+//           keys are masked by bits that go with the tile.
+//   8 bits  the rows land in a raw tile, and four more warps turn it into the f16 tile that the
 //           products read: exact, as f16 holds every e4m3 number (the scales are folded into the
 //           exponent's factor and the last division). An MMA's operands are of one type, so Q
-//           becomes f16 too, each row times a power of two, and P is f16. Two row tiles at either
-//           d, so that a tile is converted once for 256 rows.
-// Values behind the sequence's end (the next sequence's rows, a page's stale rows) would meet
+//           becomes f16 too, each row times a power of two, and P is f16.
+// Dense values behind the sequence's end (the next sequence's rows) would meet
 // P = 0 in the product, and 0 times infinity or NaN is NaN: a spare warp zeroes them in shared
 // memory when the issuer of that product has seen the tile land and asks for it.
 //
@@ -78,26 +77,22 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, boo
 
 template <int D, int KIND>
 struct Cfg {
-  static constexpr bool SINGLE = D == 64 && KIND != PAGED8;
+  static constexpr bool SINGLE = D == 64 && KIND == DENSE;
   static constexpr int Q_TILES = SINGLE ? 1 : 2;
   static constexpr int ROWS = Q_TILES * BM;
   static constexpr int CTAS_PER_SM = SINGLE ? 2 : 1;
   static constexpr int CHUNKS = D / 64;
   static constexpr int CHUNK_BYTES = BM * 128;
   static constexpr int TILE_BYTES = BM * D * 2;
-  static constexpr int Q_BUFS = SINGLE ? 2 : 1;  // SINGLE: the next unit's Q is there when the last S is issued
-  static constexpr int SLOTS = SINGLE ? 5 : 4;   // K and V tiles in turn
-  static constexpr int RAW_BYTES = KIND == PAGED8 ? BN * 128 : 0;  // 128-byte row pitch for single rows at d = 64
+  static constexpr int Q_BUFS = D == 64 && KIND != PAGED8 ? 2 : 1;  // 2: the next unit's Q is there when the last S is issued
+  static constexpr int SLOTS = SINGLE ? 5 : D == 64 ? 8 : 4;        // K and V tiles in turn
+  static constexpr int RAW_BYTES = KIND == PAGED8 ? BN * D : 0;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = OFF_Q + Q_BUFS * Q_TILES * TILE_BYTES;
   static constexpr int OFF_RAW = OFF_KV + SLOTS * TILE_BYTES;  // [K, V]
   static constexpr int OFF_UNITS = OFF_RAW + 2 * RAW_BYTES;    // Entry [UNITS]
   static constexpr int OFF_FLAGS = OFF_UNITS + UNITS * 64;     // uint32 [FLAGS][8]: any, four words of key bits
-  // rows on their way out, 32 rows x 64 columns per softmax warp: a place of their own, or the unit's Q
-  // (SINGLE), or none (8-bit pages at d = 128: shared memory is full, rows are stored as they lie)
-  static constexpr bool STAGED = KIND != PAGED8 || D == 64, OWN_STAGE = STAGED && !SINGLE;
-  static constexpr int OFF_STAGE = (OFF_FLAGS + (KIND == DENSE ? 0 : FLAGS * 32) + 127) & ~127;
-  static constexpr int OFF_BAR = OWN_STAGE ? OFF_STAGE + 4 * Q_TILES * 4096 : OFF_FLAGS + (KIND == DENSE ? 0 : FLAGS * 32);
+  static constexpr int OFF_BAR = OFF_FLAGS + (KIND == DENSE ? 0 : FLAGS * 32);
   static constexpr int B_QFULL = 0;                  // [Q_BUFS]
   static constexpr int B_QEMPTY = B_QFULL + 2;       // [Q_BUFS]
   static constexpr int B_QREADY = B_QEMPTY + 2;      // PAGED8: Q in f16
@@ -111,7 +106,7 @@ struct Cfg {
   static constexpr int B_TAIL = B_TAILREQ + 1;       // they are zeroed
   static constexpr int B_RAWFULL = B_TAIL + 1;       // [K, V]
   static constexpr int B_RAWEMPTY = B_RAWFULL + 2;
-  static constexpr int B_DRAIN = B_RAWEMPTY + 2;     // [2] MMAs after an abort, one per issuer
+  static constexpr int B_DRAIN = B_RAWEMPTY + 2;     // [2] the last MMAs and commits, one per issuer
   static constexpr int B_UNITFULL = B_DRAIN + 2;     // [UNITS]
   static constexpr int B_UNITEMPTY = B_UNITFULL + UNITS;
   static constexpr int NUM_BARS = B_UNITEMPTY + UNITS;
@@ -119,19 +114,19 @@ struct Cfg {
   static constexpr int OFF_ABORT = OFF_SLOT + 4;
   static constexpr int SMEM_BYTES = OFF_ABORT + 4;
   static constexpr uint32_t TMEM_COLS = SINGLE ? 256 : 512;
-  // warps: softmax (4 per row tile); copies; MMA issuer (SINGLE: of S); tail; SINGLE: PV issuer;
-  // PAGED8: four converting warps
+  // warps: softmax (4 per row tile); units and copies; MMA issuer (SINGLE: of S); tail; SINGLE: PV issuer.
+  // PAGED: four more copy pages. PAGED8: four more convert, the third and fourth control warp copy
   static constexpr int SOFTMAX_WARPS = 4 * Q_TILES;
   static constexpr int WARP_LOAD = SOFTMAX_WARPS, WARP_MMA = SOFTMAX_WARPS + 1, WARP_TAIL = SOFTMAX_WARPS + 2,
-                       WARP_PV = SOFTMAX_WARPS + 3, WARP_CVT = SOFTMAX_WARPS + 4;
-  static constexpr int THREADS = 32 * (SOFTMAX_WARPS + 4 + (KIND == PAGED8 ? 4 : 0));
-  // readers of a unit's entry: softmax warps, MMA issuers, tail warp or converting warps
-  static constexpr int UNIT_READERS = SOFTMAX_WARPS + (SINGLE ? 2 : 1) + (KIND == PAGED8 ? 4 : 1);
-  static constexpr int REGS_CONTROL = SINGLE ? 48 : KIND == PAGED8 ? 56 : 80;
-  static constexpr int REGS_CVT = 40;
+                       WARP_PV = SOFTMAX_WARPS + 3, WARP_MORE = SOFTMAX_WARPS + 4;
+  static constexpr int THREADS = 32 * (SOFTMAX_WARPS + 4 + (KIND == DENSE ? 0 : 4));
+  // readers of a unit's entry: softmax warps, MMA issuers, tail or copying warps, converting warps
+  static constexpr int UNIT_READERS = SOFTMAX_WARPS + (SINGLE ? 2 : 1) + (KIND == DENSE ? 1 : KIND == PAGED ? 4 : 6);
+  static constexpr int REGS_CONTROL = SINGLE ? 48 : KIND == DENSE ? 80 : KIND == PAGED ? 48 : 56;
+  static constexpr int REGS_MORE = KIND == PAGED ? 48 : 40;
   static constexpr int REGS_SOFTMAX = 208;
   static constexpr int LAUNCH_REGS = (65536 / (THREADS * CTAS_PER_SM)) & ~7;
-  static_assert(128 * REGS_CONTROL + (KIND == PAGED8 ? 128 * REGS_CVT : 0) + 32 * SOFTMAX_WARPS * REGS_SOFTMAX <=
+  static_assert(128 * REGS_CONTROL + (KIND == DENSE ? 0 : 128 * REGS_MORE) + 32 * SOFTMAX_WARPS * REGS_SOFTMAX <=
                     THREADS * LAUNCH_REGS,
                 "register split");
   static constexpr uint32_t TMEM_P = SINGLE ? BN : 0;  // else P_t over S_t
@@ -168,8 +163,10 @@ struct Params {
   float scale_log2;
   float* part;  // partial results: per slot [ROWS][D] sums, [ROWS] maxima, [ROWS] row sums
   // pages
+  const uint8_t* k_pages;
+  const uint8_t* v_pages;
   const int32_t* page_table;
-  int max_pages, n_pages, page_size, box;  // box: rows per copy
+  int max_pages, n_pages, page_size, box;  // box: rows that are in one page, in any tile
   int h_kv;
   const float* k_scale;
   const float* v_scale;
@@ -237,6 +234,125 @@ __device__ __forceinline__ int tile_of(const plan::Entry& e, int j) {
   return l + (l >= e.n_first ? e.skip : 0);
 }
 
+// 16 bytes global -> shared, past L1; with n = 0 zeros, and src is not read.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// Arrives on `bar` when this thread's copies so far have landed (an arrival that the barrier counts).
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// A copy warp's view of the pages: where the 128 rows of a key tile lie, and their copies into a tile (bf16:
+// 128-byte swizzle, a slab per 64 columns; 8 bits: rows of d bytes). Rows come in boxes of
+// gcd(page size, 128), which no page border cuts.
+// By cp.async and not TMA: a TMA copy of 16 rows of 128 bytes takes some 100 ns of the SM's TMA throughput.
+template <int D, int KIND>
+struct PageRows {
+  static constexpr int ROW = KIND == PAGED8 ? D : 2 * D;     // bytes
+  static constexpr int LPR = ROW / 16, RPS = 32 / LPR;       // lanes per row, rows per step of the warp
+  const Params& p;
+  const int lane, boxes, per;  // boxes per tile; tiles per look-up
+  const bool ahead;            // 32 boxes a look-up cover whole tiles: page numbers are asked for early
+  static constexpr int NONE = INT32_MIN;  // no key there
+  int id = NONE, in = 0, next_id = NONE, next_in = 0;  // of this lane's box: page number, first row in it
+  int base[4];  // lane x: first row in the pool of box x (of row x, x + 32 .. without `ahead`); -1: zeros; -2: bad page
+
+  __device__ __forceinline__ PageRows(const Params& p_, int lane_)
+      : p(p_), lane(lane_), boxes(KIND == DENSE ? 32 : BN / p_.box), per(KIND == DENSE ? 1 : max(1, 32 * p_.box / BN)),
+        ahead(KIND == DENSE || p_.box >= 4) {}
+
+  __device__ __forceinline__ void look(int key, int seq, int len, int& id_, int& in_) const {
+    id_ = NONE;
+    in_ = 0;
+    if (key < len) {
+      const int page = key / p.page_size;
+      in_ = key - page * p.page_size;
+      id_ = p.page_table[(size_t)seq * p.max_pages + page];
+    }
+  }
+  // Page numbers of list entries j .. j + per - 1 of a unit, for take(); nothing waits for them here.
+  __device__ __forceinline__ void ask(const plan::Entry& e, int j) {
+    const int at = j + lane / boxes;
+    look(at < e.n ? tile_of(e, at) * BN + lane % boxes * p.box : e.str_len, e.str_row, e.str_len, next_id, next_in);
+  }
+  __device__ __forceinline__ void take() {
+    id = next_id;
+    in = next_in;
+  }
+  __device__ __forceinline__ int place(int id_, int in_, int hk) const {
+    if (id_ == NONE) return -1;
+    if (id_ < 0 || id_ >= p.n_pages) return -2;
+    return (id_ * p.h_kv + hk) * p.page_size + in_;
+  }
+  // The rows of list entry j, whose tile starts at key0.
+  __device__ __forceinline__ void tile(int j, int key0, const plan::Entry& e) {
+    if (ahead) {
+      const int from = j % per * boxes + lane % boxes;
+      base[0] = place(__shfl_sync(0xffffffffu, id, from), __shfl_sync(0xffffffffu, in, from), e.hk);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        int i, r;
+        look(key0 + k * 32 + lane, e.str_row, e.str_len, i, r);
+        base[k] = place(i, r, e.hk);
+      }
+    }
+  }
+  __device__ __forceinline__ bool bad() const {
+    return base[0] == -2 || (!ahead && (base[1] == -2 || base[2] == -2 || base[3] == -2));
+  }
+  // Bits of the keys of bad pages (rare).
+  __device__ __forceinline__ void mark(uint32_t* bits) const {
+    if (ahead) {
+      if (lane < boxes && base[0] == -2)
+        for (int key = lane * p.box; key < (lane + 1) * p.box; ++key) atomicOr(bits + (key >> 5), 1u << (key & 31));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (base[k] == -2) atomicOr(bits + k, 1u << lane);
+    }
+  }
+  static __device__ __forceinline__ uint32_t offset(int r, int c) {  // of row r's 16-byte unit c in the tile
+    if constexpr (KIND == PAGED8) return r * ROW + c * 16;
+    else return (c >> 3) * (BM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  }
+  // Rows [r0, r0 + rows) of the tile, 64 or 128 of them.
+  __device__ __forceinline__ void copy(uint32_t dst, const uint8_t* pool, int key0, int len, int r0, int rows) const {
+    const int c = lane % LPR, r_lane = lane / LPR;
+    pool += c * 16;
+    if (ahead && p.box >= 8) {
+      // box by box, eight rows at a time (the swizzle repeats)
+      const int some = min(p.box, rows);  // rows per round
+      for (int r = r0; r < r0 + rows; r += some) {
+        const int row = __shfl_sync(0xffffffffu, base[0], r / p.box) ;
+        const int there = row < 0 ? 0 : len - key0 - r;  // rows that exist, or more
+        const uint8_t* src = pool + (size_t)(max(row, 0) + r % p.box + r_lane) * ROW;
+        const uint32_t to = dst + r * (KIND == PAGED8 ? ROW : 128);
+#pragma unroll 2
+        for (int st = 0; st < some; st += 8) {
+#pragma unroll
+          for (int y = 0; y < 8; y += RPS)
+            copy16(to + st * (KIND == PAGED8 ? ROW : 128) + offset(y + r_lane, c), src + (st + y) * ROW, st + y + r_lane < there ? 16 : 0);
+        }
+      }
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {  // small boxes, row by row
+      if (k * 32 < r0 || k * 32 >= r0 + rows) continue;
+      for (int st = 0; st < 32; st += RPS) {
+        const int r = k * 32 + st + r_lane;
+        int row = __shfl_sync(0xffffffffu, ahead ? base[0] : base[k], ahead ? r / p.box : r & 31);
+        if (ahead && row >= 0) row += r % p.box;
+        const bool there = row >= 0 && key0 + r < len;
+        copy16(dst + offset(r, c), pool + (size_t)(there ? row : 0) * ROW, there ? 16 : 0);
+      }
+    }
+  }
+};
+
 template <int D, int KIND>
 __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_SM)
     attn_packed_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -267,7 +383,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
     }
     ptx::mbar_init(bar(C::B_QREADY), 2 * BM);
     for (int s = 0; s < C::SLOTS; ++s) {
-      ptx::mbar_init(bar(C::B_FULL + s), RAW ? 4 : 1);  // converting warps, or the copies' bytes
+      // converting warps; two copy warps' lanes and lane 0 of one; or the copies' bytes
+      ptx::mbar_init(bar(C::B_FULL + s), RAW ? 4 : KIND == PAGED ? 65 : 1);
       ptx::mbar_init(bar(C::B_EMPTY + s), 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -276,7 +393,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
       ptx::mbar_init(bar(C::B_SFULL + t), KIND == DENSE ? 1 : 2);
       ptx::mbar_init(bar(C::B_PFULL + t), BM);
       ptx::mbar_init(bar(C::B_ODONE + t), 1);
-      ptx::mbar_init(bar(C::B_RAWFULL + t), 1);
+      ptx::mbar_init(bar(C::B_RAWFULL + t), 33);
       ptx::mbar_init(bar(C::B_RAWEMPTY + t), 4);
       ptx::mbar_init(bar(C::B_DRAIN + t), 1);
     }
@@ -311,6 +428,65 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
   auto unit_wait = [&](uint32_t un) -> bool { return wait_bar(bar(C::B_UNITFULL + un % UNITS), (un / UNITS) & 1, abort_flag, SINGLE); };
   auto unit_done = [&](uint32_t un) { ptx::mbar_arrive(bar(C::B_UNITEMPTY + un % UNITS)); };
   bool ok = true;
+
+  // A copying warp's part of K (kv = 0) or V (1) of all units: rows [128 part / parts, + 128 / parts) of every
+  // tile. The first of K's also leaves the bits of the keys whose pages are not there.
+  auto page_copies = [&](int kv, int part, int parts) -> bool {
+    bool good = true;
+    PageRows<D, KIND> pages(p, lane);
+    const uint8_t* pool = kv ? p.v_pages : p.k_pages;
+    uint32_t n_kv = 0;
+    Pos pos;
+    pos.step(kv);
+    bool asked = false;  // the unit's first look-up is done already
+    for (uint32_t un = 0;; ++un) {
+      good = __all_sync(0xffffffffu, unit_wait(un));
+      if (!good) break;
+      const plan::Entry& e = units[un % UNITS];
+      const int n = e.n;
+      if (n < 0) break;
+      if (pages.ahead && n > 0) {
+        if (!asked) pages.ask(e, 0);
+        pages.take();
+        asked = false;
+      }
+      for (int j = 0; j < n; ++j, ++n_kv) {
+        if (pages.ahead && j % pages.per == 0) {
+          if (j + pages.per < n) {
+            pages.ask(e, j + pages.per);
+          } else if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar(C::B_UNITFULL + (un + 1) % UNITS), ((un + 1) / UNITS) & 1))) {
+            pages.ask(units[(un + 1) % UNITS], 0);  // the next unit is known already
+            asked = true;
+          }
+        }
+        const int key0 = tile_of(e, j) * BN;
+        const uint32_t full = bar(RAW ? C::B_RAWFULL + kv : C::B_FULL + (int)pos.s);
+        pages.tile(j, key0, e);
+        good = __all_sync(0xffffffffu, wait_bar(bar(RAW ? C::B_RAWEMPTY + kv : C::B_EMPTY + (int)pos.s),
+                                                (RAW ? n_kv & 1 : pos.ph) ^ 1, abort_flag));
+        if (!good) break;
+        if (kv == 0 && part == 0) {
+          volatile uint32_t* fl = flags + (n_kv % FLAGS) * 8;
+          const bool any = __any_sync(0xffffffffu, pages.bad());
+          if (lane < 5) fl[lane] = lane == 0 && any ? 1u : 0u;
+          __syncwarp();
+          if (any) pages.mark(const_cast<uint32_t*>(fl) + 1);
+          __syncwarp();
+        }
+        pages.copy(RAW ? s_base + C::OFF_RAW + kv * C::RAW_BYTES : s_kv(pos.s), pool, key0, e.str_len, part * (BN / parts), BN / parts);
+        copies_arrive(full);
+        if (lane == 0 && part == 0) ptx::mbar_arrive(full);  // for the bits
+        if (pages.ahead && (j + 1) % pages.per == 0 && j + 1 < n) pages.take();
+        pos.step(2);
+      }
+      if (!good) break;
+      __syncwarp();
+      if (lane == 0) unit_done(un);
+      __syncwarp();
+    }
+    copies_wait();
+    return good;
+  };
 
   if (warp < C::SOFTMAX_WARPS) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
@@ -581,7 +757,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         const long long row = (long long)e.own_row + t * p.tok + rt;
         const int head_q = e.hk * p.group + r - rt * p.group;
         const long long at = row_valid ? row * p.out_ts + head_q * p.out_hs : -1;
-        const uint32_t stage = SINGLE ? s_q((n_q - 1) % C::Q_BUFS) + (warp & 3) * 4096 : s_base + C::OFF_STAGE + warp * 4096;
+        const uint32_t stage = s_q((n_q - 1) % C::Q_BUFS) + (warp & 3) * 4096;
 #pragma unroll
         for (int c64 = 0; c64 < D / 64; ++c64) {
           uint32_t w[32];
@@ -599,10 +775,10 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
             for (int x = 0; x < 16; ++x)
               w[half * 16 + x] = ptx::pack_bf16x2(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
           }
-          if (C::STAGED && (!SINGLE || e.n > 0)) {
-            // through shared memory (16-byte units swizzled by the row), so that eight lanes store one row's
-            // 128 bytes: a lane's own row would be 16 bytes of 32 lines in every store
-            __syncwarp();
+          if (SINGLE && e.n > 0) {
+            // through the unit's Q, which no S reads any more (16-byte units swizzled by the row), so that eight
+            // lanes store one row's 128 bytes: a lane's own row would be 16 bytes of 32 lines in every store
+            // (64 x 256 tokens, 16 heads: 51.0 -> 43.7 us; at d = 128, through a place of its own, 1 to 8 % slower)
 #pragma unroll
             for (int u = 0; u < 8; ++u)
               ptx::st_shared_v4(stage + lane * 128 + ((u ^ (lane & 7)) << 4), w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
@@ -634,13 +810,16 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         unit_done(un);
       }
     }
-  } else if (RAW && warp >= C::WARP_CVT) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CVT));
+  } else if (KIND == PAGED && warp >= C::WARP_MORE) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_MORE));
+    // ================================================================ pages: two warps for K, two for V
+    ok = page_copies((warp - C::WARP_MORE) >> 1, (warp - C::WARP_MORE) & 1, 2);
+  } else if (RAW && warp >= C::WARP_MORE) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_MORE));
     // ================================================================ 8 bits to f16
-    // Sixteen numbers per thread and step: D / 16 lanes a row. Rows behind the end become zero.
-    const int id = threadIdx.x - 32 * C::WARP_CVT;
+    // Sixteen numbers per thread and step: D / 16 lanes a row.
+    const int id = threadIdx.x - 32 * C::WARP_MORE;
     constexpr int LPR = D / 16, STEP = 128 / LPR;  // lanes per row, rows per step
-    const uint32_t raw_pitch = p.box == 1 ? 128u : (uint32_t)D;
     const int unit = ((id % LPR) & 3) * 2;
     uint32_t n_raw = 0;
     Pos pos;
@@ -648,21 +827,19 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
       ok = __all_sync(0xffffffffu, unit_wait(un));
       if (!ok) break;
       const plan::Entry& e = units[un % UNITS];
-      const int n = e.n, len = e.str_len;
+      const int n = e.n;
       if (n < 0) break;
       for (int j = 0; j < n && ok; ++j, ++n_raw) {
-        const int there = len - tile_of(e, j) * BN;
         for (int kv = 0; kv < 2; ++kv, pos.step(1)) {
           ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_RAWFULL + kv), n_raw & 1, abort_flag, true) &&
                                            wait_bar(bar(C::B_EMPTY + pos.s), pos.ph ^ 1, abort_flag, true));
           if (!ok) break;
-          const uint32_t src = s_base + C::OFF_RAW + kv * C::RAW_BYTES + (id / LPR) * raw_pitch + (id % LPR) * 16;
+          const uint32_t src = s_base + C::OFF_RAW + kv * C::RAW_BYTES + (id / LPR) * D + (id % LPR) * 16;
           const uint32_t slab = s_kv(pos.s) + ((id % LPR) >> 2) * C::CHUNK_BYTES;
 #pragma unroll 4
           for (int r0 = 0; r0 < BN; r0 += STEP) {
             const int r = r0 + id / LPR;
-            uint4 w = ld_shared_v4(src + r0 * raw_pitch);
-            if (r >= there) w = make_uint4(0, 0, 0, 0);
+            const uint4 w = ld_shared_v4(src + r0 * D);
             const uint32_t row = slab + r * 128;
             ptx::st_shared_v4(row + ((unit ^ (r & 7)) << 4), e4m3_pair(w.x), e4m3_pair(w.x >> 16), e4m3_pair(w.y),
                               e4m3_pair(w.y >> 16));
@@ -694,49 +871,16 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
       auto word_of = [&](int u) -> int { return turn.word(p.list, u, lane & 15); };
       int word = word_of(next_unit());  // lane x: word x of the entry; all -1: no more units
       uint32_t n_q = 0;   // units with keys so far
-      uint32_t n_kv = 0;  // tiles so far
       Pos pos;
-      // pages cut into boxes of 4 rows or more: the page table is looked up for 32 boxes at a time, ahead
-      const int boxes = KIND == DENSE ? 1 : BN / p.box;
-      const bool ahead = boxes <= 32;
-      const int per = ahead ? 32 / boxes : 1;  // tiles per look-up
-      // box `lane % boxes` of list entry l of a unit; l at or behind `end`: none
-      struct Box {
-        int row, z;  // in the page; which page and head
-        bool bad;    // a key there, but no page
-      };
-      auto look = [&](int key, int seq, int len, int hk) -> Box {
-        Box b{0, p.n_pages * p.h_kv, false};  // outside the tensor: zeros
-        if (key < len) {
-          const int page = key / p.page_size;
-          const int id = p.page_table[(size_t)seq * p.max_pages + page];
-          b.bad = id < 0 || id >= p.n_pages;
-          if (!b.bad) {
-            b.row = key - page * p.page_size;
-            b.z = id * p.h_kv + hk;
-          }
-        }
-        return b;
-      };
-      auto field = [&](int w, int x) { return __shfl_sync(0xffffffffu, w, x); };
-      auto look_ahead = [&](int w, int j) -> Box {  // boxes of tiles j .. j + per - 1 of the unit whose words are w
-        const int seq = field(w, 2), len = field(w, 3), n_first = field(w, 6), skip = field(w, 7), j0 = field(w, 8),
-                  n = field(w, 9), hk = field(w, 15);
-        const int at = j + lane / boxes, l = j0 + at;
-        if (at >= n) return Box{0, p.n_pages * p.h_kv, false};
-        return look((l + (l >= n_first ? skip : 0)) * BN + lane % boxes * p.box, seq, len, hk);
-      };
-      Box box{0, 0, false}, next_box{0, 0, false};
-      if (KIND != DENSE && ahead) box = look_ahead(word, 0);
       for (uint32_t un = 0;; ++un) {
         ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_UNITEMPTY + un % UNITS), ((un / UNITS) & 1) ^ 1, abort_flag, SINGLE));
         if (!ok) break;
         if (lane < 16) reinterpret_cast<int*>(smem + C::OFF_UNITS)[(un % UNITS) * 16 + lane] = word;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(C::B_UNITFULL + un % UNITS));
-        const int n = field(word, 9);
+        const int n = __shfl_sync(0xffffffffu, word, 9);
         if (n < 0) break;
-        const int next_word = word_of(next_unit());
+        word = word_of(next_unit());
         const plan::Entry& e = units[un % UNITS];  // stays: this warp alone replaces it
         if (n > 0) {
           const uint32_t qb = n_q % C::Q_BUFS;
@@ -752,89 +896,28 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           }
           ++n_q;
         }
-        for (int j = 0; j < n && ok; ++j, ++n_kv) {
+        for (int j = 0; KIND == DENSE && j < n && ok; ++j) {
           const int key0 = tile_of(e, j) * BN;
-          if constexpr (KIND == DENSE) {
-            for (int kv = 0; kv < 2; ++kv) {
-              ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_EMPTY + pos.s), pos.ph ^ 1, abort_flag, SINGLE));
-              if (!ok) break;
-              if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(bar(C::B_FULL + pos.s), C::TILE_BYTES);
-                for (int c = 0; c < C::CHUNKS; ++c)
-                  ptx::tma_load_3d(s_kv(pos.s) + c * C::CHUNK_BYTES, kv ? &tm_v : &tm_k, bar(C::B_FULL + pos.s), c * 64,
-                                   e.str_row + key0, e.hk, pol_kv);
-              }
-              pos.step(1);
-            }
-          } else {
-            // this tile's boxes: lane i has box i
-            Box mine{0, 0, false};
-            if (ahead) {
-              const int k = j % per, from = k * boxes + lane % boxes;
-              mine.row = __shfl_sync(0xffffffffu, box.row, from);
-              mine.z = __shfl_sync(0xffffffffu, box.z, from);
-              mine.bad = __shfl_sync(0xffffffffu, (int)box.bad, from) != 0;
-              if (k == 0) next_box = j + per < n ? look_ahead(word, j + per) : look_ahead(next_word, 0);
-              if (k == per - 1 || j == n - 1) box = next_box;
-            }
-            const uint32_t fph = RAW ? n_kv & 1 : pos.ph;
-            ok = __all_sync(0xffffffffu, wait_bar(bar(RAW ? (int)C::B_RAWEMPTY : C::B_EMPTY + (int)pos.s), fph ^ 1, abort_flag, SINGLE));
+          for (int kv = 0; kv < 2; ++kv) {
+            ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_EMPTY + pos.s), pos.ph ^ 1, abort_flag, SINGLE));
             if (!ok) break;
-            volatile uint32_t* fl = flags + (n_kv % FLAGS) * 8;
-            bool bad = ahead && lane < boxes && mine.bad;
-            if (!ahead)
-              for (int i = lane; i < boxes; i += 32) bad |= look(key0 + i * p.box, e.str_row, e.str_len, e.hk).bad;
-            const bool any = __any_sync(0xffffffffu, bad);
-            if (lane < 5) fl[lane] = lane == 0 && any ? 1u : 0u;
-            __syncwarp();
-            if (any) {
-              for (int i = lane; i < boxes; i += 32) {
-                if (ahead ? !mine.bad : !look(key0 + i * p.box, e.str_row, e.str_len, e.hk).bad) continue;
-                for (int key = i * p.box; key < (i + 1) * p.box; ++key)
-                  atomicOr(const_cast<uint32_t*>(fl) + 1 + (key >> 5), 1u << (key & 31));
-              }
-              __syncwarp();
+            if (lane == 0) {
+              ptx::mbar_arrive_expect_tx(bar(C::B_FULL + pos.s), C::TILE_BYTES);
+              for (int c = 0; c < C::CHUNKS; ++c)
+                ptx::tma_load_3d(s_kv(pos.s) + c * C::CHUNK_BYTES, kv ? &tm_v : &tm_k, bar(C::B_FULL + pos.s), c * 64,
+                                 e.str_row + key0, e.hk, pol_kv);
             }
-            const uint32_t pitch = RAW ? max(p.box * D, 128) : p.box * 128;
-            for (int kv = 0; kv < 2; ++kv) {
-              const int full_i = RAW ? C::B_RAWFULL + kv : C::B_FULL + (int)pos.s;
-              const uint32_t full = bar(full_i), dst = RAW ? s_base + C::OFF_RAW + kv * C::RAW_BYTES : s_kv(pos.s);
-              if (kv) {
-                ok = __all_sync(0xffffffffu, wait_bar(bar(RAW ? C::B_RAWEMPTY + 1 : C::B_EMPTY + (int)pos.s),
-                                                      (RAW ? n_kv & 1 : pos.ph) ^ 1, abort_flag, SINGLE));
-                if (!ok) break;
-              }
-              if (lane == 0) ptx::mbar_arrive_expect_tx(full, RAW ? BN * D : C::TILE_BYTES);
-              __syncwarp();
-              for (int i = lane; i < boxes; i += 32) {
-                const Box b = ahead ? mine : look(key0 + i * p.box, e.str_row, e.str_len, e.hk);
-                if constexpr (RAW) {
-                  ptx::tma_load_3d(dst + i * pitch, kv ? &tm_v : &tm_k, full, 0, b.row, b.z, pol_kv);
-                } else {
-                  for (int c = 0; c < C::CHUNKS; ++c)
-                    ptx::tma_load_3d(dst + c * C::CHUNK_BYTES + i * pitch, kv ? &tm_v : &tm_k, full, c * 64, b.row, b.z, pol_kv);
-                }
-              }
-              __syncwarp();
-              pos.step(1);
-            }
+            pos.step(1);
           }
         }
         if (!ok) break;
-        if (KIND != DENSE && ahead && n == 0) box = look_ahead(next_word, 0);
-        word = next_word;
       }
       if (!ok && lane == 0) {
         // copies in flight must land before this CTA's shared memory goes away: every barrier's last
         // phase that was armed, told by its parity after the last use of the slot
         for (int b = 0; b < C::Q_BUFS; ++b)
           if (n_q > (uint32_t)b) drain_wait(bar(C::B_QFULL + b), ((n_q - 1 - b) / C::Q_BUFS) & 1);
-        if (RAW) {
-          for (int kv = 0; kv < 2; ++kv) {
-            if (n_kv > 0) drain_wait(bar(C::B_RAWFULL + kv), (n_kv - 1) & 1);
-            drain_wait(bar(C::B_RAWFULL + kv), n_kv & 1);
-          }
-        } else {
+        if (KIND == DENSE) {
           for (int s = 0; s < C::SLOTS; ++s) drain_wait(bar(C::B_FULL + s), s < (int)pos.s ? pos.ph : pos.ph ^ 1);
         }
       }
@@ -854,9 +937,13 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           ok = wait_bar(bar(C::B_QFULL + qb), (n_q / C::Q_BUFS) & 1, abort_flag, true);
           ++n_q;
           for (int j = 0; j < n && ok; ++j, ++tiles) {
-            ok = wait_bar(bar(C::B_FULL + pos.s), pos.ph, abort_flag, true) &&
-                 (tiles == 0 || wait_bar(bar(C::B_SFREE), (tiles - 1) & 1, abort_flag, true));
+            // S loaded first: with an odd number of places this one's last phase was a V tile's, which only the
+            // PV issuer waits for, and a wait for a phase is a wait for its parity. That S(j - 1) was loaded says
+            // that P(j - 2) was stored, so PV(j - 3), which read that tile, is complete.
+            ok = (tiles == 0 || wait_bar(bar(C::B_SFREE), (tiles - 1) & 1, abort_flag, true)) &&
+                 wait_bar(bar(C::B_FULL + pos.s), pos.ph, abort_flag, true);
             if (!ok) break;
+            if (KIND == PAGED) ptx::fence_proxy_async_smem();  // written by cp.async, read by the tensor cores
             ptx::tc_fence_after();
             const uint32_t k_tile = s_kv(pos.s);
 #pragma unroll
@@ -872,10 +959,10 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           }
           if (!ok) break;
         }
-        if (!ok) {
-          ptx::mma_commit(bar(C::B_DRAIN));
-          drain_wait(bar(C::B_DRAIN), 0);
-        }
+        // every MMA and every arrival of this warp's commits is done before the CTA's shared memory goes: the
+        // last commits may come after those that the softmax has waited for
+        ptx::mma_commit(bar(C::B_DRAIN));
+        drain_wait(bar(C::B_DRAIN), 0);
       }
       __syncwarp();
     } else if (SINGLE && warp == C::WARP_PV) {
@@ -890,7 +977,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           const int n = e.n, len = e.str_len;
           if (n < 0) break;
           for (int j = 0; j < n && ok; ++j, ++tiles) {
-            const bool tail = (tile_of(e, j) + 1) * BN > len;
+            const bool tail = KIND == DENSE && (tile_of(e, j) + 1) * BN > len;
             ok = wait_bar(bar(C::B_FULL + pos.s), pos.ph, abort_flag, true);
             if (!ok) break;
             if (tail) ptx::mbar_arrive(bar(C::B_TAILREQ));
@@ -898,6 +985,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
                  (!tail || wait_bar(bar(C::B_TAIL), tails & 1, abort_flag, true));
             if (!ok) break;
             tails += tail;
+            if (KIND == PAGED) ptx::fence_proxy_async_smem();
             ptx::tc_fence_after();
             const uint32_t v_tile = s_kv(pos.s);
 #pragma unroll
@@ -912,10 +1000,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           if (!ok) break;
           unit_done(un);
         }
-        if (!ok) {
-          ptx::mma_commit(bar(C::B_DRAIN + 1));
-          drain_wait(bar(C::B_DRAIN + 1), 0);
-        }
+        ptx::mma_commit(bar(C::B_DRAIN + 1));
+        drain_wait(bar(C::B_DRAIN + 1), 0);
       }
       __syncwarp();
     } else if (!SINGLE && warp == C::WARP_MMA) {
@@ -925,7 +1011,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
       // keys are on their way. Only where a unit starts do both PVs come first, since S needs
       // the new Q.
       if (lane == 0) {
-        uint32_t n_q = 0, tails = 0;
+        uint32_t n_q = 0, qb = 0, tails = 0;
         uint32_t cnt0 = 0, cnt1 = 0;  // key tiles of row tile 0 and 1 so far
         bool pend = false, pend0 = false, pend1 = false, acc0 = false, acc1 = false, pend_tail = false;  // PVs not yet issued
         Pos kpos, vpos;  // this tile's keys; the values of the PVs not yet issued
@@ -943,7 +1029,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           return true;
         };
         auto issue_s = [&](int t) {
-          const uint32_t q_tile = s_q(0) + t * C::TILE_BYTES, k_tile = s_kv(kpos.s);
+          const uint32_t q_tile = s_q(qb) + t * C::TILE_BYTES, k_tile = s_kv(kpos.s);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t koff = (kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32;
@@ -956,6 +1042,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         // the values for the PVs still to come have landed
         auto values = [&]() -> bool {
           if (!wait_bar(bar(C::B_FULL + vpos.s), vpos.ph, abort_flag)) return false;
+          if (KIND == PAGED) ptx::fence_proxy_async_smem();
           if (!pend_tail) return true;
           ptx::mbar_arrive(bar(C::B_TAILREQ));
           pend_tail = false;
@@ -978,12 +1065,14 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           if (n < 0) break;
           const int lo0 = e.lo0, hi0 = e.hi0, lo1 = e.lo1, hi1 = e.hi1;
           if (n > 0) {
-            ok = wait_bar(bar(RAW ? C::B_QREADY : C::B_QFULL), n_q & 1, abort_flag);
+            qb = n_q % C::Q_BUFS;
+            ok = wait_bar(bar(RAW ? C::B_QREADY : C::B_QFULL + (int)qb), (n_q / C::Q_BUFS) & 1, abort_flag);
             ++n_q;
           }
           for (int j = 0; j < n && ok; ++j) {
             ok = wait_bar(bar(C::B_FULL + kpos.s), kpos.ph, abort_flag) && (!pend || values());
             if (!ok) break;
+            if (KIND == PAGED) ptx::fence_proxy_async_smem();  // written by cp.async, read by the tensor cores
             ptx::tc_fence_after();
             if (pend && pend0 && !(ok = issue_pv(0, cnt0, acc0))) break;
             const bool in0 = j >= lo0 && j < hi0, in1 = j >= lo1 && j < hi1;
@@ -1007,19 +1096,22 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
             pend1 = in1;
             acc0 = j > lo0;
             acc1 = j > lo1;
-            pend_tail = !RAW && (tile_of(e, j) + 1) * BN > len;
+            pend_tail = KIND == DENSE && (tile_of(e, j) + 1) * BN > len;
           }
           if (!ok) break;
-          if (n > 0) ptx::mma_commit(bar(C::B_QEMPTY));
+          if (n > 0) ptx::mma_commit(bar(C::B_QEMPTY + qb));
           unit_done(un);
         }
-        if (!ok) {
-          ptx::mma_commit(bar(C::B_DRAIN));
-          drain_wait(bar(C::B_DRAIN), 0);
-        }
+        // every MMA and every arrival of this warp's commits is done before the CTA's shared memory goes: the
+        // last commits may come after those that the softmax has waited for
+        ptx::mma_commit(bar(C::B_DRAIN));
+        drain_wait(bar(C::B_DRAIN), 0);
       }
       __syncwarp();
-    } else if (!RAW && warp == C::WARP_TAIL) {
+    } else if (RAW && (warp == C::WARP_TAIL || warp == C::WARP_PV)) {
+      // ================================================================ 8-bit pages: a warp for V, one for K
+      ok = page_copies(warp == C::WARP_TAIL, 0, 1);
+    } else if (KIND == DENSE && warp == C::WARP_TAIL) {
       // ================================================================ values behind the end: zero
       uint32_t tails = 0;
       Pos pos;
@@ -1166,17 +1258,15 @@ CUresult encode_q(PFN_encodeTiled enc, CUtensorMap* map, const PackedArgs& a, in
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-// (d, row, z) with the given strides in elements.
-CUresult encode_rows(PFN_encodeTiled enc, CUtensorMap* map, const void* base, int d, long long rows, long long z,
-                     long long row_stride, long long z_stride, int box_rows, bool bytes) {
-  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)z};
-  const int size = bytes ? 1 : 2;
-  cuuint64_t strides[2] = {(cuuint64_t)row_stride * size, (cuuint64_t)z_stride * size};
-  cuuint32_t box[3] = {(cuuint32_t)(bytes ? d : 64), (cuuint32_t)box_rows, 1};
+// k or v [T, heads, d] as (d, token, head): a key tile is one box per 64 columns.
+CUresult encode_rows(PFN_encodeTiled enc, CUtensorMap* map, const void* base, int d, long long rows, int heads,
+                     long long ts, long long hs) {
+  cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)heads};
+  cuuint64_t strides[2] = {(cuuint64_t)ts * 2, (cuuint64_t)hs * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)BN, 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  return enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
-             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
@@ -1234,14 +1324,12 @@ int run(const PackedArgs& a, PFN_encodeTiled enc, void* workspace) {
   CUtensorMap mq, mk, mv;
   const int box = KIND == DENSE ? BN : gcd_128(a.page_size);
   if (encode_q(enc, &mq, a, D, g.group, g.tok) != CUDA_SUCCESS) return ATTN_ERR_UNSUPPORTED;
-  for (int x = 0; x < 2; ++x) {
-    const CUresult st =
-        KIND == DENSE
-            ? encode_rows(enc, x ? &mv : &mk, x ? a.v : a.k, D, a.T_k, a.h_kv, x ? a.v_ts : a.k_ts, x ? a.v_hs : a.k_hs,
-                          BN, false)
-            : encode_rows(enc, x ? &mv : &mk, x ? a.v : a.k, D, a.page_size, (long long)a.n_pages * a.h_kv, D,
-                          (long long)D * a.page_size, box, KIND == PAGED8);
-    if (st != CUDA_SUCCESS) return ATTN_ERR_UNSUPPORTED;
+  if (KIND == DENSE) {
+    if (encode_rows(enc, &mk, a.k, D, a.T_k, a.h_kv, a.k_ts, a.k_hs) != CUDA_SUCCESS ||
+        encode_rows(enc, &mv, a.v, D, a.T_k, a.h_kv, a.v_ts, a.v_hs) != CUDA_SUCCESS)
+      return ATTN_ERR_UNSUPPORTED;
+  } else {
+    mk = mv = mq;  // not read
   }
   const long long reach = KIND == DENSE ? a.T_k : (long long)a.max_pages * a.page_size;
   // no sequence has more tiles than a CTA's least share, so none is longer than one: nothing to cut
@@ -1282,6 +1370,8 @@ int run(const PackedArgs& a, PFN_encodeTiled enc, void* workspace) {
   p.sinks = a.sinks;
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634074);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + g.plan_bytes);
+  p.k_pages = static_cast<const uint8_t*>(a.k);
+  p.v_pages = static_cast<const uint8_t*>(a.v);
   p.page_table = a.page_table;
   p.max_pages = a.max_pages;
   p.n_pages = a.n_pages;
