@@ -230,3 +230,36 @@ def test_two_graphs_share_a_workspace_and_lengths_change():
                 continue
             want, _ = run(q, k, v, q_at, q_at, True)
             assert torch.equal(out[:900], want[:900])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_calls_in_a_row_over_more_than_the_l2(d):
+    """Hundreds of calls that nothing waits between, over inputs that the L2 cannot hold: short row tiles
+    and long key lists, whose copies come late. (Once a wait for a tile passed early here.)"""
+    g = torch.Generator().manual_seed(19)
+    h, i32 = 16, lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    q_lens = [1 + 257 * i // 47 for i in range(48)]
+    k_lens = [[33 + 988 * int(i) // 47 for i in torch.randperm(48, generator=g)] for _ in range(3)]
+    T_q, T_k = sum(q_lens), sum(k_lens[0])
+    states = []
+    for k_len in k_lens:
+        q, k, v = (torch.randn(h, n, d, device="cuda").bfloat16().transpose(0, 1) for n in (T_q, T_k, T_k))
+        ws = torch.empty(attn.attn_packed_fwd_workspace_size(T_q, 48, h, h, d), dtype=torch.uint8, device="cuda")
+        states.append((q, k, v, torch.empty(T_q, h, d, dtype=torch.bfloat16, device="cuda"), i32(starts(q_lens)), ws,
+                       i32(starts(k_len))))
+    want = []
+    for s in states:
+        attn.attn_packed_fwd(*s[:6], k_starts=s[6])
+        torch.cuda.synchronize()
+        want.append(s[3].clone())
+    for s, w, k_len in zip(states, want, k_lens):
+        at, ka = starts(q_lens), starts(k_len)
+        out, _, qb, _ = ref.packed(*s[:3], at, ka, 1 / math.sqrt(d), False)
+        assert torch.all((w.double() - out).abs() <= 6 * qb)
+    for i in range(600):
+        s = states[i % 3]
+        attn.attn_packed_fwd(*s[:6], k_starts=s[6])
+    torch.cuda.synchronize()
+    assert attn.attn_fault_status() == (attn.ATTN_OK, 0)
+    for s, w in zip(states, want):
+        assert torch.equal(s[3], w)

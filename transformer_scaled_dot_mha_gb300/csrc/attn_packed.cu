@@ -66,6 +66,7 @@ constexpr int UNITS = 4;    // units whose entries a CTA holds at a time
 constexpr int FLAGS = 8;    // tiles whose page bits are held: more than the roles are apart
 constexpr int kMinShare = 2;   // tiles
 constexpr int kMaxDeal = 2;    // units per CTA above which they are not cut
+constexpr int kTmaShift = 5;   // 2^5 rows of a page or more go by one TMA copy, fewer by cp.async
 constexpr float kBias = 7.0f;  // P in f16 is 2^7 times the weight
 
 enum { DENSE = 0, PAGED = 1, PAGED8 = 2 };
@@ -122,6 +123,7 @@ struct Cfg {
   static constexpr int THREADS = 32 * (SOFTMAX_WARPS + 4 + (KIND == DENSE ? 0 : 4));
   // readers of a unit's entry: softmax warps, MMA issuers, tail or copying warps, converting warps
   static constexpr int UNIT_READERS = SOFTMAX_WARPS + (SINGLE ? 2 : 1) + (KIND == DENSE ? 1 : KIND == PAGED ? 4 : 6);
+  static constexpr bool SLEEPY = SINGLE || KIND != DENSE;  // control warps' waits suspend: fewer issue slots taken
   static constexpr int REGS_CONTROL = SINGLE ? 48 : KIND == DENSE ? 80 : KIND == PAGED ? 48 : 56;
   static constexpr int REGS_MORE = KIND == PAGED ? 48 : 40;
   static constexpr int REGS_SOFTMAX = 208;
@@ -166,7 +168,7 @@ struct Params {
   const uint8_t* k_pages;
   const uint8_t* v_pages;
   const int32_t* page_table;
-  int max_pages, n_pages, page_size, box;  // box: rows that are in one page, in any tile
+  int max_pages, n_pages, page_size, box_shift;  // boxes of 2^box_shift rows are in one page, in any tile
   int h_kv;
   const float* k_scale;
   const float* v_scale;
@@ -247,21 +249,24 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;
 // A copy warp's view of the pages: where the 128 rows of a key tile lie, and their copies into a tile (bf16:
 // 128-byte swizzle, a slab per 64 columns; 8 bits: rows of d bytes). Rows come in boxes of
 // gcd(page size, 128), which no page border cuts.
-// By cp.async and not TMA: a TMA copy of 16 rows of 128 bytes takes some 100 ns of the SM's TMA throughput.
+// Boxes of 32 rows and more go by TMA, smaller and partly filled ones by cp.async: a TMA copy, whatever its
+// size, takes some 100 ns of one warp's time, in which cp.async moves 2 KB.
 template <int D, int KIND>
 struct PageRows {
-  static constexpr int ROW = KIND == PAGED8 ? D : 2 * D;     // bytes
-  static constexpr int LPR = ROW / 16, RPS = 32 / LPR;       // lanes per row, rows per step of the warp
-  const Params& p;
-  const int lane, boxes, per;  // boxes per tile; tiles per look-up
-  const bool ahead;            // 32 boxes a look-up cover whole tiles: page numbers are asked for early
+  static constexpr int ROW = KIND == PAGED8 ? D : 2 * D;  // bytes
+  static constexpr int LPR = ROW / 16, RPS = 32 / LPR;    // lanes per row, rows per step of the warp
+  static constexpr int PITCH = KIND == PAGED8 ? ROW : 128;
   static constexpr int NONE = INT32_MIN;  // no key there
+  const Params& p;
+  const int lane, shift;  // a box has 2^shift rows
+  const bool ahead;       // 32 boxes, a look-up, cover whole tiles: page numbers are asked for early
   int id = NONE, in = 0, next_id = NONE, next_in = 0;  // of this lane's box: page number, first row in it
-  int base[4];  // lane x: first row in the pool of box x (of row x, x + 32 .. without `ahead`); -1: zeros; -2: bad page
+  int base = -1;  // lane x: first row in the pool of box x; -1: zeros; -2: bad page (not used without `ahead`)
 
   __device__ __forceinline__ PageRows(const Params& p_, int lane_)
-      : p(p_), lane(lane_), boxes(KIND == DENSE ? 32 : BN / p_.box), per(KIND == DENSE ? 1 : max(1, 32 * p_.box / BN)),
-        ahead(KIND == DENSE || p_.box >= 4) {}
+      : p(p_), lane(lane_), shift(p_.box_shift), ahead(p_.box_shift >= 2) {}
+  __device__ __forceinline__ int boxes() const { return BN >> shift; }                     // per tile
+  __device__ __forceinline__ int tiles() const { return 1 << (shift >= 2 ? shift - 2 : 0); }  // per look-up
 
   __device__ __forceinline__ void look(int key, int seq, int len, int& id_, int& in_) const {
     id_ = NONE;
@@ -272,10 +277,10 @@ struct PageRows {
       id_ = p.page_table[(size_t)seq * p.max_pages + page];
     }
   }
-  // Page numbers of list entries j .. j + per - 1 of a unit, for take(); nothing waits for them here.
+  // Page numbers of list entries j .. j + tiles() - 1 of a unit, for take(); nothing waits for them here.
   __device__ __forceinline__ void ask(const plan::Entry& e, int j) {
-    const int at = j + lane / boxes;
-    look(at < e.n ? tile_of(e, at) * BN + lane % boxes * p.box : e.str_len, e.str_row, e.str_len, next_id, next_in);
+    const int at = j + (lane >> (7 - shift));
+    look(at < e.n ? tile_of(e, at) * BN + ((lane & (boxes() - 1)) << shift) : e.str_len, e.str_row, e.str_len, next_id, next_in);
   }
   __device__ __forceinline__ void take() {
     id = next_id;
@@ -286,70 +291,101 @@ struct PageRows {
     if (id_ < 0 || id_ >= p.n_pages) return -2;
     return (id_ * p.h_kv + hk) * p.page_size + in_;
   }
-  // The rows of list entry j, whose tile starts at key0.
-  __device__ __forceinline__ void tile(int j, int key0, const plan::Entry& e) {
-    if (ahead) {
-      const int from = j % per * boxes + lane % boxes;
-      base[0] = place(__shfl_sync(0xffffffffu, id, from), __shfl_sync(0xffffffffu, in, from), e.hk);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        int i, r;
-        look(key0 + k * 32 + lane, e.str_row, e.str_len, i, r);
-        base[k] = place(i, r, e.hk);
+  // The boxes of list entry j.
+  __device__ __forceinline__ void tile(int j, const plan::Entry& e) {
+    if (!ahead) return;
+    const int from = ((j & (tiles() - 1)) << (7 - shift)) + (lane & (boxes() - 1));
+    base = place(__shfl_sync(0xffffffffu, id, from), __shfl_sync(0xffffffffu, in, from), e.hk);
+  }
+  // Without `ahead` (pages of one or two rows, or odd ones): row 32 k + lane of the tile.
+  __device__ __forceinline__ int row_of(int k, int key0, const plan::Entry& e) const {
+    int i, r;
+    look(key0 + k * 32 + lane, e.str_row, e.str_len, i, r);
+    return place(i, r, e.hk);
+  }
+  // The bits of keys of bad pages go to fl[1 .. 4], and whether there are any to fl[0].
+  __device__ __forceinline__ void mark(uint32_t* fl, int key0, const plan::Entry& e) const {
+    bool bad = ahead && lane < boxes() && base == -2;
+    if (!ahead)
+      for (int k = 0; k < 4; ++k) bad |= row_of(k, key0, e) == -2;
+    const bool any = __any_sync(0xffffffffu, bad);
+    if (lane < 5) *(volatile uint32_t*)(fl + lane) = lane == 0 && any ? 1u : 0u;
+    __syncwarp();
+    if (any) {  // rare
+      if (ahead) {
+        if (bad)
+          for (int key = lane << shift; key < (lane + 1) << shift; ++key) atomicOr(fl + 1 + (key >> 5), 1u << (key & 31));
+      } else {
+        for (int k = 0; k < 4; ++k)
+          if (row_of(k, key0, e) == -2) atomicOr(fl + 1 + k, 1u << lane);
       }
     }
-  }
-  __device__ __forceinline__ bool bad() const {
-    return base[0] == -2 || (!ahead && (base[1] == -2 || base[2] == -2 || base[3] == -2));
-  }
-  // Bits of the keys of bad pages (rare).
-  __device__ __forceinline__ void mark(uint32_t* bits) const {
-    if (ahead) {
-      if (lane < boxes && base[0] == -2)
-        for (int key = lane * p.box; key < (lane + 1) * p.box; ++key) atomicOr(bits + (key >> 5), 1u << (key & 31));
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (base[k] == -2) atomicOr(bits + k, 1u << lane);
-    }
+    __syncwarp();
   }
   static __device__ __forceinline__ uint32_t offset(int r, int c) {  // of row r's 16-byte unit c in the tile
     if constexpr (KIND == PAGED8) return r * ROW + c * 16;
     else return (c >> 3) * (BM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
   }
-  // Rows [r0, r0 + rows) of the tile, 64 or 128 of them.
-  __device__ __forceinline__ void copy(uint32_t dst, const uint8_t* pool, int key0, int len, int r0, int rows) const {
+  // n rows from row r of the tile on, of one box that starts at row `row` of the pool; n a multiple of 8, of which
+  // `there` exist. Eight rows at a time: the swizzle repeats.
+  __device__ __forceinline__ void copy_box(uint32_t dst, const uint8_t* pool, int r, int row, int n, int there) const {
     const int c = lane % LPR, r_lane = lane / LPR;
-    pool += c * 16;
-    if (ahead && p.box >= 8) {
-      // box by box, eight rows at a time (the swizzle repeats)
-      const int some = min(p.box, rows);  // rows per round
-      for (int r = r0; r < r0 + rows; r += some) {
-        const int row = __shfl_sync(0xffffffffu, base[0], r / p.box) ;
-        const int there = row < 0 ? 0 : len - key0 - r;  // rows that exist, or more
-        const uint8_t* src = pool + (size_t)(max(row, 0) + r % p.box + r_lane) * ROW;
-        const uint32_t to = dst + r * (KIND == PAGED8 ? ROW : 128);
+    const uint8_t* src = pool + (size_t)(max(row, 0) + r_lane) * ROW + c * 16;
+    const uint32_t to = dst + r * PITCH;
 #pragma unroll 2
-        for (int st = 0; st < some; st += 8) {
+    for (int st = 0; st < n; st += 8) {
 #pragma unroll
-          for (int y = 0; y < 8; y += RPS)
-            copy16(to + st * (KIND == PAGED8 ? ROW : 128) + offset(y + r_lane, c), src + (st + y) * ROW, st + y + r_lane < there ? 16 : 0);
-        }
+      for (int y = 0; y < 8; y += RPS)
+        copy16(to + st * PITCH + offset(y + r_lane, c), src + (st + y) * ROW, st + y + r_lane < there ? 16 : 0);
+    }
+  }
+  // Rows [r0, r0 + rows) of the tile, 64 or 128 of them. Every lane arrives on `full` when its copies have
+  // landed, and lane 0 once more, for the TMA copies' bytes.
+  __device__ __forceinline__ void copy(uint32_t dst, const uint8_t* pool, const CUtensorMap* map, uint32_t full, int key0,
+                                       const plan::Entry& e, int r0, int rows) const {
+    const int len = e.str_len;
+    if (p.box_shift >= kTmaShift) {
+      // boxes whose rows are all there: by TMA, a lane each (here a box may be cut at r0)
+      const int n = min(1 << shift, rows), r = r0 + lane * n;
+      const bool mine = lane * n < rows;
+      const int first = __shfl_sync(0xffffffffu, base, (r >> shift) & 31);
+      const int row = first < 0 ? first : first + (r & ((1 << shift) - 1));
+      const bool whole = mine && row >= 0 && key0 + r + n <= len;
+      const uint32_t by_tma = __ballot_sync(0xffffffffu, whole);
+      if (lane == 0) ptx::mbar_arrive_expect_tx(full, __popc(by_tma) * n * ROW);
+      __syncwarp();
+      if (whole) {
+        for (int x = 0; x < (KIND == PAGED8 ? 1 : D / 64); ++x)
+          ptx::tma_load_2d(dst + r * PITCH + x * (BM * 128), map, full, x * 64, row, ptx::policy_evict_last());
       }
+      __syncwarp();
+      for (uint32_t rest = __ballot_sync(0xffffffffu, mine && !whole); rest; rest &= rest - 1) {
+        const int i = __ffs(rest) - 1, row_i = __shfl_sync(0xffffffffu, row, i);
+        copy_box(dst, pool, r0 + i * n, row_i, n, row_i < 0 ? 0 : len - key0 - r0 - i * n);
+      }
+      copies_arrive(full);
       return;
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {  // small boxes, row by row
-      if (k * 32 < r0 || k * 32 >= r0 + rows) continue;
-      for (int st = 0; st < 32; st += RPS) {
-        const int r = k * 32 + st + r_lane;
-        int row = __shfl_sync(0xffffffffu, ahead ? base[0] : base[k], ahead ? r / p.box : r & 31);
-        if (ahead && row >= 0) row += r % p.box;
-        const bool there = row >= 0 && key0 + r < len;
-        copy16(dst + offset(r, c), pool + (size_t)(there ? row : 0) * ROW, there ? 16 : 0);
+    if (shift >= 3) {
+      for (int b = r0 >> shift; b << shift < r0 + rows; ++b) {
+        const int row = __shfl_sync(0xffffffffu, base, b);
+        copy_box(dst, pool, b << shift, row, 1 << shift, row < 0 ? 0 : len - key0 - (b << shift));
+      }
+    } else {
+      const int c = lane % LPR, r_lane = lane / LPR;
+      for (int k = r0 >> 5; k < (r0 + rows) >> 5; ++k) {  // small boxes, row by row
+        const int rows32 = ahead ? base : row_of(k, key0, e);
+        for (int st = 0; st < 32; st += RPS) {
+          const int r = k * 32 + st + r_lane;
+          int row = __shfl_sync(0xffffffffu, rows32, ahead ? r >> shift : r & 31);
+          if (ahead && row >= 0) row += r & ((1 << shift) - 1);
+          const bool there = row >= 0 && key0 + r < len;
+          copy16(dst + offset(r, c), pool + (size_t)(there ? row : 0) * ROW + c * 16, there ? 16 : 0);
+        }
       }
     }
+    copies_arrive(full);
+    if (lane == 0) ptx::mbar_arrive(full);
   }
 };
 
@@ -383,8 +419,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
     }
     ptx::mbar_init(bar(C::B_QREADY), 2 * BM);
     for (int s = 0; s < C::SLOTS; ++s) {
-      // converting warps; two copy warps' lanes and lane 0 of one; or the copies' bytes
-      ptx::mbar_init(bar(C::B_FULL + s), RAW ? 4 : KIND == PAGED ? 65 : 1);
+      // converting warps; two copy warps' lanes and their lanes 0 again; or the copies' bytes
+      ptx::mbar_init(bar(C::B_FULL + s), RAW ? 4 : KIND == PAGED ? 66 : 1);
       ptx::mbar_init(bar(C::B_EMPTY + s), 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -425,7 +461,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
 
   // The copy warp passes the units' entries on through a ring of UNITS places; every other warp
   // runs through them in that order, each at its own pace. n < 0: no more units.
-  auto unit_wait = [&](uint32_t un) -> bool { return wait_bar(bar(C::B_UNITFULL + un % UNITS), (un / UNITS) & 1, abort_flag, SINGLE); };
+  auto unit_wait = [&](uint32_t un) -> bool { return wait_bar(bar(C::B_UNITFULL + un % UNITS), (un / UNITS) & 1, abort_flag, C::SLEEPY); };
   auto unit_done = [&](uint32_t un) { ptx::mbar_arrive(bar(C::B_UNITEMPTY + un % UNITS)); };
   bool ok = true;
 
@@ -451,9 +487,9 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         asked = false;
       }
       for (int j = 0; j < n; ++j, ++n_kv) {
-        if (pages.ahead && j % pages.per == 0) {
-          if (j + pages.per < n) {
-            pages.ask(e, j + pages.per);
+        if (pages.ahead && (j & (pages.tiles() - 1)) == 0) {
+          if (j + pages.tiles() < n) {
+            pages.ask(e, j + pages.tiles());
           } else if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar(C::B_UNITFULL + (un + 1) % UNITS), ((un + 1) / UNITS) & 1))) {
             pages.ask(units[(un + 1) % UNITS], 0);  // the next unit is known already
             asked = true;
@@ -461,22 +497,14 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         }
         const int key0 = tile_of(e, j) * BN;
         const uint32_t full = bar(RAW ? C::B_RAWFULL + kv : C::B_FULL + (int)pos.s);
-        pages.tile(j, key0, e);
+        pages.tile(j, e);
         good = __all_sync(0xffffffffu, wait_bar(bar(RAW ? C::B_RAWEMPTY + kv : C::B_EMPTY + (int)pos.s),
-                                                (RAW ? n_kv & 1 : pos.ph) ^ 1, abort_flag));
+                                                (RAW ? n_kv & 1 : pos.ph) ^ 1, abort_flag, true));
         if (!good) break;
-        if (kv == 0 && part == 0) {
-          volatile uint32_t* fl = flags + (n_kv % FLAGS) * 8;
-          const bool any = __any_sync(0xffffffffu, pages.bad());
-          if (lane < 5) fl[lane] = lane == 0 && any ? 1u : 0u;
-          __syncwarp();
-          if (any) pages.mark(const_cast<uint32_t*>(fl) + 1);
-          __syncwarp();
-        }
-        pages.copy(RAW ? s_base + C::OFF_RAW + kv * C::RAW_BYTES : s_kv(pos.s), pool, key0, e.str_len, part * (BN / parts), BN / parts);
-        copies_arrive(full);
-        if (lane == 0 && part == 0) ptx::mbar_arrive(full);  // for the bits
-        if (pages.ahead && (j + 1) % pages.per == 0 && j + 1 < n) pages.take();
+        if (kv == 0 && part == 0) pages.mark(const_cast<uint32_t*>(flags) + (n_kv % FLAGS) * 8, key0, e);
+        pages.copy(RAW ? s_base + C::OFF_RAW + kv * C::RAW_BYTES : s_kv(pos.s), pool, kv ? &tm_v : &tm_k, full, key0, e,
+                   part * (BN / parts), BN / parts);
+        if (pages.ahead && ((j + 1) & (pages.tiles() - 1)) == 0 && j + 1 < n) pages.take();
         pos.step(2);
       }
       if (!good) break;
@@ -821,6 +849,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
     const int id = threadIdx.x - 32 * C::WARP_MORE;
     constexpr int LPR = D / 16, STEP = 128 / LPR;  // lanes per row, rows per step
     const int unit = ((id % LPR) & 3) * 2;
+    const bool swap = D == 128 && (id & 4) != 0;
     uint32_t n_raw = 0;
     Pos pos;
     for (uint32_t un = 0;; ++un) {
@@ -840,11 +869,15 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           for (int r0 = 0; r0 < BN; r0 += STEP) {
             const int r = r0 + id / LPR;
             const uint4 w = ld_shared_v4(src + r0 * D);
-            const uint32_t row = slab + r * 128;
-            ptx::st_shared_v4(row + ((unit ^ (r & 7)) << 4), e4m3_pair(w.x), e4m3_pair(w.x >> 16), e4m3_pair(w.y),
-                              e4m3_pair(w.y >> 16));
-            ptx::st_shared_v4(row + (((unit + 1) ^ (r & 7)) << 4), e4m3_pair(w.z), e4m3_pair(w.z >> 16), e4m3_pair(w.w),
-                              e4m3_pair(w.w >> 16));
+            const uint32_t lo[4] = {e4m3_pair(w.x), e4m3_pair(w.x >> 16), e4m3_pair(w.y), e4m3_pair(w.y >> 16)};
+            const uint32_t hi[4] = {e4m3_pair(w.z), e4m3_pair(w.z >> 16), e4m3_pair(w.w), e4m3_pair(w.w >> 16)};
+            // d = 128: a row's lanes store their two units in opposite orders in the two slabs, so that eight
+            // lanes' units lie in eight different bank groups (at d = 64 their two rows' swizzles see to it)
+            const uint32_t row = slab + r * 128, first = swap ? 1 : 0;
+            ptx::st_shared_v4(row + (((unit + first) ^ (r & 7)) << 4), swap ? hi[0] : lo[0], swap ? hi[1] : lo[1],
+                              swap ? hi[2] : lo[2], swap ? hi[3] : lo[3]);
+            ptx::st_shared_v4(row + (((unit + 1 - first) ^ (r & 7)) << 4), swap ? lo[0] : hi[0], swap ? lo[1] : hi[1],
+                              swap ? lo[2] : hi[2], swap ? lo[3] : hi[3]);
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();
@@ -873,7 +906,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
       uint32_t n_q = 0;   // units with keys so far
       Pos pos;
       for (uint32_t un = 0;; ++un) {
-        ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_UNITEMPTY + un % UNITS), ((un / UNITS) & 1) ^ 1, abort_flag, SINGLE));
+        ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_UNITEMPTY + un % UNITS), ((un / UNITS) & 1) ^ 1, abort_flag, C::SLEEPY));
         if (!ok) break;
         if (lane < 16) reinterpret_cast<int*>(smem + C::OFF_UNITS)[(un % UNITS) * 16 + lane] = word;
         __syncwarp();
@@ -884,7 +917,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         const plan::Entry& e = units[un % UNITS];  // stays: this warp alone replaces it
         if (n > 0) {
           const uint32_t qb = n_q % C::Q_BUFS;
-          ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_QEMPTY + qb), ((n_q / C::Q_BUFS) & 1) ^ 1, abort_flag, SINGLE));
+          ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_QEMPTY + qb), ((n_q / C::Q_BUFS) & 1) ^ 1, abort_flag, C::SLEEPY));
           if (!ok) break;
           if (lane == 0) {
             const int n_qt = e.own_n > p.tok ? 2 : 1;
@@ -1241,12 +1274,6 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const JoinParams p) {
   }
 }
 
-int gcd_128(int x) {
-  int r = 1;
-  while (r < 128 && x % (2 * r) == 0) r *= 2;
-  return r;
-}
-
 // q [T, heads, d] as (d, head of the group, token, key/value head): a row tile is one box.
 CUresult encode_q(PFN_encodeTiled enc, CUtensorMap* map, const PackedArgs& a, int d, int group, int tok) {
   cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)group, (cuuint64_t)a.T_q, (cuuint64_t)a.h_kv};
@@ -1267,6 +1294,18 @@ CUresult encode_rows(PFN_encodeTiled enc, CUtensorMap* map, const void* base, in
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+// All pages' rows as (d, row): boxes of `rows` rows that no page border cuts.
+CUresult encode_pages(PFN_encodeTiled enc, CUtensorMap* map, const void* base, int d, long long all, int rows, bool bytes) {
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)all};
+  cuuint64_t strides[1] = {(cuuint64_t)d * (bytes ? 1 : 2)};
+  cuuint32_t box[2] = {(cuuint32_t)(bytes ? d : 64), (cuuint32_t)rows};
+  cuuint32_t estr[2] = {1, 1};
+  return enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             bytes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
@@ -1322,11 +1361,17 @@ int run(const PackedArgs& a, PFN_encodeTiled enc, void* workspace) {
     attr_done[dev].store(true, std::memory_order_release);
   }
   CUtensorMap mq, mk, mv;
-  const int box = KIND == DENSE ? BN : gcd_128(a.page_size);
+  int box_shift = 0;
+  while (box_shift < 7 && a.page_size % (2 << box_shift) == 0) ++box_shift;
   if (encode_q(enc, &mq, a, D, g.group, g.tok) != CUDA_SUCCESS) return ATTN_ERR_UNSUPPORTED;
   if (KIND == DENSE) {
     if (encode_rows(enc, &mk, a.k, D, a.T_k, a.h_kv, a.k_ts, a.k_hs) != CUDA_SUCCESS ||
         encode_rows(enc, &mv, a.v, D, a.T_k, a.h_kv, a.v_ts, a.v_hs) != CUDA_SUCCESS)
+      return ATTN_ERR_UNSUPPORTED;
+  } else if (box_shift >= kTmaShift) {
+    const int rows = std::min(1 << box_shift, KIND == PAGED ? BN / 2 : BN);  // at most a copy warp's part of a tile
+    if (encode_pages(enc, &mk, a.k, D, (long long)a.n_pages * a.h_kv * a.page_size, rows, KIND == PAGED8) != CUDA_SUCCESS ||
+        encode_pages(enc, &mv, a.v, D, (long long)a.n_pages * a.h_kv * a.page_size, rows, KIND == PAGED8) != CUDA_SUCCESS)
       return ATTN_ERR_UNSUPPORTED;
   } else {
     mk = mv = mq;  // not read
@@ -1376,7 +1421,7 @@ int run(const PackedArgs& a, PFN_encodeTiled enc, void* workspace) {
   p.max_pages = a.max_pages;
   p.n_pages = a.n_pages;
   p.page_size = a.page_size;
-  p.box = box;
+  p.box_shift = box_shift;
   p.h_kv = a.h_kv;
   p.k_scale = a.k_scale;
   p.v_scale = a.v_scale;
