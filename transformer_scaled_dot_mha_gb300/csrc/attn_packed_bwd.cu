@@ -53,22 +53,25 @@ constexpr uint64_t kDrainLimitNs = 200000000ull;
 constexpr uint32_t FAULT_PACKED_BWD = 1024;
 constexpr int UNITS = 4;      // units whose entries a CTA holds at a time
 constexpr int kMinShare = 2;  // tiles
-constexpr int kMaxDeal = 2;   // units per CTA above which they are not cut
+constexpr int kMaxDeal = 4;   // units per CTA above which they are not cut
 
 template <int D>
 struct BCfg {
-  static constexpr int STAGES = D == 64 ? 4 : 2;
+  static constexpr int STAGES = D == 64 ? 3 : 2;
+  static constexpr int A_BUFS = D == 64 ? 2 : 1;  // 2: the next unit's own tiles are there when the last S and dP are issued
   static constexpr int CHUNKS = D / 64;
   static constexpr int CHUNK_BYTES = T * 128;
   static constexpr int TILE_BYTES = T * D * 2;
-  static constexpr int OFF_A0 = 0;                             // K, or Q
-  static constexpr int OFF_A1 = OFF_A0 + TILE_BYTES;           // V, or dO
-  static constexpr int OFF_R0 = OFF_A1 + TILE_BYTES;           // ring: Q, or K
+  static constexpr int OFF_A0 = 0;                                      // [A_BUFS] K, or Q; and behind each
+  static constexpr int OFF_A1 = OFF_A0 + TILE_BYTES;                    // V, or dO
+  static constexpr int OFF_R0 = OFF_A0 + A_BUFS * 2 * TILE_BYTES;       // ring: Q, or K
   static constexpr int OFF_R1 = OFF_R0 + STAGES * TILE_BYTES;  // ring: dO, or V
   static constexpr int OFF_VEC = OFF_R1 + STAGES * TILE_BYTES;  // float [STAGES][-lse log2(e)[T], -D[T]]
-  static constexpr int OFF_UNITS = OFF_VEC + STAGES * 2 * T * 4;
+  // d = 64: rows on their way out, 32 per elementwise warp
+  static constexpr int OFF_STAGE = OFF_VEC + STAGES * 2 * T * 4;
+  static constexpr int OFF_UNITS = OFF_STAGE + (D == 64 ? 8 * 4096 : 0);
   static constexpr int OFF_BAR = OFF_UNITS + UNITS * 64;
-  static constexpr int B_AFULL = 0, B_AEMPTY = 1, B_FULL = 2, B_EMPTY = B_FULL + STAGES, B_MMFULL = B_EMPTY + STAGES;
+  static constexpr int B_AFULL = 0, B_AEMPTY = 2, B_FULL = 4, B_EMPTY = B_FULL + STAGES, B_MMFULL = B_EMPTY + STAGES;
   static constexpr int B_PFULL = B_MMFULL + 2, B_ACC = B_PFULL + 2, B_TAILREQ = B_ACC + 1, B_TAIL = B_TAILREQ + 2;
   static constexpr int B_DRAIN = B_TAIL + 2, B_UNITFULL = B_DRAIN + 2, B_UNITEMPTY = B_UNITFULL + UNITS,
                        NUM_BARS = B_UNITEMPTY + UNITS;
@@ -241,8 +244,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int row_tile = p.tok * p.group;  // rows of a row tile
 
   if (threadIdx.x == 0) {
-    ptx::mbar_init(bar(C::B_AFULL), 1);
-    ptx::mbar_init(bar(C::B_AEMPTY), SPLIT ? 2 : 1);
+    for (int b = 0; b < C::A_BUFS; ++b) {
+      ptx::mbar_init(bar(C::B_AFULL + b), 1);
+      ptx::mbar_init(bar(C::B_AEMPTY + b), SPLIT ? 2 : 1);
+    }
     for (int s = 0; s < STAGES; ++s) {
       ptx::mbar_init(bar(C::B_FULL + s), DKDV ? 33 : 1);  // bytes, and the copy warp's lanes for the table
       ptx::mbar_init(bar(C::B_EMPTY + s), SPLIT ? 2 : 1);
@@ -321,18 +326,19 @@ __global__ void __launch_bounds__(THREADS, 1)
         word = word_of(next_unit());
         const plan::Entry& e = units[un % UNITS];  // stays: this warp alone replaces it
         if (n == 0) continue;
-        ok = __all_sync(0xffffffffu, n_a == 0 || wait_bar(bar(C::B_AEMPTY), (n_a - 1) & 1, abort_flag));
+        const uint32_t ab = n_a % C::A_BUFS, a_full = bar(C::B_AFULL + ab);
+        ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_AEMPTY + ab), ((n_a / C::A_BUFS) & 1) ^ 1, abort_flag));
         if (!ok) break;
         if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(bar(C::B_AFULL), 2 * C::CHUNKS * (DKDV ? T : row_tile) * 128);
+          ptx::mbar_arrive_expect_tx(a_full, 2 * C::CHUNKS * (DKDV ? T : row_tile) * 128);
           for (int c = 0; c < C::CHUNKS; ++c) {
-            const uint32_t a0 = s_base + C::OFF_A0 + c * C::CHUNK_BYTES, a1 = s_base + C::OFF_A1 + c * C::CHUNK_BYTES;
+            const uint32_t a0 = s_base + C::OFF_A0 + ab * 2 * C::TILE_BYTES + c * C::CHUNK_BYTES, a1 = a0 + C::TILE_BYTES;
             if (DKDV) {
-              tma_load_rows(a0, &tm_a0, bar(C::B_AFULL), c * 64, e.own_row, e.hk);
-              tma_load_rows(a1, &tm_a1, bar(C::B_AFULL), c * 64, e.own_row, e.hk);
+              tma_load_rows(a0, &tm_a0, a_full, c * 64, e.own_row, e.hk);
+              tma_load_rows(a1, &tm_a1, a_full, c * 64, e.own_row, e.hk);
             } else {
-              tma_load_4d(a0, &tm_a0, bar(C::B_AFULL), c * 64, 0, e.own_row, e.hk);
-              tma_load_4d(a1, &tm_a1, bar(C::B_AFULL), c * 64, 0, e.own_row, e.hk);
+              tma_load_4d(a0, &tm_a0, a_full, c * 64, 0, e.own_row, e.hk);
+              tma_load_4d(a1, &tm_a1, a_full, c * 64, 0, e.own_row, e.hk);
             }
           }
         }
@@ -373,7 +379,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok) break;
       }
       if (!ok && lane == 0) {
-        if (n_a > 0) drain_wait(bar(C::B_AFULL), (n_a - 1) & 1);
+        for (int b = 0; b < C::A_BUFS; ++b)
+          if (n_a > (uint32_t)b) drain_wait(bar(C::B_AFULL + b), ((n_a - 1 - b) / C::A_BUFS) & 1);
         for (uint32_t x = ring > STAGES ? ring - STAGES : 0; x < ring; ++x) drain_wait(bar(C::B_FULL + x % STAGES), (x / STAGES) & 1);
       }
     }
@@ -384,6 +391,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // dP need the new own tiles.
     const int hs = warp - WARP_MMA;
     uint32_t n_a = 0, tails = 0;
+    uint64_t d_own = 0;  // offset of this unit's own tiles, in descriptors
     bool pend = false, pend_tail = false, first = false;  // sums of the tile before not yet issued
     const uint64_t d_a0 = ptx::sdesc_sw128(s_base + C::OFF_A0, 16, 1024);
     const uint64_t d_a1 = ptx::sdesc_sw128(s_base + C::OFF_A1, 16, 1024);
@@ -396,10 +404,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint64_t so = (uint64_t)(((x % STAGES) * C::TILE_BYTES + h * (T / 2) * 128) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        ptx::mma_ss(tmem + C::tm_x(h), d_a0 + koff16(kk), d_r0k + so + koff16(kk), C::IDESC_NN, kk > 0 ? 1u : 0u);
+        ptx::mma_ss(tmem + C::tm_x(h), d_a0 + d_own + koff16(kk), d_r0k + so + koff16(kk), C::IDESC_NN, kk > 0 ? 1u : 0u);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        ptx::mma_ss(tmem + C::tm_y(h), d_a1 + koff16(kk), d_r1k + so + koff16(kk), C::IDESC_NN, kk > 0 ? 1u : 0u);
+        ptx::mma_ss(tmem + C::tm_y(h), d_a1 + d_own + koff16(kk), d_r1k + so + koff16(kk), C::IDESC_NN, kk > 0 ? 1u : 0u);
       ptx::mma_commit(bar(C::B_MMFULL + h));
     };
     // the sums of ring use x's half h, once its P and dS are stored
@@ -451,8 +459,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             unit_done(un);
             continue;
           }
-          if (!(ok = wait_bar(bar(C::B_AFULL), n_a & 1, abort_flag))) break;
+          const uint32_t ab = n_a % C::A_BUFS;
+          if (!(ok = wait_bar(bar(C::B_AFULL + ab), (n_a / C::A_BUFS) & 1, abort_flag))) break;
           ++n_a;
+          d_own = (uint64_t)((ab * 2 * C::TILE_BYTES) >> 4);
           for (int j = 0; j < n; ++j) {
             if (!(ok = wait_bar(bar(C::B_FULL + ring % STAGES), (ring / STAGES) & 1, abort_flag))) break;
             ptx::tc_fence_after();
@@ -475,7 +485,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             ++ring;
           }
           if (!ok) break;
-          ptx::mma_commit(bar(C::B_AEMPTY));
+          ptx::mma_commit(bar(C::B_AEMPTY + ab));
           unit_done(un);
         }
         if (!ok) {
@@ -653,40 +663,75 @@ __global__ void __launch_bounds__(THREADS, 1)
             to = p.g0 + (e.own_row + rt) * p.g0_ts + (e.hk * p.group + r - rt * p.group) * p.g0_hs + g * (D / 2);
         }
         const float mul = DKDV && g == 1 ? 1.0f : p.scale;
-#pragma unroll
-        for (int q4 = 0; q4 < NCH; ++q4) {
-          uint32_t o[32];
-          if (n > 0) {
-            ptx::tmem_ld32(tmem + lane_off + col0 + q4 * 32, o);
-            if (SPLIT) {
-              uint32_t o1[32];
-              ptx::tmem_ld32(tmem + lane_off + col1 + q4 * 32, o1);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(o1[x]));
-            } else {
-              ptx::tmem_wait_ld();
-            }
-          } else {
+        auto sums = [&](int q4, uint32_t (&o)[32]) {  // 32 columns of this row
+          if (n == 0) {
 #pragma unroll
             for (int x = 0; x < 32; ++x) o[x] = 0u;
+            return;
           }
-          if (part != nullptr) {
-            if (row_valid) {
+          ptx::tmem_ld32(tmem + lane_off + col0 + q4 * 32, o);
+          if (SPLIT) {
+            uint32_t o1[32];
+            ptx::tmem_ld32(tmem + lane_off + col1 + q4 * 32, o1);
+            ptx::tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 8; ++x)
-                reinterpret_cast<uint4*>(part + q4 * 32)[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-            }
-          } else if (row_valid) {
-            uint32_t w[16];
+            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(o1[x]));
+          } else {
+            ptx::tmem_wait_ld();
+          }
+        };
+        if (D == 64 && part == nullptr) {
+          // through shared memory, so that neighbouring lanes store one row's 128 (dQ: this half's 64) bytes:
+          // units of 16 bytes, swizzled by the row
+          constexpr int U = NCH * 4;  // units per row
+          const uint32_t stage = s_base + C::OFF_STAGE + warp * 4096;
+#pragma unroll
+          for (int q4 = 0; q4 < NCH; ++q4) {
+            uint32_t o[32], w[16];
+            sums(q4, o);
 #pragma unroll
             for (int x = 0; x < 16; ++x)
               w[x] = ptx::pack_bf16x2(__uint_as_float(o[2 * x]) * mul, __uint_as_float(o[2 * x + 1]) * mul);
-            uint4* dst = reinterpret_cast<uint4*>(to + q4 * 32);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) dst[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+            for (int u = 0; u < 4; ++u)
+              ptx::st_shared_v4(stage + lane * (U * 16) + (((q4 * 4 + u) ^ (lane & (U - 1))) << 4), w[4 * u], w[4 * u + 1],
+                                w[4 * u + 2], w[4 * u + 3]);
           }
           __syncwarp();
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            const int from = i * (32 / U) + lane / U, u = lane % U;
+            uint16_t* dst = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), from));
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(stage + from * (U * 16) + ((u ^ (from & (U - 1))) << 4))
+                         : "memory");
+            if (dst != nullptr) *reinterpret_cast<uint4*>(dst + u * 8) = v;
+          }
+          __syncwarp();
+        } else {
+#pragma unroll
+          for (int q4 = 0; q4 < NCH; ++q4) {
+            uint32_t o[32];
+            sums(q4, o);
+            if (part != nullptr) {
+              if (row_valid) {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                  reinterpret_cast<uint4*>(part + q4 * 32)[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+              }
+            } else if (row_valid) {
+              uint32_t w[16];
+#pragma unroll
+              for (int x = 0; x < 16; ++x)
+                w[x] = ptx::pack_bf16x2(__uint_as_float(o[2 * x]) * mul, __uint_as_float(o[2 * x + 1]) * mul);
+              uint4* dst = reinterpret_cast<uint4*>(to + q4 * 32);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) dst[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+            }
+            __syncwarp();
+          }
         }
         if (lane == 0) unit_done(un);
         __syncwarp();
