@@ -303,6 +303,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     return DKDV ? (left >= p.tok ? T : left * p.group) : left;
   };
 
+  // All lanes of a warp together.
+  auto wait_warp = [&](uint32_t b, uint32_t parity, volatile int* flag) -> bool {
+    return __all_sync(0xffffffffu, wait_bar(b, parity, flag));
+  };
+
   uint32_t ring = 0;  // streamed tiles so far
   bool ok = true;
 
@@ -389,7 +394,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Per streamed tile and half: the sums of the tile before, then S and dP. SPLIT: a warp per half,
     // else warp WARP_MMA serves both. Where a unit starts, both halves' sums come first, since S and
     // dP need the new own tiles.
-    const int hs = warp - WARP_MMA;
+    // The whole warp runs the loops, one lane issues: what goes into descriptors and addresses is uniform.
+    auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const int hs = (int)uniform(warp - WARP_MMA);
+    const uint32_t issue = lane == 0, acc = uniform(tmem);
     uint32_t n_a = 0, tails = 0;
     uint64_t d_own = 0;  // offset of this unit's own tiles, in descriptors
     bool pend = false, pend_tail = false, first = false;  // sums of the tile before not yet issued
@@ -401,38 +409,36 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint64_t d_r1m = ptx::sdesc_sw128(s_base + C::OFF_R1, C::CHUNK_BYTES, 1024);
     auto koff16 = [](int kk) { return (uint64_t)(((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4); };
     auto issue_sdp = [&](uint32_t x, int h) {
-      const uint64_t so = (uint64_t)(((x % STAGES) * C::TILE_BYTES + h * (T / 2) * 128) >> 4);
+      const uint64_t so = (uint64_t)((uniform(x % STAGES) * C::TILE_BYTES + h * (T / 2) * 128) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        ptx::mma_ss(tmem + C::tm_x(h), d_a0 + d_own + koff16(kk), d_r0k + so + koff16(kk), C::IDESC_NN, kk > 0 ? 1u : 0u);
+        ptx::mma_ss_warp(acc + C::tm_x(h), d_a0 + d_own + koff16(kk), d_r0k + so + koff16(kk), C::IDESC_NN, kk > 0 ? 1u : 0u, issue);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        ptx::mma_ss(tmem + C::tm_y(h), d_a1 + d_own + koff16(kk), d_r1k + so + koff16(kk), C::IDESC_NN, kk > 0 ? 1u : 0u);
-      ptx::mma_commit(bar(C::B_MMFULL + h));
+        ptx::mma_ss_warp(acc + C::tm_y(h), d_a1 + d_own + koff16(kk), d_r1k + so + koff16(kk), C::IDESC_NN, kk > 0 ? 1u : 0u, issue);
+      ptx::mma_commit_warp(bar(C::B_MMFULL + h), issue);
     };
     // the sums of ring use x's half h, once its P and dS are stored
     auto issue_acc = [&](uint32_t x, int h) -> bool {
-      if (!wait_bar(bar(C::B_PFULL + h), x & 1, abort_flag)) return false;
+      if (!wait_warp(bar(C::B_PFULL + h), x & 1, abort_flag)) return false;
       ptx::tc_fence_after();
-      const uint64_t so = (uint64_t)(((x % STAGES) * C::TILE_BYTES) >> 4);
+      const uint64_t so = (uint64_t)((uniform(x % STAGES) * C::TILE_BYTES) >> 4);
       const uint32_t start = first && (SPLIT || h == 0) ? 0u : 1u;
+      // one accumulator after the other: MMAs that change it in turn run slower
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        const uint64_t brow = (uint64_t)(((h * 4 + kk) * 2048) >> 4);
-        const uint32_t accum = kk > 0 ? 1u : start;
-        if (DKDV) {
-          ptx::mma_ts(tmem + acc_col(1, h), tmem + C::tm_x(h) + kk * 8, d_r1m + so + brow, C::IDESC_ACC, accum);
-          ptx::mma_ts(tmem + acc_col(0, h), tmem + C::tm_y(h) + kk * 8, d_r0m + so + brow, C::IDESC_ACC, accum);
-        } else {
-          ptx::mma_ts(tmem + acc_col(0, h), tmem + C::tm_x(h) + kk * 8, d_r0m + so + brow, C::IDESC_ACC, accum);
+      for (int which = DKDV ? 1 : 0; which >= 0; --which)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t brow = (uint64_t)(((h * 4 + kk) * 2048) >> 4);
+          const uint32_t a = acc + (which == 0 && DKDV ? C::tm_y(h) : C::tm_x(h)) + kk * 8;
+          ptx::mma_ts_warp(acc + acc_col(which, h), a, (which ? d_r1m : d_r0m) + so + brow, C::IDESC_ACC, kk > 0 ? 1u : start, issue);
         }
-      }
       return true;
     };
     auto tail_done = [&]() -> bool {
       if (!pend_tail) return true;
       pend_tail = false;
-      return wait_bar(bar(C::B_TAIL + (SPLIT ? hs : 0)), tails++ & 1, abort_flag);
+      return wait_warp(bar(C::B_TAIL + (SPLIT ? hs : 0)), tails++ & 1, abort_flag);
     };
     // both halves (SPLIT: this warp's) of the unit's last tile; the accumulators are complete after them
     auto flush = [&]() -> bool {
@@ -442,54 +448,56 @@ __global__ void __launch_bounds__(THREADS, 1)
       } else if (!issue_acc(ring - 1, 0) || !issue_acc(ring - 1, 1)) {
         return false;
       }
-      ptx::mma_commit(bar(C::B_EMPTY + (ring - 1) % STAGES));
-      ptx::mma_commit(bar(C::B_ACC));
+      ptx::mma_commit_warp(bar(C::B_EMPTY + (ring - 1) % STAGES), issue);
+      ptx::mma_commit_warp(bar(C::B_ACC), issue);
       pend = false;
       return true;
     };
     {
-      if (lane == 0 && (SPLIT || hs == 0)) {
+      if (SPLIT || hs == 0) {
         for (uint32_t un = 0;; ++un) {
           if (pend && !(ok = flush())) break;
-          if (!(ok = unit_wait(un))) break;
+          if (!(ok = __all_sync(0xffffffffu, unit_wait(un)))) break;
           const plan::Entry& e = units[un % UNITS];
           const int n = e.n;
           if (n < 0) break;
           if (n == 0) {
-            unit_done(un);
+            __syncwarp();
+            if (issue) unit_done(un);
             continue;
           }
           const uint32_t ab = n_a % C::A_BUFS;
-          if (!(ok = wait_bar(bar(C::B_AFULL + ab), (n_a / C::A_BUFS) & 1, abort_flag))) break;
+          if (!(ok = wait_warp(bar(C::B_AFULL + ab), (n_a / C::A_BUFS) & 1, abort_flag))) break;
           ++n_a;
-          d_own = (uint64_t)((ab * 2 * C::TILE_BYTES) >> 4);
+          d_own = (uint64_t)((uniform(ab) * 2 * C::TILE_BYTES) >> 4);
           for (int j = 0; j < n; ++j) {
-            if (!(ok = wait_bar(bar(C::B_FULL + ring % STAGES), (ring / STAGES) & 1, abort_flag))) break;
+            if (!(ok = wait_warp(bar(C::B_FULL + ring % STAGES), (ring / STAGES) & 1, abort_flag))) break;
             ptx::tc_fence_after();
             if (pend && !(ok = tail_done())) break;
             if (SPLIT) {
               if (pend && !(ok = issue_acc(ring - 1, hs))) break;
-              if (pend) ptx::mma_commit(bar(C::B_EMPTY + (ring - 1) % STAGES));
+              if (pend) ptx::mma_commit_warp(bar(C::B_EMPTY + (ring - 1) % STAGES), issue);
               issue_sdp(ring, hs);
             } else {
               if (pend && !(ok = issue_acc(ring - 1, 0))) break;
               issue_sdp(ring, 0);
               if (pend && !(ok = issue_acc(ring - 1, 1))) break;
-              if (pend) ptx::mma_commit(bar(C::B_EMPTY + (ring - 1) % STAGES));
+              if (pend) ptx::mma_commit_warp(bar(C::B_EMPTY + (ring - 1) % STAGES), issue);
               issue_sdp(ring, 1);
             }
             pend = true;
             first = j == 0;
             pend_tail = there(e, j) < T;
-            if (pend_tail) ptx::mbar_arrive(bar(C::B_TAILREQ + (SPLIT ? hs : 0)));
+            if (pend_tail && issue) ptx::mbar_arrive(bar(C::B_TAILREQ + (SPLIT ? hs : 0)));
             ++ring;
           }
           if (!ok) break;
-          ptx::mma_commit(bar(C::B_AEMPTY + ab));
-          unit_done(un);
+          ptx::mma_commit_warp(bar(C::B_AEMPTY + ab), issue);
+          __syncwarp();
+          if (issue) unit_done(un);
         }
         if (!ok) {
-          ptx::mma_commit(bar(C::B_DRAIN + hs));
+          ptx::mma_commit_warp(bar(C::B_DRAIN + hs), issue);
           drain_wait(bar(C::B_DRAIN + hs), 0);
         }
       }
