@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
   const plan::Entry* units = reinterpret_cast<const plan::Entry*>(smem + C::OFF_UNITS);
   const float* vec = reinterpret_cast<const float*>(smem + C::OFF_VEC);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // uniform: see the issuing warps
   const int row_tile = p.tok * p.group;  // rows of a row tile
 
   if (threadIdx.x == 0) {
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (pend && !(ok = flush())) break;
           if (!(ok = __all_sync(0xffffffffu, unit_wait(un)))) break;
           const plan::Entry& e = units[un % UNITS];
-          const int n = e.n;
+          const int n = (int)uniform(e.n);
           if (n < 0) break;
           if (n == 0) {
             __syncwarp();
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             pend = true;
             first = j == 0;
-            pend_tail = there(e, j) < T;
+            pend_tail = uniform(there(e, j) < T) != 0;
             if (pend_tail && issue) ptx::mbar_arrive(bar(C::B_TAILREQ + (SPLIT ? hs : 0)));
             ++ring;
           }
