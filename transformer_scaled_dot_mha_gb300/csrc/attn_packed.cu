@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_SLOT);
   const plan::Entry* units = reinterpret_cast<const plan::Entry*>(smem + C::OFF_UNITS);
   volatile uint32_t* flags = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_FLAGS);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // uniform: see the issuing warps
 
   if (threadIdx.x == 0) {
     for (int b = 0; b < C::Q_BUFS; ++b) {
@@ -463,6 +463,15 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
   // runs through them in that order, each at its own pace. n < 0: no more units.
   auto unit_wait = [&](uint32_t un) -> bool { return wait_bar(bar(C::B_UNITFULL + un % UNITS), (un / UNITS) & 1, abort_flag, C::SLEEPY); };
   auto unit_done = [&](uint32_t un) { ptx::mbar_arrive(bar(C::B_UNITEMPTY + un % UNITS)); };
+  // The issuing warps run their loops together, and one lane issues: with control flow and operands that are
+  // the same for the warp, descriptors and addresses are computed in uniform registers, where the MMA
+  // takes them from. (In a branch of one thread every operand is moved there first; an MMA then costs the
+  // issuing warp some 90 cycles between the softmax warps' instructions.)
+  auto uniform = [](uint32_t x) -> uint32_t { return __shfl_sync(0xffffffffu, x, 0); };
+  auto wait_warp = [&](uint32_t b, uint32_t parity, bool sleepy = false) -> bool {
+    return __all_sync(0xffffffffu, wait_bar(b, parity, abort_flag, sleepy));
+  };
+  const uint32_t issue = lane == 0;
   bool ok = true;
 
   // A copying warp's part of K (kv = 0) or V (1) of all units: rows [128 part / parts, + 128 / parts) of every
@@ -957,24 +966,25 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
       __syncwarp();
     } else if (SINGLE && warp == C::WARP_MMA) {
       // ================================================================ S = Q K^T (one row tile)
-      if (lane == 0) {
+      {
+        const uint32_t t_mem = uniform(tmem);
         uint32_t n_q = 0, tiles = 0;
         Pos pos;
         for (uint32_t un = 0;; ++un) {
-          if (!(ok = unit_wait(un))) break;
-          const int n = units[un % UNITS].n;
-          unit_done(un);
+          if (!(ok = __all_sync(0xffffffffu, unit_wait(un)))) break;
+          const int n = (int)uniform(units[un % UNITS].n);
+          if (issue) unit_done(un);
           if (n < 0) break;
           if (n == 0) continue;
           const uint32_t qb = n_q % C::Q_BUFS, q_tile = s_q(qb);
-          ok = wait_bar(bar(C::B_QFULL + qb), (n_q / C::Q_BUFS) & 1, abort_flag, true);
+          ok = wait_warp(bar(C::B_QFULL + qb), (n_q / C::Q_BUFS) & 1, true);
           ++n_q;
           for (int j = 0; j < n && ok; ++j, ++tiles) {
             // S loaded first: with an odd number of places this one's last phase was a V tile's, which only the
             // PV issuer waits for, and a wait for a phase is a wait for its parity. That S(j - 1) was loaded says
             // that P(j - 2) was stored, so PV(j - 3), which read that tile, is complete.
-            ok = (tiles == 0 || wait_bar(bar(C::B_SFREE), (tiles - 1) & 1, abort_flag, true)) &&
-                 wait_bar(bar(C::B_FULL + pos.s), pos.ph, abort_flag, true);
+            ok = (tiles == 0 || wait_warp(bar(C::B_SFREE), (tiles - 1) & 1, true)) &&
+                 wait_warp(bar(C::B_FULL + pos.s), pos.ph, true);
             if (!ok) break;
             if (KIND == PAGED) ptx::fence_proxy_async_smem();  // written by cp.async, read by the tensor cores
             ptx::tc_fence_after();
@@ -982,40 +992,41 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t koff = (kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32;
-              ptx::mma_ss(tmem, ptx::sdesc_sw128(q_tile + koff, 16, 1024), ptx::sdesc_sw128(k_tile + koff, 16, 1024),
-                          C::IDESC_S, kk > 0 ? 1u : 0u);
+              ptx::mma_ss_warp(t_mem, ptx::sdesc_sw128(q_tile + koff, 16, 1024), ptx::sdesc_sw128(k_tile + koff, 16, 1024),
+                               C::IDESC_S, kk > 0 ? 1u : 0u, issue);
             }
-            ptx::mma_commit(bar(C::B_SFULL));
-            if (KIND != DENSE) ptx::mbar_arrive(bar(C::B_SFULL));
-            ptx::mma_commit(bar(C::B_EMPTY + pos.s));
+            ptx::mma_commit_warp(bar(C::B_SFULL), issue);
+            if (KIND != DENSE && issue) ptx::mbar_arrive(bar(C::B_SFULL));
+            ptx::mma_commit_warp(bar(C::B_EMPTY + pos.s), issue);
             pos.step(2);
           }
           if (!ok) break;
         }
         // every MMA and every arrival of this warp's commits is done before the CTA's shared memory goes: the
         // last commits may come after those that the softmax has waited for
-        ptx::mma_commit(bar(C::B_DRAIN));
+        ptx::mma_commit_warp(bar(C::B_DRAIN), issue);
         drain_wait(bar(C::B_DRAIN), 0);
       }
       __syncwarp();
     } else if (SINGLE && warp == C::WARP_PV) {
       // ================================================================ O += P V (one row tile)
-      if (lane == 0) {
+      {
+        const uint32_t t_mem = uniform(tmem);
         uint32_t tiles = 0, tails = 0;
         Pos pos;
         pos.step(1);
         for (uint32_t un = 0;; ++un) {
-          if (!(ok = unit_wait(un))) break;
+          if (!(ok = __all_sync(0xffffffffu, unit_wait(un)))) break;
           const plan::Entry& e = units[un % UNITS];
-          const int n = e.n, len = e.str_len;
+          const int n = (int)uniform(e.n), len = (int)uniform(e.str_len);
           if (n < 0) break;
           for (int j = 0; j < n && ok; ++j, ++tiles) {
-            const bool tail = KIND == DENSE && (tile_of(e, j) + 1) * BN > len;
-            ok = wait_bar(bar(C::B_FULL + pos.s), pos.ph, abort_flag, true);
+            const bool tail = KIND == DENSE && uniform((tile_of(e, j) + 1) * BN > len) != 0;
+            ok = wait_warp(bar(C::B_FULL + pos.s), pos.ph, true);
             if (!ok) break;
-            if (tail) ptx::mbar_arrive(bar(C::B_TAILREQ));
-            ok = wait_bar(bar(C::B_PFULL), tiles & 1, abort_flag, true) &&
-                 (!tail || wait_bar(bar(C::B_TAIL), tails & 1, abort_flag, true));
+            if (tail && issue) ptx::mbar_arrive(bar(C::B_TAILREQ));
+            ok = wait_warp(bar(C::B_PFULL), tiles & 1, true) &&
+                 (!tail || wait_warp(bar(C::B_TAIL), tails & 1, true));
             if (!ok) break;
             tails += tail;
             if (KIND == PAGED) ptx::fence_proxy_async_smem();
@@ -1023,17 +1034,18 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
             const uint32_t v_tile = s_kv(pos.s);
 #pragma unroll
             for (int kk = 0; kk < BN / 16; ++kk)
-              ptx::mma_ts(tmem + C::TMEM_O, tmem + C::TMEM_P + kk * 8,
+              ptx::mma_ts_warp(t_mem + C::TMEM_O, t_mem + C::TMEM_P + kk * 8,
                           ptx::sdesc_sw128(v_tile + kk * 2048, C::CHUNK_BYTES, 1024), C::IDESC_PV,
-                          (j > 0 || kk > 0) ? 1u : 0u);
-            ptx::mma_commit(bar(C::B_ODONE));
-            ptx::mma_commit(bar(C::B_EMPTY + pos.s));
+                          (j > 0 || kk > 0) ? 1u : 0u, issue);
+            ptx::mma_commit_warp(bar(C::B_ODONE), issue);
+            ptx::mma_commit_warp(bar(C::B_EMPTY + pos.s), issue);
             pos.step(2);
           }
           if (!ok) break;
-          unit_done(un);
+          __syncwarp();
+          if (issue) unit_done(un);
         }
-        ptx::mma_commit(bar(C::B_DRAIN + 1));
+        ptx::mma_commit_warp(bar(C::B_DRAIN + 1), issue);
         drain_wait(bar(C::B_DRAIN + 1), 0);
       }
       __syncwarp();
@@ -1043,22 +1055,23 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
       // over all units as one stream: a unit's last PV waits for the softmax while the next one's
       // keys are on their way. Only where a unit starts do both PVs come first, since S needs
       // the new Q.
-      if (lane == 0) {
+      {
+        const uint32_t t_mem = uniform(tmem);
         uint32_t n_q = 0, qb = 0, tails = 0;
         uint32_t cnt0 = 0, cnt1 = 0;  // key tiles of row tile 0 and 1 so far
         bool pend = false, pend0 = false, pend1 = false, acc0 = false, acc1 = false, pend_tail = false;  // PVs not yet issued
         Pos kpos, vpos;  // this tile's keys; the values of the PVs not yet issued
         vpos.step(1);
         auto issue_pv = [&](int t, uint32_t cnt, bool acc) -> bool {
-          if (!wait_bar(bar(C::B_PFULL + t), (cnt - 1) & 1, abort_flag)) return false;
+          if (!wait_warp(bar(C::B_PFULL + t), (cnt - 1) & 1)) return false;
           ptx::tc_fence_after();
           const uint32_t v_tile = s_kv(vpos.s);
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
-            ptx::mma_ts(tmem + C::TMEM_O + t * D, tmem + t * BN + kk * 8,
+            ptx::mma_ts_warp(t_mem + C::TMEM_O + t * D, t_mem + t * BN + kk * 8,
                         ptx::sdesc_sw128(v_tile + kk * 2048, C::CHUNK_BYTES, 1024), C::IDESC_PV,
-                        (acc || kk > 0) ? 1u : 0u);
-          ptx::mma_commit(bar(C::B_ODONE + t));
+                        (acc || kk > 0) ? 1u : 0u, issue);
+          ptx::mma_commit_warp(bar(C::B_ODONE + t), issue);
           return true;
         };
         auto issue_s = [&](int t) {
@@ -1066,44 +1079,44 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t koff = (kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32;
-            ptx::mma_ss(tmem + t * BN, ptx::sdesc_sw128(q_tile + koff, 16, 1024),
-                        ptx::sdesc_sw128(k_tile + koff, 16, 1024), C::IDESC_S, kk > 0 ? 1u : 0u);
+            ptx::mma_ss_warp(t_mem + t * BN, ptx::sdesc_sw128(q_tile + koff, 16, 1024),
+                        ptx::sdesc_sw128(k_tile + koff, 16, 1024), C::IDESC_S, kk > 0 ? 1u : 0u, issue);
           }
-          ptx::mma_commit(bar(C::B_SFULL + t));
-          if (KIND != DENSE) ptx::mbar_arrive(bar(C::B_SFULL + t));
+          ptx::mma_commit_warp(bar(C::B_SFULL + t), issue);
+          if (KIND != DENSE && issue) ptx::mbar_arrive(bar(C::B_SFULL + t));
         };
         // the values for the PVs still to come have landed
         auto values = [&]() -> bool {
-          if (!wait_bar(bar(C::B_FULL + vpos.s), vpos.ph, abort_flag)) return false;
+          if (!wait_warp(bar(C::B_FULL + vpos.s), vpos.ph)) return false;
           if (KIND == PAGED) ptx::fence_proxy_async_smem();
           if (!pend_tail) return true;
-          ptx::mbar_arrive(bar(C::B_TAILREQ));
+          if (issue) ptx::mbar_arrive(bar(C::B_TAILREQ));
           pend_tail = false;
-          return wait_bar(bar(C::B_TAIL), tails++ & 1, abort_flag);
+          return wait_warp(bar(C::B_TAIL), tails++ & 1);
         };
         auto flush = [&]() -> bool {
           if (!values()) return false;
           if (pend0 && !issue_pv(0, cnt0, acc0)) return false;
           if (pend1 && !issue_pv(1, cnt1, acc1)) return false;
-          ptx::mma_commit(bar(C::B_EMPTY + vpos.s));
+          ptx::mma_commit_warp(bar(C::B_EMPTY + vpos.s), issue);
           vpos.step(2);
           pend = false;
           return true;
         };
         for (uint32_t un = 0;; ++un) {
           if (pend && !(ok = flush())) break;
-          if (!(ok = unit_wait(un))) break;
+          if (!(ok = __all_sync(0xffffffffu, unit_wait(un)))) break;
           const plan::Entry& e = units[un % UNITS];
-          const int n = e.n, len = e.str_len;
+          const int n = (int)uniform(e.n), len = (int)uniform(e.str_len);
           if (n < 0) break;
-          const int lo0 = e.lo0, hi0 = e.hi0, lo1 = e.lo1, hi1 = e.hi1;
+          const int lo0 = (int)uniform(e.lo0), hi0 = (int)uniform(e.hi0), lo1 = (int)uniform(e.lo1), hi1 = (int)uniform(e.hi1);
           if (n > 0) {
             qb = n_q % C::Q_BUFS;
-            ok = wait_bar(bar(RAW ? C::B_QREADY : C::B_QFULL + (int)qb), (n_q / C::Q_BUFS) & 1, abort_flag);
+            ok = wait_warp(bar(RAW ? C::B_QREADY : C::B_QFULL + (int)qb), (n_q / C::Q_BUFS) & 1);
             ++n_q;
           }
           for (int j = 0; j < n && ok; ++j) {
-            ok = wait_bar(bar(C::B_FULL + kpos.s), kpos.ph, abort_flag) && (!pend || values());
+            ok = wait_warp(bar(C::B_FULL + kpos.s), kpos.ph) && (!pend || values());
             if (!ok) break;
             if (KIND == PAGED) ptx::fence_proxy_async_smem();  // written by cp.async, read by the tensor cores
             ptx::tc_fence_after();
@@ -1118,10 +1131,10 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
               issue_s(1);
               ++cnt1;
             }
-            ptx::mma_commit(bar(C::B_EMPTY + kpos.s));
+            ptx::mma_commit_warp(bar(C::B_EMPTY + kpos.s), issue);
             kpos.step(2);
             if (pend) {
-              ptx::mma_commit(bar(C::B_EMPTY + vpos.s));
+              ptx::mma_commit_warp(bar(C::B_EMPTY + vpos.s), issue);
               vpos.step(2);
             }
             pend = true;
@@ -1129,15 +1142,16 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
             pend1 = in1;
             acc0 = j > lo0;
             acc1 = j > lo1;
-            pend_tail = KIND == DENSE && (tile_of(e, j) + 1) * BN > len;
+            pend_tail = KIND == DENSE && uniform((tile_of(e, j) + 1) * BN > len) != 0;
           }
           if (!ok) break;
-          if (n > 0) ptx::mma_commit(bar(C::B_QEMPTY + qb));
-          unit_done(un);
+          if (n > 0) ptx::mma_commit_warp(bar(C::B_QEMPTY + qb), issue);
+          __syncwarp();
+          if (issue) unit_done(un);
         }
         // every MMA and every arrival of this warp's commits is done before the CTA's shared memory goes: the
         // last commits may come after those that the softmax has waited for
-        ptx::mma_commit(bar(C::B_DRAIN));
+        ptx::mma_commit_warp(bar(C::B_DRAIN), issue);
         drain_wait(bar(C::B_DRAIN), 0);
       }
       __syncwarp();
