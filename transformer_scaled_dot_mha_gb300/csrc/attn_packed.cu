@@ -81,7 +81,6 @@ struct Cfg {
   static constexpr bool SINGLE = D == 64 && KIND == DENSE;
   static constexpr int Q_TILES = SINGLE ? 1 : 2;
   static constexpr int ROWS = Q_TILES * BM;
-  static constexpr int PARTS = SINGLE ? 1 : 2;  // softmax threads per row, each with BN / PARTS columns
   static constexpr int CTAS_PER_SM = SINGLE ? 2 : 1;
   static constexpr int CHUNKS = D / 64;
   static constexpr int CHUNK_BYTES = BM * 128;
@@ -94,8 +93,7 @@ struct Cfg {
   static constexpr int OFF_RAW = OFF_KV + SLOTS * TILE_BYTES;  // [K, V]
   static constexpr int OFF_UNITS = OFF_RAW + 2 * RAW_BYTES;    // Entry [UNITS]
   static constexpr int OFF_FLAGS = OFF_UNITS + UNITS * 64;     // uint32 [FLAGS][8]: any, four words of key bits
-  static constexpr int OFF_XCH = OFF_FLAGS + (KIND == DENSE ? 0 : FLAGS * 32);  // float [Q_TILES][PARTS][BM]
-  static constexpr int OFF_BAR = OFF_XCH + (PARTS == 1 ? 0 : ROWS * PARTS * 4);
+  static constexpr int OFF_BAR = OFF_FLAGS + (KIND == DENSE ? 0 : FLAGS * 32);
   static constexpr int B_QFULL = 0;                  // [Q_BUFS]
   static constexpr int B_QEMPTY = B_QFULL + 2;       // [Q_BUFS]
   static constexpr int B_QREADY = B_QEMPTY + 2;      // PAGED8: Q in f16
@@ -110,26 +108,25 @@ struct Cfg {
   static constexpr int B_RAWFULL = B_TAIL + 1;       // [K, V]
   static constexpr int B_RAWEMPTY = B_RAWFULL + 2;
   static constexpr int B_DRAIN = B_RAWEMPTY + 2;     // [2] the last MMAs and commits, one per issuer
-  static constexpr int B_XCH = B_DRAIN + 2;          // [2][4] a row quarter's two warps
-  static constexpr int B_UNITFULL = B_XCH + 8;       // [UNITS]
+  static constexpr int B_UNITFULL = B_DRAIN + 2;     // [UNITS]
   static constexpr int B_UNITEMPTY = B_UNITFULL + UNITS;
   static constexpr int NUM_BARS = B_UNITEMPTY + UNITS;
   static constexpr int OFF_SLOT = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_ABORT = OFF_SLOT + 4;
   static constexpr int SMEM_BYTES = OFF_ABORT + 4;
   static constexpr uint32_t TMEM_COLS = SINGLE ? 256 : 512;
-  // warps: softmax (4 per row tile and part); units and copies; MMA issuer (SINGLE: of S); tail; SINGLE: PV issuer.
+  // warps: softmax (4 per row tile); units and copies; MMA issuer (SINGLE: of S); tail; SINGLE: PV issuer.
   // PAGED: four more copy pages. PAGED8: four more convert, the third and fourth control warp copy
-  static constexpr int SOFTMAX_WARPS = 4 * Q_TILES * PARTS;
+  static constexpr int SOFTMAX_WARPS = 4 * Q_TILES;
   static constexpr int WARP_LOAD = SOFTMAX_WARPS, WARP_MMA = SOFTMAX_WARPS + 1, WARP_TAIL = SOFTMAX_WARPS + 2,
                        WARP_PV = SOFTMAX_WARPS + 3, WARP_MORE = SOFTMAX_WARPS + 4;
   static constexpr int THREADS = 32 * (SOFTMAX_WARPS + 4 + (KIND == DENSE ? 0 : 4));
   // readers of a unit's entry: softmax warps, MMA issuers, tail or copying warps, converting warps
   static constexpr int UNIT_READERS = SOFTMAX_WARPS + (SINGLE ? 2 : 1) + (KIND == DENSE ? 1 : KIND == PAGED ? 4 : 6);
   static constexpr bool SLEEPY = SINGLE || KIND != DENSE;  // control warps' waits suspend: fewer issue slots taken
-  static constexpr int REGS_CONTROL = !SINGLE && KIND == DENSE ? 64 : 48;
-  static constexpr int REGS_MORE = 48;
-  static constexpr int REGS_SOFTMAX = SINGLE ? 208 : KIND == DENSE ? 104 : 96;
+  static constexpr int REGS_CONTROL = SINGLE ? 48 : KIND == DENSE ? 80 : KIND == PAGED ? 48 : 56;
+  static constexpr int REGS_MORE = KIND == PAGED ? 48 : 40;
+  static constexpr int REGS_SOFTMAX = 208;
   static constexpr int LAUNCH_REGS = (65536 / (THREADS * CTAS_PER_SM)) & ~7;
   static_assert(128 * REGS_CONTROL + (KIND == DENSE ? 0 : 128 * REGS_MORE) + 32 * SOFTMAX_WARPS * REGS_SOFTMAX <=
                     THREADS * LAUNCH_REGS,
@@ -420,7 +417,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
       ptx::mbar_init(bar(C::B_QFULL + b), 1);
       ptx::mbar_init(bar(C::B_QEMPTY + b), SINGLE ? 4 : 1);  // the softmax warps, or the last S
     }
-    ptx::mbar_init(bar(C::B_QREADY), C::PARTS * 2 * BM);
+    ptx::mbar_init(bar(C::B_QREADY), 2 * BM);
     for (int s = 0; s < C::SLOTS; ++s) {
       // converting warps; two copy warps' lanes and their lanes 0 again; or the copies' bytes
       ptx::mbar_init(bar(C::B_FULL + s), RAW ? 4 : KIND == PAGED ? 66 : 1);
@@ -430,8 +427,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
       // pages: the issuer arrives besides its commit, so that the page bits, written before the
       // copies, are ordered before the softmax reads them
       ptx::mbar_init(bar(C::B_SFULL + t), KIND == DENSE ? 1 : 2);
-      ptx::mbar_init(bar(C::B_PFULL + t), C::PARTS * BM);
-      for (int x = 0; x < 4; ++x) ptx::mbar_init(bar(C::B_XCH + 4 * t + x), C::PARTS);
+      ptx::mbar_init(bar(C::B_PFULL + t), BM);
       ptx::mbar_init(bar(C::B_ODONE + t), 1);
       ptx::mbar_init(bar(C::B_RAWFULL + t), 33);
       ptx::mbar_init(bar(C::B_RAWEMPTY + t), 4);
@@ -532,9 +528,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
   if (warp < C::SOFTMAX_WARPS) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
     // ================================================================ softmax
-    const int t = (warp >> 2) % C::Q_TILES;           // row tile
-    const int part = warp / (4 * C::Q_TILES);         // columns [part CW, + CW) of it
-    constexpr int CW = BN / C::PARTS, DW = D / C::PARTS;
+    const int t = warp >> 2;               // row tile
     const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
     const int rt = r / p.group;            // its token
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -544,25 +538,6 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
     uint32_t cnt0 = 0;   // key tiles of this row tile so far
     uint32_t tiles = 0;  // key tiles of the units so far (pages: their bits' place)
     uint32_t n_q = 0;    // units with keys so far
-    uint32_t n_xch = 0;
-    // Both warps of these rows are here.
-    auto meet = [&]() -> bool {
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(C::B_XCH + 4 * t + (warp & 3)));
-      if (!__all_sync(0xffffffffu, wait_bar(bar(C::B_XCH + 4 * t + (warp & 3)), n_xch++ & 1, abort_flag))) return false;
-      ptx::tc_fence_after();
-      return true;
-    };
-    // The other thread of this row gives its v for ours. Between one call and the next something has to show that it
-    // has read: an MMA that needs a later arrival of both, or meet().
-    auto exchange = [&](float& v) -> bool {
-      const uint32_t at = s_base + C::OFF_XCH + t * (C::PARTS * BM * 4) + r * 4;
-      asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + part * (BM * 4)), "f"(v) : "memory");
-      if (!meet()) return false;
-      asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at + (part ^ 1) * (BM * 4)) : "memory");
-      return true;
-    };
     for (uint32_t un = 0;; ++un) {
       ok = __all_sync(0xffffffffu, unit_wait(un));
       if (!ok) break;
@@ -583,24 +558,20 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
             const uint32_t row = s_q(0) + t * C::TILE_BYTES + r * 128;
             float top = 0.0f;
 #pragma unroll
-            for (int u = part * (DW / 8); u < (part + 1) * (DW / 8); ++u) {
+            for (int u = 0; u < D / 8; ++u) {
               const uint4 w = ld_shared_v4(row + (u >> 3) * C::CHUNK_BYTES + (((u & 7) ^ (r & 7)) << 4));
               const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 top = ptx::max3(top, fabsf(__uint_as_float(in[i] << 16)), fabsf(__uint_as_float(in[i] & 0xffff0000u)));
             }
-            float other = top;
-            ok = exchange(other) && meet();
-            if (!ok) break;
-            top = fmaxf(top, other);
             // exponents of two normal numbers; zero, subnormal, infinite rows stay as they are
             const int field = (int)(__float_as_uint(top) >> 23);
             const int up = field == 0 || field >= 255 ? 0 : min(max(127 + 14 - field, -126), 126);
             const float mul = __uint_as_float((uint32_t)(127 + up) << 23);
             c *= __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
-            for (int u = part * (DW / 8); u < (part + 1) * (DW / 8); ++u) {
+            for (int u = 0; u < D / 8; ++u) {
               const uint32_t at = row + (u >> 3) * C::CHUNK_BYTES + (((u & 7) ^ (r & 7)) << 4);
               const uint4 w = ld_shared_v4(at);
               const uint32_t in[4] = {w.x, w.y, w.z, w.w};
@@ -637,9 +608,9 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_SFULL + t), cnt & 1, abort_flag));
         if (!ok) break;
         ptx::tc_fence_after();
-        uint32_t sr[CW / 32][32];
+        uint32_t sr[4][32];
 #pragma unroll
-        for (int q4 = 0; q4 < CW / 32; ++q4) ptx::tmem_ld32(t_s + part * CW + q4 * 32, sr[q4]);
+        for (int q4 = 0; q4 < 4; ++q4) ptx::tmem_ld32(t_s + q4 * 32, sr[q4]);
         ptx::tmem_wait_ld();
         if constexpr (SINGLE) {  // S is in registers
           ptx::tc_fence_before();
@@ -649,7 +620,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         volatile const uint32_t* fl = flags + ((tiles + lo + j) % FLAGS) * 8;
         if constexpr (KIND != DENSE) masked = masked || fl[0];  // keys of pages that are not there
         if (masked) {
-          const int key0 = tile_of(e, lo + j) * BN + part * CW;
+          const int key0 = tile_of(e, lo + j) * BN;
           const int pos = e.pos + t * p.tok + rt;
           int lim = e.str_len - key0;  // columns [first, lim) are legal, and those below `sink`
           if (p.causal) lim = min(lim, pos + 1 - key0);
@@ -661,27 +632,26 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           }
           // as bits, a word for 32 columns
 #pragma unroll
-          for (int q4 = 0; q4 < CW / 32; ++q4) {
+          for (int q4 = 0; q4 < 4; ++q4) {
             uint32_t legal = bits_below(lim - q4 * 32) & (~bits_below(first - q4 * 32) | bits_below(sink - q4 * 32));
-            if constexpr (KIND != DENSE) legal &= fl[0] ? ~fl[1 + part * (CW / 32) + q4] : ~0u;
+            if constexpr (KIND != DENSE) legal &= fl[0] ? ~fl[1 + q4] : ~0u;
 #pragma unroll
             for (int x = 0; x < 32; ++x)
               if (!((legal >> x) & 1u)) sr[q4][x] = __float_as_uint(-INFINITY);
           }
         }
-        uint32_t pk[CW / 64][32];
+        uint32_t pk[2][32];
         auto col = [&](int a, int x) { return __uint_as_float(sr[a >> 1][(a & 1) * 16 + x]); };
-        // maximum of this thread's columns: independent chains of three-way maxima
+        // row maximum: eight independent chains of three-way maxima
         auto row_max = [&]() -> float {
-          float mc[CW / 16];
+          float mc[8];
 #pragma unroll
-          for (int a = 0; a < CW / 16; ++a) {
+          for (int a = 0; a < 8; ++a) {
             mc[a] = fmaxf(col(a, 0), col(a, 1));
 #pragma unroll
             for (int x = 2; x < 16; x += 2) mc[a] = ptx::max3(mc[a], col(a, x), col(a, x + 1));
           }
-          if constexpr (CW == 64) return fmaxf(ptx::max3(mc[0], mc[1], mc[2]), mc[3]) * c;
-          else return ptx::max3(ptx::max3(mc[0], mc[1], mc[2]), ptx::max3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7])) * c;
+          return ptx::max3(ptx::max3(mc[0], mc[1], mc[2]), ptx::max3(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7])) * c;
         };
         // P, rounded for the tensor cores (the row sum takes it unrounded). bf16: each weight moves by at
         // most 2^-8 of itself, independently, less than the output's own rounding in the mean. f16, with
@@ -690,20 +660,20 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           const float m_use = ((m_now == -INFINITY) ? 0.0f : m_now) - (RAW ? kBias : 0.0f);
           const uint64_t c2 = ptx::f2_pack(c, c);
           const uint64_t negm2 = ptx::f2_pack(-m_use, -m_use);
-          uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+          uint64_t part[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-          for (int q4 = 0; q4 < CW / 32; ++q4)
+          for (int q4 = 0; q4 < 4; ++q4)
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
               const uint64_t sx = ptx::f2_pack(__uint_as_float(sr[q4][x]), __uint_as_float(sr[q4][x + 1]));
               float a0, a1;
               ptx::f2_unpack(ptx::f2_fma(sx, c2, negm2), a0, a1);
               const float p0 = ptx::ex2(a0), p1 = ptx::ex2(a1);
-              sum[CW == 64 ? (x >> 1) & 3 : q4] = ptx::f2_add(sum[CW == 64 ? (x >> 1) & 3 : q4], ptx::f2_pack(p0, p1));
+              part[q4] = ptx::f2_add(part[q4], ptx::f2_pack(p0, p1));
               pk[q4 >> 1][(q4 & 1) * 16 + (x >> 1)] = RAW ? pack_f16x2(p0, p1) : ptx::pack_bf16x2(p0, p1);
             }
           float l0, l1;
-          ptx::f2_unpack(ptx::f2_add(ptx::f2_add(sum[0], sum[1]), ptx::f2_add(sum[2], sum[3])), l0, l1);
+          ptx::f2_unpack(ptx::f2_add(ptx::f2_add(part[0], part[1]), ptx::f2_add(part[2], part[3])), l0, l1);
           return l0 + l1;
         };
         bool pv_done = j == 0;  // the PV before this tile is known to be complete
@@ -713,13 +683,13 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           pv_done = true;
           ptx::tc_fence_after();
 #pragma unroll
-          for (int q4 = 0; q4 < DW / 32; ++q4) {
+          for (int q4 = 0; q4 < D / 32; ++q4) {
             uint32_t o[32];
-            ptx::tmem_ld32(t_o + part * DW + q4 * 32, o);
+            ptx::tmem_ld32(t_o + q4 * 32, o);
             ptx::tmem_wait_ld();
 #pragma unroll
             for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-            ptx::tmem_st32(t_o + part * DW + q4 * 32, o);
+            ptx::tmem_st32(t_o + q4 * 32, o);
           }
           return true;
         };
@@ -751,10 +721,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
             l += l_tile;
           }
         } else {
-          const float m_part = row_max();
-          float m_tile = m_part;
-          if (!(ok = exchange(m_tile))) break;  // also: both parts of S are loaded, and P may be written over them
-          m_tile = fmaxf(m_tile, m_part);
+          const float m_tile = row_max();
           const bool grow = m_tile > m_ref + kRescaleThreshold;
           float alpha = 1.0f;
           if (grow) {
@@ -771,8 +738,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           if (!ok) break;
           ptx::tc_fence_after();
         }
-#pragma unroll
-        for (int q = 0; q < CW / 64; ++q) ptx::tmem_st32(t_p + part * 32 + q * 32, pk[q]);
+        ptx::tmem_st32(t_p, pk[0]);
+        ptx::tmem_st32(t_p + 32, pk[1]);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         ptx::mbar_arrive(bar(C::B_PFULL + t));
@@ -788,20 +755,15 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
       }
       cnt0 += n_tiles;
       tiles += e.n;
-      if (C::PARTS > 1 && n_tiles > 0) {
-        float other = l;
-        if (!(ok = exchange(other) && meet())) break;
-        l += other;
-      }
       if (e.slot >= 0) {
         // a piece: unnormalised sums, their reference, the row sum
-        float* piece = p.part + (size_t)e.slot * (C::ROWS * (D + 2)) + (size_t)(t * BM + r) * D + part * DW;
+        float* part = p.part + (size_t)e.slot * (C::ROWS * (D + 2)) + (size_t)(t * BM + r) * D;
         float* stat = p.part + (size_t)e.slot * (C::ROWS * (D + 2)) + (size_t)C::ROWS * D + t * BM + r;
 #pragma unroll
-        for (int q4 = 0; q4 < DW / 32; ++q4) {
+        for (int q4 = 0; q4 < D / 32; ++q4) {
           uint32_t o[32];
           if (n_tiles > 0) {
-            ptx::tmem_ld32(t_o + part * DW + q4 * 32, o);
+            ptx::tmem_ld32(t_o + q4 * 32, o);
             ptx::tmem_wait_ld();
           } else {
 #pragma unroll
@@ -810,16 +772,15 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           if (row_valid) {
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-              reinterpret_cast<uint4*>(piece + q4 * 32)[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+              reinterpret_cast<uint4*>(part + q4 * 32)[x] = make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
           }
           __syncwarp();
         }
-        if (row_valid && part == 0) {
+        if (row_valid) {
           stat[0] = m_ref - (RAW ? kBias : 0.0f);
           stat[C::ROWS] = l;
         }
       } else {
-        constexpr int CO = SINGLE ? 64 : 32;  // columns at a time
         const float v_mul = RAW ? p.v_scale[e.hk] : 1.0f;
         const float inv = l == 0.0f ? 0.0f : v_mul / l;  // no legal key: zeros
         const long long row = (long long)e.own_row + t * p.tok + rt;
@@ -827,13 +788,13 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         const long long at = row_valid ? row * p.out_ts + head_q * p.out_hs : -1;
         const uint32_t stage = s_q((n_q - 1) % C::Q_BUFS) + (warp & 3) * 4096;
 #pragma unroll
-        for (int c0 = 0; c0 < DW; c0 += CO) {
-          uint32_t w[CO / 2];
+        for (int c64 = 0; c64 < D / 64; ++c64) {
+          uint32_t w[32];
 #pragma unroll
-          for (int c1 = 0; c1 < CO; c1 += 32) {
+          for (int half = 0; half < 2; ++half) {
             uint32_t o[32];
             if (n_tiles > 0) {
-              ptx::tmem_ld32(t_o + part * DW + c0 + c1, o);
+              ptx::tmem_ld32(t_o + c64 * 64 + half * 32, o);
               ptx::tmem_wait_ld();
             } else {
 #pragma unroll
@@ -841,14 +802,14 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
             }
 #pragma unroll
             for (int x = 0; x < 16; ++x)
-              w[c1 / 2 + x] = ptx::pack_bf16x2(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
+              w[half * 16 + x] = ptx::pack_bf16x2(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv);
           }
           if (SINGLE && e.n > 0) {
             // through the unit's Q, which no S reads any more (16-byte units swizzled by the row), so that eight
             // lanes store one row's 128 bytes: a lane's own row would be 16 bytes of 32 lines in every store
             // (64 x 256 tokens, 16 heads: 51.0 -> 43.7 us; at d = 128, through a place of its own, 1 to 8 % slower)
 #pragma unroll
-            for (int u = 0; u < CO / 8; ++u)
+            for (int u = 0; u < 8; ++u)
               ptx::st_shared_v4(stage + lane * 128 + ((u ^ (lane & 7)) << 4), w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
             __syncwarp();
 #pragma unroll
@@ -856,18 +817,18 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
               const int from = i * 4 + (lane >> 3);
               const long long to = __shfl_sync(0xffffffffu, at, from);
               const uint4 v = ld_shared_v4(stage + from * 128 + (((lane & 7) ^ (from & 7)) << 4));
-              if (to >= 0) *reinterpret_cast<uint4*>(p.out + to + c0 + (lane & 7) * 8) = v;
+              if (to >= 0) *reinterpret_cast<uint4*>(p.out + to + c64 * 64 + (lane & 7) * 8) = v;
             }
           } else {
             if (row_valid) {
-              uint4* dst = reinterpret_cast<uint4*>(p.out + at + part * DW + c0);
+              uint4* dst = reinterpret_cast<uint4*>(p.out + at + c64 * 64);
 #pragma unroll
-              for (int x = 0; x < CO / 8; ++x) dst[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+              for (int x = 0; x < 8; ++x) dst[x] = make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
             }
             __syncwarp();
           }
         }
-        if (row_valid && part == 0 && p.lse)
+        if (row_valid && p.lse)
           p.lse[row * p.h_q + head_q] =
               l == 0.0f ? -INFINITY : (m_ref - (RAW ? kBias : 0.0f) + __log2f(l)) * 0.69314718055994530942f;
       }
