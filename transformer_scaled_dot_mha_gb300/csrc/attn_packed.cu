@@ -104,11 +104,12 @@ struct Cfg {
   static constexpr int B_PFULL = B_SFREE + 1;        // [2] P_t stored
   static constexpr int B_ODONE = B_PFULL + 2;        // [2] PV_t completed
   static constexpr int B_TAILREQ = B_ODONE + 2;      // a tile with values behind the end has landed
-  static constexpr int B_TAIL = B_TAILREQ + 1;       // they are zeroed
-  static constexpr int B_RAWFULL = B_TAIL + 1;       // [K, V]
+  static constexpr int B_TAIL = B_TAILREQ + 1;       // [2] they are zeroed, by the place of the values (SINGLE: [0])
+  static constexpr int B_RAWFULL = B_TAIL + 2;       // [K, V]
   static constexpr int B_RAWEMPTY = B_RAWFULL + 2;
   static constexpr int B_DRAIN = B_RAWEMPTY + 2;     // [2] the last MMAs and commits, one per issuer
-  static constexpr int B_UNITFULL = B_DRAIN + 2;     // [UNITS]
+  static constexpr int B_TURN = B_DRAIN + 2;         // [2] an issuer's turn
+  static constexpr int B_UNITFULL = B_TURN + 2;      // [UNITS]
   static constexpr int B_UNITEMPTY = B_UNITFULL + UNITS;
   static constexpr int NUM_BARS = B_UNITEMPTY + UNITS;
   static constexpr int OFF_SLOT = OFF_BAR + NUM_BARS * 8;
@@ -120,9 +121,10 @@ struct Cfg {
   static constexpr int SOFTMAX_WARPS = 4 * Q_TILES;
   static constexpr int WARP_LOAD = SOFTMAX_WARPS, WARP_MMA = SOFTMAX_WARPS + 1, WARP_TAIL = SOFTMAX_WARPS + 2,
                        WARP_PV = SOFTMAX_WARPS + 3, WARP_MORE = SOFTMAX_WARPS + 4;
+  static constexpr int ISSUERS = SINGLE || KIND == PAGED8 ? 1 : 2;  // of both products; SINGLE: one for each product
   static constexpr int THREADS = 32 * (SOFTMAX_WARPS + 4 + (KIND == DENSE ? 0 : 4));
   // readers of a unit's entry: softmax warps, MMA issuers, tail or copying warps, converting warps
-  static constexpr int UNIT_READERS = SOFTMAX_WARPS + (SINGLE ? 2 : 1) + (KIND == DENSE ? 1 : KIND == PAGED ? 4 : 6);
+  static constexpr int UNIT_READERS = SOFTMAX_WARPS + (SINGLE ? 2 : ISSUERS) + (KIND == DENSE ? 1 : KIND == PAGED ? 4 : 6);
   static constexpr bool SLEEPY = SINGLE || KIND != DENSE;  // control warps' waits suspend: fewer issue slots taken
   static constexpr int REGS_CONTROL = SINGLE ? 48 : KIND == DENSE ? 80 : KIND == PAGED ? 48 : 56;
   static constexpr int REGS_MORE = KIND == PAGED ? 48 : 40;
@@ -415,13 +417,13 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
   if (threadIdx.x == 0) {
     for (int b = 0; b < C::Q_BUFS; ++b) {
       ptx::mbar_init(bar(C::B_QFULL + b), 1);
-      ptx::mbar_init(bar(C::B_QEMPTY + b), SINGLE ? 4 : 1);  // the softmax warps, or the last S
+      ptx::mbar_init(bar(C::B_QEMPTY + b), SINGLE ? 4 : C::ISSUERS);  // the softmax warps, or the last S
     }
     ptx::mbar_init(bar(C::B_QREADY), 2 * BM);
     for (int s = 0; s < C::SLOTS; ++s) {
       // converting warps; two copy warps' lanes and their lanes 0 again; or the copies' bytes
       ptx::mbar_init(bar(C::B_FULL + s), RAW ? 4 : KIND == PAGED ? 66 : 1);
-      ptx::mbar_init(bar(C::B_EMPTY + s), 1);
+      ptx::mbar_init(bar(C::B_EMPTY + s), C::ISSUERS);
     }
     for (int t = 0; t < 2; ++t) {
       // pages: the issuer arrives besides its commit, so that the page bits, written before the
@@ -432,10 +434,11 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
       ptx::mbar_init(bar(C::B_RAWFULL + t), 33);
       ptx::mbar_init(bar(C::B_RAWEMPTY + t), 4);
       ptx::mbar_init(bar(C::B_DRAIN + t), 1);
+      ptx::mbar_init(bar(C::B_TURN + t), 1);
+      ptx::mbar_init(bar(C::B_TAIL + t), 1);
     }
     ptx::mbar_init(bar(C::B_SFREE), BM);
     ptx::mbar_init(bar(C::B_TAILREQ), 1);
-    ptx::mbar_init(bar(C::B_TAIL), 1);
     for (int u = 0; u < UNITS; ++u) {
       ptx::mbar_init(bar(C::B_UNITFULL + u), 1);
       ptx::mbar_init(bar(C::B_UNITEMPTY + u), C::UNIT_READERS);
@@ -1039,99 +1042,121 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         drain_wait(bar(C::B_DRAIN + 1), 0);
       }
       __syncwarp();
-    } else if (!SINGLE && warp == C::WARP_MMA) {
-      // ================================================================ both products of two row tiles
-      // P_t lies in S_t, so S_t(j) follows PV_t(j - 1). In order PV0(j - 1), S0(j), PV1(j - 1), S1(j),
-      // over all units as one stream: a unit's last PV waits for the softmax while the next one's
-      // keys are on their way. Only where a unit starts do both PVs come first, since S needs
-      // the new Q.
+    } else if (!SINGLE && (warp == C::WARP_MMA || (C::ISSUERS == 2 && warp == C::WARP_PV))) {
+      // ================================================================ both products of one or two row tiles
+      // P_t lies in S_t, so S_t(j) follows PV_t(j - 1), over all units as one stream: a unit's last PV waits for the
+      // softmax while the next one's keys are on their way. Only where a unit starts does the PV come first, since S
+      // needs the new Q. The issue of an MMA blocks while two or three wait to run, and a barrier or a commit takes
+      // the issuer 80 to 150 cycles, so one warp cannot keep the tensor cores busy. An issuer per row tile waits for
+      // its operands beforehand and the two take turns, in the order PV0 S0 PV1 S1 (8192 causal tokens, 32/8 heads
+      // of 128: 838 us with one issuer, 738 with two; 925 without the turns, as then the two tiles' products
+      // mix and both softmaxes wait at the same time).
       {
+        constexpr int TILES = 2 / C::ISSUERS;  // row tiles of this warp, from t0 on
+        const int t0 = TILES == 1 && warp == C::WARP_PV ? 1 : 0;
         const uint32_t t_mem = uniform(tmem);
-        uint32_t n_q = 0, qb = 0, tails = 0;
-        uint32_t cnt0 = 0, cnt1 = 0;  // key tiles of row tile 0 and 1 so far
-        bool pend = false, pend0 = false, pend1 = false, acc0 = false, acc1 = false, pend_tail = false;  // PVs not yet issued
+        uint32_t n_q = 0, qb = 0, turns = 0, tails = 0;  // tails: a parity bit per place of values
+        uint32_t cnt[TILES] = {};             // key tiles of the row tiles so far
+        bool pend = false, pend_tail = false, pend_in[TILES] = {}, acc[TILES] = {};  // the PVs not yet issued
         Pos kpos, vpos;  // this tile's keys; the values of the PVs not yet issued
         vpos.step(1);
-        auto issue_pv = [&](int t, uint32_t cnt, bool acc) -> bool {
-          if (!wait_warp(bar(C::B_PFULL + t), (cnt - 1) & 1)) return false;
-          ptx::tc_fence_after();
+        // the values for the PVs still to come have landed
+        auto values = [&]() -> bool {
+          if (!wait_warp(bar(C::B_FULL + vpos.s), vpos.ph)) return false;
+          if (KIND == PAGED) ptx::fence_proxy_async_smem();  // written by cp.async, read by the tensor cores
+          if (!pend_tail) return true;
+          if (issue && t0 == 0) ptx::mbar_arrive(bar(C::B_TAILREQ));
+          const uint32_t place = vpos.s >> 1, parity = (tails >> place) & 1;
+          tails ^= 1u << place;
+          return wait_warp(bar(C::B_TAIL + (int)place), parity);
+        };
+        auto stored = [&](int x) -> bool { return !pend_in[x] || wait_warp(bar(C::B_PFULL + t0 + x), (cnt[x] - 1) & 1); };
+        auto issue_pv = [&](int x) {
+          const int t = t0 + x;
           const uint32_t v_tile = s_kv(vpos.s);
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
             ptx::mma_ts_warp(t_mem + C::TMEM_O + t * D, t_mem + t * BN + kk * 8,
-                        ptx::sdesc_sw128(v_tile + kk * 2048, C::CHUNK_BYTES, 1024), C::IDESC_PV,
-                        (acc || kk > 0) ? 1u : 0u, issue);
-          ptx::mma_commit_warp(bar(C::B_ODONE + t), issue);
-          return true;
+                             ptx::sdesc_sw128(v_tile + kk * 2048, C::CHUNK_BYTES, 1024), C::IDESC_PV,
+                             (acc[x] || kk > 0) ? 1u : 0u, issue);
         };
-        auto issue_s = [&](int t) {
-          const uint32_t q_tile = s_q(qb) + t * C::TILE_BYTES, k_tile = s_kv(kpos.s);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t koff = (kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32;
-            ptx::mma_ss_warp(t_mem + t * BN, ptx::sdesc_sw128(q_tile + koff, 16, 1024),
-                        ptx::sdesc_sw128(k_tile + koff, 16, 1024), C::IDESC_S, kk > 0 ? 1u : 0u, issue);
-          }
-          ptx::mma_commit_warp(bar(C::B_SFULL + t), issue);
-          if (KIND != DENSE && issue) ptx::mbar_arrive(bar(C::B_SFULL + t));
-        };
-        // the values for the PVs still to come have landed
-        auto values = [&]() -> bool {
-          if (!wait_warp(bar(C::B_FULL + vpos.s), vpos.ph)) return false;
-          if (KIND == PAGED) ptx::fence_proxy_async_smem();
-          if (!pend_tail) return true;
-          if (issue) ptx::mbar_arrive(bar(C::B_TAILREQ));
-          pend_tail = false;
-          return wait_warp(bar(C::B_TAIL), tails++ & 1);
-        };
-        auto flush = [&]() -> bool {
-          if (!values()) return false;
-          if (pend0 && !issue_pv(0, cnt0, acc0)) return false;
-          if (pend1 && !issue_pv(1, cnt1, acc1)) return false;
+        auto values_done = [&]() {
           ptx::mma_commit_warp(bar(C::B_EMPTY + vpos.s), issue);
           vpos.step(2);
           pend = false;
-          return true;
         };
         for (uint32_t un = 0;; ++un) {
-          if (pend && !(ok = flush())) break;
+          if (pend) {
+            ok = values();
+#pragma unroll
+            for (int x = 0; x < TILES; ++x) {
+              ok = ok && stored(x);
+              ptx::tc_fence_after();
+              if (!ok) break;
+              if (!pend_in[x]) continue;
+              issue_pv(x);
+              ptx::mma_commit_warp(bar(C::B_ODONE + t0 + x), issue);
+            }
+            if (!ok) break;
+            values_done();
+          }
           if (!(ok = __all_sync(0xffffffffu, unit_wait(un)))) break;
           const plan::Entry& e = units[un % UNITS];
           const int n = (int)uniform(e.n), len = (int)uniform(e.str_len);
           if (n < 0) break;
-          const int lo0 = (int)uniform(e.lo0), hi0 = (int)uniform(e.hi0), lo1 = (int)uniform(e.lo1), hi1 = (int)uniform(e.hi1);
+          int lo[TILES], hi[TILES];
+#pragma unroll
+          for (int x = 0; x < TILES; ++x) {
+            lo[x] = (int)uniform(t0 + x ? e.lo1 : e.lo0);
+            hi[x] = (int)uniform(t0 + x ? e.hi1 : e.hi0);
+          }
           if (n > 0) {
             qb = n_q % C::Q_BUFS;
             ok = wait_warp(bar(RAW ? C::B_QREADY : C::B_QFULL + (int)qb), (n_q / C::Q_BUFS) & 1);
             ++n_q;
           }
           for (int j = 0; j < n && ok; ++j) {
-            ok = wait_warp(bar(C::B_FULL + kpos.s), kpos.ph) && (!pend || values());
+            // also where no row of this warp's has a key in the tile: its arrivals below must not run ahead
+            ok = !pend || values();
+#pragma unroll
+            for (int x = 0; x < TILES; ++x) {
+              const int t = t0 + x;
+              if (x == 0) {
+                ok = ok && wait_warp(bar(C::B_FULL + kpos.s), kpos.ph);
+                if (KIND == PAGED) ptx::fence_proxy_async_smem();
+              }
+              if (pend) ok = ok && stored(x);
+              if (TILES == 1) ok = ok && (t0 == 0 ? turns == 0 || wait_warp(bar(C::B_TURN), (turns - 1) & 1)
+                                                  : wait_warp(bar(C::B_TURN + 1), turns & 1));
+              if (!ok) break;
+              ptx::tc_fence_after();
+              const bool before = pend && pend_in[x];
+              if (before) issue_pv(x);
+              pend_in[x] = j >= lo[x] && j < hi[x];
+              acc[x] = j > lo[x];
+              if (pend_in[x]) {
+                const uint32_t q_tile = s_q(qb) + t * C::TILE_BYTES, k_tile = s_kv(kpos.s);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint32_t koff = (kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32;
+                  ptx::mma_ss_warp(t_mem + t * BN, ptx::sdesc_sw128(q_tile + koff, 16, 1024),
+                                   ptx::sdesc_sw128(k_tile + koff, 16, 1024), C::IDESC_S, kk > 0 ? 1u : 0u, issue);
+                }
+              }
+              if (TILES == 1 && issue) ptx::mbar_arrive(bar(C::B_TURN + (t0 ^ 1)));
+              if (pend_in[x]) {
+                ptx::mma_commit_warp(bar(C::B_SFULL + t), issue);
+                if (KIND != DENSE && issue) ptx::mbar_arrive(bar(C::B_SFULL + t));
+                ++cnt[x];
+              }
+              if (before) ptx::mma_commit_warp(bar(C::B_ODONE + t), issue);
+            }
             if (!ok) break;
-            if (KIND == PAGED) ptx::fence_proxy_async_smem();  // written by cp.async, read by the tensor cores
-            ptx::tc_fence_after();
-            if (pend && pend0 && !(ok = issue_pv(0, cnt0, acc0))) break;
-            const bool in0 = j >= lo0 && j < hi0, in1 = j >= lo1 && j < hi1;
-            if (in0) {
-              issue_s(0);
-              ++cnt0;
-            }
-            if (pend && pend1 && !(ok = issue_pv(1, cnt1, acc1))) break;
-            if (in1) {
-              issue_s(1);
-              ++cnt1;
-            }
+            ++turns;
             ptx::mma_commit_warp(bar(C::B_EMPTY + kpos.s), issue);
             kpos.step(2);
-            if (pend) {
-              ptx::mma_commit_warp(bar(C::B_EMPTY + vpos.s), issue);
-              vpos.step(2);
-            }
+            if (pend) values_done();
             pend = true;
-            pend0 = in0;
-            pend1 = in1;
-            acc0 = j > lo0;
-            acc1 = j > lo1;
             pend_tail = KIND == DENSE && uniform((tile_of(e, j) + 1) * BN > len) != 0;
           }
           if (!ok) break;
@@ -1141,8 +1166,8 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         }
         // every MMA and every arrival of this warp's commits is done before the CTA's shared memory goes: the
         // last commits may come after those that the softmax has waited for
-        ptx::mma_commit_warp(bar(C::B_DRAIN), issue);
-        drain_wait(bar(C::B_DRAIN), 0);
+        ptx::mma_commit_warp(bar(C::B_DRAIN + t0), issue);
+        drain_wait(bar(C::B_DRAIN + t0), 0);
       }
       __syncwarp();
     } else if (RAW && (warp == C::WARP_TAIL || warp == C::WARP_PV)) {
@@ -1169,7 +1194,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
               ptx::st_shared_v4(s_kv(pos.s) + c * C::CHUNK_BYTES + x * 16, 0, 0, 0, 0);
           ptx::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar(C::B_TAIL));
+          if (lane == 0) ptx::mbar_arrive(bar(C::B_TAIL + (SINGLE ? 0 : (int)pos.s >> 1)));
           __syncwarp();
         }
         if (!ok) break;
