@@ -42,6 +42,7 @@ __device__ unsigned int g_packed_bwd_fault_word;
 namespace {
 
 constexpr int T = 128;  // rows per tile
+constexpr int H = 64;   // rows per half of a streamed tile
 // warps 0-7 elementwise (a warpgroup per half of every streamed tile), 8 copies, 9 and 10 MMA
 // issuers, 11 zeroes rows of other sequences
 constexpr int EW_THREADS = 256, THREADS = 384;
@@ -57,23 +58,28 @@ constexpr int kMaxDeal = 4;   // units per CTA above which they are not cut
 
 template <int D>
 struct BCfg {
-  static constexpr int STAGES = D == 64 ? 3 : 2;
+  // The ring holds half tiles: at d = 128 whole ones leave room for two, and a tile's place is free only when
+  // the sums over the tile before are done, just when its rows are needed (8192 causal tokens, 32/8 heads of 128:
+  // 1935 us with two tiles, 1663 with four halves; a fifth changes nothing).
+  static constexpr int SLOTS = D == 64 ? 6 : 4;
   static constexpr int A_BUFS = D == 64 ? 2 : 1;  // 2: the next unit's own tiles are there when the last S and dP are issued
   static constexpr int CHUNKS = D / 64;
   static constexpr int CHUNK_BYTES = T * 128;
   static constexpr int TILE_BYTES = T * D * 2;
   static constexpr int OFF_A0 = 0;                                      // [A_BUFS] K, or Q; and behind each
   static constexpr int OFF_A1 = OFF_A0 + TILE_BYTES;                    // V, or dO
-  static constexpr int OFF_R0 = OFF_A0 + A_BUFS * 2 * TILE_BYTES;       // ring: Q, or K
-  static constexpr int OFF_R1 = OFF_R0 + STAGES * TILE_BYTES;  // ring: dO, or V
-  static constexpr int OFF_VEC = OFF_R1 + STAGES * TILE_BYTES;  // float [STAGES][-lse log2(e)[T], -D[T]]
+  static constexpr int HCHUNK_BYTES = H * 128;
+  static constexpr int HALF_BYTES = H * D * 2;
+  static constexpr int OFF_R0 = OFF_A0 + A_BUFS * 2 * TILE_BYTES;       // ring: Q, or K; and behind each
+  static constexpr int OFF_R1 = OFF_R0 + HALF_BYTES;                    // dO, or V
+  static constexpr int OFF_VEC = OFF_R0 + SLOTS * 2 * HALF_BYTES;       // float [SLOTS][-lse log2(e)[H], -D[H]]
   // d = 64: rows on their way out, 32 per elementwise warp
-  static constexpr int OFF_STAGE = OFF_VEC + STAGES * 2 * T * 4;
+  static constexpr int OFF_STAGE = OFF_VEC + SLOTS * 2 * H * 4;
   static constexpr int OFF_UNITS = OFF_STAGE + (D == 64 ? 8 * 4096 : 0);
   static constexpr int OFF_BAR = OFF_UNITS + UNITS * 64;
-  static constexpr int B_AFULL = 0, B_AEMPTY = 2, B_FULL = 4, B_EMPTY = B_FULL + STAGES, B_MMFULL = B_EMPTY + STAGES;
+  static constexpr int B_AFULL = 0, B_AEMPTY = 2, B_FULL = 4, B_EMPTY = B_FULL + SLOTS, B_MMFULL = B_EMPTY + SLOTS;
   static constexpr int B_PFULL = B_MMFULL + 2, B_ACC = B_PFULL + 2, B_TAILREQ = B_ACC + 1, B_TAIL = B_TAILREQ + 2;
-  static constexpr int B_DRAIN = B_TAIL + 2, B_UNITFULL = B_DRAIN + 2, B_UNITEMPTY = B_UNITFULL + UNITS,
+  static constexpr int B_DRAIN = B_TAIL + 2, B_TURN = B_DRAIN + 2, B_UNITFULL = B_TURN + 2, B_UNITEMPTY = B_UNITFULL + UNITS,
                        NUM_BARS = B_UNITEMPTY + UNITS;
   static constexpr int OFF_SLOT = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_ABORT = OFF_SLOT + 4;
@@ -97,7 +103,9 @@ struct BwdParams {
   uint16_t* g0;        // dK, or dQ
   uint16_t* g1;        // dV
   long long g0_ts, g0_hs, g1_ts, g1_hs;
-  int group, tok, T_q, h_kv;
+  int group, tok, T_q, h_kv;  // tok: tokens per row tile
+  // keys own: a half of a row tile is half_tok tokens times half_per rows; half 1 starts half_step tokens behind half 0
+  int half_tok, half_per, half_step;
   int causal, window;
   float scale, scale_log2;
   float* part;  // [slots][T][accumulator columns]
@@ -224,11 +232,9 @@ __global__ void __launch_bounds__(THREADS, 1)
                            const __grid_constant__ CUtensorMap tm_r0, const __grid_constant__ CUtensorMap tm_r1,
                            const BwdParams p) {
   using C = BCfg<D>;
-  constexpr int STAGES = C::STAGES;
-  // one issuer per half, each with an accumulator of its own, as in attn_bwd.cu
-  constexpr bool SPLIT = !DKDV && D == 128;
+  constexpr int SLOTS = C::SLOTS;
   constexpr int ACC_COLS = DKDV ? 2 * D : D;  // of a piece
-  auto acc_col = [](int which, int h) -> uint32_t { return DKDV ? 256u + which * D : 256u + (SPLIT ? h : 0) * D; };
+  auto acc_col = [](int which) -> uint32_t { return 256u + which * D; };
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t s_base = ptx::smem_u32(smem);
   if ((s_base & 1023u) != 0) {
@@ -241,16 +247,17 @@ __global__ void __launch_bounds__(THREADS, 1)
   const plan::Entry* units = reinterpret_cast<const plan::Entry*>(smem + C::OFF_UNITS);
   const float* vec = reinterpret_cast<const float*>(smem + C::OFF_VEC);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // uniform: see the issuing warps
-  const int row_tile = p.tok * p.group;  // rows of a row tile
+  const int row_tile = p.tok * p.group;            // rows of a row tile (rows own)
+  const int half_rows = p.half_tok * p.half_per;  // rows that a half's copies write (keys own)
 
   if (threadIdx.x == 0) {
     for (int b = 0; b < C::A_BUFS; ++b) {
       ptx::mbar_init(bar(C::B_AFULL + b), 1);
-      ptx::mbar_init(bar(C::B_AEMPTY + b), SPLIT ? 2 : 1);
+      ptx::mbar_init(bar(C::B_AEMPTY + b), 2);
     }
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < SLOTS; ++s) {
       ptx::mbar_init(bar(C::B_FULL + s), DKDV ? 33 : 1);  // bytes, and the copy warp's lanes for the table
-      ptx::mbar_init(bar(C::B_EMPTY + s), SPLIT ? 2 : 1);
+      ptx::mbar_init(bar(C::B_EMPTY + s), 1);
     }
     for (int h = 0; h < 2; ++h) {
       ptx::mbar_init(bar(C::B_MMFULL + h), 1);
@@ -258,22 +265,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       ptx::mbar_init(bar(C::B_TAILREQ + h), 1);
       ptx::mbar_init(bar(C::B_TAIL + h), 1);
       ptx::mbar_init(bar(C::B_DRAIN + h), 1);
+      ptx::mbar_init(bar(C::B_TURN + h), 1);
     }
-    ptx::mbar_init(bar(C::B_ACC), SPLIT ? 2 : 1);
+    ptx::mbar_init(bar(C::B_ACC), 2);
     for (int u = 0; u < UNITS; ++u) {
       ptx::mbar_init(bar(C::B_UNITFULL + u), 1);
-      ptx::mbar_init(bar(C::B_UNITEMPTY + u), 8 + (SPLIT ? 2 : 1) + 1);  // elementwise, issuing and tail warps
+      ptx::mbar_init(bar(C::B_UNITEMPTY + u), 8 + 2 + 1);  // elementwise, issuing and tail warps
     }
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
-  if (DKDV && row_tile < T) {
+  if (DKDV) {
     // rows of the ring, and of the table, that no copy writes
-    for (int x = threadIdx.x; x < 2 * STAGES * C::CHUNKS * (T - row_tile) * 8; x += THREADS) {
-      const int slab = x / ((T - row_tile) * 8), at = x % ((T - row_tile) * 8);
-      ptx::st_shared_v4(s_base + C::OFF_R0 + slab * C::CHUNK_BYTES + row_tile * 128 + at * 16, 0, 0, 0, 0);
+    for (int x = threadIdx.x; x < SLOTS * 2 * C::CHUNKS * (H - half_rows) * 8; x += THREADS) {
+      const int slab = x / ((H - half_rows) * 8), at = x % ((H - half_rows) * 8);
+      ptx::st_shared_v4(s_base + C::OFF_R0 + slab * C::HCHUNK_BYTES + half_rows * 128 + at * 16, 0, 0, 0, 0);
     }
-    for (int x = threadIdx.x; x < STAGES * 2 * T; x += THREADS) reinterpret_cast<float*>(smem + C::OFF_VEC)[x] = 0.0f;
+    for (int x = threadIdx.x; x < SLOTS * 2 * H; x += THREADS) reinterpret_cast<float*>(smem + C::OFF_VEC)[x] = 0.0f;
     ptx::fence_proxy_async_smem();
   }
   if (warp == WARP_MMA) {
@@ -297,10 +305,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   // runs through them in that order, each at its own pace. n < 0: no more units.
   auto unit_wait = [&](uint32_t un) -> bool { return wait_bar(bar(C::B_UNITFULL + un % UNITS), (un / UNITS) & 1, abort_flag); };
   auto unit_done = [&](uint32_t un) { ptx::mbar_arrive(bar(C::B_UNITEMPTY + un % UNITS)); };
-  // Rows of streamed tile j that belong to the sequence, when they are not all (else T or more).
-  auto there = [&](const plan::Entry& e, int j) -> int {
-    const int left = e.str_len - (e.j0 + j + e.skip) * (DKDV ? p.tok : T);
-    return DKDV ? (left >= p.tok ? T : left * p.group) : left;
+  // Rows of half h of streamed tile j that belong to the sequence, when they are not all (else H or more).
+  auto there = [&](const plan::Entry& e, int j, int h) -> int {
+    const int tile = e.j0 + j + e.skip;
+    const int left = max(e.str_len - tile * (DKDV ? p.tok : T) - h * (DKDV ? p.half_step : H), 0);
+    return DKDV ? (left >= p.half_tok ? H : left * p.half_per) : left;
   };
 
   // All lanes of a warp together.
@@ -308,7 +317,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     return __all_sync(0xffffffffu, wait_bar(b, parity, flag));
   };
 
-  uint32_t ring = 0;  // streamed tiles so far
+  uint32_t ring = 0;  // streamed tiles so far (copies: half tiles)
+  auto half_use = [](uint32_t tile, int h) -> uint32_t { return 2 * tile + h; };  // of the ring: place modulo SLOTS
   bool ok = true;
 
   if (warp == WARP_LOAD) {
@@ -348,34 +358,33 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         ++n_a;
-        for (int j = 0; j < n; ++j) {
-          const int st = ring % STAGES;
-          ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_EMPTY + st), ((ring / STAGES) & 1) ^ 1, abort_flag));
+        for (int jh = 0; jh < 2 * n; ++jh) {
+          const int st = ring % SLOTS, h = jh & 1, tile = e.j0 + (jh >> 1) + e.skip;
+          ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_EMPTY + st), ((ring / SLOTS) & 1) ^ 1, abort_flag));
           if (!ok) break;
-          const int tile = e.j0 + j + e.skip;
           const uint32_t full = bar(C::B_FULL + st);
+          const int tok0 = e.str_row + tile * p.tok + h * p.half_step;          // keys own: first token of the half
+          const int head0 = DKDV && p.half_step == 0 ? h * H : 0;               // and first head (more than H of them)
           if (lane == 0) {
-            ptx::mbar_arrive_expect_tx(full, 2 * C::CHUNKS * (DKDV ? row_tile : T) * 128);
+            ptx::mbar_arrive_expect_tx(full, 2 * C::CHUNKS * (DKDV ? half_rows : H) * 128);
             for (int c = 0; c < C::CHUNKS; ++c) {
-              const uint32_t r0 = s_base + C::OFF_R0 + st * C::TILE_BYTES + c * C::CHUNK_BYTES,
-                             r1 = s_base + C::OFF_R1 + st * C::TILE_BYTES + c * C::CHUNK_BYTES;
+              const uint32_t r0 = s_base + C::OFF_R0 + st * 2 * C::HALF_BYTES + c * C::HCHUNK_BYTES, r1 = r0 + C::HALF_BYTES;
               if (DKDV) {
-                tma_load_4d(r0, &tm_r0, full, c * 64, 0, e.str_row + tile * p.tok, e.hk);
-                tma_load_4d(r1, &tm_r1, full, c * 64, 0, e.str_row + tile * p.tok, e.hk);
+                tma_load_4d(r0, &tm_r0, full, c * 64, head0, tok0, e.hk);
+                tma_load_4d(r1, &tm_r1, full, c * 64, head0, tok0, e.hk);
               } else {
-                tma_load_rows(r0, &tm_r0, full, c * 64, e.str_row + tile * T, e.hk);
-                tma_load_rows(r1, &tm_r1, full, c * 64, e.str_row + tile * T, e.hk);
+                tma_load_rows(r0, &tm_r0, full, c * 64, e.str_row + tile * T + h * H, e.hk);
+                tma_load_rows(r1, &tm_r1, full, c * 64, e.str_row + tile * T + h * H, e.hk);
               }
             }
           }
           if (DKDV) {
-            const int tok0 = e.str_row + tile * p.tok;
-            const int rows = min(row_tile, (p.T_q - tok0) * p.group);
-            const float* src = p.stats + e.hk * p.rows + (long long)tok0 * p.group;
-            const uint32_t dst = s_base + C::OFF_VEC + st * 2 * T * 4;
+            const int rows = min(min(half_rows, p.group * p.half_tok - head0), (p.T_q - tok0) * p.group - head0);
+            const float* src = p.stats + e.hk * p.rows + (long long)tok0 * p.group + head0;
+            const uint32_t dst = s_base + C::OFF_VEC + st * 2 * H * 4;
             for (int x = lane; x < rows; x += 32) {
               copy_word(dst + x * 4, src + x);
-              copy_word(dst + (T + x) * 4, src + p.stat_size + x);
+              copy_word(dst + (H + x) * 4, src + p.stat_size + x);
             }
             copies_arrive(full);
           }
@@ -386,126 +395,116 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (!ok && lane == 0) {
         for (int b = 0; b < C::A_BUFS; ++b)
           if (n_a > (uint32_t)b) drain_wait(bar(C::B_AFULL + b), ((n_a - 1 - b) / C::A_BUFS) & 1);
-        for (uint32_t x = ring > STAGES ? ring - STAGES : 0; x < ring; ++x) drain_wait(bar(C::B_FULL + x % STAGES), (x / STAGES) & 1);
+        for (uint32_t x = ring > SLOTS ? ring - SLOTS : 0; x < ring; ++x) drain_wait(bar(C::B_FULL + x % SLOTS), (x / SLOTS) & 1);
       }
     }
   } else if (warp == WARP_MMA || warp == WARP_MMA + 1) {
     // ================================================================ MMA issuers
-    // Per streamed tile and half: the sums of the tile before, then S and dP. SPLIT: a warp per half,
-    // else warp WARP_MMA serves both. Where a unit starts, both halves' sums come first, since S and
-    // dP need the new own tiles.
+    // A warp per half of the streamed tiles: the sums of the tile before, then S and dP; where a unit starts, the
+    // sums come first, since S and dP need the new own tiles. They take turns, half 0 before half 1: one waits for
+    // its operands while the other issues, and the sums' order is always the same.
     // The whole warp runs the loops, one lane issues: what goes into descriptors and addresses is uniform.
     auto uniform = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
     const int hs = (int)uniform(warp - WARP_MMA);
     const uint32_t issue = lane == 0, acc = uniform(tmem);
-    uint32_t n_a = 0, tails = 0;
+    uint32_t n_a = 0, tails = 0, turns = 0;
     uint64_t d_own = 0;  // offset of this unit's own tiles, in descriptors
     bool pend = false, pend_tail = false, first = false;  // sums of the tile before not yet issued
     const uint64_t d_a0 = ptx::sdesc_sw128(s_base + C::OFF_A0, 16, 1024);
     const uint64_t d_a1 = ptx::sdesc_sw128(s_base + C::OFF_A1, 16, 1024);
     const uint64_t d_r0k = ptx::sdesc_sw128(s_base + C::OFF_R0, 16, 1024);
     const uint64_t d_r1k = ptx::sdesc_sw128(s_base + C::OFF_R1, 16, 1024);
-    const uint64_t d_r0m = ptx::sdesc_sw128(s_base + C::OFF_R0, C::CHUNK_BYTES, 1024);
-    const uint64_t d_r1m = ptx::sdesc_sw128(s_base + C::OFF_R1, C::CHUNK_BYTES, 1024);
-    auto koff16 = [](int kk) { return (uint64_t)(((kk >> 2) * C::CHUNK_BYTES + (kk & 3) * 32) >> 4); };
-    auto issue_sdp = [&](uint32_t x, int h) {
-      const uint64_t so = (uint64_t)((uniform(x % STAGES) * C::TILE_BYTES + h * (T / 2) * 128) >> 4);
+    const uint64_t d_r0m = ptx::sdesc_sw128(s_base + C::OFF_R0, C::HCHUNK_BYTES, 1024);
+    const uint64_t d_r1m = ptx::sdesc_sw128(s_base + C::OFF_R1, C::HCHUNK_BYTES, 1024);
+    auto koff16 = [](int kk, int chunk) { return (uint64_t)(((kk >> 2) * chunk + (kk & 3) * 32) >> 4); };
+    auto place = [&](uint32_t x) { return (int)uniform(half_use(x, hs) % SLOTS); };
+    auto issue_sdp = [&](uint32_t x) {
+      const uint64_t so = (uint64_t)((place(x) * 2 * C::HALF_BYTES) >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        ptx::mma_ss_warp(acc + C::tm_x(h), d_a0 + d_own + koff16(kk), d_r0k + so + koff16(kk), C::IDESC_NN, kk > 0 ? 1u : 0u, issue);
+        ptx::mma_ss_warp(acc + C::tm_x(hs), d_a0 + d_own + koff16(kk, C::CHUNK_BYTES), d_r0k + so + koff16(kk, C::HCHUNK_BYTES), C::IDESC_NN, kk > 0 ? 1u : 0u, issue);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
-        ptx::mma_ss_warp(acc + C::tm_y(h), d_a1 + d_own + koff16(kk), d_r1k + so + koff16(kk), C::IDESC_NN, kk > 0 ? 1u : 0u, issue);
-      ptx::mma_commit_warp(bar(C::B_MMFULL + h), issue);
+        ptx::mma_ss_warp(acc + C::tm_y(hs), d_a1 + d_own + koff16(kk, C::CHUNK_BYTES), d_r1k + so + koff16(kk, C::HCHUNK_BYTES), C::IDESC_NN, kk > 0 ? 1u : 0u, issue);
     };
-    // the sums of ring use x's half h, once its P and dS are stored
-    auto issue_acc = [&](uint32_t x, int h) -> bool {
-      if (!wait_warp(bar(C::B_PFULL + h), x & 1, abort_flag)) return false;
-      ptx::tc_fence_after();
-      const uint64_t so = (uint64_t)((uniform(x % STAGES) * C::TILE_BYTES) >> 4);
-      const uint32_t start = first && (SPLIT || h == 0) ? 0u : 1u;
+    // the sums of this half of ring use x
+    auto issue_acc = [&](uint32_t x) {
+      const uint64_t so = (uint64_t)((place(x) * 2 * C::HALF_BYTES) >> 4);
+      const uint32_t start = first && hs == 0 ? 0u : 1u;
       // one accumulator after the other: MMAs that change it in turn run slower
 #pragma unroll
       for (int which = DKDV ? 1 : 0; which >= 0; --which)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-          const uint64_t brow = (uint64_t)(((h * 4 + kk) * 2048) >> 4);
-          const uint32_t a = acc + (which == 0 && DKDV ? C::tm_y(h) : C::tm_x(h)) + kk * 8;
-          ptx::mma_ts_warp(acc + acc_col(which, h), a, (which ? d_r1m : d_r0m) + so + brow, C::IDESC_ACC, kk > 0 ? 1u : start, issue);
+          const uint64_t brow = (uint64_t)((kk * 2048) >> 4);
+          const uint32_t a = acc + (which == 0 && DKDV ? C::tm_y(hs) : C::tm_x(hs)) + kk * 8;
+          ptx::mma_ts_warp(acc + acc_col(which), a, (which ? d_r1m : d_r0m) + so + brow, C::IDESC_ACC, kk > 0 ? 1u : start, issue);
         }
-      return true;
     };
-    auto tail_done = [&]() -> bool {
-      if (!pend_tail) return true;
-      pend_tail = false;
-      return wait_warp(bar(C::B_TAIL + (SPLIT ? hs : 0)), tails++ & 1, abort_flag);
+    // what the sums of ring use x read is there: this half's P and dS; and with a unit's first tile the other half's
+    // too, which says that the warps of both have read the accumulators of the unit before
+    auto stored = [&](uint32_t x) -> bool {
+      if (pend_tail && !wait_warp(bar(C::B_TAIL + hs), tails++ & 1, abort_flag)) return false;
+      return wait_warp(bar(C::B_PFULL + hs), x & 1, abort_flag) &&
+             (!first || wait_warp(bar(C::B_PFULL + (hs ^ 1)), x & 1, abort_flag));
     };
-    // both halves (SPLIT: this warp's) of the unit's last tile; the accumulators are complete after them
-    auto flush = [&]() -> bool {
-      if (!tail_done()) return false;
-      if (SPLIT) {
-        if (!issue_acc(ring - 1, hs)) return false;
-      } else if (!issue_acc(ring - 1, 0) || !issue_acc(ring - 1, 1)) {
-        return false;
+    auto my_turn = [&]() -> bool {
+      const bool good = hs == 0 ? turns == 0 || wait_warp(bar(C::B_TURN), (turns - 1) & 1, abort_flag)
+                                : wait_warp(bar(C::B_TURN + 1), turns & 1, abort_flag);
+      ++turns;
+      ptx::tc_fence_after();
+      return good;
+    };
+    auto pass_on = [&]() {
+      if (issue) ptx::mbar_arrive(bar(C::B_TURN + (hs ^ 1)));
+    };
+    for (uint32_t un = 0;; ++un) {
+      if (pend) {
+        // the unit's last tile; the accumulators are complete after it
+        if (!(ok = stored(ring - 1) && my_turn())) break;
+        issue_acc(ring - 1);
+        pass_on();
+        ptx::mma_commit_warp(bar(C::B_ACC), issue);
+        ptx::mma_commit_warp(bar(C::B_EMPTY + place(ring - 1)), issue);
+        pend = false;
       }
-      ptx::mma_commit_warp(bar(C::B_EMPTY + (ring - 1) % STAGES), issue);
-      ptx::mma_commit_warp(bar(C::B_ACC), issue);
-      pend = false;
-      return true;
-    };
-    {
-      if (SPLIT || hs == 0) {
-        for (uint32_t un = 0;; ++un) {
-          if (pend && !(ok = flush())) break;
-          if (!(ok = __all_sync(0xffffffffu, unit_wait(un)))) break;
-          const plan::Entry& e = units[un % UNITS];
-          const int n = (int)uniform(e.n);
-          if (n < 0) break;
-          if (n == 0) {
-            __syncwarp();
-            if (issue) unit_done(un);
-            continue;
-          }
-          const uint32_t ab = n_a % C::A_BUFS;
-          if (!(ok = wait_warp(bar(C::B_AFULL + ab), (n_a / C::A_BUFS) & 1, abort_flag))) break;
-          ++n_a;
-          d_own = (uint64_t)((uniform(ab) * 2 * C::TILE_BYTES) >> 4);
-          for (int j = 0; j < n; ++j) {
-            if (!(ok = wait_warp(bar(C::B_FULL + ring % STAGES), (ring / STAGES) & 1, abort_flag))) break;
-            ptx::tc_fence_after();
-            if (pend && !(ok = tail_done())) break;
-            if (SPLIT) {
-              if (pend && !(ok = issue_acc(ring - 1, hs))) break;
-              if (pend) ptx::mma_commit_warp(bar(C::B_EMPTY + (ring - 1) % STAGES), issue);
-              issue_sdp(ring, hs);
-            } else {
-              if (pend && !(ok = issue_acc(ring - 1, 0))) break;
-              issue_sdp(ring, 0);
-              if (pend && !(ok = issue_acc(ring - 1, 1))) break;
-              if (pend) ptx::mma_commit_warp(bar(C::B_EMPTY + (ring - 1) % STAGES), issue);
-              issue_sdp(ring, 1);
-            }
-            pend = true;
-            first = j == 0;
-            pend_tail = uniform(there(e, j) < T) != 0;
-            if (pend_tail && issue) ptx::mbar_arrive(bar(C::B_TAILREQ + (SPLIT ? hs : 0)));
-            ++ring;
-          }
-          if (!ok) break;
-          ptx::mma_commit_warp(bar(C::B_AEMPTY + ab), issue);
-          __syncwarp();
-          if (issue) unit_done(un);
-        }
-        if (!ok) {
-          ptx::mma_commit_warp(bar(C::B_DRAIN + hs), issue);
-          drain_wait(bar(C::B_DRAIN + hs), 0);
-        }
+      if (!(ok = __all_sync(0xffffffffu, unit_wait(un)))) break;
+      const plan::Entry& e = units[un % UNITS];
+      const int n = (int)uniform(e.n);
+      if (n < 0) break;
+      const uint32_t ab = n_a % C::A_BUFS;
+      if (n > 0) {
+        if (!(ok = wait_warp(bar(C::B_AFULL + ab), (n_a / C::A_BUFS) & 1, abort_flag))) break;
+        ++n_a;
+        d_own = (uint64_t)((uniform(ab) * 2 * C::TILE_BYTES) >> 4);
       }
+      for (int j = 0; j < n; ++j) {
+        if (!(ok = (!pend || stored(ring - 1)) && wait_warp(bar(C::B_FULL + place(ring)), (half_use(ring, hs) / SLOTS) & 1, abort_flag) &&
+                   my_turn()))
+          break;
+        if (pend) issue_acc(ring - 1);
+        issue_sdp(ring);
+        pass_on();
+        ptx::mma_commit_warp(bar(C::B_MMFULL + hs), issue);
+        if (pend) ptx::mma_commit_warp(bar(C::B_EMPTY + place(ring - 1)), issue);
+        pend = true;
+        first = j == 0;
+        pend_tail = uniform(there(e, j, hs) < H) != 0;
+        if (pend_tail && issue) ptx::mbar_arrive(bar(C::B_TAILREQ + hs));
+        ++ring;
+      }
+      if (!ok) break;
+      if (n > 0) ptx::mma_commit_warp(bar(C::B_AEMPTY + ab), issue);
       __syncwarp();
+      if (issue) unit_done(un);
     }
+    // every MMA and every arrival of this warp's commits is done before the CTA's shared memory goes
+    ptx::mma_commit_warp(bar(C::B_DRAIN + hs), issue);
+    drain_wait(bar(C::B_DRAIN + hs), 0);
+    __syncwarp();
   } else if (warp == WARP_TAIL) {
     // ================================================================ rows of other sequences: zero
-    uint32_t tails = 0;
+    uint32_t tails[2] = {};
     {
       for (uint32_t un = 0;; ++un) {
         ok = __all_sync(0xffffffffu, unit_wait(un));
@@ -514,24 +513,22 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int n = e.n;
         if (n < 0) break;
         for (int j = 0; j < n && ok; ++j, ++ring) {
-          const int from = there(e, j);
-          if (from >= T) continue;
-          for (int h = 0; h < (SPLIT ? 2 : 1); ++h) {
-            ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_TAILREQ + h), tails & 1, abort_flag));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int from = there(e, j, h);
+            if (from >= H) continue;
+            ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_TAILREQ + h), tails[h]++ & 1, abort_flag));
             if (!ok) break;
-            // SPLIT: the half that its issuer reads; else the whole tile. Keys own: Q and dO; rows own: K
-            const int lo = SPLIT ? max(from, h * (T / 2)) : from, hi = SPLIT ? (h + 1) * (T / 2) : T;
+            // what the sums read. Keys own: Q and dO; rows own: K
             for (int c = 0; c < (DKDV ? 2 : 1) * C::CHUNKS; ++c) {
-              const uint32_t slab = s_base + (c < C::CHUNKS ? C::OFF_R0 : C::OFF_R1) + (ring % STAGES) * C::TILE_BYTES +
-                                    (c % C::CHUNKS) * C::CHUNK_BYTES;
-              for (int x = lo * 8 + lane; x < hi * 8; x += 32) ptx::st_shared_v4(slab + x * 16, 0, 0, 0, 0);
+              const uint32_t slab = s_base + C::OFF_R0 + (half_use(ring, h) % SLOTS) * 2 * C::HALF_BYTES + c * C::HCHUNK_BYTES;
+              for (int x = from * 8 + lane; x < H * 8; x += 32) ptx::st_shared_v4(slab + x * 16, 0, 0, 0, 0);
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(bar(C::B_TAIL + h));
             __syncwarp();
           }
-          ++tails;
         }
         if (!ok) break;
         if (lane == 0) unit_done(un);
@@ -581,10 +578,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
         for (int j = 0; j < n; ++j, ++ring) {
-          const int st = ring % STAGES;
+          const int st = half_use(ring, g) % SLOTS;
           ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_MMFULL + g), ring & 1, abort_flag));
-          // the stage's table: complete already, waited on for its order
-          if (DKDV && ok) ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_FULL + st), (ring / STAGES) & 1, abort_flag));
+          // the place's table: complete already, waited on for its order
+          if (DKDV && ok) ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_FULL + st), (half_use(ring, g) / SLOTS) & 1, abort_flag));
           if (!ok) break;
           ptx::tc_fence_after();
           // columns [lo, hi) of this half are legal; the others' P and dS are 0. Rows of a row tile
@@ -592,17 +589,17 @@ __global__ void __launch_bounds__(THREADS, 1)
           int lo, hi;
           const int tile = e.j0 + j + e.skip;
           if (DKDV) {
-            const int t0 = tile * p.tok;
-            lo = min(max(my_lo - t0, 0), p.tok) * p.group - g * 64;
-            hi = my_hi - t0 >= p.tok ? T : max(my_hi - t0, 0) * p.group;
-            hi -= g * 64;
+            const int t0 = tile * p.tok + g * p.half_step;
+            lo = min(max(my_lo - t0, 0), p.half_tok) * p.half_per;
+            hi = my_hi - t0 >= p.half_tok ? H : max(my_hi - t0, 0) * p.half_per;
+            if (p.half_step == 0 && g == 1) hi = min(hi, p.group - H);  // one token's other heads: the table ends with them
           } else {
             lo = my_lo - tile * T - g * 64;
             hi = my_hi - tile * T - g * 64;
           }
           const bool full = lo <= 0 && hi >= 64;
-          const float* vnl = vec + st * 2 * T + g * 64;
-          const float* vnd = vnl + T;
+          const float* vnl = vec + st * 2 * H;
+          const float* vnd = vnl + H;
 #pragma unroll
           for (int ch = 0; ch < 2; ++ch) {
             uint32_t xs[32], ys[32];
@@ -660,8 +657,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           ptx::tc_fence_after();
         }
         constexpr int NCH = DKDV ? D / 32 : D / 64;
-        const uint32_t col0 = DKDV ? acc_col(g, 0) : acc_col(0, 0) + g * (D / 2);
-        const uint32_t col1 = DKDV ? col0 : acc_col(0, 1) + g * (D / 2);  // SPLIT: the other half's sums
+        const uint32_t col0 = DKDV ? acc_col(g) : acc_col(0) + g * (D / 2);
         float* part = e.slot < 0 ? nullptr : p.part + ((size_t)e.slot * T + r) * ACC_COLS + (DKDV ? g * D : g * (D / 2));
         uint16_t* to = nullptr;
         if (row_valid) {
@@ -678,15 +674,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             return;
           }
           ptx::tmem_ld32(tmem + lane_off + col0 + q4 * 32, o);
-          if (SPLIT) {
-            uint32_t o1[32];
-            ptx::tmem_ld32(tmem + lane_off + col1 + q4 * 32, o1);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) + __uint_as_float(o1[x]));
-          } else {
-            ptx::tmem_wait_ld();
-          }
+          ptx::tmem_wait_ld();
         };
         if (D == 64 && part == nullptr) {
           // through shared memory, so that neighbouring lanes store one row's 128 (dQ: this half's 64) bytes:
@@ -808,12 +796,12 @@ __global__ void __launch_bounds__(256) attn_packed_sum_kernel(const SumParams p)
   }
 }
 
-// [tokens, heads, d] as (d, head of the group, token, key/value head), boxes of a row tile.
+// [tokens, heads, d] as (d, head of the group, token, key/value head), boxes of tok tokens times so many heads.
 CUresult encode_group(PFN_encodeTiled enc, CUtensorMap* map, const void* base, int d, long long tokens, int h_kv, int group,
-                      int tok, long long ts, long long hs) {
+                      int heads, int tok, long long ts, long long hs) {
   cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)group, (cuuint64_t)tokens, (cuuint64_t)h_kv};
   cuuint64_t strides[3] = {(cuuint64_t)hs * 2, (cuuint64_t)ts * 2, (cuuint64_t)hs * 2 * group};
-  cuuint32_t box[4] = {64, (cuuint32_t)group, (cuuint32_t)tok, 1};
+  cuuint32_t box[4] = {64, (cuuint32_t)heads, (cuuint32_t)tok, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -821,10 +809,10 @@ CUresult encode_group(PFN_encodeTiled enc, CUtensorMap* map, const void* base, i
 }
 
 CUresult encode_keys(PFN_encodeTiled enc, CUtensorMap* map, const void* base, int d, long long tokens, int h_kv, long long ts,
-                     long long hs) {
+                     long long hs, int rows) {
   cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)tokens, (cuuint64_t)h_kv};
   cuuint64_t strides[2] = {(cuuint64_t)ts * 2, (cuuint64_t)hs * 2};
-  cuuint32_t box[3] = {64, (cuuint32_t)T, 1};
+  cuuint32_t box[3] = {64, (cuuint32_t)rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -832,7 +820,9 @@ CUresult encode_keys(PFN_encodeTiled enc, CUtensorMap* map, const void* base, in
 }
 
 struct Sizes {
-  int group, tok;
+  int group, tok;                         // rows own: tokens per row tile
+  int half_tok, half_per, half_step;  // keys own: see BwdParams
+  int str_tok;                        // tokens per streamed row tile
   long long key_items, row_items;
   size_t key_plan, row_plan, stats, key_part, row_part;
 };
@@ -841,6 +831,12 @@ Sizes sizes_of(int T_q, int T_k, int B, int h_q, int h_kv, int d) {
   Sizes s;
   s.group = h_q / h_kv;
   s.tok = T / s.group;
+  // each half of a streamed row tile is whole tokens; one token of more than H heads is cut between heads
+  const bool cut = s.group > H;
+  s.half_tok = cut ? 1 : H / s.group;
+  s.half_per = cut ? H : s.group;
+  s.half_step = cut ? 0 : s.half_tok;
+  s.str_tok = cut ? 1 : 2 * s.half_tok;
   s.key_items = T_k / T + B;
   s.row_items = T_q / s.tok + B;
   s.key_plan = plan::bytes(s.key_items, h_kv, B, kSms);
@@ -881,11 +877,16 @@ int run(const PackedBwdArgs& a, PFN_encodeTiled enc, void* workspace) {
     attr_done[dev].store(true, std::memory_order_release);
   }
   const Sizes s = sizes_of(a.T_q, a.T_k, a.B, a.h_q, a.h_kv, D);
-  CUtensorMap mq, mdo, mk, mv;
-  if (encode_group(enc, &mq, a.q, D, a.T_q, a.h_kv, s.group, s.tok, a.q_ts, a.q_hs) != CUDA_SUCCESS ||
-      encode_group(enc, &mdo, a.dout, D, a.T_q, a.h_kv, s.group, s.tok, a.dout_ts, a.dout_hs) != CUDA_SUCCESS ||
-      encode_keys(enc, &mk, a.k, D, a.T_k, a.h_kv, a.k_ts, a.k_hs) != CUDA_SUCCESS ||
-      encode_keys(enc, &mv, a.v, D, a.T_k, a.h_kv, a.v_ts, a.v_hs) != CUDA_SUCCESS)
+  CUtensorMap own[4], str[4];  // q, dout, k, v as own tiles and as halves of streamed ones
+  const int heads = std::min(s.group, H);
+  if (encode_group(enc, &own[0], a.q, D, a.T_q, a.h_kv, s.group, s.group, s.tok, a.q_ts, a.q_hs) != CUDA_SUCCESS ||
+      encode_group(enc, &own[1], a.dout, D, a.T_q, a.h_kv, s.group, s.group, s.tok, a.dout_ts, a.dout_hs) != CUDA_SUCCESS ||
+      encode_keys(enc, &own[2], a.k, D, a.T_k, a.h_kv, a.k_ts, a.k_hs, T) != CUDA_SUCCESS ||
+      encode_keys(enc, &own[3], a.v, D, a.T_k, a.h_kv, a.v_ts, a.v_hs, T) != CUDA_SUCCESS ||
+      encode_group(enc, &str[0], a.q, D, a.T_q, a.h_kv, s.group, heads, s.half_tok, a.q_ts, a.q_hs) != CUDA_SUCCESS ||
+      encode_group(enc, &str[1], a.dout, D, a.T_q, a.h_kv, s.group, heads, s.half_tok, a.dout_ts, a.dout_hs) != CUDA_SUCCESS ||
+      encode_keys(enc, &str[2], a.k, D, a.T_k, a.h_kv, a.k_ts, a.k_hs, H) != CUDA_SUCCESS ||
+      encode_keys(enc, &str[3], a.v, D, a.T_k, a.h_kv, a.v_ts, a.v_hs, H) != CUDA_SUCCESS)
     return ATTN_ERR_UNSUPPORTED;
   uint8_t* at = static_cast<uint8_t*>(workspace);
   plan::Args keys = {};
@@ -904,7 +905,8 @@ int run(const PackedBwdArgs& a, PFN_encodeTiled enc, void* workspace) {
   keys.max_deal = kMaxDeal;
   plan::Args rows = keys;
   keys.own_keys = 1;
-  keys.may_cut = (a.T_q + s.tok - 1) / s.tok > kMinShare;
+  keys.tok = s.str_tok;
+  keys.may_cut = (a.T_q + s.str_tok - 1) / s.str_tok > kMinShare;
   rows.may_cut = (a.T_k + T - 1) / T > kMinShare;
   plan::place(keys, at, s.key_items);
   at += s.key_plan;
@@ -937,7 +939,10 @@ int run(const PackedBwdArgs& a, PFN_encodeTiled enc, void* workspace) {
   p.g1_ts = a.dv_ts;
   p.g1_hs = a.dv_hs;
   p.group = s.group;
-  p.tok = s.tok;
+  p.tok = s.str_tok;
+  p.half_tok = s.half_tok;
+  p.half_per = s.half_per;
+  p.half_step = s.half_step;
   p.T_q = a.T_q;
   p.h_kv = a.h_kv;
   p.causal = a.causal;
@@ -945,7 +950,8 @@ int run(const PackedBwdArgs& a, PFN_encodeTiled enc, void* workspace) {
   p.scale = a.scale;
   p.scale_log2 = (float)((double)a.scale * 1.4426950408889634074);
   p.part = key_part;
-  if (!launch(attn_packed_bwd_kernel<D, true>, kSms, THREADS, C::SMEM_BYTES, a.stream, mk, mv, mq, mdo, p)) return ATTN_ERR_CUDA;
+  if (!launch(attn_packed_bwd_kernel<D, true>, kSms, THREADS, C::SMEM_BYTES, a.stream, own[2], own[3], str[0], str[1], p)) return ATTN_ERR_CUDA;
+  p.tok = s.tok;
   p.head = rows.head;
   p.range = rows.range;
   p.list = rows.list;
@@ -954,7 +960,7 @@ int run(const PackedBwdArgs& a, PFN_encodeTiled enc, void* workspace) {
   p.g0_hs = a.dq_hs;
   p.g1 = nullptr;
   p.part = row_part;
-  if (!launch(attn_packed_bwd_kernel<D, false>, kSms, THREADS, C::SMEM_BYTES, a.stream, mq, mdo, mk, mv, p)) return ATTN_ERR_CUDA;
+  if (!launch(attn_packed_bwd_kernel<D, false>, kSms, THREADS, C::SMEM_BYTES, a.stream, own[0], own[1], str[2], str[3], p)) return ATTN_ERR_CUDA;
   if (keys.may_cut || rows.may_cut) {
     const SumParams sum = {{keys.head, keys.joins, key_part},
                            {rows.head, rows.joins, row_part},
