@@ -66,6 +66,44 @@ def test_many_short_sequences(d):
     verify(q, k, v, q_at, k_at, True)
 
 
+@pytest.mark.parametrize("group", [5, 7, 12, 33, 48, 64, 65, 96, 127, 128])
+def test_head_groups(group):
+    """Groups that do not divide half a row tile, and those of which one token fills more than half."""
+    for d, causal, window in ((64, True, -1), (128, True, 20)):
+        q, k, v, q_at, k_at = make(group, [3, 0, 70, 1, 33], [5, 4, 200, 129, 0], group, 1, d, back=1)
+        verify(q, k, v, q_at, k_at, causal, window)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_calls_in_a_row_over_more_than_the_l2(d):
+    """Hundreds of calls that nothing waits between, over inputs that the L2 cannot hold, so that tiles come late: the
+    same bits each time. (Once an issuer missed a tile's phase here, one call in ten thousand.)"""
+    lens, h_q, h_kv = [1 + 470 * i % 3301 for i in range(24)], 12, 4
+    T = sum(lens)
+    at = torch.tensor(starts(lens), dtype=torch.int32, device="cuda")
+    ws = torch.empty(attn.attn_packed_bwd_workspace_size(T, T, len(lens), h_q, h_kv, d), dtype=torch.uint8, device="cuda")
+    states = []
+    for seed in range(2):
+        q, k, v, q_at, k_at = make(seed, lens, None, h_q, h_kv, d)
+        out, lse = forward(q, k, v, q_at, k_at, True, 511)
+        dout = torch.randn(q.shape, generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+        grads = [torch.empty_like(x) for x in (q, k, v)]
+        states.append((q, k, v, out, dout, lse, *grads, at, ws))
+    call = lambda s: attn.attn_packed_bwd(*s, mask_mode=attn.MASK_CAUSAL, window=511)  # noqa: E731
+    want = []
+    for s in states:
+        call(s)
+        torch.cuda.synchronize()
+        want.append([x.clone() for x in s[6:9]])
+    for i in range(400):
+        call(states[i % 2])
+    torch.cuda.synchronize()
+    assert attn.attn_fault_status() == (attn.ATTN_OK, 0)
+    for s, w in zip(states, want):
+        for x, y in zip(s[6:9], w):
+            assert torch.equal(x, y)
+
+
 def test_thousands_of_sequences():
     g = torch.Generator().manual_seed(8)
     lens = torch.randint(0, 4, (5000,), generator=g).tolist()

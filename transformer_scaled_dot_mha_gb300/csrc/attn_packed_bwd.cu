@@ -72,7 +72,7 @@ struct BCfg {
   static constexpr int HALF_BYTES = H * D * 2;
   static constexpr int OFF_R0 = OFF_A0 + A_BUFS * 2 * TILE_BYTES;       // ring: Q, or K; and behind each
   static constexpr int OFF_R1 = OFF_R0 + HALF_BYTES;                    // dO, or V
-  static constexpr int OFF_VEC = OFF_R0 + SLOTS * 2 * HALF_BYTES;       // float [SLOTS][-lse log2(e)[H], -D[H]]
+  static constexpr int OFF_VEC = OFF_R0 + SLOTS * 2 * HALF_BYTES;       // float [SLOTS][-lse log2(e)[H], -D[H]], or of the own rows
   // d = 64: rows on their way out, 32 per elementwise warp
   static constexpr int OFF_STAGE = OFF_VEC + SLOTS * 2 * H * 4;
   static constexpr int OFF_UNITS = OFF_STAGE + (D == 64 ? 8 * 4096 : 0);
@@ -90,6 +90,7 @@ struct BCfg {
   __host__ __device__ static constexpr uint32_t tm_y(int h) { return 128u * h + 64u; }
   static constexpr uint32_t IDESC_NN = ptx::idesc_bf16_f32(T, T / 2, false);
   static constexpr uint32_t IDESC_ACC = ptx::idesc_bf16_f32(T, D, true);
+  static_assert(SLOTS * H >= A_BUFS * T, "tables");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 
@@ -252,8 +253,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int b = 0; b < C::A_BUFS; ++b) {
-      ptx::mbar_init(bar(C::B_AFULL + b), 1);
-      ptx::mbar_init(bar(C::B_AEMPTY + b), 2);
+      ptx::mbar_init(bar(C::B_AFULL + b), DKDV ? 1 : 33);  // bytes, and the copy warp's lanes for the table
+      ptx::mbar_init(bar(C::B_AEMPTY + b), DKDV ? 2 : 2 + 8);  // issuers; elementwise warps, which read the table
     }
     for (int s = 0; s < SLOTS; ++s) {
       ptx::mbar_init(bar(C::B_FULL + s), DKDV ? 33 : 1);  // bytes, and the copy warp's lanes for the table
@@ -357,6 +358,16 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
         }
+        if (!DKDV) {
+          const int rows = min(row_tile, (p.T_q - e.own_row) * p.group);
+          const float* src = p.stats + e.hk * p.rows + (long long)e.own_row * p.group;
+          const uint32_t dst = s_base + C::OFF_VEC + ab * 2 * T * 4;
+          for (int x = lane; x < rows; x += 32) {
+            copy_word(dst + x * 4, src + x);
+            copy_word(dst + (T + x) * 4, src + p.stat_size + x);
+          }
+          copies_arrive(a_full);
+        }
         ++n_a;
         for (int jh = 0; jh < 2 * n; ++jh) {
           const int st = ring % SLOTS, h = jh & 1, tile = e.j0 + (jh >> 1) + e.skip;
@@ -441,12 +452,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           ptx::mma_ts_warp(acc + acc_col(which), a, (which ? d_r1m : d_r0m) + so + brow, C::IDESC_ACC, kk > 0 ? 1u : start, issue);
         }
     };
-    // what the sums of ring use x read is there: this half's P and dS; and with a unit's first tile the other half's
-    // too, which says that the warps of both have read the accumulators of the unit before
+    // what the sums of ring use x read is there: this half's P and dS; and with a unit's first tile, for the issuer that
+    // goes first and overwrites the accumulators, the other half's too, which says that the warps of both have
+    // read them for the unit before. (Not for the second: the first may be a tile ahead by then, and a wait for a
+    // phase is a wait for its parity.)
     auto stored = [&](uint32_t x) -> bool {
       if (pend_tail && !wait_warp(bar(C::B_TAIL + hs), tails++ & 1, abort_flag)) return false;
-      return wait_warp(bar(C::B_PFULL + hs), x & 1, abort_flag) &&
-             (!first || wait_warp(bar(C::B_PFULL + (hs ^ 1)), x & 1, abort_flag));
+      const bool good = (!first || hs == 1 || wait_warp(bar(C::B_PFULL + 1), x & 1, abort_flag)) &&
+                        wait_warp(bar(C::B_PFULL + hs), x & 1, abort_flag);
+      ptx::tc_fence_after();
+      return good;
     };
     auto my_turn = [&]() -> bool {
       const bool good = hs == 0 ? turns == 0 || wait_warp(bar(C::B_TURN), (turns - 1) & 1, abort_flag)
@@ -571,11 +586,17 @@ __global__ void __launch_bounds__(THREADS, 1)
               my_lo = max(0, at - p.window);
               if (!p.causal) my_hi = min(my_hi, at + p.window + 1);
             }
-            const long long x = e.hk * p.rows + (long long)e.own_row * p.group + r;
-            const float nl = p.stats[x], nd = p.stats[p.stat_size + x];
-            nl2 = ptx::f2_pack(nl, nl);
-            nd2 = ptx::f2_pack(nd, nd);
           }
+        }
+        if (!DKDV && n > 0) {
+          const uint32_t ab = n_a % C::A_BUFS;
+          ok = __all_sync(0xffffffffu, wait_bar(bar(C::B_AFULL + ab), (n_a / C::A_BUFS) & 1, abort_flag));
+          if (!ok) break;
+          const float nl = vec[ab * 2 * T + r], nd = vec[(ab * 2 + 1) * T + r];  // of rows that are no row: any
+          nl2 = ptx::f2_pack(nl, nl);
+          nd2 = ptx::f2_pack(nd, nd);
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(C::B_AEMPTY + ab));
         }
         for (int j = 0; j < n; ++j, ++ring) {
           const int st = half_use(ring, g) % SLOTS;
