@@ -612,8 +612,11 @@ size_t attn_paged_chunk_workspace_size(int T, int n_seqs, int h_q, int h_kv, int
  * behind the length are never used, whatever they hold.
  * Supported: d in {64, 128}, h_q a multiple of h_kv (of at most 128 h_kv), scale > 0, any page size
  * (limits as in attn_paged_append; copies are of gcd(page_size, 128) rows, so page sizes that are
- * multiples of 16 or more are the fast ones), T below 2^28. Numerics as attn_packed_fwd; an 8-bit
- * cache's numbers enter the products exactly, as bf16. Two or three launches on `stream`.
+ * multiples of 8 or more are the fast ones), T below 2^28. Numerics as attn_packed_fwd, except with an
+ * 8-bit cache: its numbers enter the products exactly, as f16, and the operands beside them are f16
+ * too, each row of q times a power of two (exact but for entries below 2^-28 of the row's largest, which
+ * are rounded to 2^-39 of it) and the weights (rounded to 11 bits; those below 2^-32 of the row's largest
+ * may vanish). Two or three launches on `stream`.
  */
 int attn_paged_chunk(const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,
                      const int32_t* q_starts, const int32_t* page_table, const int32_t* cache_lens, int n_seqs, int T,

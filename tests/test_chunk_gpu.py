@@ -49,8 +49,12 @@ def verify(q, q_at, kp, vp, table, ln, sc, window=-1, sinks=0):
     ref.check(got, lse, *ref.chunk(q, q_at, kp, vp, table, ln, 1 / math.sqrt(q.shape[2]), window, sinks, *sc))
     assert torch.all(got[q_at[-1]:] == 7.0) and torch.all(lse[q_at[-1]:] == 7.0)
     again = run(q, q_at, kp, vp, table, ln, sc, window, sinks, fill=0)
-    assert torch.equal(got.view(torch.int16), again[0].view(torch.int16))  # bits: NaN stays NaN
-    assert torch.equal(lse.view(torch.int32), again[1].view(torch.int32))
+    assert same(got, again[0]) and same(lse, again[1])
+
+
+def same(x, y):  # bits: NaN stays NaN
+    as_int = torch.int16 if x.dtype == torch.bfloat16 else torch.int32
+    return torch.equal(x.contiguous().view(as_int), y.contiguous().view(as_int))
 
 
 CASES = [  # new tokens, lengths, h_q, h_kv, d, page, window, sinks, max_pages
@@ -99,7 +103,7 @@ def test_entries_that_name_no_page(d, e4m3, page):
 
 @pytest.mark.parametrize("d", [64, 128])
 def test_every_number_of_8_bits(d):
-    """All 254 finite e4m3 numbers, subnormal ones among them, as keys and values; one weight each."""
+    """All 254 finite e4m3 numbers, subnormal ones among them, as keys and values, with equal weights."""
     codes = torch.arange(256, dtype=torch.uint8)
     codes = codes[(codes & 0x7f) != 0x7f]
     n = 300
@@ -109,9 +113,6 @@ def test_every_number_of_8_bits(d):
     page = page.cuda()
     sc = [torch.tensor([2.0 ** -9], device="cuda"), torch.tensor([1.0], device="cuda")]
     q = torch.zeros(300, 1, d, dtype=torch.bfloat16, device="cuda")
-    for t in range(n):  # every query picks out its own key: a large multiple of the key that differs from the others'
-        q[t, 0] = 0
-    q[:, 0] = 0
     table, ln = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.tensor([n], dtype=torch.int32, device="cuda")
     verify(q, [0, n], page, page, table, ln, sc)           # equal weights: running means of the values
     verify(q, [0, n], page, page, table, ln, sc, window=0)  # only the own key: its value, exactly
@@ -127,6 +128,87 @@ def test_8_bit_nan_stays():
     got, lse = run(q, q_at, kp, vp, table, ln, sc)
     assert torch.isnan(got[:20]).any(-1).all() and torch.isnan(lse[:20]).all()
     assert torch.isfinite(got[20:40]).all()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page", [4, 16, 64])
+def test_pages_beyond_32_bits(e4m3, page):
+    """A pool of more than 2^32 bytes whose last pages are in use: the bits of a small pool with the same pages."""
+    q, q_at, kp, vp, table, ln, sc = make(35, [70, 3], [500, 130], 4, 2, 128, page, e4m3)
+    per_page = kp[0].numel() * kp.element_size()
+    n = (1 << 32) // per_page + 2 * kp.shape[0]
+    want = run(q, q_at, kp, vp, table, ln, sc)
+    big = []
+    for x in (kp, vp):
+        pool = torch.empty(n, *x.shape[1:], dtype=x.dtype, device="cuda")
+        pool.view(torch.uint8)[n - x.shape[0]:] = x.view(torch.uint8)
+        big.append(pool)
+    got = run(q, q_at, *big, table + (n - kp.shape[0]), ln, sc)
+    for x, y in zip(want, got):
+        assert same(x[:73], y[:73])
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_captured_calls_follow_the_lengths(e4m3):
+    """Two graphs on one workspace, replayed with other lengths and offsets than at capture."""
+    cases = [make(36 + i, [300, 20], [900, 700], 8, 2, 64, 16, e4m3, back=0) for i in range(2)]
+    size = attn.attn_paged_chunk_workspace_size(320, 2, 8, 2, 64)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    at, ln = torch.tensor([0, 300, 320], dtype=torch.int32, device="cuda"), cases[0][5].clone()
+    outs = [torch.zeros_like(c[0]) for c in cases]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for (q, _, kp, vp, table, _, sc), out in zip(cases, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=stream):
+            attn.attn_paged_chunk(q, kp, vp, out, at, table, ln, ws, k_scale=sc[0], v_scale=sc[1])
+    for new, lens in (([300, 20], [900, 700]), ([1, 319], [1, 640]), ([0, 1], [0, 77]), ([320, 0], [333, 5])):
+        at.copy_(torch.tensor(starts(new), dtype=torch.int32))
+        ln.copy_(torch.tensor(lens, dtype=torch.int32))
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            for g in graphs + graphs:
+                g.replay()
+        stream.synchronize()
+        for (q, _, kp, vp, table, _, sc), out in zip(cases, outs):
+            want, _ = run(q, starts(new), kp, vp, table, ln, sc)
+            assert same(out[:sum(new)], want[:sum(new)])
+
+
+def test_two_calls_at_once():
+    """On two streams, each with a workspace of its own: the results of calls that run alone."""
+    cases = [make(38 + i, [200, 1, 90], [900, 3000, 90], 8, 2, 128, 16, i == 1, back=0) for i in range(2)]
+    want = [run(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    at = torch.tensor(cases[0][1], dtype=torch.int32, device="cuda")
+    state = []
+    for q, *_ in cases:
+        ws = torch.empty(attn.attn_paged_chunk_workspace_size(291, 3, 8, 2, 128), dtype=torch.uint8, device="cuda")
+        state.append((torch.zeros_like(q), torch.zeros(291, 8, device="cuda"), ws))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for stream, (q, _, kp, vp, table, ln, sc), (out, lse, ws) in zip(streams, cases, state):
+            attn.attn_paged_chunk(q, kp, vp, out, at, table, ln, ws, lse=lse, k_scale=sc[0], v_scale=sc[1], stream=stream)
+    torch.cuda.synchronize()
+    for w, (out, lse, _) in zip(want, state):
+        assert same(w[0], out) and same(w[1], lse)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page", [4, 16])
+def test_calls_in_a_row_over_more_than_the_l2(e4m3, page):
+    """Hundreds of calls that nothing waits between, over caches that the L2 cannot hold."""
+    new, lens = [65, 1, 1, 300, 1, 129], [9000, 20000, 41, 30000, 7777, 16000]
+    q, q_at, kp, vp, table, ln, sc = make(40, new, lens, 16, 8, 128, page, e4m3, back=0)
+    want = run(q, q_at, kp, vp, table, ln, sc)
+    out, lse, at = torch.empty_like(want[0]), torch.empty_like(want[1]), torch.tensor(q_at, dtype=torch.int32, device="cuda")
+    ws = torch.empty(attn.attn_paged_chunk_workspace_size(sum(new), 6, 16, 8, 128), dtype=torch.uint8, device="cuda")
+    for _ in range(300):
+        attn.attn_paged_chunk(q, kp, vp, out, at, table, ln, ws, lse=lse, k_scale=sc[0], v_scale=sc[1])
+    torch.cuda.synchronize()
+    assert attn.attn_fault_status() == (attn.ATTN_OK, 0)
+    assert same(out, want[0]) and same(lse, want[1])
 
 
 def test_as_one_decode_step():

@@ -104,6 +104,45 @@ def test_calls_in_a_row_over_more_than_the_l2(d):
             assert torch.equal(x, y)
 
 
+def test_two_calls_at_once_and_captured():
+    """On two streams, then from two graphs on one workspace: the results of calls that run alone."""
+    lens, h_q, h_kv, d = [700, 3, 0, 260], 6, 2, 64
+    T = sum(lens)
+    cases, want = [], []
+    for seed in (50, 51):
+        q, k, v, q_at, k_at = make(seed, lens, None, h_q, h_kv, d)
+        out, lse = forward(q, k, v, q_at, k_at, True, -1)
+        dout = torch.randn(q.shape, generator=torch.Generator().manual_seed(seed)).bfloat16().cuda()
+        want.append(backward(q, k, v, out, lse, dout, q_at, k_at, True, -1))
+        cases.append((q, k, v, out, dout, lse, *[torch.zeros_like(x) for x in (q, k, v)]))
+    at = torch.tensor(starts(lens), dtype=torch.int32, device="cuda")
+    size = attn.attn_packed_bwd_workspace_size(T, T, 4, h_q, h_kv, d)
+    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, c, w in zip(streams, cases, ws):
+            attn.attn_packed_bwd(*c, at, w, mask_mode=attn.MASK_CAUSAL, stream=s)
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        for x, y in zip(c[6:], w):
+            assert torch.equal(x, y)
+            x.zero_()
+    torch.cuda.synchronize()
+    graphs = []
+    for c in cases:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=streams[0]):
+            attn.attn_packed_bwd(*c, at, ws[0], mask_mode=attn.MASK_CAUSAL)
+    with torch.cuda.stream(streams[0]):
+        for g in graphs + graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        for x, y in zip(c[6:], w):
+            assert torch.equal(x, y)
+
+
 def test_thousands_of_sequences():
     g = torch.Generator().manual_seed(8)
     lens = torch.randint(0, 4, (5000,), generator=g).tolist()

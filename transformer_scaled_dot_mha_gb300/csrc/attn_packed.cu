@@ -22,13 +22,13 @@
 // adds the pieces up.
 //
 // Tiles. As in attn_fwd_tc.cu: at d = 64 a CTA has one row tile, two CTAs share an SM, and P has
-// TMEM columns of its own; at d = 128, and with pages, whose copies cost more, a CTA has two row
-// tiles, P written over S. Keys come as
-// 128-row tiles through a shared-memory ring:
+// TMEM columns of its own, with an MMA issuer for each product; at d = 128, and with pages, whose copies cost
+// more, a CTA has two row tiles, P written over S, with an issuer for each row tile (8 bits: one for both,
+// as four more warps have other work). Keys come as 128-row tiles through a shared-memory ring:
 //   dense   one TMA box per 64 columns;
-//   pages   warps for K and warps for V copy a tile row by row with cp.async, page numbers looked
-//           up ahead. Rows of no page (a bad entry, or behind the length) are zeros. Bad entries'
-//           keys are masked by bits that go with the tile.
+//   pages   warps for K and warps for V copy a tile page by page (TMA, or cp.async for the smallest), page
+//           numbers looked up ahead. Rows of no page (a bad entry, or behind the length) are zeros. Bad
+//           entries' keys are masked by bits that go with the tile.
 //   8 bits  the rows land in a raw tile, and four more warps turn it into the f16 tile that the
 //           products read: exact, as f16 holds every e4m3 number (the scales are folded into the
 //           exponent's factor and the last division). An MMA's operands are of one type, so Q
@@ -66,7 +66,7 @@ constexpr int UNITS = 4;    // units whose entries a CTA holds at a time
 constexpr int FLAGS = 8;    // tiles whose page bits are held: more than the roles are apart
 constexpr int kMinShare = 2;   // tiles
 constexpr int kMaxDeal = 2;    // units per CTA above which they are not cut
-constexpr int kTmaShift = 5;   // 2^5 rows of a page or more go by one TMA copy, fewer by cp.async
+constexpr int kTmaShift = 3;   // 2^3 rows of a page or more go by one TMA copy, fewer by cp.async
 constexpr float kBias = 7.0f;  // P in f16 is 2^7 times the weight
 
 enum { DENSE = 0, PAGED = 1, PAGED8 = 2 };
@@ -251,8 +251,10 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;
 // A copy warp's view of the pages: where the 128 rows of a key tile lie, and their copies into a tile (bf16:
 // 128-byte swizzle, a slab per 64 columns; 8 bits: rows of d bytes). Rows come in boxes of
 // gcd(page size, 128), which no page border cuts.
-// Boxes of 32 rows and more go by TMA, smaller and partly filled ones by cp.async: a TMA copy, whatever its
-// size, takes some 100 ns of one warp's time, in which cp.async moves 2 KB.
+// Boxes of 8 rows and more (the swizzle's period) go by TMA, a lane issuing each, smaller and partly filled ones by
+// cp.async. With 16 rows a page, TMA against cp.async: 509 tokens over 60001 keys of 8 bits, 64/8 heads of 128,
+// 826 us against 1122; 16 prompts' pieces, 16/4 heads of 64, window 1023, 110 against 116. With 8 rows 886
+// against 1384 and 110 against 123.
 template <int D, int KIND>
 struct PageRows {
   static constexpr int ROW = KIND == PAGED8 ? D : 2 * D;  // bytes
@@ -368,22 +370,15 @@ struct PageRows {
       copies_arrive(full);
       return;
     }
-    if (shift >= 3) {
-      for (int b = r0 >> shift; b << shift < r0 + rows; ++b) {
-        const int row = __shfl_sync(0xffffffffu, base, b);
-        copy_box(dst, pool, b << shift, row, 1 << shift, row < 0 ? 0 : len - key0 - (b << shift));
-      }
-    } else {
-      const int c = lane % LPR, r_lane = lane / LPR;
-      for (int k = r0 >> 5; k < (r0 + rows) >> 5; ++k) {  // small boxes, row by row
-        const int rows32 = ahead ? base : row_of(k, key0, e);
-        for (int st = 0; st < 32; st += RPS) {
-          const int r = k * 32 + st + r_lane;
-          int row = __shfl_sync(0xffffffffu, rows32, ahead ? r >> shift : r & 31);
-          if (ahead && row >= 0) row += r & ((1 << shift) - 1);
-          const bool there = row >= 0 && key0 + r < len;
-          copy16(dst + offset(r, c), pool + (size_t)(there ? row : 0) * ROW + c * 16, there ? 16 : 0);
-        }
+    const int c = lane % LPR, r_lane = lane / LPR;
+    for (int k = r0 >> 5; k < (r0 + rows) >> 5; ++k) {  // small boxes, row by row
+      const int rows32 = ahead ? base : row_of(k, key0, e);
+      for (int st = 0; st < 32; st += RPS) {
+        const int r = k * 32 + st + r_lane;
+        int row = __shfl_sync(0xffffffffu, rows32, ahead ? r >> shift : r & 31);
+        if (ahead && row >= 0) row += r & ((1 << shift) - 1);
+        const bool there = row >= 0 && key0 + r < len;
+        copy16(dst + offset(r, c), pool + (size_t)(there ? row : 0) * ROW + c * 16, there ? 16 : 0);
       }
     }
     copies_arrive(full);

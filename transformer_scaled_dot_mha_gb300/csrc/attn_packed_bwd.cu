@@ -8,8 +8,8 @@
 // Rows are packed as in attn_packed.cu: a row tile is floor(128 / g) tokens times g heads, so the
 // sums over the group are part of the products' own sums over rows, without atomics or copies.
 //
-// Two passes of one kernel, whose tiles and steps are those of attn_bwd.cu: own rows stay in
-// shared memory, the other side's tiles stream through a ring.
+// Two passes of one kernel: own rows stay in shared memory, the other side's tiles of 128 rows stream through a ring
+// in halves, with an MMA issuer and a warpgroup for the elementwise part per half.
 //   keys own   (dK, dV) S^T = K Q_i^T, dP^T = V dO_i^T, then dV += P^T dO_i, dK += dS^T Q_i
 //   rows own   (dQ)     S = Q K_j^T,  dP = dO V_j^T,    then dQ += dS K_j
 // Seven products where the formulas have five, and in return no sums whose order varies: the same
@@ -18,9 +18,15 @@
 //
 // Streamed rows that belong to other sequences (behind a sequence's last row in its last tile)
 // count nothing, whatever they hold: their P and dS are set to 0, and a spare warp zeroes them in
-// shared memory before the products whose sums run over them (0 times infinity is NaN). Row tiles
-// of fewer than 128 rows (g not a power of two) leave rows of the ring that no copy writes: they
-// are zeroed once.
+// shared memory before the products whose sums run over them (0 times infinity is NaN). A half of a
+// streamed row tile is floor(64 / g) tokens, or, for g above 64, one token's first 64 heads or the others;
+// rows of the ring that no copy writes are zeroed once.
+//
+// What bounds it: at d = 128 the issue of the products (S and dP of half a tile are MMAs of 64 columns, which
+// shared memory feeds at 49 cycles each instead of 32: both operands are read from there), then the
+// seven products against five; at d = 64 the chain product, elementwise part, product of each half, and
+// for short sequences the units' starts and ends. 8192 causal tokens, 32/8 heads of 128: 1670 us, 823 TFLOP/s
+// of the formulas' five products; 64 sentences of 21 to 500 tokens, 8 heads of 64: 125 us.
 //
 // Every wait is bounded, as in attn_bwd.cu.
 #include <cuda.h>
@@ -154,13 +160,6 @@ __device__ __forceinline__ void copy_word(uint32_t dst, const float* src) {
 // Arrives on `bar` when this thread's copies so far have landed (an arrival that the barrier counts).
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
 }
 
 // ------------------------------------------------------------------ plans and D_i = dO_i . O_i
@@ -660,8 +659,8 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (DKDV) pw[x >> 1] = ptx::pack_bf16x2(p0, p1);
               dw[x >> 1] = ptx::pack_bf16x2(d0, d1);
             }
-            if (DKDV) tmem_st16(t_x + ch * 16, pw);
-            tmem_st16((DKDV ? t_y : t_x) + ch * 16, dw);
+            if (DKDV) ptx::tmem_st16(t_x + ch * 16, pw);
+            ptx::tmem_st16((DKDV ? t_y : t_x) + ch * 16, dw);
           }
           ptx::tmem_wait_st();
           ptx::tc_fence_before();
