@@ -21,6 +21,7 @@ namespace plan {
 
 constexpr int TILE = 128;      // streamed keys per tile, own rows per tile
 constexpr int THREADS = 1024;  // of the planning CTA
+constexpr int SMEM_LENS = 512;  // sequences whose offsets are kept from the first reading
 constexpr int SMEM_SEQS = 2047, SMEM_ITEMS = 2048;  // with more, these lists are in the workspace
 constexpr int BINS = 640;
 
@@ -237,6 +238,7 @@ __device__ __forceinline__ long long scan(long long v, long long* warps, long lo
 struct Scratch {  // shared memory
   long long warps[THREADS / 32];
   int first[SMEM_SEQS + 1];
+  Seq seq[SMEM_LENS];
   long long at[SMEM_ITEMS];  // cost of the items before each
   int rank[SMEM_ITEMS];      // its place among the items of its bin
   int bin[BINS];
@@ -296,7 +298,12 @@ __device__ __forceinline__ void write(const Args& a, Scratch& sh) {
   long long items = 0;
   for (int b0 = 0; b0 < a.B; b0 += THREADS) {
     const int b = b0 + t;
-    const int mine = b < a.B ? blocks_of(a, sequence(a, b)) : 0;
+    int mine = 0;
+    if (b < a.B) {
+      const Seq s = sequence(a, b);
+      if (b < SMEM_LENS) sh.seq[b] = s;
+      mine = blocks_of(a, s);
+    }
     long long total;
     const long long at = scan(mine, sh.warps, total);
     if (b < a.B) first[b] = (int)(items + at);
@@ -314,7 +321,7 @@ __device__ __forceinline__ void write(const Args& a, Scratch& sh) {
       if (first[mid] <= i) lo = mid;
       else hi = mid - 1;
     }
-    return item(a, sequence(a, lo), i - first[lo]);
+    return item(a, lo < SMEM_LENS ? sh.seq[lo] : sequence(a, lo), i - first[lo]);
   };
   // costs: the sum before every item, the largest, and how many there are of each
   long long sum = 0;
