@@ -48,7 +48,7 @@
 
 #include "attn_internal.h"
 #include "attn_plan.cuh"
-#include "ptx_sm103.cuh"
+#include "ptx_warp.cuh"
 
 namespace attn {
 
