@@ -534,7 +534,8 @@ size_t attn_packed_fwd_workspace_size(int T_q, int n_seqs, int h_q, int h_kv, in
  *           q_starts[b] .. q_starts[b + 1] - 1, its keys rows k_starts[b] .. of k and v.
  *           k_starts NULL: the queries' rows. Rows of no sequence (before the first, behind the
  *           last) are not used, and left as they were in out and lse. Offsets outside the
- *           arrays are clamped to them; a sequence that ends before it starts is empty.
+ *           arrays are clamped to them; a sequence that ends before it starts is empty. (Offsets that
+ *           decrease and so name rows more than once leave rows with any or no result.)
  *   mask_mode  ATTN_MASK_NONE or ATTN_MASK_CAUSAL. Query i of a sequence of n_q queries and n_k
  *           keys stands at position x = n_k - n_q + i (the last query at the last key); causal:
  *           key j is legal for j <= x only.

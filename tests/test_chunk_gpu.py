@@ -97,6 +97,7 @@ def test_entries_that_name_no_page(d, e4m3, page):
     table[0, 1::3] = -7
     table[0, 0] = kp.shape[0]
     table[1] = 1 << 29
+    table[0, 2:3] = -2 ** 31  # the lowest number, like any other
     verify(q, q_at, kp, vp, table, ln, sc)
     verify(q, q_at, kp, vp, table, ln, sc, window=90, sinks=5)
 

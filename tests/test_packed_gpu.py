@@ -191,6 +191,32 @@ def test_offsets_outside_the_arrays(d):
             ref.check(out, lse, *ref.packed(q, k, v, meant, meant, 1 / math.sqrt(d), True))
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_offsets_that_name_rows_again(d):
+    """Offsets that go back and forth would make more units than the work list has places for: nothing is written
+    outside the workspace or the rows, forward and backward."""
+    q, k, v, _, _ = make(21, [300], None, 2, 1, d)
+    at = torch.tensor([0, 300] * 200, dtype=torch.int32, device="cuda")
+    n = at.shape[0] - 1
+    dev = dict(dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.full((302, 2, d), 7.0, **dev), torch.zeros(300, 2, device="cuda")
+    grads = [torch.full((302, h, d), 7.0, **dev) for h in (2, 1, 1)]
+
+    def workspace(size):
+        ws = torch.full((size + 512,), 91, dtype=torch.uint8, device="cuda")
+        return ws, ws[:size]
+
+    (w0, ws), (w1, ws_bwd) = (workspace(f) for f in (attn.attn_packed_fwd_workspace_size(300, n, 2, 1, d),
+                                                     attn.attn_packed_bwd_workspace_size(300, 300, n, 2, 1, d)))
+    attn.attn_packed_fwd(q, k, v, out[:300], at, ws, lse=lse, mask_mode=attn.MASK_CAUSAL)
+    attn.attn_packed_bwd(q, k, v, out[:300], q, lse, *(x[:300] for x in grads), at, ws_bwd, mask_mode=attn.MASK_CAUSAL)
+    torch.cuda.synchronize()
+    assert attn.attn_fault_status() == (attn.ATTN_OK, 0)
+    assert torch.all(w0[-512:] == 91) and torch.all(w1[-512:] == 91)
+    for x in (out, *grads):
+        assert torch.all(x[300:] == 7.0)
+
+
 def test_without_lse_and_on_another_stream():
     q, k, v, q_at, k_at = make(14, [500, 3, 800], None, 4, 2, 128)
     want, _ = run(q, k, v, q_at, k_at, True)

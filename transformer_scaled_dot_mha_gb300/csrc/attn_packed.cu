@@ -278,7 +278,7 @@ struct PageRows {
     if (key < len) {
       const int page = key / p.page_size;
       in_ = key - page * p.page_size;
-      id_ = p.page_table[(size_t)seq * p.max_pages + page];
+      id_ = max(p.page_table[(size_t)seq * p.max_pages + page], -1);  // any bad one, but never NONE
     }
   }
   // Page numbers of list entries j .. j + tiles() - 1 of a unit, for take(); nothing waits for them here.

@@ -69,6 +69,7 @@ struct Args {
   int min_share;              // least tiles of a CTA's share when units are cut
   int max_deal;               // units per CTA from which on they are dealt whole
   int may_cut;
+  long long items;  // places for items; offsets that do not decrease have no more
   Header* head;
   int2* range;   // [ctas]
   Join* joins;   // [ctas]
@@ -87,6 +88,7 @@ inline size_t bytes(long long items, int h_kv, int B, int ctas) {
 
 inline void place(Args& a, void* base, long long items) {
   uint8_t* p = static_cast<uint8_t*>(base);
+  a.items = items;
   a.head = reinterpret_cast<Header*>(p);
   p += sizeof(Header);
   a.list = reinterpret_cast<Entry*>(p);
@@ -306,12 +308,12 @@ __device__ __forceinline__ void write(const Args& a, Scratch& sh) {
     }
     long long total;
     const long long at = scan(mine, sh.warps, total);
-    if (b < a.B) first[b] = (int)(items + at);
+    if (b < a.B) first[b] = (int)min(items + at, 0x7fffffffLL);
     items += total;
   }
-  if (t == 0) first[a.B] = (int)items;
   __syncthreads();
-  const int N = (int)items;
+  // offsets that decrease may name rows again and again: what has no place in the list is left out
+  const int N = (int)min(items, a.items);
   long long* at = N <= SMEM_ITEMS ? sh.at : a.at;
   int* rank = N <= SMEM_ITEMS ? sh.rank : a.rank;
   auto find = [&](int i) -> Entry {  // item i: the last sequence that starts at or before it and has items
