@@ -549,7 +549,7 @@ size_t attn_packed_fwd_workspace_size(int T_q, int n_seqs, int h_q, int h_kv, in
  * Supported: d in {64, 128}, h_q a multiple of h_kv (of at most 128 h_kv), scale > 0, T_q and
  * T_k below 2^28, n_seqs h_kv and the numbers of 128-row tiles below 2^30 together.
  * Numerics as attn_fwd: fp32 accumulation on the tensor cores, weights rounded to bf16 for the
- * second product, one rounding of the output. Two or three launches on `stream`; no atomics on
+ * second product, one rounding of the output. One to three launches on `stream`; no atomics on
  * results: the same bits on every run.
  */
 int attn_packed_fwd(const void* q, const void* k, const void* v, void* out, float* lse, int64_t q_stride,
@@ -617,7 +617,7 @@ size_t attn_paged_chunk_workspace_size(int T, int n_seqs, int h_q, int h_kv, int
  * 8-bit cache: its numbers enter the products exactly, as f16, and the operands beside them are f16
  * too, each row of q times a power of two (exact but for entries below 2^-28 of the row's largest, which
  * are rounded to 2^-39 of it) and the weights (rounded to 11 bits; those below 2^-32 of the row's largest
- * may vanish). Two or three launches on `stream`.
+ * may vanish). One to three launches on `stream`.
  */
 int attn_paged_chunk(const void* q, const void* k_pages, const void* v_pages, void* out, float* lse,
                      const int32_t* q_starts, const int32_t* page_table, const int32_t* cache_lens, int n_seqs, int T,

@@ -191,30 +191,44 @@ def test_offsets_outside_the_arrays(d):
             ref.check(out, lse, *ref.packed(q, k, v, meant, meant, 1 / math.sqrt(d), True))
 
 
+@pytest.mark.parametrize("d,h_q,h_kv", [(64, 1, 1), (128, 2, 1), (64, 3, 3), (128, 100, 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_small_batches_of_many_sequences(d, h_q, h_kv, causal):
+    """Up to a unit for every CTA: each finds its own, over more than one warp's width of sequences."""
+    for lens in ([i % 3 for i in range(100)], [0] * 70 + [5, 0, 140], [0, 0, 0]):
+        if sum(lens):
+            verify(*make(22, lens, None, h_q, h_kv, d, back=3), causal)
+        else:
+            q, k, v, q_at, k_at = make(22, lens, None, h_q, h_kv, d, back=3)
+            out, lse = run(q, k, v, q_at, k_at, causal)
+            assert torch.all(out == 7.0) and torch.all(lse == 7.0)
+
+
 @pytest.mark.parametrize("d", [64, 128])
-def test_offsets_that_name_rows_again(d):
+@pytest.mark.parametrize("T", [300, 40])
+def test_offsets_that_name_rows_again(d, T):
     """Offsets that go back and forth would make more units than the work list has places for: nothing is written
     outside the workspace or the rows, forward and backward."""
-    q, k, v, _, _ = make(21, [300], None, 2, 1, d)
-    at = torch.tensor([0, 300] * 200, dtype=torch.int32, device="cuda")
+    q, k, v, _, _ = make(21, [T], None, 2, 1, d)
+    at = torch.tensor([0, T] * (200 if T == 300 else 50), dtype=torch.int32, device="cuda")
     n = at.shape[0] - 1
     dev = dict(dtype=torch.bfloat16, device="cuda")
-    out, lse = torch.full((302, 2, d), 7.0, **dev), torch.zeros(300, 2, device="cuda")
-    grads = [torch.full((302, h, d), 7.0, **dev) for h in (2, 1, 1)]
+    out, lse = torch.full((T + 2, 2, d), 7.0, **dev), torch.zeros(T, 2, device="cuda")
+    grads = [torch.full((T + 2, h, d), 7.0, **dev) for h in (2, 1, 1)]
 
     def workspace(size):
         ws = torch.full((size + 512,), 91, dtype=torch.uint8, device="cuda")
         return ws, ws[:size]
 
-    (w0, ws), (w1, ws_bwd) = (workspace(f) for f in (attn.attn_packed_fwd_workspace_size(300, n, 2, 1, d),
-                                                     attn.attn_packed_bwd_workspace_size(300, 300, n, 2, 1, d)))
-    attn.attn_packed_fwd(q, k, v, out[:300], at, ws, lse=lse, mask_mode=attn.MASK_CAUSAL)
-    attn.attn_packed_bwd(q, k, v, out[:300], q, lse, *(x[:300] for x in grads), at, ws_bwd, mask_mode=attn.MASK_CAUSAL)
+    (w0, ws), (w1, ws_bwd) = (workspace(f) for f in (attn.attn_packed_fwd_workspace_size(T, n, 2, 1, d),
+                                                     attn.attn_packed_bwd_workspace_size(T, T, n, 2, 1, d)))
+    attn.attn_packed_fwd(q, k, v, out[:T], at, ws, lse=lse, mask_mode=attn.MASK_CAUSAL)
+    attn.attn_packed_bwd(q, k, v, out[:T], q, lse, *(x[:T] for x in grads), at, ws_bwd, mask_mode=attn.MASK_CAUSAL)
     torch.cuda.synchronize()
     assert attn.attn_fault_status() == (attn.ATTN_OK, 0)
     assert torch.all(w0[-512:] == 91) and torch.all(w1[-512:] == 91)
     for x in (out, *grads):
-        assert torch.all(x[300:] == 7.0)
+        assert torch.all(x[T:] == 7.0)
 
 
 def test_without_lse_and_on_another_stream():

@@ -702,10 +702,11 @@ def attn_paged_decode(q, k_pages, v_pages, out, page_table, cache_lens, workspac
 def _need_heads(t, name, shape, dev):
     """Data pointer, token stride and head stride of a bf16 ``[tokens, heads, d]`` tensor, tokens or
     heads outermost."""
-    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev or t.stride(2) != 1:
+    st = t.stride()
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev or st[2] != 1:
         raise ValueError(f"{name} must be a bfloat16 tensor of shape {list(shape)} on cuda:{dev} with d side by side, got "
-                         f"{t.dtype} {list(t.shape)} with strides {t.stride()} on {t.device}")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+                         f"{t.dtype} {list(t.shape)} with strides {st} on {t.device}")
+    return t.data_ptr(), st[0], st[1]
 
 
 def _need_starts(starts, name, dev):

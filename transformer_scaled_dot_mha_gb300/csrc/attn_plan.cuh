@@ -10,7 +10,8 @@
 //            CTA's first and last units may be pieces, whose partial results a second kernel
 //            joins. Taken when the units are few for every CTA, or one of them is longer than
 //            a CTA's even share.
-// Everything about a unit is in its entry, so a CTA needs one load to know its work.
+// Everything about a unit is in its entry, so a CTA needs one load to know its work. Where a call cannot have more
+// units than CTAs, nor any that would be cut, there is no list: each CTA finds its one unit itself.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -395,6 +396,42 @@ static __global__ void __launch_bounds__(THREADS, 1) attn_plan_kernel(const Args
   __shared__ Scratch scratch;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   write(a, scratch);
+}
+
+// Word `lane` (< 16) of unit u's entry, found without a list by a warp of its own; all are -1 for no unit.
+__device__ __forceinline__ int word_without_list(const Args& a, int u) {
+  const int lane = threadIdx.x & 31, i = u / a.h_kv;
+  int before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    Seq s = {};
+    int n = 0;
+    if (b0 + lane < a.B) {
+      s = sequence(a, b0 + lane);
+      n = blocks_of(a, s);
+    }
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const int own = i - (before + upto - n);
+    const uint32_t has = __ballot_sync(0xffffffffu, own >= 0 && own < n);
+    if (has) {
+      const Entry e = item(a, s, own);  // in one lane
+      const int w[16] = {e.own_row, e.own_n, e.str_row, e.str_len, e.pos, e.off, e.n_first, e.skip,
+                         e.j0,      e.n,     e.lo0,     e.hi0,     e.lo1, e.hi1, e.slot,    u - i * a.h_kv};
+      int word = -1;
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const int v = __shfl_sync(0xffffffffu, w[x], __ffs(has) - 1);
+        if (lane == x) word = v;
+      }
+      return word;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return -1;
 }
 
 // The copy warp's way through the list: the number of its CTA's next unit, or -1. Lane 0 asks.
