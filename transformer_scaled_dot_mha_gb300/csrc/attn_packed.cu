@@ -17,7 +17,7 @@
 // Work. attn_plan.cuh lists the units (row tiles of a sequence for one key/value head) with the
 // key tiles that each streams; the CTAs are persistent and their roles run through their units
 // without meeting, so the copies and the products of the next unit start while the softmax warps
-// still write the last one's rows. When the units are few the plan cuts them: a piece leaves its
+// still write the last one's rows. Units that are too long the plan cuts: a piece leaves its
 // rows' unnormalised sums, reference maxima and row sums in the workspace, and attn_join_kernel
 // adds the pieces up.
 //
@@ -65,7 +65,6 @@ constexpr uint32_t FAULT_PACKED = 512;
 constexpr int UNITS = 4;    // units whose entries a CTA holds at a time
 constexpr int FLAGS = 8;    // tiles whose page bits are held: more than the roles are apart
 constexpr int kMinShare = 2;   // tiles
-constexpr int kMaxDeal = 2;    // units per CTA above which they are not cut
 constexpr int kTmaShift = 3;   // 2^3 rows of a page or more go by one TMA copy, fewer by cp.async
 constexpr float kBias = 7.0f;  // P in f16 is 2^7 times the weight
 
@@ -1430,7 +1429,6 @@ int run(const PackedArgs& a, PFN_encodeTiled enc, void* workspace) {
   pa.sinks = a.sinks;
   pa.ctas = g.ctas;
   pa.min_share = kMinShare;
-  pa.max_deal = kMaxDeal;
   pa.may_cut = may_cut;
   plan::place(pa, workspace, g.items);
   Params p = {};

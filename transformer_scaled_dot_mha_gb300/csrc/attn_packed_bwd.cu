@@ -60,7 +60,6 @@ constexpr uint64_t kDrainLimitNs = 200000000ull;
 constexpr uint32_t FAULT_PACKED_BWD = 1024;
 constexpr int UNITS = 4;      // units whose entries a CTA holds at a time
 constexpr int kMinShare = 2;  // tiles
-constexpr int kMaxDeal = 4;   // units per CTA above which they are not cut
 
 template <int D>
 struct BCfg {
@@ -922,7 +921,6 @@ int run(const PackedBwdArgs& a, PFN_encodeTiled enc, void* workspace) {
   keys.window = a.window;
   keys.ctas = kSms;
   keys.min_share = kMinShare;
-  keys.max_deal = kMaxDeal;
   plan::Args rows = keys;
   keys.own_keys = 1;
   keys.tok = s.str_tok;

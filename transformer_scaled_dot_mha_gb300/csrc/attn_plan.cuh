@@ -8,8 +8,7 @@
 //            units for every CTA. (Who computes a unit does not change its result.)
 //   cut      the units' tiles one after the other, in equal shares of consecutive tiles, so a
 //            CTA's first and last units may be pieces, whose partial results a second kernel
-//            joins. Taken when the units are few for every CTA, or one of them is longer than
-//            a CTA's even share.
+//            joins. Taken when one unit is far longer than a CTA's even share, or few are long.
 // Everything about a unit is in its entry, so a CTA needs one load to know its work. Where a call cannot have more
 // units than CTAs, nor any that would be cut, there is no list: each CTA finds its one unit itself.
 #pragma once
@@ -25,6 +24,7 @@ constexpr int THREADS = 1024;  // of the planning CTA
 constexpr int SMEM_LENS = 512;  // sequences whose offsets are kept from the first reading
 constexpr int SMEM_SEQS = 2047, SMEM_ITEMS = 2048;  // with more, these lists are in the workspace
 constexpr int BINS = 640;
+constexpr int FEW = 4, LONG_SHARE = 128;  // units per CTA, tiles: see where `cut` is decided
 
 struct Entry {        // 64 bytes
   int own_row;        // first own row (token or key) in the packed array
@@ -68,7 +68,6 @@ struct Args {
   int h_kv, causal, window, sinks;  // window -1: none
   int ctas;                   // CTAs of the kernel that works the list off
   int min_share;              // least tiles of a CTA's share when units are cut
-  int max_deal;               // units per CTA from which on they are dealt whole
   int may_cut;
   long long items;  // places for items; offsets that do not decrease have no more
   Header* head;
@@ -349,9 +348,13 @@ __device__ __forceinline__ void write(const Args& a, Scratch& sh) {
   const int top = sh.max;
   const long long units = (long long)N * a.h_kv, work = sum * a.h_kv;
   const long long share = max((work + a.ctas - 1) / a.ctas, (long long)a.min_share);
-  // cut: few units for every CTA, or one that is far longer than an even share. A piece costs its CTA
-  // some tiles' time (its sums go through memory), so a little unevenness is the better choice.
-  const bool cut = a.may_cut && (units <= (long long)a.max_deal * a.ctas || top > share + share / 2);
+  // cut: one is far longer than an even share, or a few long ones would leave CTAs without work at the end. A piece
+  // costs its CTA some ten tiles' time (its sums go through memory), so unevenness is often the better choice:
+  // cut against whole, forward, 4096 positions, 16 heads of 128, causal (shares of 28 tiles) 110.7 and 72.7 us, 4 x 1024
+  // unmasked (14) 60.8 and 42.1, but 8192 unmasked (216) 358.8 and 386, 509 tokens over 60510 keys of 8 bits (398; 128
+  // units for 152 CTAs) 785 and 868; gradients, 4096 causal (56) 383 and 246, but 8192 causal, 32/8 heads (438) 1690
+  // and 1724.
+  const bool cut = a.may_cut && (top > share + share / 2 || (share >= LONG_SHARE && units <= (long long)FEW * a.ctas));
   if (t == 0) {
     a.head->cut = cut;
     a.head->n_units = (int)units;
