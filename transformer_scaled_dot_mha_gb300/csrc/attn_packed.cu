@@ -492,11 +492,11 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
       const plan::Entry& e = units[un % UNITS];
       const int n = e.n;
       if (n < 0) break;
-      if (pages.ahead && n > 0) {
+      if (n > 0 && pages.ahead) {
         if (!asked) pages.ask(e, 0);
         pages.take();
-        asked = false;
       }
+      asked = false;  // what was asked for a unit without keys is of no use to the one after it
       for (int j = 0; j < n; ++j, ++n_kv) {
         if (pages.ahead && (j & (pages.tiles() - 1)) == 0) {
           if (j + pages.tiles() < n) {
