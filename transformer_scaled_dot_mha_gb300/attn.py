@@ -109,6 +109,8 @@ def lib() -> ctypes.CDLL:
         L.attn_status_string.restype = ctypes.c_char_p
         L.attn_internal_arm_wait_timeout.argtypes = [ctypes.c_ulonglong, i]
         L.attn_internal_arm_wait_timeout.restype = None
+        L.attn_internal_arm_chunk_give_up.argtypes = [i]
+        L.attn_internal_arm_chunk_give_up.restype = None
         _lib = L
     return _lib
 
@@ -828,6 +830,12 @@ def _internal_arm_wait_timeout(wait_ns: int, skip_v_tile: int) -> None:
     made on this host thread gives up its waits after ``wait_ns`` and never copies the
     V tile of K/V tile ``skip_v_tile``, so it ends through the bounded-wait abort path."""
     lib().attn_internal_arm_wait_timeout(int(wait_ns), int(skip_v_tile))
+
+
+def _internal_arm_chunk_give_up(v_tile: int) -> None:
+    """Test hook (not part of the C ABI header): in the next attn_paged_chunk call made on this host thread the
+    copying warps of V give up before their tile ``v_tile``, as if a wait had run out there."""
+    lib().attn_internal_arm_chunk_give_up(int(v_tile))
 
 
 def attn_fault_status(stream=None, clear=True):

@@ -578,6 +578,10 @@ void attn_internal_arm_wait_timeout(unsigned long long wait_ns, int skip_v_tile)
   attn::arm_wait_timeout_injection(wait_ns, skip_v_tile < 0 ? 0 : skip_v_tile);
 }
 
+// As attn_internal_arm_wait_timeout, for the next attn_paged_chunk call made on this host thread: in every CTA the
+// copying warps of V give up before their tile v_tile, with the copies before it in flight.
+void attn_internal_arm_chunk_give_up(int v_tile) { attn::arm_chunk_give_up(v_tile < 0 ? 0 : v_tile); }
+
 const char* attn_status_string(int status) {
   switch (status) {
     case ATTN_OK: return "ATTN_OK";

@@ -252,6 +252,7 @@ int launch_attn_tc(const TcArgs& a, PFN_encodeTiled enc);   // attn_fwd_tc.cu
 int launch_attn_f32(const F32Args& a);                       // attn_fwd_f32.cu
 int read_fault_word(cudaStream_t stream, int clear, uint32_t* out);  // attn_fwd_tc.cu
 void arm_wait_timeout_injection(uint64_t wait_ns, int skip_v_tile);  // attn_fwd_tc.cu (tests only)
+void arm_chunk_give_up(int v_tile);                                  // attn_packed.cu (tests only)
 int decode_splits(int B, int H, int n_q, int n_max, int d);               // attn_decode.cu
 int decode_chunk_keys(int B, int H, int n_max, int d);                    // attn_decode.cu
 size_t decode_workspace_bytes(int B, int H, int n_q, int n_max, int d);  // attn_decode.cu

@@ -45,6 +45,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "attn_internal.h"
 #include "attn_plan.cuh"
@@ -178,6 +179,7 @@ struct Params {
   int h_kv;
   const float* k_scale;
   const float* v_scale;
+  int inject_v_tile;  // INJECT: the values' copying warps give up before this tile
 };
 
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, bool sleepy = false) {
@@ -390,7 +392,9 @@ struct PageRows {
   }
 };
 
-template <int D, int KIND>
+// INJECT is a test-only instantiation over pages: the copying warps of V give up before tile p.inject_v_tile, as if
+// a wait had run out there, with whatever copies are in flight. INJECT = false compiles to the plain kernel.
+template <int D, int KIND, bool INJECT>
 __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_SM)
     attn_packed_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const Params p) {
@@ -509,6 +513,12 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
         const int key0 = tile_of(e, j) * BN;
         const uint32_t full = bar(RAW ? C::B_RAWFULL + kv : C::B_FULL + (int)pos.s);
         pages.tile(j, e);
+        if (INJECT && kv == 1 && n_kv == (uint32_t)p.inject_v_tile) {
+          *abort_flag = 1;
+          if (lane == 0) atomicOr(&g_packed_fault_word, FAULT_PACKED);
+          good = false;
+          break;
+        }
         good = __all_sync(0xffffffffu, wait_bar(bar(RAW ? C::B_RAWEMPTY + kv : C::B_EMPTY + (int)pos.s),
                                                 (RAW ? n_kv & 1 : pos.ph) ^ 1, abort_flag, true));
         if (!good) break;
@@ -524,6 +534,18 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
       __syncwarp();
     }
     copies_wait();
+    if (!good && lane == 0) {
+      // boxes in flight must land before this CTA's shared memory goes away: the phases that this warp armed last. (bf16:
+      // one that the other half's warp has not armed as well does not end; the limit is then the boxes' time.)
+      if (RAW) {
+        if (n_kv > 0) drain_wait(bar(C::B_RAWFULL + kv), (n_kv - 1) & 1);
+      } else {
+#pragma unroll 1
+        for (uint32_t x = n_kv < C::SLOTS / 2 ? 0 : n_kv - C::SLOTS / 2; x < n_kv; ++x)
+          drain_wait(bar(C::B_FULL + kv + (int)(2 * x % C::SLOTS)), (2 * x / C::SLOTS) & 1);
+      }
+    }
+    __syncwarp();
     return good;
   };
 
@@ -1378,7 +1400,10 @@ bool launch(Kernel* kernel, dim3 grid, unsigned threads, size_t smem, cudaStream
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
-template <int D, int KIND>
+// The tile of the INJECT instantiation, for the next call over pages on the arming host thread; -1: not armed.
+thread_local int t_inject_v_tile = -1;
+
+template <int D, int KIND, bool INJECT = false>
 int run(const PackedArgs& a, PFN_encodeTiled enc, void* workspace) {
   using C = Cfg<D, KIND>;
   const Geometry g = geometry_of<D, KIND>(a.T_q, a.B, a.h_q, a.h_kv);
@@ -1386,8 +1411,8 @@ int run(const PackedArgs& a, PFN_encodeTiled enc, void* workspace) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return ATTN_ERR_CUDA;
   if (!attr_done[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(attn_packed_kernel<D, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES) !=
-        cudaSuccess)
+    if (cudaFuncSetAttribute(attn_packed_kernel<D, KIND, INJECT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::SMEM_BYTES) != cudaSuccess)
       return ATTN_ERR_CUDA;
     attr_done[dev].store(true, std::memory_order_release);
   }
@@ -1459,9 +1484,11 @@ int run(const PackedArgs& a, PFN_encodeTiled enc, void* workspace) {
   p.h_kv = a.h_kv;
   p.k_scale = a.k_scale;
   p.v_scale = a.v_scale;
+  p.inject_v_tile = -1;
+  if (INJECT) std::swap(p.inject_v_tile, t_inject_v_tile);
   const unsigned grid = no_list ? (unsigned)(g.items * a.h_kv) : (unsigned)g.ctas;
   if (!no_list && !launch(plan::attn_plan_kernel, 1, plan::THREADS, 0, a.stream, pa)) return ATTN_ERR_CUDA;
-  if (!launch(attn_packed_kernel<D, KIND>, grid, C::THREADS, C::SMEM_BYTES, a.stream, mq, mk, mv, p))
+  if (!launch(attn_packed_kernel<D, KIND, INJECT>, grid, C::THREADS, C::SMEM_BYTES, a.stream, mq, mk, mv, p))
     return ATTN_ERR_CUDA;
   if (may_cut) {
     const JoinParams j = {pa.head, pa.joins, p.part, p.out,  p.lse,  p.out_ts,
@@ -1490,9 +1517,15 @@ size_t paged_chunk_workspace_bytes(int T_q, int B, int h_q, int h_kv, int d) {
 
 int launch_attn_packed(const PackedArgs& a, PFN_encodeTiled enc, void* workspace) {
   if (!a.page_table) return a.d == 64 ? run<64, DENSE>(a, enc, workspace) : run<128, DENSE>(a, enc, workspace);
+  if (t_inject_v_tile >= 0) {
+    if (!a.k_scale) return a.d == 64 ? run<64, PAGED, true>(a, enc, workspace) : run<128, PAGED, true>(a, enc, workspace);
+    return a.d == 64 ? run<64, PAGED8, true>(a, enc, workspace) : run<128, PAGED8, true>(a, enc, workspace);
+  }
   if (!a.k_scale) return a.d == 64 ? run<64, PAGED>(a, enc, workspace) : run<128, PAGED>(a, enc, workspace);
   return a.d == 64 ? run<64, PAGED8>(a, enc, workspace) : run<128, PAGED8>(a, enc, workspace);
 }
+
+void arm_chunk_give_up(int v_tile) { t_inject_v_tile = v_tile; }
 
 int read_packed_fault_word(int clear, uint32_t* out) {
   uint32_t w = 0;
