@@ -97,8 +97,8 @@ bool bad_packed(const void* x, long long tokens, int heads, int d, int64_t& ts, 
   if (heads == 1) hs = tokens == 1 || ts >= d ? d : ts;
   if (tokens == 1) ts = heads == 1 || hs >= d ? d : hs;
   if (ts < d || hs < d || ts % 8 != 0 || hs % 8 != 0 || ts > (1LL << 38) || hs > (1LL << 38)) return true;
-  if (tokens == 1 || heads == 1) return (tokens - 1) * ts > (1LL << 40) || (heads - 1) * hs > (1LL << 40);
   if (ts > (1LL << 40) / tokens || hs > (1LL << 40) / heads) return true;
+  if (tokens == 1 || heads == 1) return false;
   return ts < (heads - 1) * hs + d && hs < (tokens - 1) * ts + d;  // neither token-major nor head-major: rows overlap
 }
 
