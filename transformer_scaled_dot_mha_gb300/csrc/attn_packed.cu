@@ -1014,7 +1014,6 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
                                C::IDESC_S, kk > 0 ? 1u : 0u, issue);
             }
             ptx::mma_commit_warp(bar(C::B_SFULL), issue);
-            if (KIND != DENSE && issue) ptx::mbar_arrive(bar(C::B_SFULL));
             ptx::mma_commit_warp(bar(C::B_EMPTY + pos.s), issue);
             pos.step(2);
           }
@@ -1039,7 +1038,7 @@ __global__ void __launch_bounds__(Cfg<D, KIND>::THREADS, Cfg<D, KIND>::CTAS_PER_
           const int n = (int)uniform(e.n), len = (int)uniform(e.str_len);
           if (n < 0) break;
           for (int j = 0; j < n && ok; ++j, ++tiles) {
-            const bool tail = KIND == DENSE && uniform((tile_of(e, j) + 1) * BN > len) != 0;
+            const bool tail = uniform((tile_of(e, j) + 1) * BN > len) != 0;
             ok = wait_warp(bar(C::B_FULL + pos.s), pos.ph, true);
             if (!ok) break;
             if (tail && issue) ptx::mbar_arrive(bar(C::B_TAILREQ));
