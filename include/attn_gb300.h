@@ -610,7 +610,8 @@ size_t attn_paged_chunk_workspace_size(int T, int n_seqs, int h_q, int h_kv, int
  *   window, sinks: as in attn_paged_decode
  *   workspace: as in attn_packed_fwd, of at least attn_paged_chunk_workspace_size(...) bytes
  * A page table entry outside [0, n_pages) names no page: its keys count as illegal. Cache rows
- * behind the length are never used, whatever they hold.
+ * behind the length are never used, whatever they hold; nor are pages of which no new token may see a row (behind
+ * its sequence's first tokens and before all windows), whatever their entries name: they may be given to others.
  * Supported: d in {64, 128}, h_q a multiple of h_kv (of at most 128 h_kv), scale > 0, any page size
  * (limits as in attn_paged_append; copies are of gcd(page_size, 128) rows, so page sizes that are
  * multiples of 8 or more are the fast ones), T below 2^28. Numerics as attn_packed_fwd, except with an

@@ -179,6 +179,7 @@ struct Params {
   int h_kv;
   const float* k_scale;
   const float* v_scale;
+  int back;  // keys further before a unit's first token are not for it, unless they are first tokens
   int inject_v_tile;  // INJECT: the values' copying warps give up before this tile
 };
 
@@ -278,19 +279,22 @@ struct PageRows {
   __device__ __forceinline__ int boxes() const { return BN >> shift; }                     // per tile
   __device__ __forceinline__ int tiles() const { return 1 << (shift >= 2 ? shift - 2 : 0); }  // per look-up
 
-  __device__ __forceinline__ void look(int key, int seq, int len, int& id_, int& in_) const {
+  // The page of the n keys from `key` on (a box, or one row). NONE behind the length, and where all of them lie between
+  // the first tokens and the windows of the unit's tokens: such a page may be another sequence's by now and hold
+  // anything, and 0 times infinity is NaN.
+  __device__ __forceinline__ void look(int key, int n, const plan::Entry& e, int& id_, int& in_) const {
     id_ = NONE;
     in_ = 0;
-    if (key < len) {
+    if (key < e.str_len && (key + n > e.pos - p.back || key < p.sinks)) {
       const int page = key / p.page_size;
       in_ = key - page * p.page_size;
-      id_ = max(p.page_table[(size_t)seq * p.max_pages + page], -1);  // any bad one, but never NONE
+      id_ = max(p.page_table[(size_t)e.str_row * p.max_pages + page], -1);  // any bad one, but never NONE
     }
   }
   // Page numbers of list entries j .. j + tiles() - 1 of a unit, for take(); nothing waits for them here.
   __device__ __forceinline__ void ask(const plan::Entry& e, int j) {
     const int at = j + (lane >> (7 - shift));
-    look(at < e.n ? tile_of(e, at) * BN + ((lane & (boxes() - 1)) << shift) : e.str_len, e.str_row, e.str_len, next_id, next_in);
+    look(at < e.n ? tile_of(e, at) * BN + ((lane & (boxes() - 1)) << shift) : e.str_len, 1 << shift, e, next_id, next_in);
   }
   __device__ __forceinline__ void take() {
     id = next_id;
@@ -310,7 +314,7 @@ struct PageRows {
   // Without `ahead` (pages of one or two rows, or odd ones): row 32 k + lane of the tile.
   __device__ __forceinline__ int row_of(int k, int key0, const plan::Entry& e) const {
     int i, r;
-    look(key0 + k * 32 + lane, e.str_row, e.str_len, i, r);
+    look(key0 + k * 32 + lane, 1, e, i, r);
     return place(i, r, e.hk);
   }
   // The bits of keys of bad pages go to fl[1 .. 4], and whether there are any to fl[0].
@@ -1483,6 +1487,7 @@ int run(const PackedArgs& a, PFN_encodeTiled enc, void* workspace) {
   p.h_kv = a.h_kv;
   p.k_scale = a.k_scale;
   p.v_scale = a.v_scale;
+  p.back = a.window >= 0 ? a.window : 1 << 30;  // no sequence is longer
   p.inject_v_tile = -1;
   if (INJECT) std::swap(p.inject_v_tile, t_inject_v_tile);
   const unsigned grid = no_list ? (unsigned)(g.items * a.h_kv) : (unsigned)g.ctas;
