@@ -576,7 +576,8 @@ size_t attn_packed_bwd_workspace_size(int T_q, int T_k, int n_seqs, int h_q, int
  *   workspace: as in attn_packed_fwd, of at least attn_packed_bwd_workspace_size(...) bytes
  * Written for every row of every sequence: a key that no query may see gets dk = dv = 0, a query
  * with no legal key dq = 0. Rows of no sequence are not used and left as they were. What other
- * sequences' rows hold, infinities and NaN included, does not reach a sequence.
+ * sequences' rows hold, infinities and NaN included, does not reach a sequence; within a sequence those of a row of q,
+ * k or dout may reach the gradients of every row that meets its 128-row tile, masked or not.
  * Supported: as attn_packed_fwd. Numerics as attn_bwd: fp32 accumulation on the tensor cores, P and dS
  * rounded to bf16, results rounded to bf16 once; no atomics: the same bits on every run. Three or
  * four launches on `stream`.
@@ -612,10 +613,13 @@ size_t attn_paged_chunk_workspace_size(int T, int n_seqs, int h_q, int h_kv, int
  * A page table entry outside [0, n_pages) names no page: its keys count as illegal. Cache rows
  * behind the length are never used, whatever they hold; nor are pages of which no new token may see a row (behind
  * its sequence's first tokens and before all windows), whatever their entries name: they may be given to others.
+ * As in attn_packed_fwd, and unlike attn_paged_decode, infinities and NaN in a value row that some new token sees may
+ * reach every new token whose 128-key tile holds it, masked or not.
  * Supported: d in {64, 128}, h_q a multiple of h_kv (of at most 128 h_kv), scale > 0, any page size
  * (limits as in attn_paged_append; copies are of gcd(page_size, 128) rows, so page sizes that are
- * multiples of 8 or more are the fast ones), T below 2^28. Numerics as attn_packed_fwd, except with an
- * 8-bit cache: its numbers enter the products exactly, as f16, and the operands beside them are f16
+ * multiples of 8 or more are the fast ones), T below 2^28. Numerics as attn_packed_fwd (over bf16 pages the weights are
+ * rounded to bf16, where attn_paged_decode keeps two parts of each: where values cancel, a token's output can be off
+ * by more than its own rounding), except with an 8-bit cache: its numbers enter the products exactly, as f16, and the operands beside them are f16
  * too, each row of q times a power of two (exact but for entries below 2^-28 of the row's largest, which
  * are rounded to 2^-39 of it) and the weights (rounded to 11 bits; those below 2^-32 of the row's largest
  * may vanish). One to three launches on `stream`.

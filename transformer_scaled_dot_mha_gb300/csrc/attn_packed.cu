@@ -260,8 +260,8 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;
 // gcd(page size, 128), which no page border cuts.
 // Boxes of 8 rows and more (the swizzle's period) go by TMA, a lane issuing each, smaller and partly filled ones by
 // cp.async. With 16 rows a page, TMA against cp.async: 509 tokens over 60001 keys of 8 bits, 64/8 heads of 128,
-// 826 us against 1122; 16 prompts' pieces, 16/4 heads of 64, window 1023, 110 against 116. With 8 rows 886
-// against 1384 and 110 against 123.
+// 827 us against 1356; 16 prompts' pieces, 16/4 heads of 64, window 1023, 111 against 120. With 8 rows 892
+// against 1367 and 113 against 121.
 template <int D, int KIND>
 struct PageRows {
   static constexpr int ROW = KIND == PAGED8 ? D : 2 * D;  // bytes

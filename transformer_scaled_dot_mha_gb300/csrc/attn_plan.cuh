@@ -350,10 +350,10 @@ __device__ __forceinline__ void write(const Args& a, Scratch& sh) {
   const long long share = max((work + a.ctas - 1) / a.ctas, (long long)a.min_share);
   // cut: one is far longer than an even share, or a few long ones would leave CTAs without work at the end. A piece
   // costs its CTA some ten tiles' time (its sums go through memory), so unevenness is often the better choice:
-  // cut against whole, forward, 4096 positions, 16 heads of 128, causal (shares of 28 tiles) 110.7 and 72.7 us, 4 x 1024
-  // unmasked (14) 60.8 and 42.1, but 8192 unmasked (216) 358.8 and 386, 509 tokens over 60510 keys of 8 bits (398; 128
-  // units for 152 CTAs) 785 and 868; gradients, 4096 causal (56) 383 and 246, but 8192 causal, 32/8 heads (438) 1690
-  // and 1724.
+  // cut against whole, forward, 4096 positions, 16 heads of 128, causal (shares of 28 tiles) 111.5 and 72.7 us, 4 x 1024
+  // unmasked (14) 62.5 and 42.3, but 8192 unmasked (216) 357.5 and 383, 509 tokens over 60510 keys of 8 bits (398; 128
+  // units for 152 CTAs) 782 and 877; gradients, 4096 causal (56) 382 and 260, but 8192 causal, 32/8 heads (438), with
+  // the pass that owns keys cut (512 units) 1632 and 1697.
   const bool cut = a.may_cut && (top > share + share / 2 || (share >= LONG_SHARE && units <= (long long)FEW * a.ctas));
   if (t == 0) {
     a.head->cut = cut;
