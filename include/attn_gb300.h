@@ -613,8 +613,8 @@ size_t attn_paged_chunk_workspace_size(int T, int n_seqs, int h_q, int h_kv, int
  * A page table entry outside [0, n_pages) names no page: its keys count as illegal. Cache rows
  * behind the length are never used, whatever they hold; nor are pages of which no new token may see a row (behind
  * its sequence's first tokens and before all windows), whatever their entries name: they may be given to others.
- * As in attn_packed_fwd, and unlike attn_paged_decode, infinities and NaN in a value row that some new token sees may
- * reach every new token whose 128-key tile holds it, masked or not.
+ * As in attn_packed_fwd, and unlike attn_paged_decode, infinities and NaN in a value row of the other pages may reach
+ * every new token of its sequence whose 128-key tile holds it, masked or not.
  * Supported: d in {64, 128}, h_q a multiple of h_kv (of at most 128 h_kv), scale > 0, any page size
  * (limits as in attn_paged_append; copies are of gcd(page_size, 128) rows, so page sizes that are
  * multiples of 8 or more are the fast ones), T below 2^28. Numerics as attn_packed_fwd (over bf16 pages the weights are
